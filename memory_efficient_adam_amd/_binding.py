@@ -154,9 +154,9 @@ def _check_step_tensors(state, params, grads):
 _CHECKED_SETS = 8  # tensor sets remembered per state (callers rotate gradient buffers)
 
 
-def _checked_pointers(state, params, grads):
+def _checked_pointers(state, params, grads, check=_check_step_tensors):
     """Device pointer arrays (ctypes) of params and grads.  The full tensor
-    checks run when the (params, grads) tensor objects and their data
+    checks (`check`) run when the (params, grads) tensor objects and their data
     pointers are not among the last few sets checked on this state: a caller
     stepping the same tensors, or rotating a few gradient buffers, pays two
     passes of data_ptr() and an identity compare (~0.25 us per tensor)
@@ -170,14 +170,14 @@ def _checked_pointers(state, params, grads):
         pp = list(map(ptr, params))
         gp = list(map(ptr, grads))
     except (TypeError, AttributeError):
-        _check_step_tensors(state, params, grads)  # raises the precise error
+        check(state, params, grads)  # raises the precise error
         raise
     sets = state._checked
     for c in sets:
         if (c[2] == pp and c[3] == gp and len(c[0]) == len(params) and len(c[1]) == len(grads)
                 and all(map(operator.is_, c[0], params)) and all(map(operator.is_, c[1], grads))):
             return c[4], c[5]
-    _check_step_tensors(state, params, grads)
+    check(state, params, grads)
     n = max(len(state.numels), 1)
     P = (ctypes.c_void_p * n)(*pp)
     G = (ctypes.c_void_p * n)(*gp)

@@ -15,6 +15,7 @@
 
 #include "adam_internal.h"
 #include "adam_mi355x.h"
+#include "runtime_common.h"
 
 using namespace adam_mi355x;
 
@@ -260,6 +261,8 @@ void fill_scalars(StepArgs &a, const adam_hparams *hp) {
 }
 
 }  // namespace
+
+int adam_mi355x::set_last_error(int code, const std::string &msg) { return fail(code, msg); }
 
 extern "C" {
 

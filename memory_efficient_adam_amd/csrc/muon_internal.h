@@ -1,0 +1,133 @@
+// Internal interface between the host runtime and the gfx950 kernels of the
+// Muon step and the Newton-Schulz orthogonalisation.
+#pragma once
+
+#include <hip/hip_runtime_api.h>
+#include <stdint.h>
+
+#include "adam_internal.h"
+
+namespace adam_mi355x {
+
+// One matrix of a launch.  Its factor X is short x long (m x n, m <= n), the
+// transpose of the user's matrix when that is tall.  A factor is kept as an
+// "image": cut into row blocks of T rows, each row block into slabs of 128
+// bytes per row, a slab's T x 128 bytes contiguous, slabs of a row block
+// contiguous, row blocks contiguous.  Dimensions are padded to multiples of
+// T with zeros, which every product keeps zero.  In a row's 128 bytes the
+// eight 16-byte chunks are stored at position chunk ^ (row % 8), so that a
+// slab copied to LDS as it is can be read by rows without bank conflicts.
+//   split slabs (two fp16 values per element): 32 elements, chunks 0..3 the
+//     high parts of 8 elements each, 4..7 the remainders;
+//   plain slabs (one fp16 value per element): 64 elements, 8 per chunk.
+struct MuonMat {
+    uint64_t x_off;   // byte offset in each of the X arrays
+    uint64_t a_off;   // byte offset in the A and P arrays
+    uint64_t u_off;   // element offset of the source matrix in its array
+    uint64_t o_off;   // element offset of the output matrix in its array
+    uint64_t u_ld, o_ld;  // row strides of source and output, in elements
+    uint32_t mb, nb;  // row blocks of the short and of the long side
+    uint32_t rows, cols;
+    uint32_t tall;        // rows > cols
+    uint32_t index;       // tensor index (pointer table, scale factors)
+    uint32_t norm;        // index of its first partial sum of squares
+    uint32_t pad;
+    double scale_spectral, scale_rms;
+};
+static_assert(sizeof(MuonMat) == 96, "matrix descriptor layout");
+
+// One workgroup's tile: matrix, row block, column block.
+struct MuonTile {
+    uint32_t mat;
+    uint16_t ti, tj;
+};
+static_assert(sizeof(MuonTile) == 8, "tile descriptor is one 8-byte load");
+
+// Which matrices and tiles a launch covers: a table (tiles != NULL), or
+// `count` matrices alike, whose descriptors are `one` advanced by the
+// strides, with per_mat tiles each.
+struct MuonWork {
+    const MuonTile *tiles;
+    const MuonMat *mats;
+    uint32_t n_tiles;
+    uint32_t per_mat;
+    MuonMat one;
+    uint64_t x_stride, a_stride, u_stride, o_stride;
+    uint32_t norm_stride;
+    uint32_t pad;
+};
+
+// The factor arrays of one group of matrices.
+struct MuonArrays {
+    char *x[2], *xt[2];  // X and X^T, before and after an iteration
+    char *a, *p;         // A = X X^T and the polynomial P
+};
+
+// How one factor is held: split or plain slabs.
+enum MuonForm : int { kSplit = 0, kPlain = 1 };
+
+// Sum of squares: one fp64 partial per workgroup, per matrix n_partials.
+struct MuonSumArgs {
+    const void *u;
+    double *partials;
+    uint32_t n_partials;
+};
+
+struct MuonPrepArgs {
+    const void *u;
+    const double *partials;
+    uint32_t n_partials;
+    uint32_t pad;
+    double eps;
+    char *x, *xt;
+};
+
+struct MuonGemmArgs {
+    MuonWork work;
+    const char *left, *right;  // factor images, both with K along the rows
+    const char *add;           // A (polynomial only)
+    char *out, *out_t;         // images written (out_t: X^T)
+    float ca, cb, cc;          // polynomial coefficients
+    // last product: where O goes
+    const TensorRef *tensors;  // params (step), by MuonMat::index
+    void *o;                   // output array (orthogonalisation)
+    double lr;
+    float decay;
+    int32_t scale;
+};
+
+// ---------------------------------------------------------------- momentum
+struct MuonStepArgs {
+    const BlockDesc *desc;
+    const TensorRef *tensors;
+    const uint64_t *draw_first;
+    void *m_state;       // bf16 / int8 codes / fp32
+    float *m_scale;      // per block (Q8)
+    float *u;            // the group's update matrices, flat as the state's segments
+    double *partials;    // per block: sum of squares of u
+    uint64_t u_base;     // flat state index of u[0]
+    uint32_t slot_base;  // scale slot of partials[0]
+    uint32_t n_blocks;
+    float beta, omb;
+    uint32_t nesterov;
+    uint32_t seed_lo, seed_hi, t_lo, t_hi;
+};
+
+enum MuonStorage : int { kMuonBf16 = 1, kMuonQ8 = 2, kMuonF32 = 3 };
+
+hipError_t launch_muon_momentum(int storage, bool grad_bf16, bool stochastic, const MuonStepArgs &a, hipStream_t s);
+// sums[mats[i].norm] = the sum of matrix i's block partials
+// [ranges[i].x, ranges[i].y), in a fixed order
+hipError_t launch_muon_norms(const double *partials, const uint2 *ranges, double *sums, uint32_t n_mats,
+                             hipStream_t s);
+hipError_t launch_muon_sums(bool bf16, const MuonWork &w, const MuonSumArgs &a, uint32_t n_mats, hipStream_t s);
+hipError_t launch_muon_prep(int tile, bool bf16, int form, const MuonWork &w, const MuonPrepArgs &a, hipStream_t s);
+
+enum MuonProduct : int { kGram, kPolynomial, kUpdate, kLastBf16, kLastF32, kLastParams };
+// in: the form of the factors read; out: of the factor written
+hipError_t launch_muon_product(int tile, int product, int in, int out, const MuonGemmArgs &a, hipStream_t s);
+
+hipError_t launch_muon_decode(int storage, const BlockDesc *desc, uint32_t n_blocks, const void *m_state,
+                              const float *m_scale, void *dst, hipStream_t s);
+
+}  // namespace adam_mi355x

@@ -1,0 +1,763 @@
+// Muon on gfx950 (MI355X): the momentum update and the Newton-Schulz
+// orthogonalisation of its result.
+//
+// The orthogonalisation is matrix products: per iteration A = X X^T,
+// P = a I + b A + c A^2 and X <- P X, with X short x long (m x n).  They run
+// on the fp16 matrix cores at fp32's accuracy: a factor is held as
+// hi + lo, two fp16 values (22 bits), and hi hi + hi lo + lo hi is summed in
+// fp32 (what is left out is below 2^-22 of the product).  Three fp16 products cost
+// a quarter of what the fp32 matrix instructions take for one.  The factors
+// are scaled by a power of two, so that no part of an entry that matters
+// falls below fp16's range (X and A by 2^10, P by 2^8: an entry of 2^-13 still
+// has all 22 bits, smaller ones an error of 2^-35).  A and P are symmetric:
+// only tiles on and below the diagonal are computed, and stored twice.  The
+// term a X is a I in P, so that an update reads X once, as a factor.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "muon_internal.h"
+
+namespace adam_mi355x {
+namespace {
+
+constexpr float kTiny = 0x1p-112f;  // smallest block maximum that is encoded (8-bit momentum)
+constexpr float kScaleX = 1024.0f;  // X and A are held times 2^10
+constexpr float kScaleP = 256.0f;   // P is held times 2^8
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 half8 __attribute__((ext_vector_type(8)));
+
+// ---------------------------------------------------------------- small helpers
+__device__ __forceinline__ float bf16_to_f32(uint32_t h) { return __uint_as_float(h << 16); }
+
+// Round to nearest, ties to even, on the upper 16 bits; NaN -> 0x7FC0.
+__device__ __forceinline__ uint32_t f32_to_bf16(float x) {
+    if (x != x) return 0x7FC0u;
+    const uint32_t u = __float_as_uint(x);
+    return (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
+}
+
+template <bool kBf16>
+__device__ __forceinline__ float load_elem(const void *p, uint64_t i) {
+    if constexpr (kBf16)
+        return bf16_to_f32(static_cast<const uint16_t *>(p)[i]);
+    else
+        return static_cast<const float *>(p)[i];
+}
+
+// An fp32 value as hi + lo, packed low half first: {hi, lo}.
+__device__ __forceinline__ void split(float y, _Float16 &hi, _Float16 &lo) {
+    hi = (_Float16)y;
+    lo = (_Float16)(y - (float)hi);
+}
+__device__ __forceinline__ uint32_t pack(_Float16 a, _Float16 b) {
+    return (uint32_t)__builtin_bit_cast(uint16_t, a) | ((uint32_t)__builtin_bit_cast(uint16_t, b) << 16);
+}
+
+// Sum over the workgroup's 256 threads in a fixed order (s: 4 doubles).
+__device__ __forceinline__ double block_sum(double x, double *s) {
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) x += __shfl_xor(x, d, 64);
+    if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = x;
+    __syncthreads();
+    return (s[0] + s[1]) + (s[2] + s[3]);
+}
+
+// Consecutive tiles share factor rows, and workgroups are dealt to the 8 XCDs
+// (each with an L2 of its own) in turn: workgroup id takes the tile that
+// keeps each XCD on one run of consecutive tiles.
+__device__ __forceinline__ uint32_t xcd_order(uint32_t id, uint32_t n) {
+    const uint32_t xcd = id & 7u, per = n >> 3, rest = n & 7u;
+    return xcd * per + min(xcd, rest) + (id >> 3);
+}
+
+typedef const __attribute__((address_space(4))) MuonMat *ConstMatPtr;
+typedef const __attribute__((address_space(4))) MuonTile *ConstTilePtr;
+typedef const __attribute__((address_space(4))) BlockDesc *ConstDescPtr;
+typedef const __attribute__((address_space(4))) TensorRef *ConstTensorPtr;
+typedef const __attribute__((address_space(4))) uint64_t *ConstU64Ptr;
+
+// The matrix of a launch and, in t, the index of the tile within it (alike
+// matrices) or its packed row and column blocks (table).
+__device__ __forceinline__ MuonMat find_mat(const MuonWork &w, uint32_t id, uint32_t &t) {
+    MuonMat m;
+    if (w.tiles) {
+        const ConstTilePtr e = (ConstTilePtr)w.tiles + id;
+        const ConstMatPtr p = (ConstMatPtr)w.mats + e->mat;
+        t = (uint32_t)e->ti | ((uint32_t)e->tj << 16);
+        __builtin_memcpy(&m, (const void *)p, sizeof(m));
+    } else {
+        const uint32_t k = id / w.per_mat;
+        t = id - k * w.per_mat;
+        m = w.one;
+        m.x_off += k * w.x_stride;
+        m.a_off += k * w.a_stride;
+        m.u_off += k * w.u_stride;
+        m.o_off += k * w.o_stride;
+        m.norm += k * w.norm_stride;
+        m.index = k;
+    }
+    return m;
+}
+
+// Tile t of a lower triangle, row by row: ti >= tj.
+__device__ __forceinline__ void triangle(uint32_t t, uint32_t &ti, uint32_t &tj) {
+    uint32_t r = (uint32_t)((sqrtf(8.0f * (float)t + 1.0f) - 1.0f) * 0.5f);
+    while (r * (r + 1u) / 2u > t) --r;
+    while ((r + 1u) * (r + 2u) / 2u <= t) ++r;
+    ti = r;
+    tj = t - r * (r + 1u) / 2u;
+}
+
+// Tile t of an mb x nb grid, in bands of 8 block rows taken column by column:
+// the workgroups of an XCD that run together then share both factors' rows.
+__device__ __forceinline__ void banded(uint32_t t, uint32_t mb, uint32_t nb, uint32_t &ti, uint32_t &tj) {
+    const uint32_t band = t / (8u * nb), first = band * 8u, high = min(8u, mb - first), in = t - band * 8u * nb;
+    ti = first + in % high;
+    tj = in / high;
+}
+
+// ---------------------------------------------------------------- images
+// Byte position within one T-row block of element `k` (a multiple of 4) of
+// row `r`: its high part; the remainder is at ^ 64 (split form).
+template <int T, int kForm>
+__device__ __forceinline__ uint32_t image_pos(uint32_t r, uint32_t k) {
+    constexpr uint32_t kPer = kForm == kSplit ? 32u : 64u;
+    const uint32_t slab = k / kPer, chunk = (k % kPer) >> 3;
+    return slab * (T * 128u) + r * 128u + ((chunk ^ (r & 7u)) << 4) + (k & 7u) * 2u;
+}
+template <int kForm>
+constexpr uint32_t elem_bytes() { return kForm == kSplit ? 4u : 2u; }
+
+// ---------------------------------------------------------------- products
+// 16 bytes per lane from memory straight to LDS: lane i's go to base + 16 i.
+__device__ __forceinline__ void dma16(const char *g, char *base) {
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)g,
+                                     (__attribute__((address_space(3))) void *)base, 16, 0, 0);
+}
+
+template <int T>
+struct Tile {
+    static constexpr int kSlab = T * 128;          // bytes of one factor's slab
+    static constexpr int kWave = T / 2;            // a wave's part of the tile, square
+    static constexpr int kBlocks = kWave / 32;     // 32 x 32 blocks along it
+    static constexpr int kLds = 4 * kSlab;         // two slabs of two factors; the tile's image fits too
+    static_assert(T * T * 4 <= kLds, "image fits");
+};
+
+template <int T>
+__device__ __forceinline__ void fetch(const char *left, const char *right, char *lds, int wave, int tid) {
+#pragma unroll
+    for (int j = 0; j < Tile<T>::kSlab / 4096; ++j) {
+        dma16(left + j * 4096 + tid * 16, lds + j * 4096 + wave * 1024);
+        dma16(right + j * 4096 + tid * 16, lds + Tile<T>::kSlab + j * 4096 + wave * 1024);
+    }
+}
+
+__device__ __forceinline__ half8 frag(const char *rows, uint32_t row, uint32_t chunk) {
+    return *reinterpret_cast<const half8 *>(rows + row * 128u + ((chunk ^ (row & 7u)) << 4));
+}
+
+// sum = left right^T over `slabs` slabs, summed in runs of kRun slabs: one sum
+// that took every term of a long row in turn would lose more to fp32's
+// rounding than the split factors do.  Slab s + 1 is on its way to one half of
+// LDS while the matrix cores work on slab s from the other; one barrier a
+// slab, at which every wave has read slab s - 1 and its own part of slab s
+// has arrived.
+constexpr uint32_t kRun = 8;
+
+template <int T, int kForm>
+__device__ __forceinline__ void product(f32x16 (&sum)[Tile<T>::kBlocks][Tile<T>::kBlocks], const char *left,
+                                        const char *right, uint32_t slabs, char *lds) {
+    constexpr int kB = Tile<T>::kBlocks, kSteps = kForm == kSplit ? 2 : 4;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const uint32_t row_l = (wave >> 1) * Tile<T>::kWave + (lane & 31), row_r = (wave & 1) * Tile<T>::kWave + (lane & 31);
+    const uint32_t half = lane >> 5;
+    f32x16 acc[kB][kB];
+#pragma unroll
+    for (int i = 0; i < kB; ++i)
+#pragma unroll
+        for (int j = 0; j < kB; ++j) sum[i][j] = acc[i][j] = f32x16{};
+    fetch<T>(left, right, lds, wave, tid);
+    for (uint32_t s = 0; s < slabs; ++s) {
+        __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+        __syncthreads();
+        const char *here = lds + (s & 1u) * (2 * Tile<T>::kSlab);
+        half8 l[kSteps][kB], r[kSteps][kB], l2[kSteps][kB], r2[kSteps][kB];
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+            for (int i = 0; i < kB; ++i) {
+                const uint32_t c = k * 2 + half;
+                l[k][i] = frag(here, row_l + i * 32, c);
+                r[k][i] = frag(here + Tile<T>::kSlab, row_r + i * 32, c);
+                if constexpr (kForm == kSplit) {
+                    l2[k][i] = frag(here, row_l + i * 32, c + 4);
+                    r2[k][i] = frag(here + Tile<T>::kSlab, row_r + i * 32, c + 4);
+                }
+            }
+        if (s + 1 < slabs) {
+            left += Tile<T>::kSlab;
+            right += Tile<T>::kSlab;
+            fetch<T>(left, right, lds + ((s + 1) & 1u) * (2 * Tile<T>::kSlab), wave, tid);
+        }
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+            for (int i = 0; i < kB; ++i)
+#pragma unroll
+                for (int j = 0; j < kB; ++j) {
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(l[k][i], r[k][j], acc[i][j], 0, 0, 0);
+                    if constexpr (kForm == kSplit) {
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(l[k][i], r2[k][j], acc[i][j], 0, 0, 0);
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(l2[k][i], r[k][j], acc[i][j], 0, 0, 0);
+                    }
+                }
+        if ((s & (kRun - 1)) == kRun - 1 || s + 1 == slabs) {
+#pragma unroll
+            for (int i = 0; i < kB; ++i)
+#pragma unroll
+                for (int j = 0; j < kB; ++j) {
+                    sum[i][j] += acc[i][j];
+                    acc[i][j] = f32x16{};
+                }
+        }
+    }
+}
+
+// Four values down the rows of one column per lane -> four along a row: a
+// 4 x 4 transpose of 16-bit values over each quad of lanes (two exchanges
+// with the neighbouring lanes).  In: d = rows 0..3 of column lane % 4; out:
+// columns 0..3 of row lane % 4.
+__device__ __forceinline__ u32x2 quad_transpose(u32x2 d, uint32_t lane) {
+    const uint32_t n0 = (uint32_t)__builtin_amdgcn_mov_dpp((int)d.x, 0xB1, 0xF, 0xF, true);
+    const uint32_t n1 = (uint32_t)__builtin_amdgcn_mov_dpp((int)d.y, 0xB1, 0xF, 0xF, true);
+    // even lane: {own low, neighbour's low}; odd: {neighbour's high, own high}
+    // (v_perm_b32: selector bytes 0..3 take the second operand's bytes, 4..7 the first's)
+    const uint32_t sel = (lane & 1u) ? 0x03020706u : 0x05040100u;
+    const uint32_t e0 = __builtin_amdgcn_perm(n0, d.x, sel), e1 = __builtin_amdgcn_perm(n1, d.y, sel);
+    const uint32_t m0 = (uint32_t)__builtin_amdgcn_mov_dpp((int)e0, 0x4E, 0xF, 0xF, true);
+    const uint32_t m1 = (uint32_t)__builtin_amdgcn_mov_dpp((int)e1, 0x4E, 0xF, 0xF, true);
+    return (lane & 2u) ? u32x2{m1, e1} : u32x2{e0, m0};
+}
+
+// The tile's values as the image of C (rows r, elements along c) or, with
+// kTransposed, of C^T, assembled in LDS and copied out: one contiguous piece
+// of the destination's row block.
+template <int T, int kForm, bool kTransposed>
+__device__ __forceinline__ void store_image(const f32x16 (&v)[Tile<T>::kBlocks][Tile<T>::kBlocks], char *lds, char *dst) {
+    constexpr int kB = Tile<T>::kBlocks;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const uint32_t r00 = (wave >> 1) * Tile<T>::kWave + 4 * (lane >> 5), c00 = (wave & 1) * Tile<T>::kWave + (lane & 31);
+    __syncthreads();  // LDS is free: the last slab, or the image before, has been read
+#pragma unroll
+    for (int i = 0; i < kB; ++i)
+#pragma unroll
+        for (int j = 0; j < kB; ++j)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                _Float16 hi[4], lo[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) split(v[i][j][4 * g + q], hi[q], lo[q]);
+                u32x2 h = {pack(hi[0], hi[1]), pack(hi[2], hi[3])}, l = {pack(lo[0], lo[1]), pack(lo[2], lo[3])};
+                uint32_t at;
+                const uint32_t r = r00 + i * 32 + 8 * g, c = c00 + j * 32;
+                if constexpr (kTransposed) {
+                    at = image_pos<T, kForm>(c, r);
+                } else {
+                    h = quad_transpose(h, lane);
+                    l = quad_transpose(l, lane);
+                    at = image_pos<T, kForm>(r + (lane & 3), c & ~3u);
+                }
+                *reinterpret_cast<u32x2 *>(lds + at) = h;
+                if constexpr (kForm == kSplit) *reinterpret_cast<u32x2 *>(lds + (at ^ 64u)) = l;
+            }
+    __syncthreads();
+    constexpr int kBytes = T * T * (int)elem_bytes<kForm>();
+#pragma unroll
+    for (int o = 0; o < kBytes; o += 4096)
+        *reinterpret_cast<u32x4 *>(dst + o + tid * 16) = *reinterpret_cast<const u32x4 *>(lds + o + tid * 16);
+}
+
+// The tiles of one product over all matrices of a launch.
+//   kGram:       A = X X^T                        tiles ti >= tj, stored at both places
+//   kPolynomial: P = a I + b A + c A A^T          the same
+//   kUpdate:     X' = P X, stored as X' and X'^T
+//   kLast..:     O = P X in the user's orientation (for a tall matrix the
+//                factors change places), rounded to the output's type, or
+//                applied to the params
+template <int T, int kProduct, int kIn, int kOut>
+__global__ __launch_bounds__(256) void muon_product_kernel(MuonGemmArgs a) {
+    __shared__ __attribute__((aligned(128))) char lds[Tile<T>::kLds];
+    constexpr int kB = Tile<T>::kBlocks;
+    constexpr bool kLast = kProduct >= kLastBf16, kSquare = kProduct == kGram || kProduct == kPolynomial;
+    constexpr uint32_t kPer = kIn == kSplit ? 32u : 64u;
+    uint32_t t, ti, tj;
+    const MuonMat m = find_mat(a.work, xcd_order(blockIdx.x, a.work.n_tiles), t);
+    if (a.work.tiles) {
+        ti = t & 0xFFFFu;
+        tj = t >> 16;
+    } else if constexpr (kSquare) {
+        triangle(t, ti, tj);
+    } else {
+        banded(t, m.mb, m.nb, ti, tj);
+    }
+    const uint32_t k = (kProduct == kGram ? m.nb : m.mb) * T;  // length of the products
+    const uint64_t row_block = (uint64_t)T * k * elem_bytes<kIn>();
+    const bool swap = kLast && m.tall;
+    const char *left, *right;
+    if constexpr (kSquare) {
+        const char *f = a.left + (kProduct == kGram ? m.x_off : m.a_off);
+        left = f + ti * row_block;
+        right = f + tj * row_block;
+    } else {
+        left = a.left + m.a_off + ti * row_block;
+        right = a.right + m.x_off + tj * row_block;
+        if (swap) {
+            const char *x = left;
+            left = right;
+            right = x;
+        }
+    }
+    f32x16 acc[kB][kB];
+    product<T, kIn>(acc, left, right, k / kPer, lds);
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const uint32_t r00 = (wave >> 1) * Tile<T>::kWave + 4 * (lane >> 5), c00 = (wave & 1) * Tile<T>::kWave + (lane & 31);
+    if constexpr (kProduct == kGram) {
+#pragma unroll
+        for (int i = 0; i < kB; ++i)
+#pragma unroll
+            for (int j = 0; j < kB; ++j) acc[i][j] *= 1.0f / kScaleX;
+    } else if constexpr (kProduct == kPolynomial) {
+        // A's tile, read from its mirror image: four values down a column lie side by side
+        const char *add = a.add + m.a_off + tj * row_block + (uint64_t)ti * (T / kPer) * Tile<T>::kSlab;
+        const float cb = a.cb * (kScaleP / kScaleX), cc = a.cc * (kScaleP / (kScaleX * kScaleX)), ca = a.ca * kScaleP;
+#pragma unroll
+        for (int i = 0; i < kB; ++i)
+#pragma unroll
+            for (int j = 0; j < kB; ++j)
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const uint32_t r = r00 + i * 32 + 8 * g, c = c00 + j * 32, at = image_pos<T, kIn>(c, r);
+                    const u32x2 h = *reinterpret_cast<const u32x2 *>(add + at);
+                    u32x2 l = {0u, 0u};
+                    if constexpr (kIn == kSplit) l = *reinterpret_cast<const u32x2 *>(add + (at ^ 64u));
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const uint32_t hw = q < 2 ? h.x : h.y, lw = q < 2 ? l.x : l.y;
+                        const float av = (float)__builtin_bit_cast(_Float16, (uint16_t)(hw >> (16 * (q & 1)))) +
+                                         (float)__builtin_bit_cast(_Float16, (uint16_t)(lw >> (16 * (q & 1))));
+                        float v = fmaf(cb, av, cc * acc[i][j][4 * g + q]);
+                        if (ti == tj && r + q == c) v += ca;
+                        acc[i][j][4 * g + q] = v;
+                    }
+                }
+    } else if constexpr (kProduct == kUpdate) {
+#pragma unroll
+        for (int i = 0; i < kB; ++i)
+#pragma unroll
+            for (int j = 0; j < kB; ++j) acc[i][j] *= 1.0f / kScaleP;
+    }
+
+    if constexpr (kSquare) {
+        char *out = a.out + m.a_off;
+        constexpr uint64_t kPerOut = kOut == kSplit ? 32 : 64;
+        const uint64_t rb = (uint64_t)T * m.mb * T * elem_bytes<kOut>();
+        store_image<T, kOut, true>(acc, lds, out + tj * rb + ti * (T / kPerOut) * Tile<T>::kSlab);
+        if (ti != tj) store_image<T, kOut, false>(acc, lds, out + ti * rb + tj * (T / kPerOut) * Tile<T>::kSlab);
+    } else if constexpr (kProduct == kUpdate) {
+        constexpr uint64_t kPerOut = kOut == kSplit ? 32 : 64;
+        const uint64_t rb = (uint64_t)T * m.nb * T * elem_bytes<kOut>(), rb_t = (uint64_t)T * m.mb * T * elem_bytes<kOut>();
+        store_image<T, kOut, false>(acc, lds, a.out + m.x_off + ti * rb + tj * (T / kPerOut) * Tile<T>::kSlab);
+        store_image<T, kOut, true>(acc, lds, a.out_t + m.x_off + tj * rb_t + ti * (T / kPerOut) * Tile<T>::kSlab);
+    } else {
+        const uint32_t row0 = (swap ? tj : ti) * T + r00, col0 = (swap ? ti : tj) * T + c00;
+        constexpr float kUnscale = 1.0f / (kScaleX * kScaleP);
+        float *p = nullptr;
+        float step = 0.0f;
+        if constexpr (kProduct == kLastParams) {
+            p = ((ConstTensorPtr)a.tensors + m.index)->p;
+            step = (float)(a.lr * (a.scale == 1 ? m.scale_spectral : (a.scale == 2 ? m.scale_rms : 1.0)));
+        }
+#pragma unroll
+        for (int i = 0; i < kB; ++i)
+#pragma unroll
+            for (int j = 0; j < kB; ++j)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const uint32_t r = row0 + i * 32 + 8 * (e / 4) + (e & 3), c = col0 + j * 32;
+                    if (r >= m.rows || c >= m.cols) continue;
+                    const float o = acc[i][j][e] * kUnscale;
+                    if constexpr (kProduct == kLastParams) {
+                        float *q = p + (uint64_t)r * m.cols + c;
+                        *q = fmaf(-step, o, *q * a.decay);
+                    } else if constexpr (kProduct == kLastBf16) {
+                        static_cast<uint16_t *>(a.o)[m.o_off + r * m.o_ld + c] = (uint16_t)f32_to_bf16(o);
+                    } else {
+                        static_cast<float *>(a.o)[m.o_off + r * m.o_ld + c] = o;
+                    }
+                }
+    }
+}
+
+// ---------------------------------------------------------------- X_0
+// Partial sums of squares of each matrix, in fp64 (a square of any finite
+// fp32 value is exact there and never overflows): workgroup w of n_partials
+// takes the 64 x 64 tiles w, w + n_partials, ..
+template <bool kBf16>
+__global__ __launch_bounds__(256) void muon_sums_kernel(MuonWork w, MuonSumArgs a) {
+    __shared__ double s[4];
+    uint32_t part;
+    const MuonMat m = find_mat(w, blockIdx.x, part);
+    const uint32_t across = (m.cols + 63u) / 64u, tiles = across * ((m.rows + 63u) / 64u);
+    const uint32_t c_in = threadIdx.x & 63u, r_in = threadIdx.x >> 6;
+    double sum = 0.0;
+    for (uint32_t t = part; t < tiles; t += a.n_partials) {
+        const uint32_t r0 = (t / across) * 64u, c = (t % across) * 64u + c_in;
+        if (c >= m.cols) continue;
+#pragma unroll
+        for (uint32_t i = 0; i < 16u; ++i) {
+            const uint32_t r = r0 + r_in + 4u * i;
+            if (r < m.rows) {
+                const double x = load_elem<kBf16>(a.u, m.u_off + r * m.u_ld + c);
+                sum += x * x;
+            }
+        }
+    }
+    sum = block_sum(sum, s);
+    if (threadIdx.x == 0) a.partials[m.norm + part] = sum;
+}
+
+// The images of X_0 and X_0^T, one 64 x 64 tile of the user's matrix a
+// workgroup.  A norm that is not finite makes all of X_0 NaN.
+template <int T, bool kBf16, int kForm>
+__global__ __launch_bounds__(256) void muon_prep_kernel(MuonWork w, MuonPrepArgs a) {
+    __shared__ double s[4];
+    __shared__ float y[64][65];
+    uint32_t t;
+    const MuonMat m = find_mat(w, blockIdx.x, t);
+    const uint32_t cb = m.tall ? m.mb : m.nb, rb = m.tall ? m.nb : m.mb;  // row blocks along columns and rows
+    uint32_t ti, tj;
+    if (w.tiles) {
+        ti = t & 0xFFFFu;
+        tj = t >> 16;
+    } else {
+        ti = t / (cb * (T / 64));
+        tj = t - ti * (cb * (T / 64));
+    }
+    double part = 0.0;
+    for (uint32_t i = threadIdx.x; i < a.n_partials; i += 256u) part += a.partials[m.norm + i];
+    const double sum = block_sum(part, s);
+    const double inv = sum < __builtin_inf() ? (double)kScaleX / (sqrt(sum) + a.eps) : __builtin_nan("");
+
+    const uint32_t c_in = threadIdx.x & 63u, r_in = threadIdx.x >> 6;
+#pragma unroll
+    for (uint32_t i = 0; i < 16u; ++i) {
+        const uint32_t r = ti * 64u + r_in + 4u * i, c = tj * 64u + c_in;
+        float v = 0.0f;
+        if (r < m.rows && c < m.cols) v = (float)((double)load_elem<kBf16>(a.u, m.u_off + r * m.u_ld + c) * inv);
+        y[r_in + 4u * i][c_in] = v;
+    }
+    __syncthreads();
+    // by user rows (elements along the columns), then by user columns
+#pragma unroll
+    for (int o = 0; o < 2; ++o) {
+        char *dst = ((o == 0) == (m.tall == 0) ? a.x : a.xt) + m.x_off;
+        const uint32_t length = (o == 0 ? cb : rb) * T;  // elements along a row of this image
+        const uint32_t row0 = (o == 0 ? ti : tj) * 64u, k0 = (o == 0 ? tj : ti) * 64u;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint32_t job = j * 256u + threadIdx.x, row = job >> 3, k = (job & 7u) * 8u;
+            u32x4 h, l;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                _Float16 h0, l0, h1, l1;
+                split(o == 0 ? y[row][k + 2 * e] : y[k + 2 * e][row], h0, l0);
+                split(o == 0 ? y[row][k + 2 * e + 1] : y[k + 2 * e + 1][row], h1, l1);
+                h[e] = pack(h0, h1);
+                l[e] = pack(l0, l1);
+            }
+            const uint32_t r = row0 + row;
+            char *at = dst + (uint64_t)(r / T) * ((uint64_t)T * length * elem_bytes<kForm>());
+            constexpr uint32_t kPer = kForm == kSplit ? 32u : 64u;
+            const uint64_t slab = (uint64_t)((k0 + k) / kPer) * Tile<T>::kSlab;
+            const uint32_t in = image_pos<T, kForm>(r % T, (k0 + k) % kPer);
+            *reinterpret_cast<u32x4 *>(at + slab + in) = h;
+            if constexpr (kForm == kSplit) *reinterpret_cast<u32x4 *>(at + slab + (in ^ 64u)) = l;
+        }
+    }
+}
+
+__global__ __launch_bounds__(256) void muon_norms_kernel(const double *partials, const uint2 *ranges, double *sums) {
+    __shared__ double s[4];
+    const uint2 range = ranges[blockIdx.x];
+    double part = 0.0;
+    for (uint32_t i = range.x + threadIdx.x; i < range.y; i += 256u) part += partials[i];
+    const double sum = block_sum(part, s);
+    if (threadIdx.x == 0) sums[blockIdx.x] = sum;
+}
+
+// ---------------------------------------------------------------- momentum
+__device__ __forceinline__ void philox4x32_10(uint32_t (&c)[4], uint32_t k0, uint32_t k1) {
+#pragma unroll
+    for (int r = 0; r < 10; ++r) {
+        const uint64_t prod0 = (uint64_t)0xD2511F53u * c[0], prod1 = (uint64_t)0xCD9E8D57u * c[2];
+        c[0] = (uint32_t)(prod1 >> 32) ^ c[1] ^ k0;
+        c[1] = (uint32_t)prod1;
+        c[2] = (uint32_t)(prod0 >> 32) ^ c[3] ^ k1;
+        c[3] = (uint32_t)prod0;
+        k0 += 0x9E3779B9u;
+        k1 += 0xBB67AE85u;
+    }
+}
+
+__device__ __forceinline__ float block_max(float x, float *s) {
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) x = fmaxf(x, __shfl_xor(x, d, 64));
+    if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = x;
+    __syncthreads();
+    return fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
+}
+
+// One 2048-element block of one matrix, as the Adam step takes its blocks:
+// thread t holds elements 4t..4t+3 and 1024+4t..1024+4t+3.  Writes the new
+// momentum, the update u (fp32) and the block's sum of u^2.
+template <int kStorage, bool kGradBf16, bool kSR>
+__global__ __launch_bounds__(256) void muon_momentum_kernel(MuonStepArgs a) {
+    __shared__ double s_sum[4];
+    __shared__ float s_max[4];
+    const ConstDescPtr d = (ConstDescPtr)a.desc + blockIdx.x;
+    const uint32_t lb_n = d->lb_n, n = (lb_n & (kBlock - 1)) + 1u, npad = (n + 15u) & ~15u, slot = d->slot;
+    const uint64_t local = (uint64_t)(lb_n >> kBlockBits) * kBlock, gidx = (uint64_t)d->gidx16 * 16u;
+    const void *g = ((ConstTensorPtr)a.tensors + d->tensor)->g;
+    float mo[8], uo[8];
+    const float old_scale = kStorage == kMuonQ8 ? a.m_scale[slot] : 0.0f;
+    double sum = 0.0;
+    float top = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const uint32_t e0 = j * 1024u + 4u * threadIdx.x;
+        float gv[4] = {0.0f, 0.0f, 0.0f, 0.0f}, mv[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (e0 + 4u <= n) {
+            if constexpr (kGradBf16) {
+                const u32x2 q = *reinterpret_cast<const u32x2 *>(static_cast<const uint16_t *>(g) + local + e0);
+                gv[0] = __uint_as_float(q.x << 16);
+                gv[1] = __uint_as_float(q.x & 0xFFFF0000u);
+                gv[2] = __uint_as_float(q.y << 16);
+                gv[3] = __uint_as_float(q.y & 0xFFFF0000u);
+            } else {
+                const f32x4 q = *reinterpret_cast<const f32x4 *>(static_cast<const float *>(g) + local + e0);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) gv[i] = q[i];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (e0 + i < n) gv[i] = load_elem<kGradBf16>(g, local + e0 + i);
+        }
+        if (e0 < npad) {
+            if constexpr (kStorage == kMuonBf16) {
+                const u32x2 q = *reinterpret_cast<const u32x2 *>(static_cast<const uint16_t *>(a.m_state) + gidx + e0);
+                mv[0] = __uint_as_float(q.x << 16);
+                mv[1] = __uint_as_float(q.x & 0xFFFF0000u);
+                mv[2] = __uint_as_float(q.y << 16);
+                mv[3] = __uint_as_float(q.y & 0xFFFF0000u);
+            } else if constexpr (kStorage == kMuonQ8) {
+                const uint32_t q = *reinterpret_cast<const uint32_t *>(static_cast<const int8_t *>(a.m_state) + gidx + e0);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) mv[i] = (float)(int8_t)(q >> (8 * i)) * (1.0f / 127.0f) * old_scale;
+            } else {
+                const f32x4 q = *reinterpret_cast<const f32x4 *>(static_cast<const float *>(a.m_state) + gidx + e0);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) mv[i] = q[i];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const bool live = e0 + i < n;  // padding takes no part, whatever it holds
+            const float gp = gv[i] * a.omb, m = live ? fmaf(a.beta, mv[i], gp) : 0.0f;
+            const float u = live ? (a.nesterov ? fmaf(a.beta, m, gp) : m) : 0.0f;
+            mo[4 * j + i] = m;
+            uo[4 * j + i] = u;
+            sum += (double)u * (double)u;
+            top = fmaxf(top, fabsf(m));
+        }
+        if (e0 < npad)  // u's segments are padded as the state's are
+            *reinterpret_cast<f32x4 *>(a.u + (gidx - a.u_base) + e0) = f32x4{uo[4 * j], uo[4 * j + 1], uo[4 * j + 2], uo[4 * j + 3]};
+    }
+    sum = block_sum(sum, s_sum);
+    if (threadIdx.x == 0) a.partials[slot - a.slot_base] = sum;
+
+    float r = 0.0f;
+    bool live = true;
+    if constexpr (kStorage == kMuonQ8) {
+        top = block_max(top, s_max);
+        live = top >= kTiny;
+        r = live ? 1.0f / top * 127.0f : 0.0f;
+        if (threadIdx.x == 0) a.m_scale[slot] = live ? top : 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const uint32_t e0 = j * 1024u + 4u * threadIdx.x;
+        if (e0 >= npad) continue;
+        const float *m = mo + 4 * j;
+        if constexpr (kStorage == kMuonBf16) {
+            *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(a.m_state) + gidx + e0) =
+                u32x2{f32_to_bf16(m[0]) | (f32_to_bf16(m[1]) << 16), f32_to_bf16(m[2]) | (f32_to_bf16(m[3]) << 16)};
+        } else if constexpr (kStorage == kMuonF32) {
+            *reinterpret_cast<f32x4 *>(static_cast<float *>(a.m_state) + gidx + e0) = f32x4{m[0], m[1], m[2], m[3]};
+        } else {
+            uint32_t ctr[4] = {0u, 0u, 0u, 0u}, codes = 0u;
+            if constexpr (kSR) {
+                const uint64_t grp = (((ConstU64Ptr)a.draw_first)[d->tensor] + local + e0) >> 2;
+                ctr[0] = (uint32_t)grp;
+                ctr[1] = (uint32_t)(grp >> 32);
+                ctr[2] = a.t_lo;
+                ctr[3] = a.t_hi;
+                philox4x32_10(ctr, a.seed_lo, a.seed_hi);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float y = fminf(fabsf(m[i]) * r, 127.0f);
+                float q;
+                if constexpr (kSR) {
+                    const float down = floorf(y), u = (float)(ctr[i] & 0xFFFFu) * 0x1p-16f;
+                    q = down + (u < y - down ? 1.0f : 0.0f);
+                } else {
+                    q = rintf(y);
+                }
+                if (fabsf(m[i]) >= top) q = 127.0f;
+                const int32_t k = live ? (int32_t)(m[i] < 0.0f ? -q : q) : 0;
+                codes |= ((uint32_t)k & 0xFFu) << (8 * i);
+            }
+            *reinterpret_cast<uint32_t *>(static_cast<int8_t *>(a.m_state) + gidx + e0) = codes;
+        }
+    }
+}
+
+// The momentum's values, padding 0: fp32, or bf16 as it is.
+template <int kStorage>
+__global__ __launch_bounds__(256) void muon_decode_kernel(const BlockDesc *desc, const void *m_state, const float *m_scale,
+                                                          void *dst) {
+    const ConstDescPtr d = (ConstDescPtr)desc + blockIdx.x;
+    const uint32_t n = (d->lb_n & (kBlock - 1)) + 1u, npad = (n + 15u) & ~15u;
+    const uint64_t gidx = (uint64_t)d->gidx16 * 16u;
+    const float scale = kStorage == kMuonQ8 ? m_scale[d->slot] : 0.0f;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const uint32_t e0 = j * 1024u + 4u * threadIdx.x;
+        if (e0 >= npad) continue;
+        if constexpr (kStorage == kMuonBf16) {
+            u32x2 q = *reinterpret_cast<const u32x2 *>(static_cast<const uint16_t *>(m_state) + gidx + e0);
+            if (e0 + 4u > n) {
+                q.x = (e0 < n ? q.x & 0xFFFFu : 0u) | (e0 + 1u < n ? q.x & 0xFFFF0000u : 0u);
+                q.y = (e0 + 2u < n ? q.y & 0xFFFFu : 0u);
+            }
+            *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(dst) + gidx + e0) = q;
+        } else {
+            f32x4 v;
+            if constexpr (kStorage == kMuonQ8) {
+                const uint32_t q = *reinterpret_cast<const uint32_t *>(static_cast<const int8_t *>(m_state) + gidx + e0);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = (float)(int8_t)(q >> (8 * i)) * (1.0f / 127.0f) * scale;
+            } else {
+                v = *reinterpret_cast<const f32x4 *>(static_cast<const float *>(m_state) + gidx + e0);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (e0 + i >= n) v[i] = 0.0f;
+            *reinterpret_cast<f32x4 *>(static_cast<float *>(dst) + gidx + e0) = v;
+        }
+    }
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------- launches
+hipError_t launch_muon_momentum(int storage, bool grad_bf16, bool stochastic, const MuonStepArgs &a, hipStream_t s) {
+    const dim3 grid(a.n_blocks), block(256);
+#define MUON_MOMENTUM(st, sr)                                                                       \
+    do {                                                                                            \
+        if (grad_bf16) muon_momentum_kernel<st, true, sr><<<grid, block, 0, s>>>(a);                \
+        else muon_momentum_kernel<st, false, sr><<<grid, block, 0, s>>>(a);                         \
+    } while (0)
+    if (storage == kMuonBf16) MUON_MOMENTUM(kMuonBf16, false);
+    else if (storage == kMuonF32) MUON_MOMENTUM(kMuonF32, false);
+    else if (stochastic) MUON_MOMENTUM(kMuonQ8, true);
+    else MUON_MOMENTUM(kMuonQ8, false);
+#undef MUON_MOMENTUM
+    return hipGetLastError();
+}
+
+hipError_t launch_muon_norms(const double *partials, const uint2 *ranges, double *sums, uint32_t n_mats, hipStream_t s) {
+    muon_norms_kernel<<<dim3(n_mats), dim3(256), 0, s>>>(partials, ranges, sums);
+    return hipGetLastError();
+}
+
+hipError_t launch_muon_sums(bool bf16, const MuonWork &w, const MuonSumArgs &a, uint32_t n_mats, hipStream_t s) {
+    const dim3 grid(n_mats * a.n_partials), block(256);
+    if (bf16) muon_sums_kernel<true><<<grid, block, 0, s>>>(w, a);
+    else muon_sums_kernel<false><<<grid, block, 0, s>>>(w, a);
+    return hipGetLastError();
+}
+
+template <int T>
+static void prep(bool bf16, int form, const MuonWork &w, const MuonPrepArgs &a, hipStream_t s) {
+    const dim3 grid(w.n_tiles), block(256);
+    if (form == kSplit) {
+        if (bf16) muon_prep_kernel<T, true, kSplit><<<grid, block, 0, s>>>(w, a);
+        else muon_prep_kernel<T, false, kSplit><<<grid, block, 0, s>>>(w, a);
+    } else {
+        if (bf16) muon_prep_kernel<T, true, kPlain><<<grid, block, 0, s>>>(w, a);
+        else muon_prep_kernel<T, false, kPlain><<<grid, block, 0, s>>>(w, a);
+    }
+}
+
+hipError_t launch_muon_prep(int tile, bool bf16, int form, const MuonWork &w, const MuonPrepArgs &a, hipStream_t s) {
+    if (tile == 128) prep<128>(bf16, form, w, a, s);
+    else prep<64>(bf16, form, w, a, s);
+    return hipGetLastError();
+}
+
+template <int T>
+static hipError_t product_of(int product, int in, int out, const MuonGemmArgs &a, hipStream_t s) {
+    const dim3 grid(a.work.n_tiles), block(256);
+#define MUON_CASE(p, i, o)                                                       \
+    if (product == p && in == i && out == o) {                                   \
+        muon_product_kernel<T, p, i, o><<<grid, block, 0, s>>>(a);               \
+        return hipGetLastError();                                                \
+    }
+    MUON_CASE(kGram, kSplit, kSplit)
+    MUON_CASE(kPolynomial, kSplit, kSplit)
+    MUON_CASE(kUpdate, kSplit, kSplit)
+    MUON_CASE(kUpdate, kSplit, kPlain)
+    MUON_CASE(kGram, kPlain, kPlain)
+    MUON_CASE(kPolynomial, kPlain, kPlain)
+    MUON_CASE(kUpdate, kPlain, kPlain)
+    MUON_CASE(kLastF32, kSplit, kSplit)
+    MUON_CASE(kLastBf16, kSplit, kSplit)
+    MUON_CASE(kLastBf16, kPlain, kPlain)
+    MUON_CASE(kLastParams, kSplit, kSplit)
+#undef MUON_CASE
+    return hipErrorInvalidValue;
+}
+
+hipError_t launch_muon_product(int tile, int product, int in, int out, const MuonGemmArgs &a, hipStream_t s) {
+    return tile == 128 ? product_of<128>(product, in, out, a, s) : product_of<64>(product, in, out, a, s);
+}
+
+hipError_t launch_muon_decode(int storage, const BlockDesc *desc, uint32_t n_blocks, const void *m_state,
+                              const float *m_scale, void *dst, hipStream_t s) {
+    const dim3 grid(n_blocks), block(256);
+    if (storage == kMuonBf16) muon_decode_kernel<kMuonBf16><<<grid, block, 0, s>>>(desc, m_state, m_scale, dst);
+    else if (storage == kMuonQ8) muon_decode_kernel<kMuonQ8><<<grid, block, 0, s>>>(desc, m_state, m_scale, dst);
+    else muon_decode_kernel<kMuonF32><<<grid, block, 0, s>>>(desc, m_state, m_scale, dst);
+    return hipGetLastError();
+}
+
+}  // namespace adam_mi355x

@@ -1,0 +1,1081 @@
+// Host runtime behind the C ABI declared in include/muon_mi355x.h: argument
+// validation, the momentum's layout (that of Adam's first moment), the
+// descriptor and tile tables, workspace, and the launches of a step and of
+// the orthogonalisation.
+#include <hip/hip_runtime_api.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+#include <new>
+#include <string>
+#include <vector>
+
+#include "muon_internal.h"
+#include "muon_mi355x.h"
+#include "runtime_common.h"
+
+using namespace adam_mi355x;
+
+namespace {
+
+constexpr int kTableSlots = 4;  // resident pointer tables per state
+constexpr int kStageSlots = 8;  // pinned staging buffers per state
+
+// Matrices go through the products together up to this many (padded)
+// elements: 512 MB of factor arrays, and some 2000 tiles of 128 x 128.
+constexpr int64_t kGroupElements = int64_t(1) << 25;
+// 128 x 128 tiles where there are this many, else 64 x 64 ones.
+constexpr int64_t kLargeTiles = 512;
+constexpr int64_t kMaxDim = int64_t(1) << 21;
+constexpr int64_t kMaxPartials = 256;
+constexpr double kPlainGrowth = 12.0;
+constexpr float kDefaultCoefficients[3] = {3.4445f, -4.7750f, 2.0315f};
+
+int fail(int code, const std::string &msg) { return set_last_error(code, msg); }
+
+int hip_fail(hipError_t e, const char *what) {
+    return fail(ADAM_EDEVICE, std::string(what) + ": " + hipGetErrorString(e));
+}
+
+// Runs an entry point's body: a host allocation failure inside it comes back
+// as ADAM_ENOMEM instead of escaping through the C ABI.
+template <class F>
+auto guarded(F &&body) noexcept -> decltype(body()) {
+    try {
+        return body();
+    } catch (const std::bad_alloc &) {
+        try { return fail(ADAM_ENOMEM, "host allocation failed"); } catch (...) { return ADAM_ENOMEM; }
+    } catch (...) {
+        try { return fail(ADAM_EDEVICE, "unexpected host exception"); } catch (...) { return ADAM_EDEVICE; }
+    }
+}
+
+int64_t pad_to(int64_t n, int64_t m) { return (n + m - 1) / m * m; }
+int64_t pad16(int64_t n) { return pad_to(n, 16); }
+int64_t blocks_of(int64_t n) { return (n + kBlock - 1) / kBlock; }
+
+struct TableSlot {
+    TensorRef *dev = nullptr;
+    std::vector<TensorRef> ptrs;
+    uint64_t last_use = 0;
+    bool valid = false;
+};
+
+// A part of the list whose matrices go through the products together.
+struct Group {
+    int32_t first = 0, last = 0;  // tensors [first, last)
+    int tile = 128;
+    int64_t x_bytes = 0, a_bytes = 0;  // of one X (or X^T) array and of A (or P)
+    int64_t block0 = 0, blocks = 0;    // 2048-element blocks
+    int64_t flat0 = 0;                 // flat state index of its first element
+    std::vector<MuonMat> mats;
+    std::vector<MuonTile> prep, square, update;
+    std::vector<uint2> ranges;  // per matrix: its blocks within the group
+    // where the tables stand in the state's device table array
+    const MuonMat *d_mats = nullptr;
+    const MuonTile *d_prep = nullptr, *d_square = nullptr, *d_update = nullptr;
+    const uint2 *d_ranges = nullptr;
+};
+
+struct Shape {
+    int64_t rows, cols;
+    int64_t numel() const { return rows * cols; }
+    int64_t shorter() const { return std::min(rows, cols); }
+    int64_t longer() const { return std::max(rows, cols); }
+};
+
+int tile_for(int64_t tiles128) { return tiles128 >= kLargeTiles ? 128 : 64; }
+int64_t tiles_of(const Shape &s, int64_t tile) {
+    return (pad_to(s.shorter(), tile) / tile) * (pad_to(s.longer(), tile) / tile);
+}
+
+// The groups of a list, without their tables.
+std::vector<Group> plan(const std::vector<Shape> &shapes) {
+    std::vector<Group> groups;
+    const int32_t n = (int32_t)shapes.size();
+    int64_t block = 0, flat = 0;
+    for (int32_t k = 0; k < n;) {
+        Group g;
+        g.first = k;
+        g.block0 = block;
+        g.flat0 = flat;
+        int64_t elements = 0, tiles128 = 0;
+        for (; k < n; ++k) {
+            const int64_t t = shapes[k].numel() > 0 ? tiles_of(shapes[k], 128) : 0;
+            if (elements > 0 && elements + t * 16384 > kGroupElements) break;
+            elements += t * 16384;
+            tiles128 += t;
+            block += blocks_of(shapes[k].numel());
+            flat += pad16(shapes[k].numel());
+        }
+        g.last = k;
+        g.blocks = block - g.block0;
+        g.tile = tile_for(tiles128);
+        for (int32_t i = g.first; i < g.last; ++i) {
+            if (shapes[i].numel() == 0) continue;
+            const int64_t m = pad_to(shapes[i].shorter(), g.tile), l = pad_to(shapes[i].longer(), g.tile);
+            g.x_bytes += 4 * m * l;
+            g.a_bytes += 4 * m * m;
+        }
+        if (g.blocks > 0) groups.push_back(std::move(g));
+    }
+    return groups;
+}
+
+// The workspace a group needs: four X arrays, A and P, the blocks' partial
+// sums and the matrices' sums.
+int64_t align256(int64_t n) { return pad_to(n, 256); }
+int64_t group_bytes(const Group &g) {
+    return 4 * align256(g.x_bytes) + 2 * align256(g.a_bytes) + align256(8 * g.blocks) + align256(8 * (g.last - g.first));
+}
+
+struct Workspace {
+    MuonArrays f;
+    double *partials, *sums;
+};
+
+Workspace carve(char *base, int64_t x_bytes, int64_t a_bytes, int64_t n_partials) {
+    Workspace w;
+    auto take = [&base](int64_t n) {
+        char *p = base;
+        base += align256(n);
+        return p;
+    };
+    for (int i = 0; i < 2; ++i) {
+        w.f.x[i] = take(x_bytes);
+        w.f.xt[i] = take(x_bytes);
+    }
+    w.f.a = take(a_bytes);
+    w.f.p = take(a_bytes);
+    w.partials = reinterpret_cast<double *>(take(8 * n_partials));
+    w.sums = reinterpret_cast<double *>(base);
+    return w;
+}
+
+int check_layout(const muon_layout *l) {
+    if (!l) return fail(ADAM_EINVAL, "layout is NULL");
+    if (l->storage != MUON_STORE_BF16 && l->storage != MUON_STORE_Q8 && l->storage != MUON_STORE_F32)
+        return fail(ADAM_EINVAL, "unknown storage mode " + std::to_string(l->storage));
+    if (l->grad_dtype != ADAM_GRAD_F32 && l->grad_dtype != ADAM_GRAD_BF16)
+        return fail(ADAM_EINVAL, "unknown grad dtype " + std::to_string(l->grad_dtype));
+    if (l->block_size != ADAM_BLOCK_SIZE)
+        return fail(ADAM_EINVAL, "block_size must be " + std::to_string(ADAM_BLOCK_SIZE) + ", got " +
+                                     std::to_string(l->block_size));
+    if (l->options != 0) return fail(ADAM_EINVAL, "unknown layout option bits");
+    return ADAM_OK;
+}
+
+int check_shape(int64_t rows, int64_t cols, const std::string &what) {
+    if (rows < 0 || rows >= kMaxDim || cols < 0 || cols >= kMaxDim)
+        return fail(ADAM_EINVAL, "dimension of " + what + " outside [0, 2^21)");
+    if (rows * cols >= (int64_t(1) << 32)) return fail(ADAM_EINVAL, "rows * cols of " + what + " is 2^32 or more");
+    return ADAM_OK;
+}
+
+int check_shapes(int32_t n, const int64_t *rows, const int64_t *cols, std::vector<Shape> &out) {
+    if (n < 0) return fail(ADAM_EINVAL, "n_tensors < 0");
+    if (n > 0 && (!rows || !cols)) return fail(ADAM_EINVAL, "rows or cols is NULL");
+    out.clear();
+    out.reserve(n);
+    int64_t blocks = 0, padded = 0;
+    for (int32_t k = 0; k < n; ++k) {
+        if (int rc = check_shape(rows[k], cols[k], "tensor " + std::to_string(k))) return rc;
+        out.push_back(Shape{rows[k], cols[k]});
+        blocks += blocks_of(out[k].numel());
+        padded += pad16(out[k].numel());
+    }
+    if (blocks >= (int64_t(1) << 31) || padded >= (int64_t(1) << 36))
+        return fail(ADAM_EINVAL, "state too large: more than 2^31 - 1 blocks or 2^36 elements");
+    return ADAM_OK;
+}
+
+int check_iteration(const muon_iteration &it) {
+    if (it.steps < 1 || it.steps > MUON_MAX_STEPS)
+        return fail(ADAM_EINVAL, "steps must be in [1, " + std::to_string(MUON_MAX_STEPS) + "]");
+    if (!(it.eps > 0.0f) || !std::isfinite(it.eps)) return fail(ADAM_EINVAL, "eps must be finite and > 0");
+    if (it.coefficients)
+        for (int i = 0; i < 3 * it.steps; ++i)
+            if (!(it.coefficients[i] >= -64.0f && it.coefficients[i] <= 64.0f))
+                return fail(ADAM_EINVAL, "coefficient " + std::to_string(i) + " outside [-64, 64]");
+    return ADAM_OK;
+}
+
+int check_hparams(const muon_hparams *hp, int32_t storage) {
+    if (!hp) return fail(ADAM_EINVAL, "hparams is NULL");
+    if (hp->t < 1) return fail(ADAM_EINVAL, "t must be >= 1");
+    if (!(hp->lr >= 0.0f) || !std::isfinite(hp->lr)) return fail(ADAM_EINVAL, "lr must be finite and >= 0");
+    if (!(hp->momentum >= 0.0f && hp->momentum < 1.0f)) return fail(ADAM_EINVAL, "momentum must be in [0, 1)");
+    if (!(hp->weight_decay >= 0.0f) || !std::isfinite(hp->weight_decay))
+        return fail(ADAM_EINVAL, "weight_decay must be finite and >= 0");
+    if (hp->scale < MUON_SCALE_NONE || hp->scale > MUON_SCALE_RMS) return fail(ADAM_EINVAL, "unknown scale rule");
+    if (hp->flags & ~(uint32_t)(MUON_F_NESTEROV | MUON_F_STOCHASTIC)) return fail(ADAM_EINVAL, "unknown flag bits");
+    if (hp->reserved != 0) return fail(ADAM_EINVAL, "reserved must be 0");
+    if ((hp->flags & MUON_F_STOCHASTIC) && storage != MUON_STORE_Q8)
+        return fail(ADAM_EINVAL, "stochastic rounding applies to 8-bit storage only");
+    return check_iteration(hp->iteration);
+}
+
+constexpr int64_t kDrawIndexLimit = int64_t(1) << 62;
+
+int check_draw_first(const std::vector<Shape> &shapes, const int64_t *first) {
+    if (!shapes.empty() && !first) return fail(ADAM_EINVAL, "draw index array is NULL");
+    for (size_t k = 0; k < shapes.size(); ++k)
+        if (first[k] < 0 || first[k] % 16 != 0 || first[k] > kDrawIndexLimit - pad16(shapes[k].numel()))
+            return fail(ADAM_EINVAL, "draw index of tensor " + std::to_string(k) +
+                                         " must be a multiple of 16 in [0, 2^62 - padded size]");
+    return ADAM_OK;
+}
+
+int64_t element_bytes(int32_t storage) { return storage == MUON_STORE_F32 ? 4 : (storage == MUON_STORE_BF16 ? 2 : 1); }
+
+// The coefficients of iteration k, and how the factors are held in it.
+void coefficients_of(const muon_iteration &it, int k, float c[3]) {
+    const float *p = it.coefficients ? it.coefficients + 3 * k : kDefaultCoefficients;
+    for (int i = 0; i < 3; ++i) c[i] = p[i];
+}
+void forms_of(const muon_iteration &it, bool plain_allowed, int forms[MUON_MAX_STEPS]) {
+    double growth = 1.0;
+    for (int k = it.steps - 1; k >= 0; --k) {
+        float c[3];
+        coefficients_of(it, k, c);
+        growth *= std::fabs((double)c[0]);
+        forms[k] = plain_allowed && growth <= kPlainGrowth ? kPlain : kSplit;
+        if (forms[k] == kSplit) plain_allowed = false;
+    }
+}
+
+// The products of all iterations, X_0 and X_0^T being in f.x[0], f.xt[0].
+hipError_t run_products(int tile, const MuonArrays &f, const MuonWork &square, const MuonWork &update,
+                        const muon_iteration &it, const int *forms, int last, const MuonGemmArgs &into, hipStream_t s) {
+    hipError_t e;
+    for (int k = 0; k < it.steps; ++k) {
+        const int cur = k & 1, in = forms[k];
+        float c[3];
+        coefficients_of(it, k, c);
+        MuonGemmArgs a{};
+        a.work = square;
+        a.left = f.x[cur];
+        a.out = f.a;
+        if ((e = launch_muon_product(tile, kGram, in, in, a, s)) != hipSuccess) return e;
+        a.left = f.a;
+        a.add = f.a;
+        a.out = f.p;
+        a.ca = c[0];
+        a.cb = c[1];
+        a.cc = c[2];
+        if ((e = launch_muon_product(tile, kPolynomial, in, in, a, s)) != hipSuccess) return e;
+        if (k + 1 < it.steps) {
+            a = MuonGemmArgs{};
+            a.work = update;
+            a.left = f.p;
+            a.right = f.xt[cur];
+            a.out = f.x[cur ^ 1];
+            a.out_t = f.xt[cur ^ 1];
+            e = launch_muon_product(tile, kUpdate, in, forms[k + 1], a, s);
+        } else {
+            a = into;
+            a.work = update;
+            a.left = f.p;
+            a.right = f.xt[cur];
+            e = launch_muon_product(tile, last, in, in, a, s);
+        }
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+}  // namespace
+
+struct muon_state {
+    int device = -1;
+    muon_layout layout{};
+    std::vector<Shape> shapes;
+    int64_t padded = 0, nblocks = 0;
+    std::vector<Group> groups;
+    void *m = nullptr;
+    float *m_scale = nullptr;
+    char *workspace = nullptr;
+    char *d_tables = nullptr;  // block descriptors, draw indices, the groups' tables
+    BlockDesc *d_desc = nullptr;
+    std::vector<int64_t> draw_first;
+    uint64_t *d_draw = nullptr;
+    // device copies of the caller's pointer pairs: a few recent sets stay
+    // resident, new ones go through a ring of pinned buffers
+    TableSlot tables[kTableSlots];
+    uint64_t table_clock = 0;
+    TensorRef *stage[kStageSlots] = {};
+    hipEvent_t stage_done[kStageSlots] = {};
+    bool stage_pending[kStageSlots] = {};
+    int next_stage = 0;
+    int32_t n() const { return (int32_t)shapes.size(); }
+};
+
+namespace {
+
+void release(muon_state *s) {
+    if (!s) return;
+    if (s->device >= 0) {
+        int cur = -1;
+        (void)hipGetDevice(&cur);
+        if (cur != s->device) (void)hipSetDevice(s->device);
+        (void)hipDeviceSynchronize();
+        for (int i = 0; i < kStageSlots; ++i) {
+            if (s->stage_done[i]) (void)hipEventDestroy(s->stage_done[i]);
+            (void)hipHostFree(s->stage[i]);
+        }
+        for (int i = 0; i < kTableSlots; ++i) (void)hipFree(s->tables[i].dev);
+        (void)hipFree(s->m);
+        (void)hipFree(s->m_scale);
+        (void)hipFree(s->workspace);
+        (void)hipFree(s->d_tables);
+        if (cur >= 0 && cur != s->device) (void)hipSetDevice(cur);
+    }
+    delete s;
+}
+
+int alloc(void **p, int64_t bytes) {
+    if (bytes == 0) return ADAM_OK;
+    if (hipMalloc(p, (size_t)bytes) != hipSuccess) {
+        (void)hipGetLastError();
+        *p = nullptr;
+        return fail(ADAM_ENOMEM, "hipMalloc of " + std::to_string(bytes) + " bytes failed");
+    }
+    return ADAM_OK;
+}
+
+int alloc_zeroed(void **p, int64_t bytes, hipStream_t stream) {
+    if (int rc = alloc(p, bytes)) return rc;
+    if (bytes == 0) return ADAM_OK;
+    hipError_t e = hipMemsetAsync(*p, 0, (size_t)bytes, stream);
+    return e == hipSuccess ? ADAM_OK : hip_fail(e, "hipMemsetAsync");
+}
+
+// The descriptors and tiles of a group; long products first, so that the
+// last workgroups of a launch are short ones.
+void build_tables(Group &g, const std::vector<Shape> &shapes) {
+    std::vector<int32_t> order;
+    int64_t flat = 0, block = 0;
+    std::vector<int64_t> flats, firsts;
+    for (int32_t k = g.first; k < g.last; ++k) {
+        flats.push_back(flat);
+        firsts.push_back(block);
+        flat += pad16(shapes[k].numel());
+        block += blocks_of(shapes[k].numel());
+        if (shapes[k].numel() > 0) order.push_back(k);
+    }
+    std::stable_sort(order.begin(), order.end(),
+                     [&](int32_t a, int32_t b) { return shapes[a].longer() > shapes[b].longer(); });
+    uint64_t x_off = 0, a_off = 0;
+    const int T = g.tile;
+    for (int32_t k : order) {
+        const Shape &s = shapes[k];
+        MuonMat m{};
+        m.x_off = x_off;
+        m.a_off = a_off;
+        m.u_off = (uint64_t)flats[k - g.first];
+        m.u_ld = (uint64_t)s.cols;
+        m.mb = (uint32_t)(pad_to(s.shorter(), T) / T);
+        m.nb = (uint32_t)(pad_to(s.longer(), T) / T);
+        m.rows = (uint32_t)s.rows;
+        m.cols = (uint32_t)s.cols;
+        m.tall = s.rows > s.cols;
+        m.index = (uint32_t)k;
+        const uint32_t i = (uint32_t)g.mats.size();
+        m.norm = i;
+        m.scale_spectral = std::sqrt(std::max(1.0, (double)s.rows / (double)s.cols));
+        m.scale_rms = 0.2 * std::sqrt((double)s.longer());
+        x_off += 4ull * T * T * m.mb * m.nb;
+        a_off += 4ull * T * T * m.mb * m.mb;
+        g.mats.push_back(m);
+        const int64_t b0 = firsts[k - g.first];
+        g.ranges.push_back(uint2{(uint32_t)b0, (uint32_t)(b0 + blocks_of(s.numel()))});
+        const uint32_t pr = (m.tall ? m.nb : m.mb) * (T / 64), pc = (m.tall ? m.mb : m.nb) * (T / 64);
+        for (uint32_t a = 0; a < pr; ++a)
+            for (uint32_t b = 0; b < pc; ++b) g.prep.push_back(MuonTile{i, (uint16_t)a, (uint16_t)b});
+        for (uint32_t a = 0; a < m.mb; ++a)
+            for (uint32_t b = 0; b <= a; ++b) g.square.push_back(MuonTile{i, (uint16_t)a, (uint16_t)b});
+        for (uint32_t a0 = 0; a0 < m.mb; a0 += 8)  // bands of 8 row blocks, as the kernel takes them
+            for (uint32_t b = 0; b < m.nb; ++b)
+                for (uint32_t a = a0; a < std::min(m.mb, a0 + 8); ++a)
+                    g.update.push_back(MuonTile{i, (uint16_t)a, (uint16_t)b});
+    }
+}
+
+struct BufferView {
+    void *ptr;
+    int64_t bytes;
+};
+
+BufferView buffer_of(const muon_state *s, int32_t which) {
+    const int32_t st = s->layout.storage;
+    switch (which) {
+    case ADAM_BUF_M_CODES: return st == MUON_STORE_Q8 ? BufferView{s->m, s->padded} : BufferView{nullptr, -1};
+    case ADAM_BUF_M_SCALE: return st == MUON_STORE_Q8 ? BufferView{s->m_scale, 4 * s->nblocks} : BufferView{nullptr, -1};
+    case ADAM_BUF_M_BF16: return st == MUON_STORE_BF16 ? BufferView{s->m, 2 * s->padded} : BufferView{nullptr, -1};
+    case ADAM_BUF_M_F32: return st == MUON_STORE_F32 ? BufferView{s->m, 4 * s->padded} : BufferView{nullptr, -1};
+    default: return BufferView{nullptr, -1};
+    }
+}
+
+std::vector<int32_t> buffers_of(int32_t storage) {
+    if (storage == MUON_STORE_Q8) return {ADAM_BUF_M_CODES, ADAM_BUF_M_SCALE};
+    return {storage == MUON_STORE_BF16 ? ADAM_BUF_M_BF16 : ADAM_BUF_M_F32};
+}
+
+template <class T>
+const T *place(std::vector<char> &bytes, const std::vector<T> &v) {  // as an offset, until the array is on the device
+    bytes.resize((bytes.size() + 15) / 16 * 16);
+    const size_t at = bytes.size();
+    bytes.resize(at + v.size() * sizeof(T));
+    if (!v.empty()) std::memcpy(bytes.data() + at, v.data(), v.size() * sizeof(T));
+    return reinterpret_cast<const T *>(at);
+}
+template <class T>
+const T *rebase(char *base, const T *offset) {
+    return reinterpret_cast<const T *>(base + reinterpret_cast<size_t>(offset));
+}
+
+int create(muon_state **out, std::vector<Shape> shapes, const muon_layout *layout, const int64_t *draw_first,
+           hipStream_t stream) {
+    muon_state *s = new muon_state();
+    struct Guard {
+        muon_state *s;
+        ~Guard() { release(s); }
+    } guard{s};
+    hipError_t e = hipGetDevice(&s->device);
+    if (e != hipSuccess) {
+        s->device = -1;
+        return hip_fail(e, "hipGetDevice");
+    }
+    s->layout = *layout;
+    s->shapes = std::move(shapes);
+    const int32_t n = s->n();
+    std::vector<BlockDesc> desc;
+    s->draw_first.resize(n);
+    for (int32_t k = 0; k < n; ++k) {
+        const int64_t len = s->shapes[k].numel();
+        for (int64_t b = 0; b * kBlock < len; ++b)
+            desc.push_back(BlockDesc{(uint32_t)((s->padded + b * kBlock) / 16), (uint32_t)k,
+                                     (uint32_t)((b << kBlockBits) | (std::min<int64_t>(kBlock, len - b * kBlock) - 1)),
+                                     (uint32_t)desc.size()});
+        s->draw_first[k] = draw_first ? draw_first[k] : s->padded;
+        s->padded += pad16(len);
+    }
+    s->nblocks = (int64_t)desc.size();
+    s->groups = plan(s->shapes);
+    int64_t work_bytes = 0;
+    std::vector<char> bytes;
+    const BlockDesc *desc_at = place(bytes, desc);
+    const int64_t *draw_at = place(bytes, s->draw_first);
+    for (Group &g : s->groups) {
+        build_tables(g, s->shapes);
+        work_bytes = std::max(work_bytes, group_bytes(g));
+        g.d_mats = place(bytes, g.mats);
+        g.d_ranges = place(bytes, g.ranges);
+        g.d_prep = place(bytes, g.prep);
+        g.d_square = place(bytes, g.square);
+        g.d_update = place(bytes, g.update);
+    }
+    int rc;
+    if ((rc = alloc_zeroed(&s->m, element_bytes(layout->storage) * s->padded, stream)) ||
+        (layout->storage == MUON_STORE_Q8 && (rc = alloc_zeroed((void **)&s->m_scale, 4 * s->nblocks, stream))) ||
+        (rc = alloc((void **)&s->workspace, work_bytes)) || (rc = alloc((void **)&s->d_tables, (int64_t)bytes.size())))
+        return rc;
+    if (!bytes.empty()) {
+        if ((e = hipMemcpyAsync(s->d_tables, bytes.data(), bytes.size(), hipMemcpyHostToDevice, stream)) != hipSuccess)
+            return hip_fail(e, "table upload");
+        s->d_desc = const_cast<BlockDesc *>(rebase(s->d_tables, desc_at));
+        s->d_draw = reinterpret_cast<uint64_t *>(const_cast<int64_t *>(rebase(s->d_tables, draw_at)));
+        for (Group &g : s->groups) {
+            g.d_mats = rebase(s->d_tables, g.d_mats);
+            g.d_ranges = rebase(s->d_tables, g.d_ranges);
+            g.d_prep = rebase(s->d_tables, g.d_prep);
+            g.d_square = rebase(s->d_tables, g.d_square);
+            g.d_update = rebase(s->d_tables, g.d_update);
+        }
+    }
+    if (n > 0) {
+        const size_t tbytes = (size_t)n * sizeof(TensorRef);
+        for (int i = 0; i < kTableSlots; ++i)
+            if ((rc = alloc((void **)&s->tables[i].dev, (int64_t)tbytes))) return rc;
+        for (int i = 0; i < kStageSlots; ++i) {
+            if (hipHostMalloc((void **)&s->stage[i], tbytes, hipHostMallocDefault) != hipSuccess) {
+                (void)hipGetLastError();
+                return fail(ADAM_ENOMEM, "pinned staging allocation failed");
+            }
+            if ((e = hipEventCreateWithFlags(&s->stage_done[i], hipEventDisableTiming)) != hipSuccess)
+                return hip_fail(e, "hipEventCreate");
+        }
+    }
+    if ((e = hipStreamSynchronize(stream)) != hipSuccess) return hip_fail(e, "hipStreamSynchronize");
+    for (Group &g : s->groups) {  // the host keeps the counts alone
+        g.mats.shrink_to_fit();
+    }
+    guard.s = nullptr;
+    *out = s;
+    return ADAM_OK;
+}
+
+// The device table that holds these pointers, uploading it if it is new.
+int pointer_table(muon_state *s, float *const *params, const void *const *grads, hipStream_t stream, TensorRef **out) {
+    const int32_t n = s->n();
+    int slot = -1;
+    for (int i = 0; i < kTableSlots && slot < 0; ++i) {
+        const TableSlot &ts = s->tables[i];
+        if (!ts.valid) continue;
+        bool same = true;
+        for (int32_t k = 0; k < n && same; ++k) same = ts.ptrs[k].p == params[k] && ts.ptrs[k].g == grads[k];
+        if (same) slot = i;
+    }
+    if (slot < 0) {
+        std::vector<const void *> seen;
+        for (int32_t k = 0; k < n; ++k)
+            if (s->shapes[k].numel() > 0) seen.push_back(params[k]);
+        std::sort(seen.begin(), seen.end());
+        if (std::adjacent_find(seen.begin(), seen.end()) != seen.end())
+            return fail(ADAM_EINVAL, "two tensors have the same param pointer");
+        slot = 0;  // least recently used (or never used) table
+        for (int i = 1; i < kTableSlots; ++i)
+            if (!s->tables[i].valid || (s->tables[slot].valid && s->tables[i].last_use < s->tables[slot].last_use)) slot = i;
+        TableSlot &ts = s->tables[slot];
+        const int st = s->next_stage;
+        s->next_stage = (st + 1) % kStageSlots;
+        hipError_t e;
+        if (s->stage_pending[st]) {  // the ring wrapped onto a copy still queued
+            if ((e = hipEventSynchronize(s->stage_done[st])) != hipSuccess) return hip_fail(e, "hipEventSynchronize");
+            s->stage_pending[st] = false;
+        }
+        ts.valid = false;
+        ts.ptrs.resize(n);
+        for (int32_t k = 0; k < n; ++k) ts.ptrs[k] = TensorRef{params[k], grads[k]};
+        std::memcpy(s->stage[st], ts.ptrs.data(), n * sizeof(TensorRef));
+        e = hipMemcpyAsync(ts.dev, s->stage[st], n * sizeof(TensorRef), hipMemcpyHostToDevice, stream);
+        if (e != hipSuccess) return hip_fail(e, "pointer table upload");
+        if ((e = hipEventRecord(s->stage_done[st], stream)) != hipSuccess) return hip_fail(e, "hipEventRecord");
+        s->stage_pending[st] = true;
+        ts.valid = true;
+    }
+    s->tables[slot].last_use = ++s->table_clock;
+    *out = s->tables[slot].dev;
+    return ADAM_OK;
+}
+
+MuonWork table_work(const Group &g, const MuonTile *tiles, size_t count) {
+    MuonWork w{};
+    w.tiles = tiles;
+    w.mats = g.d_mats;
+    w.n_tiles = (uint32_t)count;
+    w.per_mat = 1;
+    return w;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t muon_state_bytes(int32_t n_tensors, const int64_t *rows, const int64_t *cols, const muon_layout *layout) {
+    return guarded([&]() -> int64_t {
+        std::vector<Shape> shapes;
+        if (int rc = check_shapes(n_tensors, rows, cols, shapes)) return rc;
+        if (int rc = check_layout(layout)) return rc;
+        int64_t total = 0;
+        for (const Shape &s : shapes)
+            total += pad16(s.numel()) * element_bytes(layout->storage) +
+                     (layout->storage == MUON_STORE_Q8 ? 4 * blocks_of(s.numel()) : 0);
+        return total;
+    });
+}
+
+int64_t muon_state_workspace_bytes(int32_t n_tensors, const int64_t *rows, const int64_t *cols,
+                                   const muon_layout *layout) {
+    return guarded([&]() -> int64_t {
+        std::vector<Shape> shapes;
+        if (int rc = check_shapes(n_tensors, rows, cols, shapes)) return rc;
+        if (int rc = check_layout(layout)) return rc;
+        int64_t most = 0;
+        for (const Group &g : plan(shapes)) most = std::max(most, group_bytes(g));
+        return most;
+    });
+}
+
+int muon_state_create(muon_state **out, int32_t n_tensors, const int64_t *rows, const int64_t *cols,
+                      const muon_layout *layout, void *hip_stream) {
+    return guarded([&]() -> int {
+        if (!out) return fail(ADAM_EINVAL, "out is NULL");
+        *out = nullptr;
+        std::vector<Shape> shapes;
+        if (int rc = check_shapes(n_tensors, rows, cols, shapes)) return rc;
+        if (int rc = check_layout(layout)) return rc;
+        return create(out, std::move(shapes), layout, nullptr, reinterpret_cast<hipStream_t>(hip_stream));
+    });
+}
+
+void muon_state_destroy(muon_state *s) { release(s); }
+
+int muon_step(muon_state *s, float *const *params, const void *const *grads, const muon_hparams *hp,
+              const muon_layout *expect, void *hip_stream) {
+    return guarded([&]() -> int {
+        if (!s) return fail(ADAM_EINVAL, "state is NULL");
+        if (!expect) return fail(ADAM_EINVAL, "expected layout is NULL");
+        if (expect->storage != s->layout.storage || expect->grad_dtype != s->layout.grad_dtype ||
+            expect->block_size != s->layout.block_size || expect->options != s->layout.options)
+            return fail(ADAM_EMODE, "layout differs from the one the state was created with");
+        int rc = check_hparams(hp, s->layout.storage);
+        if (rc) return rc;
+        const int32_t n = s->n();
+        if (n > 0 && (!params || !grads)) return fail(ADAM_EINVAL, "params or grads is NULL");
+        for (int32_t k = 0; k < n; ++k) {
+            if (s->shapes[k].numel() == 0) continue;
+            if (!params[k] || !grads[k]) return fail(ADAM_EINVAL, "NULL pointer for tensor " + std::to_string(k));
+            if ((reinterpret_cast<uintptr_t>(params[k]) | reinterpret_cast<uintptr_t>(grads[k])) & 15u)
+                return fail(ADAM_EALIGN, "tensor " + std::to_string(k) + " is not 16-byte aligned");
+        }
+        if (s->nblocks == 0) return ADAM_OK;
+        int dev = -1;
+        hipError_t e = hipGetDevice(&dev);
+        if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
+        if (dev != s->device)
+            return fail(ADAM_EINVAL, "state lives on device " + std::to_string(s->device) + ", current is " +
+                                         std::to_string(dev));
+        hipStream_t stream = reinterpret_cast<hipStream_t>(hip_stream);
+        // a graph would replay this call's t, hyperparameters and pointer table
+        hipStreamCaptureStatus capture = hipStreamCaptureStatusNone;
+        if ((e = hipStreamIsCapturing(stream, &capture)) != hipSuccess) return hip_fail(e, "hipStreamIsCapturing");
+        if (capture != hipStreamCaptureStatusNone)
+            return fail(ADAM_EINVAL, "muon_step cannot be recorded into a graph: the stream is capturing");
+        TensorRef *tensors = nullptr;
+        if ((rc = pointer_table(s, params, grads, stream, &tensors))) return rc;
+
+        int forms[MUON_MAX_STEPS];
+        forms_of(hp->iteration, false, forms);
+        for (const Group &g : s->groups) {
+            const Workspace w = carve(s->workspace, g.x_bytes, g.a_bytes, g.blocks);
+            MuonStepArgs a{};
+            a.desc = s->d_desc + g.block0;
+            a.tensors = tensors;
+            a.draw_first = s->d_draw;
+            a.m_state = s->m;
+            a.m_scale = s->m_scale;
+            a.u = reinterpret_cast<float *>(w.f.x[1]);  // free until the first iteration writes there
+            a.partials = w.partials;
+            a.u_base = (uint64_t)g.flat0;
+            a.slot_base = (uint32_t)g.block0;
+            a.n_blocks = (uint32_t)g.blocks;
+            a.beta = hp->momentum;
+            a.omb = (float)(1.0 - (double)hp->momentum);
+            a.nesterov = (hp->flags & MUON_F_NESTEROV) ? 1u : 0u;
+            a.seed_lo = (uint32_t)hp->seed;
+            a.seed_hi = (uint32_t)(hp->seed >> 32);
+            a.t_lo = (uint32_t)(uint64_t)hp->t;
+            a.t_hi = (uint32_t)((uint64_t)hp->t >> 32);
+            if ((e = launch_muon_momentum(s->layout.storage, s->layout.grad_dtype == ADAM_GRAD_BF16,
+                                          (hp->flags & MUON_F_STOCHASTIC) != 0, a, stream)) != hipSuccess)
+                return hip_fail(e, "momentum launch");
+            if ((e = launch_muon_norms(w.partials, g.d_ranges, w.sums, (uint32_t)g.mats.size(), stream)) != hipSuccess)
+                return hip_fail(e, "norm launch");
+            MuonPrepArgs p{};
+            p.u = a.u;
+            p.partials = w.sums;
+            p.n_partials = 1;
+            p.eps = (double)hp->iteration.eps;
+            p.x = w.f.x[0];
+            p.xt = w.f.xt[0];
+            if ((e = launch_muon_prep(g.tile, false, forms[0], table_work(g, g.d_prep, g.prep.size()), p, stream)) !=
+                hipSuccess)
+                return hip_fail(e, "preparation launch");
+            MuonGemmArgs into{};
+            into.tensors = tensors;
+            into.lr = (double)hp->lr;
+            into.decay = (float)(1.0 - (double)hp->lr * (double)hp->weight_decay);
+            into.scale = hp->scale;
+            if ((e = run_products(g.tile, w.f, table_work(g, g.d_square, g.square.size()),
+                                  table_work(g, g.d_update, g.update.size()), hp->iteration, forms, kLastParams, into,
+                                  stream)) != hipSuccess)
+                return hip_fail(e, "product launch");
+        }
+        return ADAM_OK;
+    });
+}
+
+int64_t muon_state_buffer_bytes(const muon_state *s, int32_t which) {
+    return guarded([&]() -> int64_t {
+        if (!s) return fail(ADAM_EINVAL, "state is NULL");
+        const BufferView b = buffer_of(s, which);
+        if (b.bytes < 0) return fail(ADAM_EINVAL, "buffer " + std::to_string(which) + " absent in this storage mode");
+        return b.bytes;
+    });
+}
+
+static int copy_buffer(muon_state *s, int32_t which, void *dst, const void *src, int64_t nbytes, void *hip_stream,
+                       bool read) {
+    return guarded([&]() -> int {
+        const int64_t have = muon_state_buffer_bytes(s, which);
+        if (have < 0) return (int)have;
+        if (nbytes != have)
+            return fail(ADAM_EINVAL, "nbytes " + std::to_string(nbytes) + " != buffer size " + std::to_string(have));
+        if (nbytes == 0) return ADAM_OK;
+        if (read ? !dst : !src) return fail(ADAM_EINVAL, "NULL buffer pointer");
+        void *at = buffer_of(s, which).ptr;
+        hipError_t e = hipMemcpyAsync(read ? dst : at, read ? at : src, (size_t)nbytes, hipMemcpyDefault,
+                                      reinterpret_cast<hipStream_t>(hip_stream));
+        return e == hipSuccess ? ADAM_OK : hip_fail(e, "hipMemcpyAsync");
+    });
+}
+
+int muon_state_read(muon_state *s, int32_t which, void *dst, int64_t nbytes, void *hip_stream) {
+    return copy_buffer(s, which, dst, nullptr, nbytes, hip_stream, true);
+}
+
+int muon_state_write(muon_state *s, int32_t which, const void *src, int64_t nbytes, void *hip_stream) {
+    return copy_buffer(s, which, nullptr, src, nbytes, hip_stream, false);
+}
+
+int muon_state_momentum(muon_state *s, void *dst, int64_t nbytes, void *hip_stream) {
+    return guarded([&]() -> int {
+        if (!s) return fail(ADAM_EINVAL, "state is NULL");
+        const int64_t need = s->padded * (s->layout.storage == MUON_STORE_BF16 ? 2 : 4);
+        if (nbytes != need)
+            return fail(ADAM_EINVAL, "nbytes " + std::to_string(nbytes) + " != momentum size " + std::to_string(need));
+        if (nbytes == 0) return ADAM_OK;
+        if (!dst) return fail(ADAM_EINVAL, "NULL destination");
+        if (reinterpret_cast<uintptr_t>(dst) & 15u) return fail(ADAM_EALIGN, "destination is not 16-byte aligned");
+        hipError_t e = launch_muon_decode(s->layout.storage, s->d_desc, (uint32_t)s->nblocks, s->m, s->m_scale, dst,
+                                          reinterpret_cast<hipStream_t>(hip_stream));
+        return e == hipSuccess ? ADAM_OK : hip_fail(e, "decode launch");
+    });
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- checkpoint
+namespace {
+constexpr char kMagic[8] = {'M', 'E', 'A', 'M', 'M', 'U', 'O', 'N'};
+constexpr uint32_t kFormatVersion = 1;
+constexpr uint32_t kEndMarker = 0xFFFFFFFFu;
+
+int64_t align8(int64_t n) { return pad_to(n, 8); }
+int64_t header_bytes(int64_t n) { return 40 + 24 * n; }
+
+// 64-bit multiply-xor hash over whole 8-byte words (little-endian).
+uint64_t stream_hash(const uint8_t *p, int64_t n) {
+    uint64_t h = 0x9E3779B97F4A7C15ull ^ (uint64_t)n;
+    for (int64_t i = 0; i + 8 <= n; i += 8) {
+        uint64_t w;
+        std::memcpy(&w, p + i, 8);
+        h = (h ^ w) * 0x100000001B3ull;
+        h ^= h >> 29;
+    }
+    return h ^ (h >> 32);
+}
+
+template <class T>
+void put(uint8_t *base, int64_t &off, T v) {
+    std::memcpy(base + off, &v, sizeof(T));
+    off += sizeof(T);
+}
+template <class T>
+T get(const uint8_t *base, int64_t &off) {
+    T v;
+    std::memcpy(&v, base + off, sizeof(T));
+    off += sizeof(T);
+    return v;
+}
+}  // namespace
+
+extern "C" {
+
+int64_t muon_state_serialized_bytes(const muon_state *s) {
+    return guarded([&]() -> int64_t {
+        if (!s) return fail(ADAM_EINVAL, "state is NULL");
+        int64_t n = header_bytes(s->n());
+        for (int32_t b : buffers_of(s->layout.storage)) n += 16 + align8(buffer_of(s, b).bytes);
+        return n + 16;
+    });
+}
+
+int muon_state_save(muon_state *s, void *dst, int64_t nbytes, void *hip_stream) {
+    return guarded([&]() -> int {
+        if (!s || !dst) return fail(ADAM_EINVAL, "state or destination is NULL");
+        const int64_t need = muon_state_serialized_bytes(s);
+        if (nbytes != need)
+            return fail(ADAM_EINVAL, "nbytes " + std::to_string(nbytes) + " != serialized size " + std::to_string(need));
+        uint8_t *out = static_cast<uint8_t *>(dst);
+        hipStream_t stream = reinterpret_cast<hipStream_t>(hip_stream);
+        std::memcpy(out, kMagic, 8);
+        int64_t off = 8;
+        put<uint32_t>(out, off, kFormatVersion);
+        put<uint32_t>(out, off, (uint32_t)header_bytes(s->n()));
+        put<int32_t>(out, off, s->layout.storage);
+        put<int32_t>(out, off, s->layout.grad_dtype);
+        put<int32_t>(out, off, s->layout.block_size);
+        put<uint32_t>(out, off, s->layout.options);
+        put<int32_t>(out, off, s->n());
+        put<uint32_t>(out, off, 0u);
+        for (const Shape &z : s->shapes) put<int64_t>(out, off, z.rows);
+        for (const Shape &z : s->shapes) put<int64_t>(out, off, z.cols);
+        for (int64_t d : s->draw_first) put<int64_t>(out, off, d);
+        const std::vector<int32_t> bufs = buffers_of(s->layout.storage);
+        hipError_t e;
+        for (int32_t b : bufs) {
+            const BufferView v = buffer_of(s, b);
+            put<uint32_t>(out, off, (uint32_t)b);
+            put<uint32_t>(out, off, 0u);
+            put<uint64_t>(out, off, (uint64_t)v.bytes);
+            if (v.bytes > 0 &&
+                (e = hipMemcpyAsync(out + off, v.ptr, (size_t)v.bytes, hipMemcpyDeviceToHost, stream)) != hipSuccess)
+                return hip_fail(e, "state copy to host");
+            std::memset(out + off + v.bytes, 0, (size_t)(align8(v.bytes) - v.bytes));
+            off += align8(v.bytes);
+        }
+        if ((e = hipStreamSynchronize(stream)) != hipSuccess) return hip_fail(e, "hipStreamSynchronize");
+        put<uint32_t>(out, off, kEndMarker);
+        put<uint32_t>(out, off, (uint32_t)bufs.size());
+        put<uint64_t>(out, off, stream_hash(out, off));
+        return ADAM_OK;
+    });
+}
+
+int muon_state_load(muon_state **out, const void *src, int64_t nbytes, void *hip_stream) {
+    return guarded([&]() -> int {
+        if (!out || !src) return fail(ADAM_EINVAL, "out or source is NULL");
+        *out = nullptr;
+        const uint8_t *in = static_cast<const uint8_t *>(src);
+        if (nbytes < header_bytes(0) + 16 || nbytes % 8 != 0 || std::memcmp(in, kMagic, 8) != 0)
+            return fail(ADAM_EINVAL, "not a serialized Muon state");
+        int64_t off = 8;
+        const uint32_t version = get<uint32_t>(in, off), hbytes = get<uint32_t>(in, off);
+        if (version != kFormatVersion)
+            return fail(ADAM_EINVAL, "unsupported state format version " + std::to_string(version));
+        muon_layout lay{};
+        lay.storage = get<int32_t>(in, off);
+        lay.grad_dtype = get<int32_t>(in, off);
+        lay.block_size = get<int32_t>(in, off);
+        lay.options = get<uint32_t>(in, off);
+        const int32_t n = get<int32_t>(in, off);
+        const uint32_t zero = get<uint32_t>(in, off);
+        if (n < 0 || zero != 0 || (int64_t)hbytes != header_bytes(n) || header_bytes(n) > nbytes - 16)
+            return fail(ADAM_EINVAL, "corrupt state header");
+        if (int rc = check_layout(&lay)) return rc;
+        std::vector<int64_t> rows(n), cols(n), draw(n);
+        for (int64_t &v : rows) v = get<int64_t>(in, off);
+        for (int64_t &v : cols) v = get<int64_t>(in, off);
+        for (int64_t &v : draw) v = get<int64_t>(in, off);
+        std::vector<Shape> shapes;
+        if (int rc = check_shapes(n, rows.data(), cols.data(), shapes)) return rc;
+        if (int rc = check_draw_first(shapes, draw.data())) return rc;
+        uint64_t want_hash = 0;
+        std::memcpy(&want_hash, in + nbytes - 8, 8);
+        if (stream_hash(in, nbytes - 8) != want_hash) return fail(ADAM_EINVAL, "serialized state checksum mismatch");
+        int64_t padded = 0, nblocks = 0;
+        for (const Shape &z : shapes) {
+            padded += pad16(z.numel());
+            nblocks += blocks_of(z.numel());
+        }
+        const std::vector<int32_t> bufs = buffers_of(lay.storage);
+        std::vector<std::pair<int64_t, int64_t>> payload;
+        for (int32_t b : bufs) {
+            if (off + 16 > nbytes - 16) return fail(ADAM_EINVAL, "truncated serialized state");
+            const uint32_t id = get<uint32_t>(in, off), pad = get<uint32_t>(in, off);
+            const int64_t len = get<int64_t>(in, off);
+            const int64_t expect = b == ADAM_BUF_M_SCALE ? 4 * nblocks : element_bytes(lay.storage) * padded;
+            if ((int32_t)id != b || pad != 0 || len != expect)
+                return fail(ADAM_EINVAL, "state record " + std::to_string(b) + " missing, out of order or of the wrong size");
+            if (align8(len) > nbytes - 16 - off) return fail(ADAM_EINVAL, "truncated serialized state");
+            payload.emplace_back(off, len);
+            off += align8(len);
+        }
+        if (off != nbytes - 16) return fail(ADAM_EINVAL, "corrupt serialized state trailer");
+        const uint32_t end = get<uint32_t>(in, off), count = get<uint32_t>(in, off);
+        if (end != kEndMarker || count != bufs.size()) return fail(ADAM_EINVAL, "corrupt serialized state trailer");
+
+        hipStream_t stream = reinterpret_cast<hipStream_t>(hip_stream);
+        muon_state *s = nullptr;
+        if (int rc = create(&s, std::move(shapes), &lay, draw.data(), stream)) return rc;
+        hipError_t e = hipSuccess;
+        for (size_t i = 0; i < bufs.size() && e == hipSuccess; ++i)
+            if (payload[i].second > 0)
+                e = hipMemcpyAsync(buffer_of(s, bufs[i]).ptr, in + payload[i].first, (size_t)payload[i].second,
+                                   hipMemcpyHostToDevice, stream);
+        if (e == hipSuccess) e = hipStreamSynchronize(stream);
+        if (e != hipSuccess) {
+            release(s);
+            return hip_fail(e, "state copy to device");
+        }
+        *out = s;
+        return ADAM_OK;
+    });
+}
+
+int muon_state_set_draw_index(muon_state *s, const int64_t *first_index, void *hip_stream) {
+    return guarded([&]() -> int {
+        if (!s) return fail(ADAM_EINVAL, "state is NULL");
+        if (int rc = check_draw_first(s->shapes, first_index)) return rc;
+        if (s->n() == 0) return ADAM_OK;
+        hipStream_t stream = reinterpret_cast<hipStream_t>(hip_stream);
+        std::copy(first_index, first_index + s->n(), s->draw_first.begin());
+        // stream order puts the copy after every earlier step that read the table
+        hipError_t e = hipMemcpyAsync(s->d_draw, s->draw_first.data(), (size_t)s->n() * 8, hipMemcpyHostToDevice, stream);
+        if (e != hipSuccess) return hip_fail(e, "draw-index upload");
+        if ((e = hipStreamSynchronize(stream)) != hipSuccess) return hip_fail(e, "hipStreamSynchronize");
+        return ADAM_OK;
+    });
+}
+
+int32_t muon_state_get_draw_index(const muon_state *s, int64_t *first_index, int32_t max_tensors) {
+    return guarded([&]() -> int32_t {
+        if (!s) return fail(ADAM_EINVAL, "state is NULL");
+        if (max_tensors > 0 && !first_index) return fail(ADAM_EINVAL, "first_index is NULL");
+        for (int32_t k = 0; k < s->n() && k < max_tensors; ++k) first_index[k] = s->draw_first[k];
+        return s->n();
+    });
+}
+
+int32_t muon_state_describe(const muon_state *s, muon_layout *layout, int64_t *rows, int64_t *cols, int32_t max_tensors) {
+    return guarded([&]() -> int32_t {
+        if (!s || !layout) return fail(ADAM_EINVAL, "state or layout is NULL");
+        if (max_tensors > 0 && (!rows || !cols)) return fail(ADAM_EINVAL, "rows or cols is NULL");
+        *layout = s->layout;
+        for (int32_t k = 0; k < s->n() && k < max_tensors; ++k) {
+            rows[k] = s->shapes[k].rows;
+            cols[k] = s->shapes[k].cols;
+        }
+        return s->n();
+    });
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- orthogonalisation
+namespace {
+
+// How a batch is cut: `chunk` matrices go through the products together.
+struct BatchPlan {
+    int64_t chunk = 1;
+    int tile = 128;
+    int64_t mb = 0, nb = 0;            // row blocks of the short and the long side
+    int64_t x_bytes = 0, a_bytes = 0;  // per matrix
+    int64_t n_partials = 1;            // per matrix
+    int64_t bytes = 0;
+};
+
+BatchPlan plan_batch(int64_t batch, const Shape &s) {
+    BatchPlan p;
+    const int64_t tiles128 = tiles_of(s, 128);
+    p.chunk = std::max<int64_t>(1, std::min<int64_t>(batch, kGroupElements / (tiles128 * 16384)));
+    p.tile = tile_for(tiles128 * p.chunk);
+    p.mb = pad_to(s.shorter(), p.tile) / p.tile;
+    p.nb = pad_to(s.longer(), p.tile) / p.tile;
+    p.x_bytes = 4 * p.tile * p.tile * p.mb * p.nb;
+    p.a_bytes = 4 * p.tile * p.tile * p.mb * p.mb;
+    p.n_partials = std::min(kMaxPartials, tiles_of(s, 64));
+    p.bytes = 4 * align256(p.x_bytes * p.chunk) + 2 * align256(p.a_bytes * p.chunk) + align256(8 * p.n_partials * p.chunk);
+    return p;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t muon_orthogonalize_workspace_bytes(int64_t batch, int64_t rows, int64_t cols) {
+    return guarded([&]() -> int64_t {
+        if (batch < 0 || batch >= (int64_t(1) << 31)) return fail(ADAM_EINVAL, "batch outside [0, 2^31)");
+        if (int rc = check_shape(rows, cols, "the matrices")) return rc;
+        if (batch == 0 || rows == 0 || cols == 0) return 0;
+        return plan_batch(batch, Shape{rows, cols}).bytes;
+    });
+}
+
+int muon_orthogonalize(const muon_matrices *mats, const void *x, void *out, const muon_iteration *iteration,
+                       void *workspace, int64_t workspace_bytes, void *hip_stream) {
+    return guarded([&]() -> int {
+        if (!mats || !iteration) return fail(ADAM_EINVAL, "matrices or iteration is NULL");
+        if (int rc = check_iteration(*iteration)) return rc;
+        for (int32_t d : {mats->x_dtype, mats->out_dtype})
+            if (d != ADAM_GRAD_F32 && d != ADAM_GRAD_BF16) return fail(ADAM_EINVAL, "unknown dtype " + std::to_string(d));
+        const int64_t need = muon_orthogonalize_workspace_bytes(mats->batch, mats->rows, mats->cols);
+        if (need < 0) return (int)need;
+        const Shape shape{mats->rows, mats->cols};
+        constexpr int64_t kMaxStride = int64_t(1) << 40;
+        for (int64_t v : {mats->x_batch_stride, mats->x_row_stride, mats->out_batch_stride, mats->out_row_stride})
+            if (v < 0 || v > kMaxStride) return fail(ADAM_EINVAL, "stride outside [0, 2^40]");
+        if (mats->x_row_stride < shape.cols || mats->out_row_stride < shape.cols)
+            return fail(ADAM_EINVAL, "row stride smaller than cols");
+        if (need == 0) return ADAM_OK;
+        if (!x || !out || !workspace) return fail(ADAM_EINVAL, "NULL pointer");
+        if (workspace_bytes < need)
+            return fail(ADAM_EINVAL, "workspace of " + std::to_string(workspace_bytes) + " bytes, " + std::to_string(need) +
+                                         " needed");
+        const int64_t xe = mats->x_dtype == ADAM_GRAD_BF16 ? 2 : 4, oe = mats->out_dtype == ADAM_GRAD_BF16 ? 2 : 4;
+        if (reinterpret_cast<uintptr_t>(x) % xe || reinterpret_cast<uintptr_t>(out) % oe)
+            return fail(ADAM_EALIGN, "x or out is not aligned to its element");
+        if (reinterpret_cast<uintptr_t>(workspace) % 256) return fail(ADAM_EALIGN, "workspace is not 256-byte aligned");
+        const int64_t out_span = (shape.rows - 1) * mats->out_row_stride + shape.cols;
+        if (mats->batch > 1 && mats->out_batch_stride < out_span)
+            return fail(ADAM_EINVAL, "out's matrices overlap: batch stride smaller than a matrix");
+        const bool in_place = x == out && xe == oe && mats->x_row_stride == mats->out_row_stride &&
+                              (mats->batch == 1 || mats->x_batch_stride == mats->out_batch_stride);
+        if (!in_place) {
+            const int64_t x_span = (shape.rows - 1) * mats->x_row_stride + shape.cols;
+            const uintptr_t x0 = reinterpret_cast<uintptr_t>(x), o0 = reinterpret_cast<uintptr_t>(out);
+            const uintptr_t x1 = x0 + (uintptr_t)(((mats->batch - 1) * mats->x_batch_stride + x_span) * xe);
+            const uintptr_t o1 = o0 + (uintptr_t)(((mats->batch - 1) * mats->out_batch_stride + out_span) * oe);
+            // interleaved views (one's rows between the other's) are refused too
+            if (x0 < o1 && o0 < x1) return fail(ADAM_EINVAL, "out overlaps x");
+        }
+
+        const BatchPlan p = plan_batch(mats->batch, shape);
+        const Workspace w = carve(static_cast<char *>(workspace), p.x_bytes * p.chunk, p.a_bytes * p.chunk,
+                                  p.n_partials * p.chunk);
+        hipStream_t stream = reinterpret_cast<hipStream_t>(hip_stream);
+        int forms[MUON_MAX_STEPS];
+        forms_of(*iteration, mats->out_dtype == ADAM_GRAD_BF16, forms);
+        MuonWork work{};
+        work.one.mb = (uint32_t)p.mb;
+        work.one.nb = (uint32_t)p.nb;
+        work.one.rows = (uint32_t)shape.rows;
+        work.one.cols = (uint32_t)shape.cols;
+        work.one.u_ld = (uint64_t)mats->x_row_stride;
+        work.one.o_ld = (uint64_t)mats->out_row_stride;
+        work.one.tall = shape.rows > shape.cols;
+        work.x_stride = (uint64_t)p.x_bytes;
+        work.a_stride = (uint64_t)p.a_bytes;
+        work.u_stride = (uint64_t)mats->x_batch_stride;
+        work.o_stride = (uint64_t)mats->out_batch_stride;
+        work.norm_stride = (uint32_t)p.n_partials;
+        hipError_t e;
+        for (int64_t first = 0; first < mats->batch; first += p.chunk) {
+            const int64_t count = std::min(p.chunk, mats->batch - first);
+            work.one.u_off = (uint64_t)(first * mats->x_batch_stride);
+            work.one.o_off = (uint64_t)(first * mats->out_batch_stride);
+            auto with = [&](int64_t per_mat) {
+                MuonWork v = work;
+                v.per_mat = (uint32_t)per_mat;
+                v.n_tiles = (uint32_t)(per_mat * count);
+                return v;
+            };
+            MuonSumArgs sums{x, w.partials, (uint32_t)p.n_partials};
+            if ((e = launch_muon_sums(xe == 2, with(p.n_partials), sums, (uint32_t)count, stream)) != hipSuccess)
+                return hip_fail(e, "sum launch");
+            MuonPrepArgs prep{};
+            prep.u = x;
+            prep.partials = w.partials;
+            prep.n_partials = (uint32_t)p.n_partials;
+            prep.eps = (double)iteration->eps;
+            prep.x = w.f.x[0];
+            prep.xt = w.f.xt[0];
+            const int64_t sub = p.tile / 64;
+            if ((e = launch_muon_prep(p.tile, xe == 2, forms[0], with(p.mb * p.nb * sub * sub), prep, stream)) != hipSuccess)
+                return hip_fail(e, "preparation launch");
+            MuonGemmArgs into{};
+            into.o = out;
+            if ((e = run_products(p.tile, w.f, with(p.mb * (p.mb + 1) / 2), with(p.mb * p.nb), *iteration, forms,
+                                  oe == 2 ? kLastBf16 : kLastF32, into, stream)) != hipSuccess)
+                return hip_fail(e, "product launch");
+        }
+        return ADAM_OK;
+    });
+}
+
+}  // extern "C"
