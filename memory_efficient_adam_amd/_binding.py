@@ -154,9 +154,9 @@ def _check_step_tensors(state, params, grads):
 _CHECKED_SETS = 8  # tensor sets remembered per state (callers rotate gradient buffers)
 
 
-def _checked_pointers(state, params, grads, check=_check_step_tensors):
+def _checked_pointers(state, params, grads, check=None):
     """Device pointer arrays (ctypes) of params and grads.  The full tensor
-    checks (`check`) run when the (params, grads) tensor objects and their data
+    checks (`check`; by default _check_step_tensors) run when the (params, grads) tensor objects and their data
     pointers are not among the last few sets checked on this state: a caller
     stepping the same tensors, or rotating a few gradient buffers, pays two
     passes of data_ptr() and an identity compare (~0.25 us per tensor)
@@ -165,6 +165,7 @@ def _checked_pointers(state, params, grads, check=_check_step_tensors):
     host), and reuses the set's pointer arrays.  The state holds the
     remembered tensors until they are pushed out or destroy()."""
     import torch
+    check = check or _check_step_tensors
     ptr = torch.Tensor.data_ptr
     try:
         pp = list(map(ptr, params))
