@@ -190,8 +190,8 @@ void muon_state_destroy(muon_state *s);
  *     not overlap one another or x, except that out may be x itself
  *     with the same strides and type.
  *   workspace: device memory, 256-byte aligned, of at least
- *     muon_orthogonalize_workspace_bytes(batch, rows, cols); written by the
- *     call.  Calls that share one must be ordered on the device; so must the
+ *     muon_orthogonalize_workspace_bytes(batch, rows, cols), which may be 0
+ *     (then NULL will do); written by the call.  Calls that share one must be ordered on the device; so must the
  *     replays of graphs that recorded one.
  * Errors (no work enqueued): EINVAL (NULL pointer with a non-empty batch, a
  * dimension < 0 or >= 2^21, rows*cols >= 2^32, batch >= 2^31, a stride

@@ -96,6 +96,27 @@ struct MuonGemmArgs {
     int32_t scale;
 };
 
+// Whole orthogonalisations of matrices whose short side is at most kSmallShort
+// and long side at most kSmallLong, one workgroup a matrix.
+constexpr int64_t kSmallShort = 64, kSmallLong = 768;
+constexpr int kMaxIterations = 16;
+
+struct MuonSmallArgs {
+    MuonWork work;
+    const void *u;
+    void *o;                   // output array (orthogonalisation)
+    const TensorRef *tensors;  // params (step)
+    double eps;
+    double lr;
+    float decay;
+    int32_t scale;
+    int32_t product;           // kLastBf16, kLastF32, kLastParams
+    int32_t u_bf16;
+    int32_t steps;
+    uint32_t plain;            // bit k: iteration k takes plain factors
+    float coefficients[3 * kMaxIterations];
+};
+
 // ---------------------------------------------------------------- momentum
 struct MuonStepArgs {
     const BlockDesc *desc;
@@ -126,6 +147,9 @@ hipError_t launch_muon_prep(int tile, bool bf16, int form, const MuonWork &w, co
 enum MuonProduct : int { kGram, kPolynomial, kUpdate, kLastBf16, kLastF32, kLastParams };
 // in: the form of the factors read; out: of the factor written
 hipError_t launch_muon_product(int tile, int product, int in, int out, const MuonGemmArgs &a, hipStream_t s);
+
+// short_side, long_side: the largest of the launch's matrices
+hipError_t launch_muon_small(int64_t short_side, int64_t long_side, const MuonSmallArgs &a, hipStream_t s);
 
 hipError_t launch_muon_decode(int storage, const BlockDesc *desc, uint32_t n_blocks, const void *m_state,
                               const float *m_scale, void *dst, hipStream_t s);

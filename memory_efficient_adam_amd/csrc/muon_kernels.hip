@@ -57,13 +57,17 @@ __device__ __forceinline__ uint32_t pack(_Float16 a, _Float16 b) {
     return (uint32_t)__builtin_bit_cast(uint16_t, a) | ((uint32_t)__builtin_bit_cast(uint16_t, b) << 16);
 }
 
-// Sum over the workgroup's 256 threads in a fixed order (s: 4 doubles).
+// Sum over the workgroup's kWaves waves in a fixed order (s: kWaves doubles).
+template <int kWaves = 4>
 __device__ __forceinline__ double block_sum(double x, double *s) {
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1) x += __shfl_xor(x, d, 64);
     if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = x;
     __syncthreads();
-    return (s[0] + s[1]) + (s[2] + s[3]);
+    double sum = s[0];
+#pragma unroll
+    for (int i = 1; i < kWaves; ++i) sum += s[i];
+    return sum;
 }
 
 // Consecutive tiles share factor rows, and workgroups are dealt to the 8 XCDs
@@ -402,6 +406,264 @@ __global__ __launch_bounds__(256) void muon_product_kernel(MuonGemmArgs a) {
                         static_cast<float *>(a.o)[m.o_off + r * m.o_ld + c] = o;
                     }
                 }
+    }
+}
+
+// ---------------------------------------------------------------- small matrices
+// A whole orthogonalisation in one workgroup of 8 waves, X staying in
+// registers.  (15 launches of the products take 70 us for a matrix of a few
+// KB; this takes one launch.)
+//
+// A wave holds blocks of 32 columns of X, block w + 8 b at wave w, as the
+// matrix cores give them: lane l holds column l % 32, rows 8 g + 4 (l / 32) + q
+// of each 32-row block in element 4 g + q.  Taken as a factor with k along the
+// rows, eight such elements are one fragment whose k runs in the order
+//   order(j, half) = j < 4 ? 4 half + j : 8 + 4 half + j - 4,
+// which is as good as any as long as the other factor keeps to it.  So, with P
+// stored in that order,
+//   P X   = mfma(P, X)  gives the next X in the same arrangement, and
+//   X^T P = mfma(X, P)  gives it transposed: lane = row of X, k along columns,
+// which is what A = X X^T takes for both factors.  Nothing of X passes through
+// LDS; the price is that P X is computed twice.  A is summed over the waves in LDS.
+constexpr int kSmallWaves = 8;
+
+__device__ __forceinline__ uint32_t k_order(uint32_t j, uint32_t half) { return (j & 3u) + 4u * half + ((j & 4u) << 1); }
+
+// Square matrices in LDS: high parts and remainders, rows of 128 bytes whose
+// 16-byte chunk 2 s + half holds elements 16 s + order(0..7, half).
+struct SmallSquare {
+    uint4 hi[64 * 8], lo[64 * 8];
+};
+__device__ __forceinline__ uint32_t small_pos(uint32_t row, uint32_t chunk) { return row * 128u + ((chunk ^ (row & 7u)) << 4); }
+__device__ __forceinline__ half8 small_frag(const uint4 *image, uint32_t row, uint32_t chunk) {
+    return *reinterpret_cast<const half8 *>(reinterpret_cast<const char *>(image) + small_pos(row, chunk));
+}
+// Four consecutive elements e..e+3 (e a multiple of 4) of a row.
+__device__ __forceinline__ u32x2 *small_quad(uint4 *image, uint32_t row, uint32_t e) {
+    const uint32_t s = e >> 4, k4 = (e >> 2) & 3u;
+    return reinterpret_cast<u32x2 *>(reinterpret_cast<char *>(image) + small_pos(row, 2u * s + (k4 & 1u)) + (k4 >> 1) * 8u);
+}
+
+__device__ __forceinline__ f32x16 mfma(half8 a, half8 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 mfma_split(half8 ah, half8 al, half8 bh, half8 bl, f32x16 c, bool plain) {
+    c = mfma(ah, bh, c);
+    if (!plain) {
+        c = mfma(ah, bl, c);
+        c = mfma(al, bh, c);
+    }
+    return c;
+}
+
+template <int kRows, int kCols, bool kBf16>
+__global__ __launch_bounds__(64 * kSmallWaves) void muon_small_kernel(MuonSmallArgs a) {
+    constexpr int kSquare = kRows * (kRows + 1) / 2;  // 32 x 32 blocks of A on and below the diagonal
+    constexpr int kSteps = 2 * kRows;                 // fragments along the rows of X
+    __shared__ SmallSquare gram, poly;
+    __shared__ float parts[kSmallWaves][kSquare * 16][64];
+    __shared__ double s_sum[kSmallWaves];
+    uint32_t t;
+    const MuonMat m = find_mat(a.work, blockIdx.x, t);
+    const uint32_t tid = threadIdx.x, lane = tid & 63u, ln = lane & 31u, half = lane >> 5;
+    const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(tid >> 6));
+    const uint32_t n = m.tall ? m.rows : m.cols, n_short = m.tall ? m.cols : m.rows;
+
+    // the norm, rows of the user's matrix dealt to the waves
+    double sum = 0.0;
+    for (uint32_t r = wave; r < m.rows; r += kSmallWaves)
+        for (uint32_t c = lane; c < m.cols; c += 64u) {
+            const double v = load_elem<kBf16>(a.u, m.u_off + r * m.u_ld + c);
+            sum += v * v;
+        }
+    // the first update multiplies by one: it only arranges X_0's columns for A
+    for (uint32_t i = tid; i < 64u * 8u; i += 64u * kSmallWaves) {
+        poly.hi[i] = uint4{0u, 0u, 0u, 0u};
+        poly.lo[i] = uint4{0u, 0u, 0u, 0u};
+    }
+    sum = block_sum<kSmallWaves>(sum, s_sum);
+    if (tid < 32u * kRows) {
+        char *quad = reinterpret_cast<char *>(small_quad(poly.hi, tid, tid & ~3u));
+        reinterpret_cast<_Float16 *>(quad)[tid & 3u] = (_Float16)kScaleP;
+    }
+    const double inv = sum < __builtin_inf() ? (double)kScaleX / (sqrt(sum) + a.eps) : __builtin_nan("");
+
+    half8 xh[kCols][kSteps], xl[kCols][kSteps];
+    const uint64_t row_step = m.tall ? 1 : m.u_ld, col_step = m.tall ? m.u_ld : 1;
+#pragma unroll
+    for (int b = 0; b < kCols; ++b) {
+        const uint32_t col = 32u * (wave + kSmallWaves * b) + ln;
+        const uint64_t at = m.u_off + 4u * half * row_step + col * col_step;
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t row = 16u * s + k_order(j, half);
+                float v = 0.0f;
+                if (row < n_short && col < n)
+                    v = (float)((double)load_elem<kBf16>(a.u, at + (16u * s + k_order(j, 0)) * row_step) * inv);
+                _Float16 h, l;
+                split(v, h, l);
+                xh[b][s][j] = h;
+                xl[b][s][j] = l;
+            }
+            __builtin_amdgcn_sched_barrier(0);  // loads of a step at a time: fewer addresses are held
+        }
+    }
+    __syncthreads();
+
+    for (int it = 0; it <= a.steps; ++it) {
+        // X <- P X (plain: how iteration it - 1 takes its factors) and, along the
+        // way, A = X X^T for iteration `it`
+        const bool last = it == a.steps, plain = it > 0 && ((a.plain >> (it - 1)) & 1u), next_plain = (a.plain >> it) & 1u;
+        f32x16 acc[kSquare];
+#pragma unroll
+        for (int i = 0; i < kSquare; ++i) acc[i] = f32x16{};
+#pragma unroll
+        for (int b = 0; b < kCols; ++b) {
+            const uint32_t col0 = 32u * (wave + kSmallWaves * b);
+            if (col0 >= n) continue;
+            if (!last) {
+                half8 gh[kRows][2], gl[kRows][2];
+#pragma unroll
+                for (int i = 0; i < kRows; ++i) {
+                    f32x16 v = {};
+#pragma unroll
+                    for (int s = 0; s < kSteps; ++s)
+                        v = mfma_split(xh[b][s], xl[b][s], small_frag(poly.hi, 32u * i + ln, 2u * s + half),
+                                       small_frag(poly.lo, 32u * i + ln, 2u * s + half), v, plain);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        _Float16 h, l;
+                        split(v[e] * (1.0f / kScaleP), h, l);
+                        gh[i][e / 8][e & 7] = h;
+                        gl[i][e / 8][e & 7] = l;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < kRows; ++i)
+#pragma unroll
+                    for (int j = 0; j <= i; ++j)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            acc[i + j] = mfma_split(gh[i][k], gl[i][k], gh[j][k], gl[j][k], acc[i + j], next_plain);
+                f32x16 v[kRows];
+#pragma unroll
+                for (int i = 0; i < kRows; ++i) {
+                    v[i] = f32x16{};
+#pragma unroll
+                    for (int s = 0; s < kSteps; ++s)
+                        v[i] = mfma_split(small_frag(poly.hi, 32u * i + ln, 2u * s + half),
+                                          small_frag(poly.lo, 32u * i + ln, 2u * s + half), xh[b][s], xl[b][s], v[i], plain);
+                }
+#pragma unroll
+                for (int i = 0; i < kRows; ++i)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        _Float16 h, l;
+                        split(v[i][e] * (1.0f / kScaleP), h, l);
+                        xh[b][2 * i + e / 8][e & 7] = h;
+                        xl[b][2 * i + e / 8][e & 7] = l;
+                    }
+            } else {
+                float *param = nullptr;
+                float step = 0.0f;
+                if (a.product == kLastParams) {
+                    param = ((ConstTensorPtr)a.tensors + m.index)->p;
+                    step = (float)(a.lr * (a.scale == 1 ? m.scale_spectral : (a.scale == 2 ? m.scale_rms : 1.0)));
+                }
+#pragma unroll
+                for (int i = 0; i < kRows; ++i) {
+                    // lane = the user's column, so that a wave writes along rows
+                    f32x16 v = {};
+#pragma unroll
+                    for (int s = 0; s < kSteps; ++s) {
+                        const half8 ph = small_frag(poly.hi, 32u * i + ln, 2u * s + half);
+                        const half8 pl = small_frag(poly.lo, 32u * i + ln, 2u * s + half);
+                        v = m.tall ? mfma_split(xh[b][s], xl[b][s], ph, pl, v, plain)
+                                   : mfma_split(ph, pl, xh[b][s], xl[b][s], v, plain);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const uint32_t in = 8u * (e / 4) + 4u * half + (e & 3);
+                        const uint32_t r = m.tall ? col0 + in : 32u * i + in, c = m.tall ? 32u * i + ln : col0 + ln;
+                        if (r >= m.rows || c >= m.cols) continue;
+                        const float o = v[e] * (1.0f / (kScaleX * kScaleP));
+                        if (a.product == kLastParams) {
+                            float *q = param + (uint64_t)r * m.cols + c;
+                            *q = fmaf(-step, o, *q * a.decay);
+                        } else if (a.product == kLastBf16) {
+                            static_cast<uint16_t *>(a.o)[m.o_off + r * m.o_ld + c] = (uint16_t)f32_to_bf16(o);
+                        } else {
+                            static_cast<float *>(a.o)[m.o_off + r * m.o_ld + c] = o;
+                        }
+                    }
+                }
+            }
+        }
+        if (last) break;
+
+        // A: the waves' sums together, stored with its mirror image
+#pragma unroll
+        for (int i = 0; i < kSquare; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) parts[wave][i * 16 + e][lane] = acc[i][e];
+        __syncthreads();
+        for (uint32_t q = wave; q < kSquare * 4u; q += kSmallWaves) {
+            float v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float x = parts[0][q * 4 + e][lane];
+#pragma unroll
+                for (int w = 1; w < kSmallWaves; ++w) x += parts[w][q * 4 + e][lane];
+                v[e] = x * (1.0f / kScaleX);
+            }
+            const uint32_t blk = q >> 2, g = q & 3u, bi = blk == 0 ? 0u : 1u, bj = blk == 2 ? 1u : 0u;
+            const uint32_t r = 32u * bi + 8u * g + 4u * half, c = 32u * bj + ln;
+            _Float16 hi[4], lo[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) split(v[e], hi[e], lo[e]);
+            const u32x2 h = {pack(hi[0], hi[1]), pack(hi[2], hi[3])}, l = {pack(lo[0], lo[1]), pack(lo[2], lo[3])};
+            *small_quad(gram.hi, c, r) = h;
+            *small_quad(gram.lo, c, r) = l;
+            if (bi != bj) {
+                *small_quad(gram.hi, r + (lane & 3u), c & ~3u) = quad_transpose(h, lane);
+                *small_quad(gram.lo, r + (lane & 3u), c & ~3u) = quad_transpose(l, lane);
+            }
+        }
+        __syncthreads();
+        // P, one 32 x 32 block a wave, stored as its transpose (it is symmetric)
+        if (wave < kRows * kRows) {
+            const uint32_t bi = wave / kRows, bj = wave % kRows;
+            f32x16 p = {};
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) {
+                const uint32_t chunk = 2u * s + half;
+                p = mfma_split(small_frag(gram.hi, 32u * bi + ln, chunk), small_frag(gram.lo, 32u * bi + ln, chunk),
+                               small_frag(gram.hi, 32u * bj + ln, chunk), small_frag(gram.lo, 32u * bj + ln, chunk), p,
+                               next_plain);
+            }
+            const float ca = a.coefficients[3 * it] * kScaleP, cb = a.coefficients[3 * it + 1] * (kScaleP / kScaleX),
+                        cc = a.coefficients[3 * it + 2] * (kScaleP / (kScaleX * kScaleX));
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const uint32_t r = 32u * bi + 8u * g + 4u * half, c = 32u * bj + ln;
+                const u32x2 h = *small_quad(gram.hi, c, r), l = *small_quad(gram.lo, c, r);
+                _Float16 hi[4], lo[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const uint32_t hw = q < 2 ? h.x : h.y, lw = q < 2 ? l.x : l.y;
+                    float av = (float)__builtin_bit_cast(_Float16, (uint16_t)(hw >> (16 * (q & 1))));
+                    if (!next_plain) av += (float)__builtin_bit_cast(_Float16, (uint16_t)(lw >> (16 * (q & 1))));
+                    float v = fmaf(cb, av, cc * p[4 * g + q]);
+                    if (r + q == c) v += ca;
+                    split(v, hi[q], lo[q]);
+                }
+                *small_quad(poly.hi, c, r) = u32x2{pack(hi[0], hi[1]), pack(hi[2], hi[3])};
+                *small_quad(poly.lo, c, r) = u32x2{pack(lo[0], lo[1]), pack(lo[2], lo[3])};
+            }
+        }
+        __syncthreads();
     }
 }
 
@@ -749,6 +1011,26 @@ static hipError_t product_of(int product, int in, int out, const MuonGemmArgs &a
 
 hipError_t launch_muon_product(int tile, int product, int in, int out, const MuonGemmArgs &a, hipStream_t s) {
     return tile == 128 ? product_of<128>(product, in, out, a, s) : product_of<64>(product, in, out, a, s);
+}
+
+hipError_t launch_muon_small(int64_t short_side, int64_t long_side, const MuonSmallArgs &a, hipStream_t s) {
+    const dim3 grid(a.work.n_tiles), block(64 * kSmallWaves);
+    const int cols = (int)((long_side + 255) / 256);
+    if (short_side > kSmallShort || cols < 1 || cols > 3) return hipErrorInvalidValue;
+#define MUON_SMALL(r, c)                                                    \
+    if ((short_side <= 32) == (r == 1) && cols == c) {                      \
+        if (a.u_bf16) muon_small_kernel<r, c, true><<<grid, block, 0, s>>>(a);  \
+        else muon_small_kernel<r, c, false><<<grid, block, 0, s>>>(a);      \
+        return hipGetLastError();                                           \
+    }
+    MUON_SMALL(1, 1)
+    MUON_SMALL(1, 2)
+    MUON_SMALL(1, 3)
+    MUON_SMALL(2, 1)
+    MUON_SMALL(2, 2)
+    MUON_SMALL(2, 3)
+#undef MUON_SMALL
+    return hipErrorInvalidValue;
 }
 
 hipError_t launch_muon_decode(int storage, const BlockDesc *desc, uint32_t n_blocks, const void *m_state,

@@ -71,11 +71,12 @@ struct Group {
     int64_t block0 = 0, blocks = 0;    // 2048-element blocks
     int64_t flat0 = 0;                 // flat state index of its first element
     std::vector<MuonMat> mats;
-    std::vector<MuonTile> prep, square, update;
+    std::vector<MuonTile> prep, square, update, small;
+    int64_t small_short = 0, small_long = 0;  // the largest sides of its small matrices
     std::vector<uint2> ranges;  // per matrix: its blocks within the group
     // where the tables stand in the state's device table array
     const MuonMat *d_mats = nullptr;
-    const MuonTile *d_prep = nullptr, *d_square = nullptr, *d_update = nullptr;
+    const MuonTile *d_prep = nullptr, *d_square = nullptr, *d_update = nullptr, *d_small = nullptr;
     const uint2 *d_ranges = nullptr;
 };
 
@@ -86,6 +87,7 @@ struct Shape {
     int64_t longer() const { return std::max(rows, cols); }
 };
 
+bool is_small(const Shape &s) { return s.shorter() <= kSmallShort && s.longer() <= kSmallLong; }
 int tile_for(int64_t tiles128) { return tiles128 >= kLargeTiles ? 128 : 64; }
 int64_t tiles_of(const Shape &s, int64_t tile) {
     return (pad_to(s.shorter(), tile) / tile) * (pad_to(s.longer(), tile) / tile);
@@ -106,7 +108,7 @@ std::vector<Group> plan(const std::vector<Shape> &shapes) {
             const int64_t t = shapes[k].numel() > 0 ? tiles_of(shapes[k], 128) : 0;
             if (elements > 0 && elements + t * 16384 > kGroupElements) break;
             elements += t * 16384;
-            tiles128 += t;
+            if (!is_small(shapes[k])) tiles128 += t;
             block += blocks_of(shapes[k].numel());
             flat += pad16(shapes[k].numel());
         }
@@ -244,6 +246,22 @@ void forms_of(const muon_iteration &it, bool plain_allowed, int forms[MUON_MAX_S
         forms[k] = plain_allowed && growth <= kPlainGrowth ? kPlain : kSplit;
         if (forms[k] == kSplit) plain_allowed = false;
     }
+}
+
+MuonSmallArgs small_args(const MuonWork &w, const void *u, bool u_bf16, const muon_iteration &it, const int *forms,
+                         int product) {
+    MuonSmallArgs a{};
+    a.work = w;
+    a.u = u;
+    a.u_bf16 = u_bf16;
+    a.eps = (double)it.eps;
+    a.product = product;
+    a.steps = it.steps;
+    for (int k = 0; k < it.steps; ++k) {
+        coefficients_of(it, k, a.coefficients + 3 * k);
+        if (forms[k] == kPlain) a.plain |= 1u << k;
+    }
+    return a;
 }
 
 // The products of all iterations, X_0 and X_0^T being in f.x[0], f.xt[0].
@@ -391,6 +409,12 @@ void build_tables(Group &g, const std::vector<Shape> &shapes) {
         g.mats.push_back(m);
         const int64_t b0 = firsts[k - g.first];
         g.ranges.push_back(uint2{(uint32_t)b0, (uint32_t)(b0 + blocks_of(s.numel()))});
+        if (is_small(s)) {
+            g.small.push_back(MuonTile{i, 0, 0});
+            g.small_short = std::max(g.small_short, s.shorter());
+            g.small_long = std::max(g.small_long, s.longer());
+            continue;
+        }
         const uint32_t pr = (m.tall ? m.nb : m.mb) * (T / 64), pc = (m.tall ? m.mb : m.nb) * (T / 64);
         for (uint32_t a = 0; a < pr; ++a)
             for (uint32_t b = 0; b < pc; ++b) g.prep.push_back(MuonTile{i, (uint16_t)a, (uint16_t)b});
@@ -477,6 +501,7 @@ int create(muon_state **out, std::vector<Shape> shapes, const muon_layout *layou
         g.d_prep = place(bytes, g.prep);
         g.d_square = place(bytes, g.square);
         g.d_update = place(bytes, g.update);
+        g.d_small = place(bytes, g.small);
     }
     int rc;
     if ((rc = alloc_zeroed(&s->m, element_bytes(layout->storage) * s->padded, stream)) ||
@@ -494,6 +519,7 @@ int create(muon_state **out, std::vector<Shape> shapes, const muon_layout *layou
             g.d_prep = rebase(s->d_tables, g.d_prep);
             g.d_square = rebase(s->d_tables, g.d_square);
             g.d_update = rebase(s->d_tables, g.d_update);
+            g.d_small = rebase(s->d_tables, g.d_small);
         }
     }
     if (n > 0) {
@@ -510,9 +536,6 @@ int create(muon_state **out, std::vector<Shape> shapes, const muon_layout *layou
         }
     }
     if ((e = hipStreamSynchronize(stream)) != hipSuccess) return hip_fail(e, "hipStreamSynchronize");
-    for (Group &g : s->groups) {  // the host keeps the counts alone
-        g.mats.shrink_to_fit();
-    }
     guard.s = nullptr;
     *out = s;
     return ADAM_OK;
@@ -673,6 +696,22 @@ int muon_step(muon_state *s, float *const *params, const void *const *grads, con
             if ((e = launch_muon_momentum(s->layout.storage, s->layout.grad_dtype == ADAM_GRAD_BF16,
                                           (hp->flags & MUON_F_STOCHASTIC) != 0, a, stream)) != hipSuccess)
                 return hip_fail(e, "momentum launch");
+            MuonGemmArgs into{};
+            into.tensors = tensors;
+            into.lr = (double)hp->lr;
+            into.decay = (float)(1.0 - (double)hp->lr * (double)hp->weight_decay);
+            into.scale = hp->scale;
+            if (!g.small.empty()) {
+                MuonSmallArgs small = small_args(table_work(g, g.d_small, g.small.size()), a.u, false, hp->iteration, forms,
+                                                 kLastParams);
+                small.tensors = into.tensors;
+                small.lr = into.lr;
+                small.decay = into.decay;
+                small.scale = into.scale;
+                if ((e = launch_muon_small(g.small_short, g.small_long, small, stream)) != hipSuccess)
+                    return hip_fail(e, "small matrices' launch");
+            }
+            if (g.update.empty()) continue;
             if ((e = launch_muon_norms(w.partials, g.d_ranges, w.sums, (uint32_t)g.mats.size(), stream)) != hipSuccess)
                 return hip_fail(e, "norm launch");
             MuonPrepArgs p{};
@@ -685,11 +724,6 @@ int muon_step(muon_state *s, float *const *params, const void *const *grads, con
             if ((e = launch_muon_prep(g.tile, false, forms[0], table_work(g, g.d_prep, g.prep.size()), p, stream)) !=
                 hipSuccess)
                 return hip_fail(e, "preparation launch");
-            MuonGemmArgs into{};
-            into.tensors = tensors;
-            into.lr = (double)hp->lr;
-            into.decay = (float)(1.0 - (double)hp->lr * (double)hp->weight_decay);
-            into.scale = hp->scale;
             if ((e = run_products(g.tile, w.f, table_work(g, g.d_square, g.square.size()),
                                   table_work(g, g.d_update, g.update.size()), hp->iteration, forms, kLastParams, into,
                                   stream)) != hipSuccess)
@@ -982,7 +1016,7 @@ int64_t muon_orthogonalize_workspace_bytes(int64_t batch, int64_t rows, int64_t 
     return guarded([&]() -> int64_t {
         if (batch < 0 || batch >= (int64_t(1) << 31)) return fail(ADAM_EINVAL, "batch outside [0, 2^31)");
         if (int rc = check_shape(rows, cols, "the matrices")) return rc;
-        if (batch == 0 || rows == 0 || cols == 0) return 0;
+        if (batch == 0 || rows == 0 || cols == 0 || is_small(Shape{rows, cols})) return 0;
         return plan_batch(batch, Shape{rows, cols}).bytes;
     });
 }
@@ -1002,8 +1036,8 @@ int muon_orthogonalize(const muon_matrices *mats, const void *x, void *out, cons
             if (v < 0 || v > kMaxStride) return fail(ADAM_EINVAL, "stride outside [0, 2^40]");
         if (mats->x_row_stride < shape.cols || mats->out_row_stride < shape.cols)
             return fail(ADAM_EINVAL, "row stride smaller than cols");
-        if (need == 0) return ADAM_OK;
-        if (!x || !out || !workspace) return fail(ADAM_EINVAL, "NULL pointer");
+        if (mats->batch == 0 || shape.numel() == 0) return ADAM_OK;
+        if (!x || !out || (need > 0 && !workspace)) return fail(ADAM_EINVAL, "NULL pointer");
         if (workspace_bytes < need)
             return fail(ADAM_EINVAL, "workspace of " + std::to_string(workspace_bytes) + " bytes, " + std::to_string(need) +
                                          " needed");
@@ -1025,26 +1059,34 @@ int muon_orthogonalize(const muon_matrices *mats, const void *x, void *out, cons
             if (x0 < o1 && o0 < x1) return fail(ADAM_EINVAL, "out overlaps x");
         }
 
-        const BatchPlan p = plan_batch(mats->batch, shape);
-        const Workspace w = carve(static_cast<char *>(workspace), p.x_bytes * p.chunk, p.a_bytes * p.chunk,
-                                  p.n_partials * p.chunk);
         hipStream_t stream = reinterpret_cast<hipStream_t>(hip_stream);
         int forms[MUON_MAX_STEPS];
         forms_of(*iteration, mats->out_dtype == ADAM_GRAD_BF16, forms);
         MuonWork work{};
-        work.one.mb = (uint32_t)p.mb;
-        work.one.nb = (uint32_t)p.nb;
         work.one.rows = (uint32_t)shape.rows;
         work.one.cols = (uint32_t)shape.cols;
         work.one.u_ld = (uint64_t)mats->x_row_stride;
         work.one.o_ld = (uint64_t)mats->out_row_stride;
         work.one.tall = shape.rows > shape.cols;
-        work.x_stride = (uint64_t)p.x_bytes;
-        work.a_stride = (uint64_t)p.a_bytes;
         work.u_stride = (uint64_t)mats->x_batch_stride;
         work.o_stride = (uint64_t)mats->out_batch_stride;
-        work.norm_stride = (uint32_t)p.n_partials;
         hipError_t e;
+        if (is_small(shape)) {
+            work.per_mat = 1;
+            work.n_tiles = (uint32_t)mats->batch;
+            MuonSmallArgs small = small_args(work, x, xe == 2, *iteration, forms, oe == 2 ? kLastBf16 : kLastF32);
+            small.o = out;
+            e = launch_muon_small(shape.shorter(), shape.longer(), small, stream);
+            return e == hipSuccess ? ADAM_OK : hip_fail(e, "launch");
+        }
+        const BatchPlan p = plan_batch(mats->batch, shape);
+        const Workspace w = carve(static_cast<char *>(workspace), p.x_bytes * p.chunk, p.a_bytes * p.chunk,
+                                  p.n_partials * p.chunk);
+        work.one.mb = (uint32_t)p.mb;
+        work.one.nb = (uint32_t)p.nb;
+        work.x_stride = (uint64_t)p.x_bytes;
+        work.a_stride = (uint64_t)p.a_bytes;
+        work.norm_stride = (uint32_t)p.n_partials;
         for (int64_t first = 0; first < mats->batch; first += p.chunk) {
             const int64_t count = std::min(p.chunk, mats->batch - first);
             work.one.u_off = (uint64_t)(first * mats->x_batch_stride);

@@ -62,7 +62,8 @@ def _check(out, x, **kw):
 
 
 SHAPES = [(1, 1), (1, 7), (5, 1), (2, 3), (16, 16), (33, 65), (63, 64), (64, 64), (65, 64), (65, 129), (200, 31),
-          (128, 128), (129, 500), (300, 300), (1000, 768), (513, 1100), (1, 5000), (5000, 3)]
+          (128, 128), (129, 500), (300, 300), (1000, 768), (513, 1100), (1, 5000), (5000, 3),
+          (64, 768), (767, 61), (20, 700), (300, 32), (64, 769), (50, 400), (65, 65)]
 
 
 @pytest.mark.parametrize("shape", SHAPES, ids=str)
@@ -73,7 +74,7 @@ def test_orthogonalize_against_the_formula(shape, dtype):
 
 
 # enough tiles for the 128 x 128 kernels, with ragged edges; wide, tall, square
-@pytest.mark.parametrize("shape", [(17, 500, 1030), (17, 1030, 500), (9, 1024, 1024), (2900, 2950)], ids=str)
+@pytest.mark.parametrize("shape", [(70, 48, 80), (5, 3, 64, 500), (17, 500, 1030), (17, 1030, 500), (9, 1024, 1024), (2900, 2950)], ids=str)
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
 def test_orthogonalize_many_tiles(shape, dtype):
     x = _matrix(3, shape).to(dtype)
