@@ -11,22 +11,24 @@ namespace adam_mi355x {
 
 // One matrix of a launch.  Its factor X is short x long (m x n, m <= n), the
 // transpose of the user's matrix when that is tall.  A factor is kept as an
-// "image": cut into row blocks of T rows, each row block into slabs of 128
-// bytes per row, a slab's T x 128 bytes contiguous, slabs of a row block
-// contiguous, row blocks contiguous.  Dimensions are padded to multiples of
-// T with zeros, which every product keeps zero.  In a row's 128 bytes the
-// eight 16-byte chunks are stored at position chunk ^ (row % 8), so that a
-// slab copied to LDS as it is can be read by rows without bank conflicts.
-//   split slabs (two fp16 values per element): 32 elements, chunks 0..3 the
-//     high parts of 8 elements each, 4..7 the remainders;
-//   plain slabs (one fp16 value per element): 64 elements, 8 per chunk.
+// "image" in the order in which the matrix instructions take it: blocks of 32
+// rows; in each, slabs of 4 KB along the rows' elements; in each slab four
+// fragments of 1 KB, whose 16 bytes at position l are what lane l holds: row
+// l % 32, elements 8 (l / 32) .. + 7 of the fragment's 16.
+//   split slabs (two fp16 values per element): 32 elements; fragments: high
+//     parts of the first 16, their remainders, the same of the second 16;
+//   plain slabs (one fp16 value per element): 64 elements, 16 per fragment.
+// So a slab goes to LDS as it is, is read there without bank conflicts, and
+// a wave's 32 x 32 block of a result is one contiguous piece of an image.
+// Dimensions are padded to multiples of the tile with zeros, which every
+// product keeps zero.
 struct MuonMat {
     uint64_t x_off;   // byte offset in each of the X arrays
     uint64_t a_off;   // byte offset in the A and P arrays
     uint64_t u_off;   // element offset of the source matrix in its array
     uint64_t o_off;   // element offset of the output matrix in its array
     uint64_t u_ld, o_ld;  // row strides of source and output, in elements
-    uint32_t mb, nb;  // row blocks of the short and of the long side
+    uint32_t mp, np;      // padded short and long side
     uint32_t rows, cols;
     uint32_t tall;        // rows > cols
     uint32_t index;       // tensor index (pointer table, scale factors)
@@ -36,7 +38,7 @@ struct MuonMat {
 };
 static_assert(sizeof(MuonMat) == 96, "matrix descriptor layout");
 
-// One workgroup's tile: matrix, row block, column block.
+// One workgroup's tile: matrix, tile row, tile column.
 struct MuonTile {
     uint32_t mat;
     uint16_t ti, tj;
@@ -142,11 +144,15 @@ hipError_t launch_muon_momentum(int storage, bool grad_bf16, bool stochastic, co
 hipError_t launch_muon_norms(const double *partials, const uint2 *ranges, double *sums, uint32_t n_mats,
                              hipStream_t s);
 hipError_t launch_muon_sums(bool bf16, const MuonWork &w, const MuonSumArgs &a, uint32_t n_mats, hipStream_t s);
-hipError_t launch_muon_prep(int tile, bool bf16, int form, const MuonWork &w, const MuonPrepArgs &a, hipStream_t s);
+hipError_t launch_muon_prep(bool bf16, int form, const MuonWork &w, const MuonPrepArgs &a, hipStream_t s);
 
 enum MuonProduct : int { kGram, kPolynomial, kUpdate, kLastBf16, kLastF32, kLastParams };
+// The tiles of the products (rows and columns of the result, waves): the
+// dimensions of a matrix are padded to multiples of both of its products'
+// tiles.
+enum MuonTiling : int { kTile64, kTile128 };
 // in: the form of the factors read; out: of the factor written
-hipError_t launch_muon_product(int tile, int product, int in, int out, const MuonGemmArgs &a, hipStream_t s);
+hipError_t launch_muon_product(int tiling, int product, int in, int out, const MuonGemmArgs &a, hipStream_t s);
 
 // short_side, long_side: the largest of the launch's matrices
 hipError_t launch_muon_small(int64_t short_side, int64_t long_side, const MuonSmallArgs &a, hipStream_t s);

@@ -116,7 +116,7 @@ __device__ __forceinline__ void triangle(uint32_t t, uint32_t &ti, uint32_t &tj)
     tj = t - r * (r + 1u) / 2u;
 }
 
-// Tile t of an mb x nb grid, in bands of 8 block rows taken column by column:
+// Tile t of an mb x nb grid of tiles, in bands of 8 tile rows taken column by column:
 // the workgroups of an XCD that run together then share both factors' rows.
 __device__ __forceinline__ void banded(uint32_t t, uint32_t mb, uint32_t nb, uint32_t &ti, uint32_t &tj) {
     const uint32_t band = t / (8u * nb), first = band * 8u, high = min(8u, mb - first), in = t - band * 8u * nb;
@@ -125,107 +125,146 @@ __device__ __forceinline__ void banded(uint32_t t, uint32_t mb, uint32_t nb, uin
 }
 
 // ---------------------------------------------------------------- images
-// Byte position within one T-row block of element `k` (a multiple of 4) of
-// row `r`: its high part; the remainder is at ^ 64 (split form).
-template <int T, int kForm>
-__device__ __forceinline__ uint32_t image_pos(uint32_t r, uint32_t k) {
-    constexpr uint32_t kPer = kForm == kSplit ? 32u : 64u;
-    const uint32_t slab = k / kPer, chunk = (k % kPer) >> 3;
-    return slab * (T * 128u) + r * 128u + ((chunk ^ (r & 7u)) << 4) + (k & 7u) * 2u;
-}
+// Byte position of element (row r, k) in an image whose rows hold `length`
+// elements, for k a multiple of 4 (four elements lie side by side); remainders
+// (split form) are 1 KB on.
 template <int kForm>
-constexpr uint32_t elem_bytes() { return kForm == kSplit ? 4u : 2u; }
+constexpr uint32_t slab_length() { return kForm == kSplit ? 32u : 64u; }
+template <int kForm>
+__device__ __forceinline__ uint64_t image_pos(uint32_t r, uint32_t k, uint32_t length) {
+    constexpr uint32_t kPer = slab_length<kForm>();
+    const uint32_t fragment = ((k % kPer) >> 4) * (kForm == kSplit ? 2u : 1u);
+    return ((uint64_t)(r >> 5) * (length / kPer) + k / kPer) * 4096u + fragment * 1024u +
+           ((r & 31u) + (((k >> 3) & 1u) << 5)) * 16u + (k & 7u) * 2u;
+}
+constexpr uint32_t kRemainder = 1024u;
 
 // ---------------------------------------------------------------- products
+// How a product's result is cut: kRows x kCols tiles, each by a workgroup of
+// kDown x kAcross waves, with kStages slabs of the factors in LDS.
+template <int R, int C, int D, int A, int S, int W>
+struct Tiling {
+    static constexpr int kRows = R, kCols = C, kDown = D, kAcross = A, kStages = S;
+    static constexpr int kWaves = D * A, kThreads = 64 * kWaves;
+    static constexpr int kI = R / D / 32, kJ = C / A / 32;         // a wave's 32 x 32 blocks
+    static constexpr int kStage = (R + C) * 128;                   // bytes of a slab of both factors
+    static constexpr int kLoads = kStage / 1024 / kWaves;          // 1 KB pieces a wave fetches per slab
+    static constexpr int kPerSimd = W;                             // waves per SIMD it is compiled for
+    static_assert(kStage % (1024 * kWaves) == 0, "every wave fetches as much");
+};
+
 // 16 bytes per lane from memory straight to LDS: lane i's go to base + 16 i.
 __device__ __forceinline__ void dma16(const char *g, char *base) {
     __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)g,
                                      (__attribute__((address_space(3))) void *)base, 16, 0, 0);
 }
 
-template <int T>
-struct Tile {
-    static constexpr int kSlab = T * 128;          // bytes of one factor's slab
-    static constexpr int kWave = T / 2;            // a wave's part of the tile, square
-    static constexpr int kBlocks = kWave / 32;     // 32 x 32 blocks along it
-    static constexpr int kLds = 4 * kSlab;         // two slabs of two factors; the tile's image fits too
-    static_assert(T * T * 4 <= kLds, "image fits");
+// Waits until at most kLeft of the wave's fetches are under way and all of its
+// LDS reads are done, then for the workgroup's other waves to get there.  (In
+// assembly because __syncthreads() would wait for every fetch; the memory
+// clobber keeps the compiler's own reads and fetches on their side of it.)
+template <int kLeft>
+__device__ __forceinline__ void wait_and_meet() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"i"(kLeft) : "memory");
+}
+
+template <class T>
+struct Sources {
+    const char *at[T::kLoads];  // this wave's pieces of the next slab
 };
 
-template <int T>
-__device__ __forceinline__ void fetch(const char *left, const char *right, char *lds, int wave, int tid) {
+// rd and wr are different stages of LDS: without that promise the compiler
+// would wait for the fetches before every read.
+template <class T, int kForm>
+__device__ __forceinline__ void slab(f32x16 (&acc)[T::kI][T::kJ], const char *__restrict rd, char *__restrict wr,
+                                     Sources<T> &src, bool fetch, int wave, int lane) {
+    constexpr int kSteps = kForm == kSplit ? 2 : 4;
+    if (fetch) {
 #pragma unroll
-    for (int j = 0; j < Tile<T>::kSlab / 4096; ++j) {
-        dma16(left + j * 4096 + tid * 16, lds + j * 4096 + wave * 1024);
-        dma16(right + j * 4096 + tid * 16, lds + Tile<T>::kSlab + j * 4096 + wave * 1024);
+        for (int i = 0; i < T::kLoads; ++i) {
+            dma16(src.at[i] + lane * 16, wr + (wave * T::kLoads + i) * 1024);
+            src.at[i] += 4096;
+        }
+    }
+    const char *left = rd + (wave / T::kAcross) * (T::kI * 4096) + lane * 16;
+    const char *right = rd + T::kRows * 128 + (wave % T::kAcross) * (T::kJ * 4096) + lane * 16;
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) {
+        half8 l[T::kI], r[T::kJ], l2[T::kI], r2[T::kJ];
+        const int at = k * (kForm == kSplit ? 2048 : 1024);
+#pragma unroll
+        for (int i = 0; i < T::kI; ++i) {
+            l[i] = *reinterpret_cast<const half8 *>(left + i * 4096 + at);
+            if constexpr (kForm == kSplit) l2[i] = *reinterpret_cast<const half8 *>(left + i * 4096 + at + kRemainder);
+        }
+#pragma unroll
+        for (int j = 0; j < T::kJ; ++j) {
+            r[j] = *reinterpret_cast<const half8 *>(right + j * 4096 + at);
+            if constexpr (kForm == kSplit) r2[j] = *reinterpret_cast<const half8 *>(right + j * 4096 + at + kRemainder);
+        }
+#pragma unroll
+        for (int i = 0; i < T::kI; ++i)
+#pragma unroll
+            for (int j = 0; j < T::kJ; ++j) {
+                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(l[i], r[j], acc[i][j], 0, 0, 0);
+                if constexpr (kForm == kSplit) {
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(l[i], r2[j], acc[i][j], 0, 0, 0);
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(l2[i], r[j], acc[i][j], 0, 0, 0);
+                }
+            }
     }
 }
 
-__device__ __forceinline__ half8 frag(const char *rows, uint32_t row, uint32_t chunk) {
-    return *reinterpret_cast<const half8 *>(rows + row * 128u + ((chunk ^ (row & 7u)) << 4));
-}
-
-// sum = left right^T over `slabs` slabs, summed in runs of kRun slabs: one sum
-// that took every term of a long row in turn would lose more to fp32's
-// rounding than the split factors do.  Slab s + 1 is on its way to one half of
-// LDS while the matrix cores work on slab s from the other; one barrier a
-// slab, at which every wave has read slab s - 1 and its own part of slab s
-// has arrived.
+// sum = left right^T over `slabs` slabs (left, right: the tile's first slab;
+// *_block: bytes from one 32-row block to the next), summed in runs of at
+// least kRun slabs: one sum that took every term of a long row in turn would
+// lose more to fp32's rounding than the split factors do.  kStages - 1 slabs
+// are under way to LDS while the matrix cores work on one; at the barrier
+// before slab s, its fetches are done and every wave has read slab s - 1,
+// whose place the next fetch takes.
 constexpr uint32_t kRun = 8;
 
-template <int T, int kForm>
-__device__ __forceinline__ void product(f32x16 (&sum)[Tile<T>::kBlocks][Tile<T>::kBlocks], const char *left,
-                                        const char *right, uint32_t slabs, char *lds) {
-    constexpr int kB = Tile<T>::kBlocks, kSteps = kForm == kSplit ? 2 : 4;
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const uint32_t row_l = (wave >> 1) * Tile<T>::kWave + (lane & 31), row_r = (wave & 1) * Tile<T>::kWave + (lane & 31);
-    const uint32_t half = lane >> 5;
-    f32x16 acc[kB][kB];
+template <class T, int kForm>
+__device__ __forceinline__ void product(f32x16 (&sum)[T::kI][T::kJ], const char *left, uint64_t left_block,
+                                        const char *right, uint64_t right_block, uint32_t slabs, char *lds) {
+    constexpr int kS = T::kStages;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    Sources<T> src;
 #pragma unroll
-    for (int i = 0; i < kB; ++i)
+    for (int i = 0; i < T::kLoads; ++i) {
+        const uint32_t piece = wave * T::kLoads + i, block = piece >> 2;
+        src.at[i] = (block < T::kRows / 32 ? left + block * left_block : right + (block - T::kRows / 32) * right_block) +
+                    (piece & 3u) * 1024u;
+    }
 #pragma unroll
-        for (int j = 0; j < kB; ++j) sum[i][j] = acc[i][j] = f32x16{};
-    fetch<T>(left, right, lds, wave, tid);
-    for (uint32_t s = 0; s < slabs; ++s) {
-        __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
-        __syncthreads();
-        const char *here = lds + (s & 1u) * (2 * Tile<T>::kSlab);
-        half8 l[kSteps][kB], r[kSteps][kB], l2[kSteps][kB], r2[kSteps][kB];
+    for (int s = 0; s < kS - 1; ++s)
+        if (s < (int)slabs)
 #pragma unroll
-        for (int k = 0; k < kSteps; ++k)
-#pragma unroll
-            for (int i = 0; i < kB; ++i) {
-                const uint32_t c = k * 2 + half;
-                l[k][i] = frag(here, row_l + i * 32, c);
-                r[k][i] = frag(here + Tile<T>::kSlab, row_r + i * 32, c);
-                if constexpr (kForm == kSplit) {
-                    l2[k][i] = frag(here, row_l + i * 32, c + 4);
-                    r2[k][i] = frag(here + Tile<T>::kSlab, row_r + i * 32, c + 4);
-                }
+            for (int i = 0; i < T::kLoads; ++i) {
+                dma16(src.at[i] + lane * 16, lds + s * T::kStage + (wave * T::kLoads + i) * 1024);
+                src.at[i] += 4096;
             }
-        if (s + 1 < slabs) {
-            left += Tile<T>::kSlab;
-            right += Tile<T>::kSlab;
-            fetch<T>(left, right, lds + ((s + 1) & 1u) * (2 * Tile<T>::kSlab), wave, tid);
+    f32x16 acc[T::kI][T::kJ];
+#pragma unroll
+    for (int i = 0; i < T::kI; ++i)
+#pragma unroll
+        for (int j = 0; j < T::kJ; ++j) sum[i][j] = acc[i][j] = f32x16{};
+    for (uint32_t s0 = 0; s0 < slabs; s0 += kS) {
+#pragma unroll
+        for (int u = 0; u < kS; ++u) {
+            const uint32_t s = s0 + u;
+            if (s >= slabs) break;
+            if (s + (kS - 2) < slabs) wait_and_meet<(kS - 2) * T::kLoads>();
+            else wait_and_meet<0>();
+            slab<T, kForm>(acc, lds + u * T::kStage, lds + ((u + kS - 1) % kS) * T::kStage, src, s + (kS - 1) < slabs, wave,
+                           lane);
         }
+        if (s0 % kRun + kS >= kRun || s0 + kS >= slabs) {
 #pragma unroll
-        for (int k = 0; k < kSteps; ++k)
+            for (int i = 0; i < T::kI; ++i)
 #pragma unroll
-            for (int i = 0; i < kB; ++i)
-#pragma unroll
-                for (int j = 0; j < kB; ++j) {
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(l[k][i], r[k][j], acc[i][j], 0, 0, 0);
-                    if constexpr (kForm == kSplit) {
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(l[k][i], r2[k][j], acc[i][j], 0, 0, 0);
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(l2[k][i], r[k][j], acc[i][j], 0, 0, 0);
-                    }
-                }
-        if ((s & (kRun - 1)) == kRun - 1 || s + 1 == slabs) {
-#pragma unroll
-            for (int i = 0; i < kB; ++i)
-#pragma unroll
-                for (int j = 0; j < kB; ++j) {
+                for (int j = 0; j < T::kJ; ++j) {
                     sum[i][j] += acc[i][j];
                     acc[i][j] = f32x16{};
                 }
@@ -249,42 +288,28 @@ __device__ __forceinline__ u32x2 quad_transpose(u32x2 d, uint32_t lane) {
     return (lane & 2u) ? u32x2{m1, e1} : u32x2{e0, m0};
 }
 
-// The tile's values as the image of C (rows r, elements along c) or, with
-// kTransposed, of C^T, assembled in LDS and copied out: one contiguous piece
-// of the destination's row block.
-template <int T, int kForm, bool kTransposed>
-__device__ __forceinline__ void store_image(const f32x16 (&v)[Tile<T>::kBlocks][Tile<T>::kBlocks], char *lds, char *dst) {
-    constexpr int kB = Tile<T>::kBlocks;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const uint32_t r00 = (wave >> 1) * Tile<T>::kWave + 4 * (lane >> 5), c00 = (wave & 1) * Tile<T>::kWave + (lane & 31);
-    __syncthreads();  // LDS is free: the last slab, or the image before, has been read
+// A 32 x 32 block of values, at rows r0.. and columns c0.., into an image whose
+// rows hold `length` elements: as it is, or (kTransposed) with rows and columns exchanged.
+template <int kForm, bool kTransposed>
+__device__ __forceinline__ void store_block(const f32x16 &v, char *image, uint32_t r0, uint32_t c0, uint32_t length, uint32_t lane) {
+    const uint32_t r = r0 + 4u * (lane >> 5), c = c0 + (lane & 31u);
 #pragma unroll
-    for (int i = 0; i < kB; ++i)
+    for (int g = 0; g < 4; ++g) {
+        _Float16 hi[4], lo[4];
 #pragma unroll
-        for (int j = 0; j < kB; ++j)
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                _Float16 hi[4], lo[4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) split(v[i][j][4 * g + q], hi[q], lo[q]);
-                u32x2 h = {pack(hi[0], hi[1]), pack(hi[2], hi[3])}, l = {pack(lo[0], lo[1]), pack(lo[2], lo[3])};
-                uint32_t at;
-                const uint32_t r = r00 + i * 32 + 8 * g, c = c00 + j * 32;
-                if constexpr (kTransposed) {
-                    at = image_pos<T, kForm>(c, r);
-                } else {
-                    h = quad_transpose(h, lane);
-                    l = quad_transpose(l, lane);
-                    at = image_pos<T, kForm>(r + (lane & 3), c & ~3u);
-                }
-                *reinterpret_cast<u32x2 *>(lds + at) = h;
-                if constexpr (kForm == kSplit) *reinterpret_cast<u32x2 *>(lds + (at ^ 64u)) = l;
-            }
-    __syncthreads();
-    constexpr int kBytes = T * T * (int)elem_bytes<kForm>();
-#pragma unroll
-    for (int o = 0; o < kBytes; o += 4096)
-        *reinterpret_cast<u32x4 *>(dst + o + tid * 16) = *reinterpret_cast<const u32x4 *>(lds + o + tid * 16);
+        for (int q = 0; q < 4; ++q) split(v[4 * g + q], hi[q], lo[q]);
+        u32x2 h = {pack(hi[0], hi[1]), pack(hi[2], hi[3])}, l = {pack(lo[0], lo[1]), pack(lo[2], lo[3])};
+        char *at;
+        if constexpr (kTransposed) {
+            at = image + image_pos<kForm>(c, r + 8u * g, length);
+        } else {
+            h = quad_transpose(h, lane);
+            l = quad_transpose(l, lane);
+            at = image + image_pos<kForm>(r + 8u * g + (lane & 3u), c & ~3u, length);
+        }
+        *reinterpret_cast<u32x2 *>(at) = h;
+        if constexpr (kForm == kSplit) *reinterpret_cast<u32x2 *>(at + kRemainder) = l;
+    }
 }
 
 // The tiles of one product over all matrices of a launch.
@@ -294,12 +319,11 @@ __device__ __forceinline__ void store_image(const f32x16 (&v)[Tile<T>::kBlocks][
 //   kLast..:     O = P X in the user's orientation (for a tall matrix the
 //                factors change places), rounded to the output's type, or
 //                applied to the params
-template <int T, int kProduct, int kIn, int kOut>
-__global__ __launch_bounds__(256) void muon_product_kernel(MuonGemmArgs a) {
-    __shared__ __attribute__((aligned(128))) char lds[Tile<T>::kLds];
-    constexpr int kB = Tile<T>::kBlocks;
+template <class T, int kProduct, int kIn, int kOut>
+__global__ __launch_bounds__(T::kThreads) __attribute__((amdgpu_waves_per_eu(T::kPerSimd)))
+void muon_product_kernel(MuonGemmArgs a) {
+    __shared__ __attribute__((aligned(1024))) char lds[T::kStages * T::kStage];
     constexpr bool kLast = kProduct >= kLastBf16, kSquare = kProduct == kGram || kProduct == kPolynomial;
-    constexpr uint32_t kPer = kIn == kSplit ? 32u : 64u;
     uint32_t t, ti, tj;
     const MuonMat m = find_mat(a.work, xcd_order(blockIdx.x, a.work.n_tiles), t);
     if (a.work.tiles) {
@@ -308,105 +332,100 @@ __global__ __launch_bounds__(256) void muon_product_kernel(MuonGemmArgs a) {
     } else if constexpr (kSquare) {
         triangle(t, ti, tj);
     } else {
-        banded(t, m.mb, m.nb, ti, tj);
+        const uint32_t across = (kLast && m.tall) ? T::kRows : T::kCols, down = (kLast && m.tall) ? T::kCols : T::kRows;
+        banded(t, m.mp / down, m.np / across, ti, tj);
     }
-    const uint32_t k = (kProduct == kGram ? m.nb : m.mb) * T;  // length of the products
-    const uint64_t row_block = (uint64_t)T * k * elem_bytes<kIn>();
-    const bool swap = kLast && m.tall;
+    const uint32_t k = kProduct == kGram ? m.np : m.mp;  // length of the products
+    const uint64_t block = (uint64_t)(k / slab_length<kIn>()) * 4096u;  // bytes of 32 rows of either factor
     const char *left, *right;
+    uint32_t row0, col0;  // of the result
     if constexpr (kSquare) {
         const char *f = a.left + (kProduct == kGram ? m.x_off : m.a_off);
-        left = f + ti * row_block;
-        right = f + tj * row_block;
+        row0 = ti * T::kRows;
+        col0 = tj * T::kCols;
+        left = f + (row0 >> 5) * block;
+        right = f + (col0 >> 5) * block;
     } else {
-        left = a.left + m.a_off + ti * row_block;
-        right = a.right + m.x_off + tj * row_block;
-        if (swap) {
-            const char *x = left;
-            left = right;
-            right = x;
-        }
+        const bool swap = kLast && m.tall;
+        row0 = (swap ? tj : ti) * T::kRows;
+        col0 = (swap ? ti : tj) * T::kCols;
+        const char *p = a.left + m.a_off, *x = a.right + m.x_off;
+        left = (swap ? x : p) + (row0 >> 5) * block;
+        right = (swap ? p : x) + (col0 >> 5) * block;
     }
-    f32x16 acc[kB][kB];
-    product<T, kIn>(acc, left, right, k / kPer, lds);
+    f32x16 acc[T::kI][T::kJ];
+    product<T, kIn>(acc, left, block, right, block, k / slab_length<kIn>(), lds);
 
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const uint32_t r00 = (wave >> 1) * Tile<T>::kWave + 4 * (lane >> 5), c00 = (wave & 1) * Tile<T>::kWave + (lane & 31);
-    if constexpr (kProduct == kGram) {
+    const uint32_t lane = threadIdx.x & 63u;
+    const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    row0 += (wave / T::kAcross) * (T::kI * 32);
+    col0 += (wave % T::kAcross) * (T::kJ * 32);
+    float *param = nullptr;
+    float step = 0.0f;
+    if constexpr (kProduct == kLastParams) {
+        param = ((ConstTensorPtr)a.tensors + m.index)->p;
+        step = (float)(a.lr * (a.scale == 1 ? m.scale_spectral : (a.scale == 2 ? m.scale_rms : 1.0)));
+    }
 #pragma unroll
-        for (int i = 0; i < kB; ++i)
+    for (int i = 0; i < T::kI; ++i)
 #pragma unroll
-            for (int j = 0; j < kB; ++j) acc[i][j] *= 1.0f / kScaleX;
-    } else if constexpr (kProduct == kPolynomial) {
-        // A's tile, read from its mirror image: four values down a column lie side by side
-        const char *add = a.add + m.a_off + tj * row_block + (uint64_t)ti * (T / kPer) * Tile<T>::kSlab;
-        const float cb = a.cb * (kScaleP / kScaleX), cc = a.cc * (kScaleP / (kScaleX * kScaleX)), ca = a.ca * kScaleP;
+        for (int j = 0; j < T::kJ; ++j) {
+            f32x16 v = acc[i][j];
+            const uint32_t r0 = row0 + 32u * i, c0 = col0 + 32u * j;
+            const uint32_t r = r0 + 4u * (lane >> 5), c = c0 + (lane & 31u);
+            if constexpr (kSquare) {
+                char *out = a.out + m.a_off;
+                if constexpr (kProduct == kGram) {
+                    v *= 1.0f / kScaleX;
+                } else {
+                    // A's block, read from its mirror image: four values down a column lie side by side
+                    const float cb = a.cb * (kScaleP / kScaleX), cc = a.cc * (kScaleP / (kScaleX * kScaleX));
+                    const float ca = a.ca * kScaleP;
 #pragma unroll
-        for (int i = 0; i < kB; ++i)
+                    for (int g = 0; g < 4; ++g) {
+                        const char *at = a.add + m.a_off + image_pos<kIn>(c, r + 8u * g, m.mp);
+                        const u32x2 h = *reinterpret_cast<const u32x2 *>(at);
+                        u32x2 l = {0u, 0u};
+                        if constexpr (kIn == kSplit) l = *reinterpret_cast<const u32x2 *>(at + kRemainder);
 #pragma unroll
-            for (int j = 0; j < kB; ++j)
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const uint32_t r = r00 + i * 32 + 8 * g, c = c00 + j * 32, at = image_pos<T, kIn>(c, r);
-                    const u32x2 h = *reinterpret_cast<const u32x2 *>(add + at);
-                    u32x2 l = {0u, 0u};
-                    if constexpr (kIn == kSplit) l = *reinterpret_cast<const u32x2 *>(add + (at ^ 64u));
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const uint32_t hw = q < 2 ? h.x : h.y, lw = q < 2 ? l.x : l.y;
-                        const float av = (float)__builtin_bit_cast(_Float16, (uint16_t)(hw >> (16 * (q & 1)))) +
-                                         (float)__builtin_bit_cast(_Float16, (uint16_t)(lw >> (16 * (q & 1))));
-                        float v = fmaf(cb, av, cc * acc[i][j][4 * g + q]);
-                        if (ti == tj && r + q == c) v += ca;
-                        acc[i][j][4 * g + q] = v;
+                        for (int q = 0; q < 4; ++q) {
+                            const uint32_t hw = q < 2 ? h.x : h.y, lw = q < 2 ? l.x : l.y;
+                            const float av = (float)__builtin_bit_cast(_Float16, (uint16_t)(hw >> (16 * (q & 1)))) +
+                                             (float)__builtin_bit_cast(_Float16, (uint16_t)(lw >> (16 * (q & 1))));
+                            float x = fmaf(cb, av, cc * v[4 * g + q]);
+                            if (r + 8u * g + q == c) x += ca;
+                            v[4 * g + q] = x;
+                        }
                     }
                 }
-    } else if constexpr (kProduct == kUpdate) {
+                store_block<kOut, true>(v, out, r0, c0, m.mp, lane);
+                if (ti != tj) store_block<kOut, false>(v, out, r0, c0, m.mp, lane);
+            } else if constexpr (kProduct == kUpdate) {
+                v *= 1.0f / kScaleP;
+                store_block<kOut, false>(v, a.out + m.x_off, r0, c0, m.np, lane);
+                store_block<kOut, true>(v, a.out_t + m.x_off, r0, c0, m.mp, lane);
+            } else {
+                constexpr float kUnscale = 1.0f / (kScaleX * kScaleP);
+                float old[16];
+                if constexpr (kProduct == kLastParams) {  // all of the block's params at once, then the stores
 #pragma unroll
-        for (int i = 0; i < kB; ++i)
-#pragma unroll
-            for (int j = 0; j < kB; ++j) acc[i][j] *= 1.0f / kScaleP;
-    }
-
-    if constexpr (kSquare) {
-        char *out = a.out + m.a_off;
-        constexpr uint64_t kPerOut = kOut == kSplit ? 32 : 64;
-        const uint64_t rb = (uint64_t)T * m.mb * T * elem_bytes<kOut>();
-        store_image<T, kOut, true>(acc, lds, out + tj * rb + ti * (T / kPerOut) * Tile<T>::kSlab);
-        if (ti != tj) store_image<T, kOut, false>(acc, lds, out + ti * rb + tj * (T / kPerOut) * Tile<T>::kSlab);
-    } else if constexpr (kProduct == kUpdate) {
-        constexpr uint64_t kPerOut = kOut == kSplit ? 32 : 64;
-        const uint64_t rb = (uint64_t)T * m.nb * T * elem_bytes<kOut>(), rb_t = (uint64_t)T * m.mb * T * elem_bytes<kOut>();
-        store_image<T, kOut, false>(acc, lds, a.out + m.x_off + ti * rb + tj * (T / kPerOut) * Tile<T>::kSlab);
-        store_image<T, kOut, true>(acc, lds, a.out_t + m.x_off + tj * rb_t + ti * (T / kPerOut) * Tile<T>::kSlab);
-    } else {
-        const uint32_t row0 = (swap ? tj : ti) * T + r00, col0 = (swap ? ti : tj) * T + c00;
-        constexpr float kUnscale = 1.0f / (kScaleX * kScaleP);
-        float *p = nullptr;
-        float step = 0.0f;
-        if constexpr (kProduct == kLastParams) {
-            p = ((ConstTensorPtr)a.tensors + m.index)->p;
-            step = (float)(a.lr * (a.scale == 1 ? m.scale_spectral : (a.scale == 2 ? m.scale_rms : 1.0)));
-        }
-#pragma unroll
-        for (int i = 0; i < kB; ++i)
-#pragma unroll
-            for (int j = 0; j < kB; ++j)
+                    for (int e = 0; e < 16; ++e) {
+                        const uint32_t q = r + 8u * (e / 4) + (e & 3);
+                        old[e] = q < m.rows && c < m.cols ? param[(uint64_t)q * m.cols + c] : 0.0f;
+                    }
+                }
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                    const uint32_t r = row0 + i * 32 + 8 * (e / 4) + (e & 3), c = col0 + j * 32;
-                    if (r >= m.rows || c >= m.cols) continue;
-                    const float o = acc[i][j][e] * kUnscale;
-                    if constexpr (kProduct == kLastParams) {
-                        float *q = p + (uint64_t)r * m.cols + c;
-                        *q = fmaf(-step, o, *q * a.decay);
-                    } else if constexpr (kProduct == kLastBf16) {
-                        static_cast<uint16_t *>(a.o)[m.o_off + r * m.o_ld + c] = (uint16_t)f32_to_bf16(o);
-                    } else {
-                        static_cast<float *>(a.o)[m.o_off + r * m.o_ld + c] = o;
-                    }
+                    const uint32_t q = r + 8u * (e / 4) + (e & 3);
+                    if (q >= m.rows || c >= m.cols) continue;
+                    const float o = v[e] * kUnscale;
+                    if constexpr (kProduct == kLastParams) param[(uint64_t)q * m.cols + c] = fmaf(-step, o, old[e] * a.decay);
+                    else if constexpr (kProduct == kLastBf16)
+                        static_cast<uint16_t *>(a.o)[m.o_off + q * m.o_ld + c] = (uint16_t)f32_to_bf16(o);
+                    else static_cast<float *>(a.o)[m.o_off + q * m.o_ld + c] = o;
                 }
-    }
+            }
+        }
 }
 
 // ---------------------------------------------------------------- small matrices
@@ -697,44 +716,49 @@ __global__ __launch_bounds__(256) void muon_sums_kernel(MuonWork w, MuonSumArgs 
 
 // The images of X_0 and X_0^T, one 64 x 64 tile of the user's matrix a
 // workgroup.  A norm that is not finite makes all of X_0 NaN.
-template <int T, bool kBf16, int kForm>
+template <bool kBf16, int kForm>
 __global__ __launch_bounds__(256) void muon_prep_kernel(MuonWork w, MuonPrepArgs a) {
     __shared__ double s[4];
     __shared__ float y[64][65];
     uint32_t t;
     const MuonMat m = find_mat(w, blockIdx.x, t);
-    const uint32_t cb = m.tall ? m.mb : m.nb, rb = m.tall ? m.nb : m.mb;  // row blocks along columns and rows
+    const uint32_t rp = m.tall ? m.np : m.mp, cp = m.tall ? m.mp : m.np;  // the user's matrix, padded
     uint32_t ti, tj;
     if (w.tiles) {
         ti = t & 0xFFFFu;
         tj = t >> 16;
     } else {
-        ti = t / (cb * (T / 64));
-        tj = t - ti * (cb * (T / 64));
+        ti = t / (cp / 64u);
+        tj = t - ti * (cp / 64u);
+    }
+    const uint32_t c_in = threadIdx.x & 63u, r_in = threadIdx.x >> 6;
+    const uint32_t c = tj * 64u + c_in;
+    float v[16];
+#pragma unroll
+    for (uint32_t i = 0; i < 16u; ++i) {
+        const uint32_t r = ti * 64u + r_in + 4u * i;
+        v[i] = r < m.rows && c < m.cols ? load_elem<kBf16>(a.u, m.u_off + r * m.u_ld + c) : 0.0f;
     }
     double part = 0.0;
     for (uint32_t i = threadIdx.x; i < a.n_partials; i += 256u) part += a.partials[m.norm + i];
     const double sum = block_sum(part, s);
     const double inv = sum < __builtin_inf() ? (double)kScaleX / (sqrt(sum) + a.eps) : __builtin_nan("");
-
-    const uint32_t c_in = threadIdx.x & 63u, r_in = threadIdx.x >> 6;
 #pragma unroll
     for (uint32_t i = 0; i < 16u; ++i) {
-        const uint32_t r = ti * 64u + r_in + 4u * i, c = tj * 64u + c_in;
-        float v = 0.0f;
-        if (r < m.rows && c < m.cols) v = (float)((double)load_elem<kBf16>(a.u, m.u_off + r * m.u_ld + c) * inv);
-        y[r_in + 4u * i][c_in] = v;
+        const bool in = ti * 64u + r_in + 4u * i < m.rows && c < m.cols;  // padding is zero, whatever the norm
+        y[r_in + 4u * i][c_in] = in ? (float)((double)v[i] * inv) : 0.0f;
     }
     __syncthreads();
-    // by user rows (elements along the columns), then by user columns
+    // by user rows (elements along the columns), then by user columns: 16 bytes
+    // a thread, the 32 rows of a fragment side by side
 #pragma unroll
     for (int o = 0; o < 2; ++o) {
         char *dst = ((o == 0) == (m.tall == 0) ? a.x : a.xt) + m.x_off;
-        const uint32_t length = (o == 0 ? cb : rb) * T;  // elements along a row of this image
+        const uint32_t length = o == 0 ? cp : rp;
         const uint32_t row0 = (o == 0 ? ti : tj) * 64u, k0 = (o == 0 ? tj : ti) * 64u;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const uint32_t job = j * 256u + threadIdx.x, row = job >> 3, k = (job & 7u) * 8u;
+            const uint32_t job = j * 256u + threadIdx.x, row = (job & 31u) + 32u * (job >> 8), k = ((job >> 5) & 7u) * 8u;
             u32x4 h, l;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -744,13 +768,9 @@ __global__ __launch_bounds__(256) void muon_prep_kernel(MuonWork w, MuonPrepArgs
                 h[e] = pack(h0, h1);
                 l[e] = pack(l0, l1);
             }
-            const uint32_t r = row0 + row;
-            char *at = dst + (uint64_t)(r / T) * ((uint64_t)T * length * elem_bytes<kForm>());
-            constexpr uint32_t kPer = kForm == kSplit ? 32u : 64u;
-            const uint64_t slab = (uint64_t)((k0 + k) / kPer) * Tile<T>::kSlab;
-            const uint32_t in = image_pos<T, kForm>(r % T, (k0 + k) % kPer);
-            *reinterpret_cast<u32x4 *>(at + slab + in) = h;
-            if constexpr (kForm == kSplit) *reinterpret_cast<u32x4 *>(at + slab + (in ^ 64u)) = l;
+            char *at = dst + image_pos<kForm>(row0 + row, k0 + k, length);
+            *reinterpret_cast<u32x4 *>(at) = h;
+            if constexpr (kForm == kSplit) *reinterpret_cast<u32x4 *>(at + kRemainder) = l;
         }
     }
 }
@@ -968,27 +988,21 @@ hipError_t launch_muon_sums(bool bf16, const MuonWork &w, const MuonSumArgs &a, 
     return hipGetLastError();
 }
 
-template <int T>
-static void prep(bool bf16, int form, const MuonWork &w, const MuonPrepArgs &a, hipStream_t s) {
+hipError_t launch_muon_prep(bool bf16, int form, const MuonWork &w, const MuonPrepArgs &a, hipStream_t s) {
     const dim3 grid(w.n_tiles), block(256);
     if (form == kSplit) {
-        if (bf16) muon_prep_kernel<T, true, kSplit><<<grid, block, 0, s>>>(w, a);
-        else muon_prep_kernel<T, false, kSplit><<<grid, block, 0, s>>>(w, a);
+        if (bf16) muon_prep_kernel<true, kSplit><<<grid, block, 0, s>>>(w, a);
+        else muon_prep_kernel<false, kSplit><<<grid, block, 0, s>>>(w, a);
     } else {
-        if (bf16) muon_prep_kernel<T, true, kPlain><<<grid, block, 0, s>>>(w, a);
-        else muon_prep_kernel<T, false, kPlain><<<grid, block, 0, s>>>(w, a);
+        if (bf16) muon_prep_kernel<true, kPlain><<<grid, block, 0, s>>>(w, a);
+        else muon_prep_kernel<false, kPlain><<<grid, block, 0, s>>>(w, a);
     }
-}
-
-hipError_t launch_muon_prep(int tile, bool bf16, int form, const MuonWork &w, const MuonPrepArgs &a, hipStream_t s) {
-    if (tile == 128) prep<128>(bf16, form, w, a, s);
-    else prep<64>(bf16, form, w, a, s);
     return hipGetLastError();
 }
 
-template <int T>
+template <class T>
 static hipError_t product_of(int product, int in, int out, const MuonGemmArgs &a, hipStream_t s) {
-    const dim3 grid(a.work.n_tiles), block(256);
+    const dim3 grid(a.work.n_tiles), block(T::kThreads);
 #define MUON_CASE(p, i, o)                                                       \
     if (product == p && in == i && out == o) {                                   \
         muon_product_kernel<T, p, i, o><<<grid, block, 0, s>>>(a);               \
@@ -1009,8 +1023,11 @@ static hipError_t product_of(int product, int in, int out, const MuonGemmArgs &a
     return hipErrorInvalidValue;
 }
 
-hipError_t launch_muon_product(int tile, int product, int in, int out, const MuonGemmArgs &a, hipStream_t s) {
-    return tile == 128 ? product_of<128>(product, in, out, a, s) : product_of<64>(product, in, out, a, s);
+typedef Tiling<64, 64, 2, 2, 4, 2> Tiling64;
+typedef Tiling<128, 128, 2, 2, 2, 2> Tiling128;
+
+hipError_t launch_muon_product(int tiling, int product, int in, int out, const MuonGemmArgs &a, hipStream_t s) {
+    return tiling == kTile128 ? product_of<Tiling128>(product, in, out, a, s) : product_of<Tiling64>(product, in, out, a, s);
 }
 
 hipError_t launch_muon_small(int64_t short_side, int64_t long_side, const MuonSmallArgs &a, hipStream_t s) {

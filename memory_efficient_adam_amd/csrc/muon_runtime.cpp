@@ -89,6 +89,7 @@ struct Shape {
 
 bool is_small(const Shape &s) { return s.shorter() <= kSmallShort && s.longer() <= kSmallLong; }
 int tile_for(int64_t tiles128) { return tiles128 >= kLargeTiles ? 128 : 64; }
+int tiling_of(int tile) { return tile == 128 ? kTile128 : kTile64; }
 int64_t tiles_of(const Shape &s, int64_t tile) {
     return (pad_to(s.shorter(), tile) / tile) * (pad_to(s.longer(), tile) / tile);
 }
@@ -265,7 +266,7 @@ MuonSmallArgs small_args(const MuonWork &w, const void *u, bool u_bf16, const mu
 }
 
 // The products of all iterations, X_0 and X_0^T being in f.x[0], f.xt[0].
-hipError_t run_products(int tile, const MuonArrays &f, const MuonWork &square, const MuonWork &update,
+hipError_t run_products(int tiling, const MuonArrays &f, const MuonWork &square, const MuonWork &update,
                         const muon_iteration &it, const int *forms, int last, const MuonGemmArgs &into, hipStream_t s) {
     hipError_t e;
     for (int k = 0; k < it.steps; ++k) {
@@ -276,14 +277,14 @@ hipError_t run_products(int tile, const MuonArrays &f, const MuonWork &square, c
         a.work = square;
         a.left = f.x[cur];
         a.out = f.a;
-        if ((e = launch_muon_product(tile, kGram, in, in, a, s)) != hipSuccess) return e;
+        if ((e = launch_muon_product(tiling, kGram, in, in, a, s)) != hipSuccess) return e;
         a.left = f.a;
         a.add = f.a;
         a.out = f.p;
         a.ca = c[0];
         a.cb = c[1];
         a.cc = c[2];
-        if ((e = launch_muon_product(tile, kPolynomial, in, in, a, s)) != hipSuccess) return e;
+        if ((e = launch_muon_product(tiling, kPolynomial, in, in, a, s)) != hipSuccess) return e;
         if (k + 1 < it.steps) {
             a = MuonGemmArgs{};
             a.work = update;
@@ -291,13 +292,13 @@ hipError_t run_products(int tile, const MuonArrays &f, const MuonWork &square, c
             a.right = f.xt[cur];
             a.out = f.x[cur ^ 1];
             a.out_t = f.xt[cur ^ 1];
-            e = launch_muon_product(tile, kUpdate, in, forms[k + 1], a, s);
+            e = launch_muon_product(tiling, kUpdate, in, forms[k + 1], a, s);
         } else {
             a = into;
             a.work = update;
             a.left = f.p;
             a.right = f.xt[cur];
-            e = launch_muon_product(tile, last, in, in, a, s);
+            e = launch_muon_product(tiling, last, in, in, a, s);
         }
         if (e != hipSuccess) return e;
     }
@@ -394,8 +395,8 @@ void build_tables(Group &g, const std::vector<Shape> &shapes) {
         m.a_off = a_off;
         m.u_off = (uint64_t)flats[k - g.first];
         m.u_ld = (uint64_t)s.cols;
-        m.mb = (uint32_t)(pad_to(s.shorter(), T) / T);
-        m.nb = (uint32_t)(pad_to(s.longer(), T) / T);
+        m.mp = (uint32_t)pad_to(s.shorter(), T);
+        m.np = (uint32_t)pad_to(s.longer(), T);
         m.rows = (uint32_t)s.rows;
         m.cols = (uint32_t)s.cols;
         m.tall = s.rows > s.cols;
@@ -404,8 +405,8 @@ void build_tables(Group &g, const std::vector<Shape> &shapes) {
         m.norm = i;
         m.scale_spectral = std::sqrt(std::max(1.0, (double)s.rows / (double)s.cols));
         m.scale_rms = 0.2 * std::sqrt((double)s.longer());
-        x_off += 4ull * T * T * m.mb * m.nb;
-        a_off += 4ull * T * T * m.mb * m.mb;
+        x_off += 4ull * m.mp * m.np;
+        a_off += 4ull * m.mp * m.mp;
         g.mats.push_back(m);
         const int64_t b0 = firsts[k - g.first];
         g.ranges.push_back(uint2{(uint32_t)b0, (uint32_t)(b0 + blocks_of(s.numel()))});
@@ -415,14 +416,15 @@ void build_tables(Group &g, const std::vector<Shape> &shapes) {
             g.small_long = std::max(g.small_long, s.longer());
             continue;
         }
-        const uint32_t pr = (m.tall ? m.nb : m.mb) * (T / 64), pc = (m.tall ? m.mb : m.nb) * (T / 64);
+        const uint32_t mb = m.mp / T, nb = m.np / T;
+        const uint32_t pr = (m.tall ? m.np : m.mp) / 64, pc = (m.tall ? m.mp : m.np) / 64;
         for (uint32_t a = 0; a < pr; ++a)
             for (uint32_t b = 0; b < pc; ++b) g.prep.push_back(MuonTile{i, (uint16_t)a, (uint16_t)b});
-        for (uint32_t a = 0; a < m.mb; ++a)
+        for (uint32_t a = 0; a < mb; ++a)
             for (uint32_t b = 0; b <= a; ++b) g.square.push_back(MuonTile{i, (uint16_t)a, (uint16_t)b});
-        for (uint32_t a0 = 0; a0 < m.mb; a0 += 8)  // bands of 8 row blocks, as the kernel takes them
-            for (uint32_t b = 0; b < m.nb; ++b)
-                for (uint32_t a = a0; a < std::min(m.mb, a0 + 8); ++a)
+        for (uint32_t a0 = 0; a0 < mb; a0 += 8)  // bands of 8 tile rows, as the kernel takes them
+            for (uint32_t b = 0; b < nb; ++b)
+                for (uint32_t a = a0; a < std::min(mb, a0 + 8); ++a)
                     g.update.push_back(MuonTile{i, (uint16_t)a, (uint16_t)b});
     }
 }
@@ -721,10 +723,10 @@ int muon_step(muon_state *s, float *const *params, const void *const *grads, con
             p.eps = (double)hp->iteration.eps;
             p.x = w.f.x[0];
             p.xt = w.f.xt[0];
-            if ((e = launch_muon_prep(g.tile, false, forms[0], table_work(g, g.d_prep, g.prep.size()), p, stream)) !=
+            if ((e = launch_muon_prep(false, forms[0], table_work(g, g.d_prep, g.prep.size()), p, stream)) !=
                 hipSuccess)
                 return hip_fail(e, "preparation launch");
-            if ((e = run_products(g.tile, w.f, table_work(g, g.d_square, g.square.size()),
+            if ((e = run_products(tiling_of(g.tile), w.f, table_work(g, g.d_square, g.square.size()),
                                   table_work(g, g.d_update, g.update.size()), hp->iteration, forms, kLastParams, into,
                                   stream)) != hipSuccess)
                 return hip_fail(e, "product launch");
@@ -988,7 +990,7 @@ namespace {
 struct BatchPlan {
     int64_t chunk = 1;
     int tile = 128;
-    int64_t mb = 0, nb = 0;            // row blocks of the short and the long side
+    int64_t mb = 0, nb = 0;            // tiles along the short and the long side
     int64_t x_bytes = 0, a_bytes = 0;  // per matrix
     int64_t n_partials = 1;            // per matrix
     int64_t bytes = 0;
@@ -1082,8 +1084,8 @@ int muon_orthogonalize(const muon_matrices *mats, const void *x, void *out, cons
         const BatchPlan p = plan_batch(mats->batch, shape);
         const Workspace w = carve(static_cast<char *>(workspace), p.x_bytes * p.chunk, p.a_bytes * p.chunk,
                                   p.n_partials * p.chunk);
-        work.one.mb = (uint32_t)p.mb;
-        work.one.nb = (uint32_t)p.nb;
+        work.one.mp = (uint32_t)(p.mb * p.tile);
+        work.one.np = (uint32_t)(p.nb * p.tile);
         work.x_stride = (uint64_t)p.x_bytes;
         work.a_stride = (uint64_t)p.a_bytes;
         work.norm_stride = (uint32_t)p.n_partials;
@@ -1108,11 +1110,11 @@ int muon_orthogonalize(const muon_matrices *mats, const void *x, void *out, cons
             prep.x = w.f.x[0];
             prep.xt = w.f.xt[0];
             const int64_t sub = p.tile / 64;
-            if ((e = launch_muon_prep(p.tile, xe == 2, forms[0], with(p.mb * p.nb * sub * sub), prep, stream)) != hipSuccess)
+            if ((e = launch_muon_prep(xe == 2, forms[0], with(p.mb * p.nb * sub * sub), prep, stream)) != hipSuccess)
                 return hip_fail(e, "preparation launch");
             MuonGemmArgs into{};
             into.o = out;
-            if ((e = run_products(p.tile, w.f, with(p.mb * (p.mb + 1) / 2), with(p.mb * p.nb), *iteration, forms,
+            if ((e = run_products(tiling_of(p.tile), w.f, with(p.mb * (p.mb + 1) / 2), with(p.mb * p.nb), *iteration, forms,
                                   oe == 2 ? kLastBf16 : kLastF32, into, stream)) != hipSuccess)
                 return hip_fail(e, "product launch");
         }
