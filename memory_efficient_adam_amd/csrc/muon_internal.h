@@ -24,7 +24,7 @@ namespace adam_mi355x {
 // product keeps zero.
 struct MuonMat {
     uint64_t x_off;   // byte offset in each of the X arrays
-    uint64_t a_off;   // byte offset in the A and P arrays
+    uint64_t a_off;   // byte offset in the square arrays
     uint64_t u_off;   // element offset of the source matrix in its array
     uint64_t o_off;   // element offset of the output matrix in its array
     uint64_t u_ld, o_ld;  // row strides of source and output, in elements
@@ -60,9 +60,10 @@ struct MuonWork {
 };
 
 // The factor arrays of one group of matrices.
+constexpr int kSquares = 5;
 struct MuonArrays {
-    char *x[2], *xt[2];  // X and X^T, before and after an iteration
-    char *a, *p;         // A = X X^T and the polynomial P
+    char *x[2], *xt[2];    // X and X^T, before and after an update
+    char *square[kSquares];  // A = X X^T, the polynomials, their products
 };
 
 // How one factor is held: split or plain slabs.
@@ -87,6 +88,8 @@ struct MuonPrepArgs {
 struct MuonGemmArgs {
     MuonWork work;
     const char *left, *right;  // factor images, both with K along the rows
+    const char *left2, *right2;  // a second product of the same launch (kCommuting; else NULL)
+    char *out2;
     const char *add;           // A (polynomial only)
     char *out, *out_t;         // images written (out_t: X^T)
     float ca, cb, cc;          // polynomial coefficients
@@ -146,7 +149,7 @@ hipError_t launch_muon_norms(const double *partials, const uint2 *ranges, double
 hipError_t launch_muon_sums(bool bf16, const MuonWork &w, const MuonSumArgs &a, uint32_t n_mats, hipStream_t s);
 hipError_t launch_muon_prep(bool bf16, int form, const MuonWork &w, const MuonPrepArgs &a, hipStream_t s);
 
-enum MuonProduct : int { kGram, kPolynomial, kUpdate, kLastBf16, kLastF32, kLastParams };
+enum MuonProduct : int { kGram, kPolynomial, kCommuting, kUpdate, kLastBf16, kLastF32, kLastParams };
 // The tiles of the products (rows and columns of the result, waves): the
 // dimensions of a matrix are padded to multiples of both of its products'
 // tiles.

@@ -315,6 +315,9 @@ __device__ __forceinline__ void store_block(const f32x16 &v, char *image, uint32
 // The tiles of one product over all matrices of a launch.
 //   kGram:       A = X X^T                        tiles ti >= tj, stored at both places
 //   kPolynomial: P = a I + b A + c A A^T          the same
+//   kCommuting:  a product of two polynomials in one A (symmetric too), or
+//                two such products in one launch; one factor is a P, the
+//                other and the result are held alike
 //   kUpdate:     X' = P X, stored as X' and X'^T
 //   kLast..:     O = P X in the user's orientation (for a tall matrix the
 //                factors change places), rounded to the output's type, or
@@ -323,9 +326,11 @@ template <class T, int kProduct, int kIn, int kOut>
 __global__ __launch_bounds__(T::kThreads) __attribute__((amdgpu_waves_per_eu(T::kPerSimd)))
 void muon_product_kernel(MuonGemmArgs a) {
     __shared__ __attribute__((aligned(1024))) char lds[T::kStages * T::kStage];
-    constexpr bool kLast = kProduct >= kLastBf16, kSquare = kProduct == kGram || kProduct == kPolynomial;
+    constexpr bool kLast = kProduct >= kLastBf16;
+    constexpr bool kSquare = kProduct == kGram || kProduct == kPolynomial || kProduct == kCommuting;
     uint32_t t, ti, tj;
-    const MuonMat m = find_mat(a.work, xcd_order(blockIdx.x, a.work.n_tiles), t);
+    const bool second = kProduct == kCommuting && blockIdx.x >= a.work.n_tiles;
+    const MuonMat m = find_mat(a.work, xcd_order(second ? blockIdx.x - a.work.n_tiles : blockIdx.x, a.work.n_tiles), t);
     if (a.work.tiles) {
         ti = t & 0xFFFFu;
         tj = t >> 16;
@@ -340,11 +345,16 @@ void muon_product_kernel(MuonGemmArgs a) {
     const char *left, *right;
     uint32_t row0, col0;  // of the result
     if constexpr (kSquare) {
-        const char *f = a.left + (kProduct == kGram ? m.x_off : m.a_off);
+        const char *f = a.left, *g = a.left;
+        if constexpr (kProduct == kCommuting) {
+            f = second ? a.left2 : a.left;
+            g = second ? a.right2 : a.right;
+        }
+        const uint64_t off = kProduct == kGram ? m.x_off : m.a_off;
         row0 = ti * T::kRows;
         col0 = tj * T::kCols;
-        left = f + (row0 >> 5) * block;
-        right = f + (col0 >> 5) * block;
+        left = f + off + (row0 >> 5) * block;
+        right = g + off + (col0 >> 5) * block;
     } else {
         const bool swap = kLast && m.tall;
         row0 = (swap ? tj : ti) * T::kRows;
@@ -374,9 +384,11 @@ void muon_product_kernel(MuonGemmArgs a) {
             const uint32_t r0 = row0 + 32u * i, c0 = col0 + 32u * j;
             const uint32_t r = r0 + 4u * (lane >> 5), c = c0 + (lane & 31u);
             if constexpr (kSquare) {
-                char *out = a.out + m.a_off;
+                char *out = (second ? a.out2 : a.out) + m.a_off;
                 if constexpr (kProduct == kGram) {
                     v *= 1.0f / kScaleX;
+                } else if constexpr (kProduct == kCommuting) {
+                    v *= 1.0f / kScaleP;
                 } else {
                     // A's block, read from its mirror image: four values down a column lie side by side
                     const float cb = a.cb * (kScaleP / kScaleX), cc = a.cc * (kScaleP / (kScaleX * kScaleX));
@@ -1002,7 +1014,7 @@ hipError_t launch_muon_prep(bool bf16, int form, const MuonWork &w, const MuonPr
 
 template <class T>
 static hipError_t product_of(int product, int in, int out, const MuonGemmArgs &a, hipStream_t s) {
-    const dim3 grid(a.work.n_tiles), block(T::kThreads);
+    const dim3 grid(a.left2 ? 2 * a.work.n_tiles : a.work.n_tiles), block(T::kThreads);
 #define MUON_CASE(p, i, o)                                                       \
     if (product == p && in == i && out == o) {                                   \
         muon_product_kernel<T, p, i, o><<<grid, block, 0, s>>>(a);               \
@@ -1010,6 +1022,7 @@ static hipError_t product_of(int product, int in, int out, const MuonGemmArgs &a
     }
     MUON_CASE(kGram, kSplit, kSplit)
     MUON_CASE(kPolynomial, kSplit, kSplit)
+    MUON_CASE(kCommuting, kSplit, kSplit)
     MUON_CASE(kUpdate, kSplit, kSplit)
     MUON_CASE(kUpdate, kSplit, kPlain)
     MUON_CASE(kGram, kPlain, kPlain)

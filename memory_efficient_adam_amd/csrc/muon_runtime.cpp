@@ -24,8 +24,8 @@ constexpr int kTableSlots = 4;  // resident pointer tables per state
 constexpr int kStageSlots = 8;  // pinned staging buffers per state
 
 // Matrices go through the products together up to this many (padded)
-// elements: 512 MB of factor arrays, and some 2000 tiles of 128 x 128.
-constexpr int64_t kGroupElements = int64_t(1) << 25;
+// elements: 1 GB of X, and some 4000 tiles of 128 x 128.
+constexpr int64_t kGroupElements = int64_t(1) << 26;
 // 128 x 128 tiles where there are this many, else 64 x 64 ones.
 constexpr int64_t kLargeTiles = 512;
 constexpr int64_t kMaxDim = int64_t(1) << 21;
@@ -63,13 +63,33 @@ struct TableSlot {
     bool valid = false;
 };
 
+struct Shape {
+    int64_t rows, cols;
+    int64_t numel() const { return rows * cols; }
+    int64_t shorter() const { return std::min(rows, cols); }
+    int64_t longer() const { return std::max(rows, cols); }
+};
+
+// m^3 and m^2 n of a group, in multiply-adds.
+struct Work {
+    double cubes = 0.0, oblongs = 0.0;
+    void add(const Shape &s, double count = 1.0) {
+        const double m = (double)s.shorter(), n = (double)s.longer();
+        cubes += count * m * m * m;
+        oblongs += count * m * m * n;
+    }
+    // whether runs save more work than their two or three further launches cost
+    bool runs_pay() const { return oblongs - cubes > 2e8; }
+};
+
 // A part of the list whose matrices go through the products together.
 struct Group {
     int32_t first = 0, last = 0;  // tensors [first, last)
     int tile = 128;
-    int64_t x_bytes = 0, a_bytes = 0;  // of one X (or X^T) array and of A (or P)
+    int64_t x_bytes = 0, a_bytes = 0;  // of one X (or X^T) array and of one square array
     int64_t block0 = 0, blocks = 0;    // 2048-element blocks
     int64_t flat0 = 0;                 // flat state index of its first element
+    Work size;
     std::vector<MuonMat> mats;
     std::vector<MuonTile> prep, square, update, small;
     int64_t small_short = 0, small_long = 0;  // the largest sides of its small matrices
@@ -78,13 +98,6 @@ struct Group {
     const MuonMat *d_mats = nullptr;
     const MuonTile *d_prep = nullptr, *d_square = nullptr, *d_update = nullptr, *d_small = nullptr;
     const uint2 *d_ranges = nullptr;
-};
-
-struct Shape {
-    int64_t rows, cols;
-    int64_t numel() const { return rows * cols; }
-    int64_t shorter() const { return std::min(rows, cols); }
-    int64_t longer() const { return std::max(rows, cols); }
 };
 
 bool is_small(const Shape &s) { return s.shorter() <= kSmallShort && s.longer() <= kSmallLong; }
@@ -109,7 +122,7 @@ std::vector<Group> plan(const std::vector<Shape> &shapes) {
             const int64_t t = shapes[k].numel() > 0 ? tiles_of(shapes[k], 128) : 0;
             if (elements > 0 && elements + t * 16384 > kGroupElements) break;
             elements += t * 16384;
-            if (!is_small(shapes[k])) tiles128 += t;
+            if (!is_small(shapes[k])) tiles128 += t, g.size.add(shapes[k]);
             block += blocks_of(shapes[k].numel());
             flat += pad16(shapes[k].numel());
         }
@@ -127,11 +140,11 @@ std::vector<Group> plan(const std::vector<Shape> &shapes) {
     return groups;
 }
 
-// The workspace a group needs: four X arrays, A and P, the blocks' partial
+// The workspace a group needs: four X arrays, the square ones, the blocks' partial
 // sums and the matrices' sums.
 int64_t align256(int64_t n) { return pad_to(n, 256); }
 int64_t group_bytes(const Group &g) {
-    return 4 * align256(g.x_bytes) + 2 * align256(g.a_bytes) + align256(8 * g.blocks) + align256(8 * (g.last - g.first));
+    return 4 * align256(g.x_bytes) + kSquares * align256(g.a_bytes) + align256(8 * g.blocks) + align256(8 * (g.last - g.first));
 }
 
 struct Workspace {
@@ -150,8 +163,7 @@ Workspace carve(char *base, int64_t x_bytes, int64_t a_bytes, int64_t n_partials
         w.f.x[i] = take(x_bytes);
         w.f.xt[i] = take(x_bytes);
     }
-    w.f.a = take(a_bytes);
-    w.f.p = take(a_bytes);
+    for (char *&p : w.f.square) p = take(a_bytes);
     w.partials = reinterpret_cast<double *>(take(8 * n_partials));
     w.sums = reinterpret_cast<double *>(base);
     return w;
@@ -265,40 +277,115 @@ MuonSmallArgs small_args(const MuonWork &w, const void *u, bool u_bf16, const mu
     return a;
 }
 
-// The products of all iterations, X_0 and X_0^T being in f.x[0], f.xt[0].
-hipError_t run_products(int tiling, const MuonArrays &f, const MuonWork &square, const MuonWork &update,
-                        const muon_iteration &it, const int *forms, int last, const MuonGemmArgs &into, hipStream_t s) {
-    hipError_t e;
-    for (int k = 0; k < it.steps; ++k) {
-        const int cur = k & 1, in = forms[k];
+// Iterations go in runs.  Within one, X stays where it is: the iterates are
+// polynomials in the run's first A = X X^T, so A' = P A P and X' = (P_2 P_1) X,
+// and a run of L costs 3 m^2 n + (4 L - 3) m^3 multiply-adds (symmetric results
+// counted by half) for the 3 L m^2 n + L m^3 of one iteration after the other.
+// What it costs in accuracy is that A' carries A's rounding, grown by a^2: two
+// iterations lose nothing that can be seen beside the rounding of X that they
+// save; three, at the start of a longer sequence, while |a_1 a_2| is at most
+// kPlainGrowth; four fail.  Factors held in single fp16 values are not put into runs.
+struct Run {
+    int first, length;
+};
+std::vector<Run> runs_of(const muon_iteration &it, const int *forms, bool allowed) {
+    auto a = [&](int k) {
         float c[3];
         coefficients_of(it, k, c);
-        MuonGemmArgs a{};
-        a.work = square;
-        a.left = f.x[cur];
-        a.out = f.a;
-        if ((e = launch_muon_product(tiling, kGram, in, in, a, s)) != hipSuccess) return e;
-        a.left = f.a;
-        a.add = f.a;
-        a.out = f.p;
-        a.ca = c[0];
-        a.cb = c[1];
-        a.cc = c[2];
-        if ((e = launch_muon_product(tiling, kPolynomial, in, in, a, s)) != hipSuccess) return e;
-        if (k + 1 < it.steps) {
-            a = MuonGemmArgs{};
-            a.work = update;
-            a.left = f.p;
-            a.right = f.xt[cur];
-            a.out = f.x[cur ^ 1];
-            a.out_t = f.xt[cur ^ 1];
-            e = launch_muon_product(tiling, kUpdate, in, forms[k + 1], a, s);
+        return std::fabs((double)c[0]);
+    };
+    int split = 0;
+    while (split < it.steps && forms[split] == kSplit) ++split;
+    std::vector<Run> runs;
+    int k = 0;
+    if (allowed && split % 2 == 1) {  // pairs from the end, three iterations or one before them
+        const bool three = split >= 3 && it.steps > 3 && a(0) * a(1) <= kPlainGrowth && a(0) * a(1) * a(2) <= 64.0;
+        runs.push_back(Run{0, three ? 3 : 1});
+        k = runs[0].length;
+    }
+    while (allowed && k + 1 < split) {
+        if (a(k) * a(k + 1) <= 64.0) {  // an entry of P_2 P_1 has to stay below 256
+            runs.push_back(Run{k, 2});
+            k += 2;
         } else {
-            a = into;
-            a.work = update;
-            a.left = f.p;
-            a.right = f.xt[cur];
-            e = launch_muon_product(tiling, last, in, in, a, s);
+            runs.push_back(Run{k++, 1});
+        }
+    }
+    while (k < it.steps) runs.push_back(Run{k++, 1});
+    return runs;
+}
+
+// The products of all iterations, X_0 and X_0^T being in f.x[0], f.xt[0].
+hipError_t run_products(int tiling, const MuonArrays &f, const MuonWork &square, const MuonWork &update, const Work &size,
+                        const muon_iteration &it, const int *forms, int last, const MuonGemmArgs &into, hipStream_t s) {
+    hipError_t e = hipSuccess;
+    int form = kSplit;
+    auto polynomial = [&](const char *a, char *p, int k) {
+        if (e != hipSuccess) return;
+        float c[3];
+        coefficients_of(it, k, c);
+        MuonGemmArgs g{};
+        g.work = square;
+        g.left = g.add = a;
+        g.out = p;
+        g.ca = c[0];
+        g.cb = c[1];
+        g.cc = c[2];
+        e = launch_muon_product(tiling, kPolynomial, form, form, g, s);
+    };
+    auto commuting = [&](const char *left, const char *right, char *out, const char *left2 = nullptr,
+                         const char *right2 = nullptr, char *out2 = nullptr) {
+        if (e != hipSuccess) return;
+        MuonGemmArgs g{};
+        g.work = square;
+        g.left = left;
+        g.right = right;
+        g.out = out;
+        g.left2 = left2;
+        g.right2 = right2;
+        g.out2 = out2;
+        e = launch_muon_product(tiling, kCommuting, form, form, g, s);
+    };
+    char *const A = f.square[0], *const T = f.square[1], *const P = f.square[2], *const R = f.square[3],
+               *const U = f.square[4];
+    int cur = 0;
+    for (const Run &run : runs_of(it, forms, size.runs_pay())) {
+        form = forms[run.first];
+        MuonGemmArgs g{};
+        g.work = square;
+        g.left = f.x[cur];
+        g.out = A;
+        if ((e = launch_muon_product(tiling, kGram, form, form, g, s)) != hipSuccess) return e;
+        polynomial(A, P, run.first);
+        const char *q = P;
+        if (run.length >= 2) {
+            commuting(P, A, T);  // A <- P A P
+            commuting(P, T, A);
+            polynomial(A, R, run.first + 1);
+            if (run.length == 2) {
+                commuting(R, P, T);
+                q = T;
+            } else {
+                commuting(R, P, U, R, A, T);
+                commuting(R, T, A);
+                polynomial(A, P, run.first + 2);
+                commuting(P, U, T);
+                q = T;
+            }
+        }
+        if (e != hipSuccess) return e;
+        const int next = run.first + run.length;
+        g = next < it.steps ? MuonGemmArgs{} : into;
+        g.work = update;
+        g.left = q;
+        g.right = f.xt[cur];
+        if (next < it.steps) {
+            g.out = f.x[cur ^ 1];
+            g.out_t = f.xt[cur ^ 1];
+            e = launch_muon_product(tiling, kUpdate, form, forms[next], g, s);
+            cur ^= 1;
+        } else {
+            e = launch_muon_product(tiling, last, form, form, g, s);
         }
         if (e != hipSuccess) return e;
     }
@@ -727,7 +814,7 @@ int muon_step(muon_state *s, float *const *params, const void *const *grads, con
                 hipSuccess)
                 return hip_fail(e, "preparation launch");
             if ((e = run_products(tiling_of(g.tile), w.f, table_work(g, g.d_square, g.square.size()),
-                                  table_work(g, g.d_update, g.update.size()), hp->iteration, forms, kLastParams, into,
+                                  table_work(g, g.d_update, g.update.size()), g.size, hp->iteration, forms, kLastParams, into,
                                   stream)) != hipSuccess)
                 return hip_fail(e, "product launch");
         }
@@ -1006,7 +1093,7 @@ BatchPlan plan_batch(int64_t batch, const Shape &s) {
     p.x_bytes = 4 * p.tile * p.tile * p.mb * p.nb;
     p.a_bytes = 4 * p.tile * p.tile * p.mb * p.mb;
     p.n_partials = std::min(kMaxPartials, tiles_of(s, 64));
-    p.bytes = 4 * align256(p.x_bytes * p.chunk) + 2 * align256(p.a_bytes * p.chunk) + align256(8 * p.n_partials * p.chunk);
+    p.bytes = 4 * align256(p.x_bytes * p.chunk) + kSquares * align256(p.a_bytes * p.chunk) + align256(8 * p.n_partials * p.chunk);
     return p;
 }
 
@@ -1114,7 +1201,9 @@ int muon_orthogonalize(const muon_matrices *mats, const void *x, void *out, cons
                 return hip_fail(e, "preparation launch");
             MuonGemmArgs into{};
             into.o = out;
-            if ((e = run_products(tiling_of(p.tile), w.f, with(p.mb * (p.mb + 1) / 2), with(p.mb * p.nb), *iteration, forms,
+            Work size;
+            size.add(shape, (double)count);
+            if ((e = run_products(tiling_of(p.tile), w.f, with(p.mb * (p.mb + 1) / 2), with(p.mb * p.nb), size, *iteration, forms,
                                   oe == 2 ? kLastBf16 : kLastF32, into, stream)) != hipSuccess)
                 return hip_fail(e, "product launch");
         }

@@ -81,6 +81,31 @@ def test_orthogonalize_many_tiles(shape, dtype):
     _check(ma.muon_orthogonalize(x), x)
 
 
+TRIPLES = [(3.0, -3.2, 1.2), (3.4445, -4.7750, 2.0315), (2.5, -2.5, 1.0), (1.875, -1.25, 0.375), (1.5, -0.5, 0.0),
+           (4.0, -6.0, 3.0), (2.0, -1.5, 0.5)]
+
+
+# runs of iterations over one Gram matrix (wide enough), and one after the other
+@pytest.mark.parametrize("steps", [1, 2, 3, 4, 5, 6, 7])
+@pytest.mark.parametrize("shape", [(6, 300, 900), (5, 1000, 333), (40, 60)], ids=str)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+def test_orthogonalize_steps_and_coefficients(steps, shape, dtype):
+    x = _matrix(steps, shape).to(dtype)
+    for coefficients in (None, TRIPLES[4], TRIPLES[:steps]):
+        kw = dict(steps=steps, coefficients=coefficients, eps=1e-6)
+        _check(ma.muon_orthogonalize(x, **kw), x, **kw)
+
+
+# large first coefficients: no run of three, no plain factors before the end
+def test_orthogonalize_steep_coefficients():
+    steep = [(8.28721, -23.5959, 17.3004), (4.1071, -2.9478, 0.5449), (3.9487, -2.9089, 0.5518),
+             (3.3184, -2.4885, 0.5101), (2.3007, -1.6689, 0.4188)]
+    for shape in ((6, 300, 900), (500, 520), (30, 700)):
+        for dtype in (torch.float32, torch.bfloat16):
+            x = _matrix(11, shape).to(dtype)
+            _check(ma.muon_orthogonalize(x, coefficients=steep), x, coefficients=steep)
+
+
 # the largest size a group of the step takes, and one matrix beyond it, are in
 # the benchmark's range; these are the shapes where tables can go wrong
 LIST = [(33, 65), (128, 64), (1, 77), (200, 31), (64, 64), (1, 1), (0, 5), (130, 257), (40, 2100), (2049, 3)]
