@@ -27,8 +27,8 @@
  * values (high part and remainder, 22 bits; X and A scaled by 2^10, the
  * polynomial by 2^8) and three of the four partial products are summed, so
  * that O agrees with a computation in fp32 to fp32's own error.
- * muon_orthogonalize to a bf16 output holds the factors of the last
- * iterations in one fp16 value each: those from the first k on for which the
+ * muon_orthogonalize to a bf16 output may hold the factors of the last
+ * iterations (of larger matrices) in one fp16 value each: those from the first k on for which the
  * product of |a_k|, .., |a_steps| is at most 12 (by which their rounding,
  * 2^-12, can still grow), which keeps the error well below bf16's rounding.
  * A matrix whose u is all zero gives O = 0; one with a NaN or an infinity

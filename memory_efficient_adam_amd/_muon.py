@@ -1,6 +1,8 @@
 """ctypes marshalling for the Muon calls of libadam_mi355x.so (names follow
 include/muon_mi355x.h)."""
+import contextlib
 import ctypes
+import functools
 
 from . import _binding as B
 from ._binding import ADAM_BLOCK_SIZE, AdamError, _check, _stream, adam_last_error
@@ -94,13 +96,19 @@ def _shapes(shapes):
 def _iteration(steps, coefficients, eps):
     """coefficients: None (the default triple), one triple for every iteration, or
     one triple per iteration.  The struct keeps the array alive."""
-    steps = int(steps)
+    if coefficients is not None:
+        coefficients = tuple(tuple(c) if isinstance(c, (tuple, list)) else c for c in coefficients)
+    return _iteration_of(int(steps), coefficients, float(eps))
+
+
+@functools.lru_cache(maxsize=64)
+def _iteration_of(steps, coefficients, eps):
     values = None
     if coefficients is not None:
-        rows = list(coefficients)
+        rows = coefficients
         if len(rows) == 3 and all(isinstance(v, (int, float)) for v in rows):
             rows = [rows] * max(steps, 0)
-        if len(rows) != steps or any(len(r) != 3 for r in rows):
+        if len(rows) != steps or any(not isinstance(r, tuple) or len(r) != 3 for r in rows):
             raise ValueError(f"coefficients: expected three numbers or {steps} triples")
         if 0 < steps <= MUON_MAX_STEPS:  # other counts are the library's to refuse
             values = (ctypes.c_float * (3 * steps))(*[float(v) for r in rows for v in r])
@@ -125,11 +133,21 @@ class MuonState:
 
     def __init__(self, handle, shapes, layout, device=None):
         self.handle = handle
-        self.shapes = [tuple(s) for s in shapes]
-        self.numels = [r * c for r, c in self.shapes]
+        self._set_shapes(shapes)
         self.layout = layout
         self.device = device
+        # held here: globals may be gone when a state is collected at exit
+        self._free = library().muon_state_destroy if handle else None
         self._checked = []  # tensor sets (held) and pointers of recent checked muon_step calls
+
+    def _set_shapes(self, shapes):
+        self.shapes = [tuple(s) for s in shapes]
+        self.numels = [r * c for r, c in self.shapes]
+        # each matrix's first entry in the padded flat state, and its length
+        self.firsts, self.padded = [], 0
+        for n in self.numels:
+            self.firsts.append(self.padded)
+            self.padded += -(-n // 16) * 16
 
     def __del__(self):
         self.destroy()
@@ -137,7 +155,7 @@ class MuonState:
     def destroy(self):
         self._checked = []
         if getattr(self, "handle", None):
-            library().muon_state_destroy(self.handle)
+            self._free(self.handle)
             self.handle = None
 
     @property
@@ -226,14 +244,13 @@ def muon_state_momentum(state, stream=None):
     """The momentum's values, one (rows, cols) tensor per matrix: fp32 (8-bit codes
     times their scale), or bf16 for bf16 storage.  A copy, in one allocation."""
     import torch
-    padded = [-(-n // 16) * 16 for n in state.numels]
     with _on(stream):
-        flat = torch.empty(sum(padded), device="cuda",
-                           dtype=torch.bfloat16 if state.storage == "bf16" else torch.float32)
+        flat = torch.empty(state.padded, device="cuda",
+                           dtype=torch.bfloat16 if state.layout.storage == 1 else torch.float32)
         _check(library().muon_state_momentum(state.handle, flat.data_ptr(),
                                              flat.numel() * flat.element_size(), _stream(None)))
-    return [part[:n].view(shape) for part, n, shape in
-            zip(flat.split(padded), state.numels, state.shapes)]
+    return [flat.as_strided(shape, (shape[1], 1), first) for shape, first in
+            zip(state.shapes, state.firsts)]
 
 
 def muon_state_describe(state):
@@ -281,8 +298,8 @@ def muon_state_load(buf, stream=None):
     h = ctypes.c_void_p()
     _check(library().muon_state_load(ctypes.byref(h), arr.ctypes.data, arr.size, _stream(stream)))
     st = MuonState(h.value, [], muon_layout(), B._current_device())
-    st.layout, st.shapes = muon_state_describe(st)
-    st.numels = [r * c for r, c in st.shapes]
+    st.layout, shapes = muon_state_describe(st)
+    st._set_shapes(shapes)
     return st
 
 
@@ -290,30 +307,29 @@ def muon_state_load(buf, stream=None):
 def _on(stream):
     """torch's current stream set to `stream` (None: as it is), so that memory
     allocated for a call belongs to the stream the call runs on."""
-    import contextlib
-
-    import torch
     if stream is None:
         return contextlib.nullcontext()
+    import torch
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream)
     return torch.cuda.stream(stream)
 
 
-def _matrices_of(name, x):
+_DTYPE_CODES = {"torch.float32": 0, "torch.bfloat16": 1}
+
+
+@functools.lru_cache(maxsize=256)
+def _matrices_of(name, shape, stride, dtype):
     """(batch, rows, cols, batch stride, row stride, dtype code) of a tensor of
     matrices whose rows are contiguous and whose batch has one stride."""
-    import torch
-    if not isinstance(x, torch.Tensor):
-        raise TypeError(f"{name} must be a torch tensor")
-    codes = {torch.float32: 0, torch.bfloat16: 1}
-    if x.dtype not in codes:
-        raise ValueError(f"{name}: dtype {x.dtype}, expected torch.float32 or torch.bfloat16")
-    if x.dim() < 2:
-        raise ValueError(f"{name}: expected (..., rows, cols), got {tuple(x.shape)}")
-    rows, cols = x.shape[-2:]
+    code = _DTYPE_CODES.get(str(dtype))
+    if code is None:
+        raise ValueError(f"{name}: dtype {dtype}, expected torch.float32 or torch.bfloat16")
+    if len(shape) < 2:
+        raise ValueError(f"{name}: expected (..., rows, cols), got {shape}")
+    rows, cols = shape[-2:]
     batch, batch_stride = 1, 0
-    for n, s in zip(reversed(x.shape[:-2]), reversed(x.stride()[:-2])):
+    for n, s in zip(reversed(shape[:-2]), reversed(stride[:-2])):
         if n == 1:
             continue
         if batch != 1 and s != batch * batch_stride:
@@ -321,16 +337,17 @@ def _matrices_of(name, x):
         if batch == 1:
             batch_stride = s
         batch *= n
-    row_stride = x.stride(-2) if rows > 1 else cols
-    if x.numel() == 0:
-        return batch, rows, cols, rows * cols, cols, codes[x.dtype]
-    if cols > 1 and x.stride(-1) != 1:
+    if batch * rows * cols == 0:
+        return batch, rows, cols, rows * cols, cols, code
+    row_stride = stride[-2] if rows > 1 else cols
+    if cols > 1 and stride[-1] != 1:
         raise ValueError(f"{name}: rows must be contiguous")
     if row_stride < cols:
         raise ValueError(f"{name}: rows overlap")
-    return batch, rows, cols, batch_stride, row_stride, codes[x.dtype]
+    return batch, rows, cols, batch_stride, row_stride, code
 
 
+@functools.lru_cache(maxsize=256)
 def muon_orthogonalize_workspace_bytes(batch, rows, cols):
     return _size(library().muon_orthogonalize_workspace_bytes(batch, rows, cols))
 
@@ -344,7 +361,9 @@ def muon_orthogonalize(x, *, out=None, steps=5, coefficients=None, eps=1e-7, wor
     muon_orthogonalize_workspace_bytes bytes that calls ordered on one stream may
     share (default: allocated for the call).  No gradient is defined through it."""
     import torch
-    batch, rows, cols, x_batch, x_row, x_code = _matrices_of("x", x)
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch tensor")
+    batch, rows, cols, x_batch, x_row, x_code = _matrices_of("x", tuple(x.shape), x.stride(), x.dtype)
     if out is not None and (not isinstance(out, torch.Tensor) or out.shape != x.shape):
         raise ValueError("out must be a tensor of x's shape")
     if torch.is_grad_enabled() and (x.requires_grad or (out is not None and out.requires_grad)):
@@ -352,22 +371,26 @@ def muon_orthogonalize(x, *, out=None, steps=5, coefficients=None, eps=1e-7, wor
                          "call it under torch.no_grad()")
     it = _iteration(steps, coefficients, eps)
     for name, t in (("x", x), ("out", out), ("workspace", workspace)):
-        if t is not None and not t.is_cuda:
+        if t is None:
+            continue
+        if not t.is_cuda:
             raise ValueError(f"{name} must be a CUDA (HIP) device tensor")
-        if t is not None and t.device.index != B._current_device():
+        if t.get_device() != B._current_device():
             raise ValueError(f"{name} is on {t.device}, the current device is "
                              f"cuda:{B._current_device()}")
+        if t is workspace and not t.is_contiguous():
+            raise ValueError("workspace must be contiguous")
     need = muon_orthogonalize_workspace_bytes(batch, rows, cols)
-    if workspace is not None and not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
     with _on(stream):
         if out is None:
             out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        if workspace is None:
+        if workspace is None and need > 0:
             workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-        _, _, _, out_batch, out_row, out_code = _matrices_of("out", out)
+        at, nbytes = ((0, 0) if workspace is None else
+                      (workspace.data_ptr(), workspace.numel() * workspace.element_size()))
+        _, _, _, out_batch, out_row, out_code = _matrices_of("out", tuple(out.shape), out.stride(),
+                                                             out.dtype)
         mats = muon_matrices(batch, rows, cols, x_batch, x_row, out_batch, out_row, x_code, out_code)
-        _check(library().muon_orthogonalize(
-            ctypes.byref(mats), x.data_ptr(), out.data_ptr(), ctypes.byref(it), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), _stream(None)))
+        _check(library().muon_orthogonalize(ctypes.byref(mats), x.data_ptr(), out.data_ptr(),
+                                            ctypes.byref(it), at, nbytes, _stream(None)))
     return out

@@ -118,7 +118,6 @@ struct MuonSmallArgs {
     int32_t product;           // kLastBf16, kLastF32, kLastParams
     int32_t u_bf16;
     int32_t steps;
-    uint32_t plain;            // bit k: iteration k takes plain factors
     float coefficients[3 * kMaxIterations];
 };
 

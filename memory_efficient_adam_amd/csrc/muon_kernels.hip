@@ -48,13 +48,39 @@ __device__ __forceinline__ float load_elem(const void *p, uint64_t i) {
         return static_cast<const float *>(p)[i];
 }
 
-// An fp32 value as hi + lo, packed low half first: {hi, lo}.
-__device__ __forceinline__ void split(float y, _Float16 &hi, _Float16 &lo) {
-    hi = (_Float16)y;
-    lo = (_Float16)(y - (float)hi);
+// Two fp32 values as hi + lo each, packed: the sums hold 22 bits.  Pairs are
+// converted in one instruction (to nearest even), and a remainder y - hi
+// (exact) is one mixed-precision fma, which the compiler does not form by itself.
+typedef _Float16 half2v __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ void split2(float y0, float y1, uint32_t &hi, uint32_t &lo) {
+    const half2v h = __builtin_convertvector((f32x2{y0, y1}), half2v);
+    hi = __builtin_bit_cast(uint32_t, h);
+    float r0, r1;
+    asm("v_fma_mix_f32 %0, -%1, 1.0, %2 op_sel:[0,0,0] op_sel_hi:[1,0,0]" : "=v"(r0) : "v"(hi), "v"(y0));
+    asm("v_fma_mix_f32 %0, -%1, 1.0, %2 op_sel:[1,0,0] op_sel_hi:[1,0,0]" : "=v"(r1) : "v"(hi), "v"(y1));
+    const half2v l = __builtin_convertvector((f32x2{r0, r1}), half2v);
+    lo = __builtin_bit_cast(uint32_t, l);
 }
-__device__ __forceinline__ uint32_t pack(_Float16 a, _Float16 b) {
-    return (uint32_t)__builtin_bit_cast(uint16_t, a) | ((uint32_t)__builtin_bit_cast(uint16_t, b) << 16);
+__device__ __forceinline__ void split4(float y0, float y1, float y2, float y3, u32x2 &hi, u32x2 &lo) {
+    uint32_t h0, h1, l0, l1;
+    split2(y0, y1, h0, l0);
+    split2(y2, y3, h1, l1);
+    hi = u32x2{h0, h1};
+    lo = u32x2{l0, l1};
+}
+// Eight values as fragments.
+__device__ __forceinline__ void split8(const float (&y)[8], half8 &hi, half8 &lo) {
+    u32x4 h, l;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t a, b;
+        split2(y[2 * i], y[2 * i + 1], a, b);
+        h[i] = a;
+        l[i] = b;
+    }
+    hi = __builtin_bit_cast(half8, h);
+    lo = __builtin_bit_cast(half8, l);
 }
 
 // Sum over the workgroup's kWaves waves in a fixed order (s: kWaves doubles).
@@ -295,10 +321,8 @@ __device__ __forceinline__ void store_block(const f32x16 &v, char *image, uint32
     const uint32_t r = r0 + 4u * (lane >> 5), c = c0 + (lane & 31u);
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
-        _Float16 hi[4], lo[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) split(v[4 * g + q], hi[q], lo[q]);
-        u32x2 h = {pack(hi[0], hi[1]), pack(hi[2], hi[3])}, l = {pack(lo[0], lo[1]), pack(lo[2], lo[3])};
+        u32x2 h, l;
+        split4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3], h, l);
         char *at;
         if constexpr (kTransposed) {
             at = image + image_pos<kForm>(c, r + 8u * g, length);
@@ -423,7 +447,7 @@ void muon_product_kernel(MuonGemmArgs a) {
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         const uint32_t q = r + 8u * (e / 4) + (e & 3);
-                        old[e] = q < m.rows && c < m.cols ? param[(uint64_t)q * m.cols + c] : 0.0f;
+                        old[e] = param[q < m.rows && c < m.cols ? (uint64_t)q * m.cols + c : 0u];
                     }
                 }
 #pragma unroll
@@ -478,13 +502,8 @@ __device__ __forceinline__ u32x2 *small_quad(uint4 *image, uint32_t row, uint32_
 __device__ __forceinline__ f32x16 mfma(half8 a, half8 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
 }
-__device__ __forceinline__ f32x16 mfma_split(half8 ah, half8 al, half8 bh, half8 bl, f32x16 c, bool plain) {
-    c = mfma(ah, bh, c);
-    if (!plain) {
-        c = mfma(ah, bl, c);
-        c = mfma(al, bh, c);
-    }
-    return c;
+__device__ __forceinline__ f32x16 mfma_split(half8 ah, half8 al, half8 bh, half8 bl, f32x16 c) {
+    return mfma(al, bh, mfma(ah, bl, mfma(ah, bh, c)));
 }
 
 template <int kRows, int kCols, bool kBf16>
@@ -499,27 +518,10 @@ __global__ __launch_bounds__(64 * kSmallWaves) void muon_small_kernel(MuonSmallA
     const uint32_t tid = threadIdx.x, lane = tid & 63u, ln = lane & 31u, half = lane >> 5;
     const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(tid >> 6));
     const uint32_t n = m.tall ? m.rows : m.cols, n_short = m.tall ? m.cols : m.rows;
+    const uint32_t active = min((uint32_t)kSmallWaves, (n + 31u) / 32u);
 
-    // the norm, rows of the user's matrix dealt to the waves
-    double sum = 0.0;
-    for (uint32_t r = wave; r < m.rows; r += kSmallWaves)
-        for (uint32_t c = lane; c < m.cols; c += 64u) {
-            const double v = load_elem<kBf16>(a.u, m.u_off + r * m.u_ld + c);
-            sum += v * v;
-        }
-    // the first update multiplies by one: it only arranges X_0's columns for A
-    for (uint32_t i = tid; i < 64u * 8u; i += 64u * kSmallWaves) {
-        poly.hi[i] = uint4{0u, 0u, 0u, 0u};
-        poly.lo[i] = uint4{0u, 0u, 0u, 0u};
-    }
-    sum = block_sum<kSmallWaves>(sum, s_sum);
-    if (tid < 32u * kRows) {
-        char *quad = reinterpret_cast<char *>(small_quad(poly.hi, tid, tid & ~3u));
-        reinterpret_cast<_Float16 *>(quad)[tid & 3u] = (_Float16)kScaleP;
-    }
-    const double inv = sum < __builtin_inf() ? (double)kScaleX / (sqrt(sum) + a.eps) : __builtin_nan("");
-
-    half8 xh[kCols][kSteps], xl[kCols][kSteps];
+    // X_0 as it comes; every load is under way before the first is needed
+    float raw[kCols][kSteps][8];
     const uint64_t row_step = m.tall ? 1 : m.u_ld, col_step = m.tall ? m.u_ld : 1;
 #pragma unroll
     for (int b = 0; b < kCols; ++b) {
@@ -529,24 +531,46 @@ __global__ __launch_bounds__(64 * kSmallWaves) void muon_small_kernel(MuonSmallA
         for (int s = 0; s < kSteps; ++s) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const uint32_t row = 16u * s + k_order(j, half);
-                float v = 0.0f;
-                if (row < n_short && col < n)
-                    v = (float)((double)load_elem<kBf16>(a.u, at + (16u * s + k_order(j, 0)) * row_step) * inv);
-                _Float16 h, l;
-                split(v, h, l);
-                xh[b][s][j] = h;
-                xl[b][s][j] = l;
+                const bool in = 16u * s + k_order(j, half) < n_short && col < n;
+                const float v = load_elem<kBf16>(a.u, in ? at + (16u * s + k_order(j, 0)) * row_step : m.u_off);
+                raw[b][s][j] = in ? v : 0.0f;
             }
-            __builtin_amdgcn_sched_barrier(0);  // loads of a step at a time: fewer addresses are held
+            __builtin_amdgcn_sched_barrier(0);  // a step at a time: fewer addresses are held
         }
     }
+    // the first update multiplies by one: it only arranges X_0's columns for A
+    for (uint32_t i = tid; i < 64u * 8u; i += 64u * kSmallWaves) {
+        poly.hi[i] = uint4{0u, 0u, 0u, 0u};
+        poly.lo[i] = uint4{0u, 0u, 0u, 0u};
+    }
+    double sum = 0.0;
+#pragma unroll
+    for (int b = 0; b < kCols; ++b)
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum += (double)raw[b][s][j] * (double)raw[b][s][j];
+    sum = block_sum<kSmallWaves>(sum, s_sum);
+    if (tid < 32u * kRows) {
+        char *quad = reinterpret_cast<char *>(small_quad(poly.hi, tid, tid & ~3u));
+        reinterpret_cast<_Float16 *>(quad)[tid & 3u] = (_Float16)kScaleP;
+    }
+    const double inv = sum < __builtin_inf() ? (double)kScaleX / (sqrt(sum) + a.eps) : __builtin_nan("");
+
+    half8 xh[kCols][kSteps], xl[kCols][kSteps];
+#pragma unroll
+    for (int b = 0; b < kCols; ++b)
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+            float y[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] = (float)((double)raw[b][s][j] * inv);
+            split8(y, xh[b][s], xl[b][s]);
+        }
     __syncthreads();
 
-    for (int it = 0; it <= a.steps; ++it) {
-        // X <- P X (plain: how iteration it - 1 takes its factors) and, along the
-        // way, A = X X^T for iteration `it`
-        const bool last = it == a.steps, plain = it > 0 && ((a.plain >> (it - 1)) & 1u), next_plain = (a.plain >> it) & 1u;
+    for (int it = 0; it < a.steps; ++it) {
+        // X <- P X and, along the way, A = X X^T
         f32x16 acc[kSquare];
 #pragma unroll
         for (int i = 0; i < kSquare; ++i) acc[i] = f32x16{};
@@ -554,107 +578,72 @@ __global__ __launch_bounds__(64 * kSmallWaves) void muon_small_kernel(MuonSmallA
         for (int b = 0; b < kCols; ++b) {
             const uint32_t col0 = 32u * (wave + kSmallWaves * b);
             if (col0 >= n) continue;
-            if (!last) {
-                half8 gh[kRows][2], gl[kRows][2];
+            half8 gh[kRows][2], gl[kRows][2];
 #pragma unroll
-                for (int i = 0; i < kRows; ++i) {
-                    f32x16 v = {};
+            for (int i = 0; i < kRows; ++i) {
+                f32x16 v = {};
 #pragma unroll
-                    for (int s = 0; s < kSteps; ++s)
-                        v = mfma_split(xh[b][s], xl[b][s], small_frag(poly.hi, 32u * i + ln, 2u * s + half),
-                                       small_frag(poly.lo, 32u * i + ln, 2u * s + half), v, plain);
+                for (int s = 0; s < kSteps; ++s)
+                    v = mfma_split(xh[b][s], xl[b][s], small_frag(poly.hi, 32u * i + ln, 2u * s + half),
+                                   small_frag(poly.lo, 32u * i + ln, 2u * s + half), v);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        _Float16 h, l;
-                        split(v[e] * (1.0f / kScaleP), h, l);
-                        gh[i][e / 8][e & 7] = h;
-                        gl[i][e / 8][e & 7] = l;
-                    }
-                }
+                for (int k = 0; k < 2; ++k) {
+                    float y[8];
 #pragma unroll
-                for (int i = 0; i < kRows; ++i)
-#pragma unroll
-                    for (int j = 0; j <= i; ++j)
-#pragma unroll
-                        for (int k = 0; k < 2; ++k)
-                            acc[i + j] = mfma_split(gh[i][k], gl[i][k], gh[j][k], gl[j][k], acc[i + j], next_plain);
-                f32x16 v[kRows];
-#pragma unroll
-                for (int i = 0; i < kRows; ++i) {
-                    v[i] = f32x16{};
-#pragma unroll
-                    for (int s = 0; s < kSteps; ++s)
-                        v[i] = mfma_split(small_frag(poly.hi, 32u * i + ln, 2u * s + half),
-                                          small_frag(poly.lo, 32u * i + ln, 2u * s + half), xh[b][s], xl[b][s], v[i], plain);
-                }
-#pragma unroll
-                for (int i = 0; i < kRows; ++i)
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        _Float16 h, l;
-                        split(v[i][e] * (1.0f / kScaleP), h, l);
-                        xh[b][2 * i + e / 8][e & 7] = h;
-                        xl[b][2 * i + e / 8][e & 7] = l;
-                    }
-            } else {
-                float *param = nullptr;
-                float step = 0.0f;
-                if (a.product == kLastParams) {
-                    param = ((ConstTensorPtr)a.tensors + m.index)->p;
-                    step = (float)(a.lr * (a.scale == 1 ? m.scale_spectral : (a.scale == 2 ? m.scale_rms : 1.0)));
-                }
-#pragma unroll
-                for (int i = 0; i < kRows; ++i) {
-                    // lane = the user's column, so that a wave writes along rows
-                    f32x16 v = {};
-#pragma unroll
-                    for (int s = 0; s < kSteps; ++s) {
-                        const half8 ph = small_frag(poly.hi, 32u * i + ln, 2u * s + half);
-                        const half8 pl = small_frag(poly.lo, 32u * i + ln, 2u * s + half);
-                        v = m.tall ? mfma_split(xh[b][s], xl[b][s], ph, pl, v, plain)
-                                   : mfma_split(ph, pl, xh[b][s], xl[b][s], v, plain);
-                    }
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const uint32_t in = 8u * (e / 4) + 4u * half + (e & 3);
-                        const uint32_t r = m.tall ? col0 + in : 32u * i + in, c = m.tall ? 32u * i + ln : col0 + ln;
-                        if (r >= m.rows || c >= m.cols) continue;
-                        const float o = v[e] * (1.0f / (kScaleX * kScaleP));
-                        if (a.product == kLastParams) {
-                            float *q = param + (uint64_t)r * m.cols + c;
-                            *q = fmaf(-step, o, *q * a.decay);
-                        } else if (a.product == kLastBf16) {
-                            static_cast<uint16_t *>(a.o)[m.o_off + r * m.o_ld + c] = (uint16_t)f32_to_bf16(o);
-                        } else {
-                            static_cast<float *>(a.o)[m.o_off + r * m.o_ld + c] = o;
-                        }
-                    }
+                    for (int e = 0; e < 8; ++e) y[e] = v[8 * k + e] * (1.0f / kScaleP);
+                    split8(y, gh[i][k], gl[i][k]);
                 }
             }
+#pragma unroll
+            for (int i = 0; i < kRows; ++i)
+#pragma unroll
+                for (int j = 0; j <= i; ++j)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        acc[i + j] = mfma_split(gh[i][k], gl[i][k], gh[j][k], gl[j][k], acc[i + j]);
+            if (it == 0) continue;  // P is still one
+            f32x16 v[kRows];
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+                v[i] = f32x16{};
+#pragma unroll
+                for (int s = 0; s < kSteps; ++s)
+                    v[i] = mfma_split(small_frag(poly.hi, 32u * i + ln, 2u * s + half),
+                                      small_frag(poly.lo, 32u * i + ln, 2u * s + half), xh[b][s], xl[b][s], v[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < kRows; ++i)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    float y[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) y[e] = v[i][8 * k + e] * (1.0f / kScaleP);
+                    split8(y, xh[b][2 * i + k], xl[b][2 * i + k]);
+                }
         }
-        if (last) break;
 
-        // A: the waves' sums together, stored with its mirror image
+        // A: the sums of the waves that hold columns together, stored with its mirror image
+        if (wave < active)
 #pragma unroll
-        for (int i = 0; i < kSquare; ++i)
+            for (int i = 0; i < kSquare; ++i)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) parts[wave][i * 16 + e][lane] = acc[i][e];
+                for (int e = 0; e < 16; ++e) parts[wave][i * 16 + e][lane] = acc[i][e];
         __syncthreads();
         for (uint32_t q = wave; q < kSquare * 4u; q += kSmallWaves) {
             float v[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float x = parts[0][q * 4 + e][lane];
+            for (int e = 0; e < 4; ++e) v[e] = parts[0][q * 4 + e][lane];
 #pragma unroll
-                for (int w = 1; w < kSmallWaves; ++w) x += parts[w][q * 4 + e][lane];
-                v[e] = x * (1.0f / kScaleX);
-            }
+            for (uint32_t w = 1; w < kSmallWaves; ++w)
+                if (w < active)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[e] += parts[w][q * 4 + e][lane];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] *= 1.0f / kScaleX;
             const uint32_t blk = q >> 2, g = q & 3u, bi = blk == 0 ? 0u : 1u, bj = blk == 2 ? 1u : 0u;
             const uint32_t r = 32u * bi + 8u * g + 4u * half, c = 32u * bj + ln;
-            _Float16 hi[4], lo[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) split(v[e], hi[e], lo[e]);
-            const u32x2 h = {pack(hi[0], hi[1]), pack(hi[2], hi[3])}, l = {pack(lo[0], lo[1]), pack(lo[2], lo[3])};
+            u32x2 h, l;
+            split4(v[0], v[1], v[2], v[3], h, l);
             *small_quad(gram.hi, c, r) = h;
             *small_quad(gram.lo, c, r) = l;
             if (bi != bj) {
@@ -671,8 +660,7 @@ __global__ __launch_bounds__(64 * kSmallWaves) void muon_small_kernel(MuonSmallA
             for (int s = 0; s < kSteps; ++s) {
                 const uint32_t chunk = 2u * s + half;
                 p = mfma_split(small_frag(gram.hi, 32u * bi + ln, chunk), small_frag(gram.lo, 32u * bi + ln, chunk),
-                               small_frag(gram.hi, 32u * bj + ln, chunk), small_frag(gram.lo, 32u * bj + ln, chunk), p,
-                               next_plain);
+                               small_frag(gram.hi, 32u * bj + ln, chunk), small_frag(gram.lo, 32u * bj + ln, chunk), p);
             }
             const float ca = a.coefficients[3 * it] * kScaleP, cb = a.coefficients[3 * it + 1] * (kScaleP / kScaleX),
                         cc = a.coefficients[3 * it + 2] * (kScaleP / (kScaleX * kScaleX));
@@ -680,21 +668,63 @@ __global__ __launch_bounds__(64 * kSmallWaves) void muon_small_kernel(MuonSmallA
             for (int g = 0; g < 4; ++g) {
                 const uint32_t r = 32u * bi + 8u * g + 4u * half, c = 32u * bj + ln;
                 const u32x2 h = *small_quad(gram.hi, c, r), l = *small_quad(gram.lo, c, r);
-                _Float16 hi[4], lo[4];
+                float x[4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     const uint32_t hw = q < 2 ? h.x : h.y, lw = q < 2 ? l.x : l.y;
-                    float av = (float)__builtin_bit_cast(_Float16, (uint16_t)(hw >> (16 * (q & 1))));
-                    if (!next_plain) av += (float)__builtin_bit_cast(_Float16, (uint16_t)(lw >> (16 * (q & 1))));
+                    const float av = (float)__builtin_bit_cast(_Float16, (uint16_t)(hw >> (16 * (q & 1)))) +
+                                     (float)__builtin_bit_cast(_Float16, (uint16_t)(lw >> (16 * (q & 1))));
                     float v = fmaf(cb, av, cc * p[4 * g + q]);
                     if (r + q == c) v += ca;
-                    split(v, hi[q], lo[q]);
+                    x[q] = v;
                 }
-                *small_quad(poly.hi, c, r) = u32x2{pack(hi[0], hi[1]), pack(hi[2], hi[3])};
-                *small_quad(poly.lo, c, r) = u32x2{pack(lo[0], lo[1]), pack(lo[2], lo[3])};
+                split4(x[0], x[1], x[2], x[3], *small_quad(poly.hi, c, r), *small_quad(poly.lo, c, r));
             }
         }
         __syncthreads();
+    }
+
+    // O = P X, lane = the user's column, so that a wave writes along rows
+    float *param = nullptr;
+    float step = 0.0f;
+    if (a.product == kLastParams) {
+        param = ((ConstTensorPtr)a.tensors + m.index)->p;
+        step = (float)(a.lr * (a.scale == 1 ? m.scale_spectral : (a.scale == 2 ? m.scale_rms : 1.0)));
+    }
+#pragma unroll
+    for (int b = 0; b < kCols; ++b) {
+        const uint32_t col0 = 32u * (wave + kSmallWaves * b);
+        if (col0 >= n) continue;
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            f32x16 v = {};
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) {
+                const half8 ph = small_frag(poly.hi, 32u * i + ln, 2u * s + half);
+                const half8 pl = small_frag(poly.lo, 32u * i + ln, 2u * s + half);
+                v = m.tall ? mfma_split(xh[b][s], xl[b][s], ph, pl, v) : mfma_split(ph, pl, xh[b][s], xl[b][s], v);
+            }
+            const uint32_t r0 = (m.tall ? col0 : 32u * i) + 4u * half, c = m.tall ? 32u * i + ln : col0 + ln;
+            float old[16];
+            if (a.product == kLastParams) {  // all of the block's params at once, then the stores
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const uint32_t r = r0 + 8u * (e / 4) + (e & 3);
+                    old[e] = param[r < m.rows && c < m.cols ? (uint64_t)r * m.cols + c : 0u];
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const uint32_t r = r0 + 8u * (e / 4) + (e & 3);
+                if (r >= m.rows || c >= m.cols) continue;
+                const float o = v[e] * (1.0f / (kScaleX * kScaleP));
+                if (a.product == kLastParams) param[(uint64_t)r * m.cols + c] = fmaf(-step, o, old[e] * a.decay);
+                else if (a.product == kLastBf16)
+                    static_cast<uint16_t *>(a.o)[m.o_off + r * m.o_ld + c] = (uint16_t)f32_to_bf16(o);
+                else static_cast<float *>(a.o)[m.o_off + r * m.o_ld + c] = o;
+            }
+            __builtin_amdgcn_sched_barrier(0);  // one block's addresses at a time
+        }
     }
 }
 
@@ -711,16 +741,16 @@ __global__ __launch_bounds__(256) void muon_sums_kernel(MuonWork w, MuonSumArgs 
     const uint32_t c_in = threadIdx.x & 63u, r_in = threadIdx.x >> 6;
     double sum = 0.0;
     for (uint32_t t = part; t < tiles; t += a.n_partials) {
-        const uint32_t r0 = (t / across) * 64u, c = (t % across) * 64u + c_in;
-        if (c >= m.cols) continue;
+        const uint32_t r0 = (t / across) * 64u + r_in, c = (t % across) * 64u + c_in;
+        float x[16];  // all of the tile's loads before the first sum
 #pragma unroll
         for (uint32_t i = 0; i < 16u; ++i) {
-            const uint32_t r = r0 + r_in + 4u * i;
-            if (r < m.rows) {
-                const double x = load_elem<kBf16>(a.u, m.u_off + r * m.u_ld + c);
-                sum += x * x;
-            }
+            const uint32_t r = r0 + 4u * i;
+            x[i] = load_elem<kBf16>(a.u, m.u_off + (r < m.rows && c < m.cols ? r * m.u_ld + c : 0u));
         }
+#pragma unroll
+        for (uint32_t i = 0; i < 16u; ++i)
+            if (r0 + 4u * i < m.rows && c < m.cols) sum += (double)x[i] * (double)x[i];
     }
     sum = block_sum(sum, s);
     if (threadIdx.x == 0) a.partials[m.norm + part] = sum;
@@ -748,8 +778,9 @@ __global__ __launch_bounds__(256) void muon_prep_kernel(MuonWork w, MuonPrepArgs
     float v[16];
 #pragma unroll
     for (uint32_t i = 0; i < 16u; ++i) {
+        // always a load, so that the sixteen are under way together
         const uint32_t r = ti * 64u + r_in + 4u * i;
-        v[i] = r < m.rows && c < m.cols ? load_elem<kBf16>(a.u, m.u_off + r * m.u_ld + c) : 0.0f;
+        v[i] = load_elem<kBf16>(a.u, m.u_off + (r < m.rows && c < m.cols ? r * m.u_ld + c : 0u));
     }
     double part = 0.0;
     for (uint32_t i = threadIdx.x; i < a.n_partials; i += 256u) part += a.partials[m.norm + i];
@@ -757,7 +788,7 @@ __global__ __launch_bounds__(256) void muon_prep_kernel(MuonWork w, MuonPrepArgs
     const double inv = sum < __builtin_inf() ? (double)kScaleX / (sqrt(sum) + a.eps) : __builtin_nan("");
 #pragma unroll
     for (uint32_t i = 0; i < 16u; ++i) {
-        const bool in = ti * 64u + r_in + 4u * i < m.rows && c < m.cols;  // padding is zero, whatever the norm
+        const bool in = ti * 64u + r_in + 4u * i < m.rows && c < m.cols;
         y[r_in + 4u * i][c_in] = in ? (float)((double)v[i] * inv) : 0.0f;
     }
     __syncthreads();
@@ -774,11 +805,11 @@ __global__ __launch_bounds__(256) void muon_prep_kernel(MuonWork w, MuonPrepArgs
             u32x4 h, l;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                _Float16 h0, l0, h1, l1;
-                split(o == 0 ? y[row][k + 2 * e] : y[k + 2 * e][row], h0, l0);
-                split(o == 0 ? y[row][k + 2 * e + 1] : y[k + 2 * e + 1][row], h1, l1);
-                h[e] = pack(h0, h1);
-                l[e] = pack(l0, l1);
+                uint32_t h0, l0;
+                split2(o == 0 ? y[row][k + 2 * e] : y[k + 2 * e][row], o == 0 ? y[row][k + 2 * e + 1] : y[k + 2 * e + 1][row],
+                       h0, l0);
+                h[e] = h0;
+                l[e] = l0;
             }
             char *at = dst + image_pos<kForm>(row0 + row, k0 + k, length);
             *reinterpret_cast<u32x4 *>(at) = h;
@@ -1036,11 +1067,19 @@ static hipError_t product_of(int product, int in, int out, const MuonGemmArgs &a
     return hipErrorInvalidValue;
 }
 
-typedef Tiling<64, 64, 2, 2, 4, 2> Tiling64;
-typedef Tiling<128, 128, 2, 2, 2, 2> Tiling128;
+// Eight waves hide more of the latency where a CU has one tile or two; with
+// many tiles the larger blocks of four waves read LDS less.  (us, 2 / 1
+// matrices of 4096^2 / 2048^2: P X 729 / 52 with four waves, 745 / 51 with
+// eight; X X^T 429 / 48 and 432 / 44.)
+typedef Tiling<64, 64, 2, 2, 3, 3> Tiling64;
+typedef Tiling<128, 128, 2, 4, 2, 4> Tiling128;
+typedef Tiling<128, 128, 2, 2, 2, 2> Tiling128Many;
+constexpr uint32_t kManyTiles = 1024;
 
 hipError_t launch_muon_product(int tiling, int product, int in, int out, const MuonGemmArgs &a, hipStream_t s) {
-    return tiling == kTile128 ? product_of<Tiling128>(product, in, out, a, s) : product_of<Tiling64>(product, in, out, a, s);
+    if (tiling == kTile64) return product_of<Tiling64>(product, in, out, a, s);
+    if (a.work.n_tiles >= kManyTiles) return product_of<Tiling128Many>(product, in, out, a, s);
+    return product_of<Tiling128>(product, in, out, a, s);
 }
 
 hipError_t launch_muon_small(int64_t short_side, int64_t long_side, const MuonSmallArgs &a, hipStream_t s) {

@@ -26,10 +26,15 @@ constexpr int kStageSlots = 8;  // pinned staging buffers per state
 // Matrices go through the products together up to this many (padded)
 // elements: 1 GB of X, and some 4000 tiles of 128 x 128.
 constexpr int64_t kGroupElements = int64_t(1) << 26;
-// 128 x 128 tiles where there are this many, else 64 x 64 ones.
-constexpr int64_t kLargeTiles = 512;
+// 128 x 128 tiles where they keep the 256 CUs busy, 64 x 64 ones elsewhere:
+// those reach about 3/4 of the rate, but spread over four times the workgroups.
+constexpr int64_t kCus = 256;
+bool large_tiles(int64_t tiles128) {
+    const int64_t rounds = (tiles128 + kCus - 1) / kCus;
+    return tiles128 >= 3 * kCus * rounds / 4;
+}
 constexpr int64_t kMaxDim = int64_t(1) << 21;
-constexpr int64_t kMaxPartials = 256;
+constexpr int64_t kMaxPartials = 1024;
 constexpr double kPlainGrowth = 12.0;
 constexpr float kDefaultCoefficients[3] = {3.4445f, -4.7750f, 2.0315f};
 
@@ -101,7 +106,7 @@ struct Group {
 };
 
 bool is_small(const Shape &s) { return s.shorter() <= kSmallShort && s.longer() <= kSmallLong; }
-int tile_for(int64_t tiles128) { return tiles128 >= kLargeTiles ? 128 : 64; }
+int tile_for(int64_t tiles128) { return large_tiles(tiles128) ? 128 : 64; }
 int tiling_of(int tile) { return tile == 128 ? kTile128 : kTile64; }
 int64_t tiles_of(const Shape &s, int64_t tile) {
     return (pad_to(s.shorter(), tile) / tile) * (pad_to(s.longer(), tile) / tile);
@@ -261,8 +266,7 @@ void forms_of(const muon_iteration &it, bool plain_allowed, int forms[MUON_MAX_S
     }
 }
 
-MuonSmallArgs small_args(const MuonWork &w, const void *u, bool u_bf16, const muon_iteration &it, const int *forms,
-                         int product) {
+MuonSmallArgs small_args(const MuonWork &w, const void *u, bool u_bf16, const muon_iteration &it, int product) {
     MuonSmallArgs a{};
     a.work = w;
     a.u = u;
@@ -270,10 +274,7 @@ MuonSmallArgs small_args(const MuonWork &w, const void *u, bool u_bf16, const mu
     a.eps = (double)it.eps;
     a.product = product;
     a.steps = it.steps;
-    for (int k = 0; k < it.steps; ++k) {
-        coefficients_of(it, k, a.coefficients + 3 * k);
-        if (forms[k] == kPlain) a.plain |= 1u << k;
-    }
+    for (int k = 0; k < it.steps; ++k) coefficients_of(it, k, a.coefficients + 3 * k);
     return a;
 }
 
@@ -791,7 +792,7 @@ int muon_step(muon_state *s, float *const *params, const void *const *grads, con
             into.decay = (float)(1.0 - (double)hp->lr * (double)hp->weight_decay);
             into.scale = hp->scale;
             if (!g.small.empty()) {
-                MuonSmallArgs small = small_args(table_work(g, g.d_small, g.small.size()), a.u, false, hp->iteration, forms,
+                MuonSmallArgs small = small_args(table_work(g, g.d_small, g.small.size()), a.u, false, hp->iteration,
                                                  kLastParams);
                 small.tensors = into.tensors;
                 small.lr = into.lr;
@@ -1163,7 +1164,7 @@ int muon_orthogonalize(const muon_matrices *mats, const void *x, void *out, cons
         if (is_small(shape)) {
             work.per_mat = 1;
             work.n_tiles = (uint32_t)mats->batch;
-            MuonSmallArgs small = small_args(work, x, xe == 2, *iteration, forms, oe == 2 ? kLastBf16 : kLastF32);
+            MuonSmallArgs small = small_args(work, x, xe == 2, *iteration, oe == 2 ? kLastBf16 : kLastF32);
             small.o = out;
             e = launch_muon_small(shape.shorter(), shape.longer(), small, stream);
             return e == hipSuccess ? ADAM_OK : hip_fail(e, "launch");
