@@ -53,6 +53,12 @@ struct MuonWork {
     const MuonMat *mats;
     uint32_t n_tiles;
     uint32_t per_mat;
+    // Tiles from n_whole on are each taken by `parts` workgroups, a part of
+    // the products' length each (parts > 1): their sums go to `partial`, and
+    // the last of them to get there (by `arrived`) adds them up in order.
+    uint32_t n_whole, parts;
+    float *partial;
+    uint32_t *arrived;
     MuonMat one;
     uint64_t x_stride, a_stride, u_stride, o_stride;
     uint32_t norm_stride;
@@ -69,6 +75,13 @@ struct MuonArrays {
 // How one factor is held: split or plain slabs.
 enum MuonForm : int { kSplit = 0, kPlain = 1 };
 
+// The 256 CUs take tiles in rounds; the tiles of a last round that would leave
+// many of them idle are split.
+constexpr uint32_t kCus = 256;
+constexpr uint32_t kMaxSplit = kCus;        // tiles that are split
+constexpr uint32_t kMaxParts = 8;
+constexpr uint32_t kMaxPartials = 4 * kCus;  // workgroups for them
+
 // Sum of squares: one fp64 partial per workgroup, per matrix n_partials.
 struct MuonSumArgs {
     const void *u;
@@ -77,6 +90,7 @@ struct MuonSumArgs {
 };
 
 struct MuonPrepArgs {
+    uint32_t *arrived;  // cleared: kMaxSplit counters
     const void *u;
     const double *partials;
     uint32_t n_partials;
@@ -153,6 +167,8 @@ enum MuonProduct : int { kGram, kPolynomial, kCommuting, kUpdate, kLastBf16, kLa
 // dimensions of a matrix are padded to multiples of both of its products'
 // tiles.
 enum MuonTiling : int { kTile64, kTile128 };
+// Bytes of a split workgroup's sums.
+inline int64_t partial_bytes(int tiling) { return tiling == kTile128 ? 128 * 128 * 4 : 64 * 64 * 4; }
 // in: the form of the factors read; out: of the factor written
 hipError_t launch_muon_product(int tiling, int product, int in, int out, const MuonGemmArgs &a, hipStream_t s);
 

@@ -26,16 +26,10 @@ constexpr int kStageSlots = 8;  // pinned staging buffers per state
 // Matrices go through the products together up to this many (padded)
 // elements: 1 GB of X, and some 4000 tiles of 128 x 128.
 constexpr int64_t kGroupElements = int64_t(1) << 26;
-// 128 x 128 tiles where they keep the 256 CUs busy, 64 x 64 ones elsewhere:
-// those reach about 3/4 of the rate, but spread over four times the workgroups.
-constexpr int64_t kCus = 256;
-bool large_tiles(int64_t tiles128) {
-    const int64_t rounds = (tiles128 + kCus - 1) / kCus;
-    return tiles128 >= 3 * kCus * rounds / 4;
-}
 constexpr int64_t kMaxDim = int64_t(1) << 21;
-constexpr int64_t kMaxPartials = 1024;
+constexpr int64_t kMaxSums = 1024;
 constexpr double kPlainGrowth = 12.0;
+constexpr int64_t kTripleShort = 256;
 constexpr float kDefaultCoefficients[3] = {3.4445f, -4.7750f, 2.0315f};
 
 int fail(int code, const std::string &msg) { return set_last_error(code, msg); }
@@ -75,22 +69,89 @@ struct Shape {
     int64_t longer() const { return std::max(rows, cols); }
 };
 
-// m^3 and m^2 n of a group, in multiply-adds.
-struct Work {
-    double cubes = 0.0, oblongs = 0.0;
-    void add(const Shape &s, double count = 1.0) {
-        const double m = (double)s.shorter(), n = (double)s.longer();
-        cubes += count * m * m * m;
-        oblongs += count * m * m * n;
+// ---------------------------------------------------------------- choice of tiles
+// A launch's time in us by what was measured: a CU takes a slab of a 128 x 128
+// tile in 0.70 us (split factors; several tiles on a CU take as much
+// each) and of a 64 x 64 tile in 0.24; with 256 CUs the tiles go in rounds.
+// The tiles beyond whole rounds may be cut into parts along the
+// products' length, whose sums are written and read at 3500 bytes a ns.
+// 5 us pass in a launch besides.
+constexpr double kSlabTime[2] = {0.24, 0.70};  // by tiling
+constexpr double kLaunchTime = 5.0;
+
+struct Cut {
+    uint32_t whole, parts;
+    double time;
+};
+// slabs: the tiles' average; least: the fewest a tile has
+Cut cut_tiles(int tiling, int64_t tiles, int64_t jobs, double slabs, int64_t least) {
+    const double one = slabs * kSlabTime[tiling];
+    const int64_t rest = tiles * jobs % kCus, rounds = tiles * jobs / kCus;
+    Cut cut{(uint32_t)tiles, 1, (rest > 0 ? (double)(rounds + 1) : (double)rounds) * one + kLaunchTime};
+    if (rest % jobs != 0) return cut;
+    for (int64_t parts = 2; parts <= (int64_t)kMaxParts && parts * rest <= kMaxPartials && least / parts >= 4; ++parts) {
+        const double time = (double)rounds * one + (double)((rest * parts + kCus - 1) / kCus) / (double)parts * one + 2.0 +
+                            2.0 * (double)(rest * parts * partial_bytes(tiling)) / 3.5e6 + kLaunchTime;
+        if (rest > 0 && time < cut.time) cut = Cut{(uint32_t)(tiles - rest / jobs), (uint32_t)parts, time};
     }
-    // whether runs save more work than their two or three further launches cost
-    bool runs_pay() const { return oblongs - cubes > 2e8; }
+    return cut;
+}
+
+// The tiles of one kind of product over a set of matrices, for either tiling,
+// and the length of the products in slabs.
+struct Load {
+    int64_t tiles[2] = {0, 0};
+    double slabs[2] = {0.0, 0.0};  // summed over tiles
+    int64_t least = kMaxDim;
+    void add(double count, int64_t down, int64_t across, bool triangle, int64_t length) {
+        for (int t = 0; t < 2; ++t) {
+            const int64_t size = t == kTile128 ? 128 : 64, r = pad_to(down, size) / size, c = pad_to(across, size) / size;
+            const int64_t n = (int64_t)count * (triangle ? r * (r + 1) / 2 : r * c);
+            tiles[t] += n;
+            slabs[t] += (double)n * (double)pad_to(length, size) / 32.0;
+        }
+        least = std::min(least, length / 32);
+    }
+    // plain slabs hold twice the elements
+    Cut cut(int tiling, int64_t n_tiles, int64_t jobs, int form) const {
+        const double per = form == kSplit ? 1.0 : 2.0;
+        return cut_tiles(tiling, n_tiles, jobs, slabs[tiling] / (double)std::max<int64_t>(1, tiles[tiling]) / per,
+                         least / (int64_t)per);
+    }
+    double time(int tiling, int64_t jobs = 1) const { return cut(tiling, tiles[tiling], jobs, kSplit).time; }
+};
+
+// What a set of matrices that go through the products together takes.
+struct Work {
+    Load gram, square, update;  // X X^T; products of square factors; P X
+    int square_tiling = kTile64, update_tiling = kTile64;
+    bool pairs = false, triples = false;  // whether runs of two or three iterations are to be taken
+    int64_t shortest = kMaxDim;
+    void add(const Shape &s, double count = 1.0) {
+        shortest = std::min(shortest, s.shorter());
+        gram.add(count, s.shorter(), s.shorter(), true, s.longer());
+        square.add(count, s.shorter(), s.shorter(), true, s.shorter());
+        update.add(count, s.shorter(), s.longer(), false, s.shorter());
+    }
+    void choose() {
+        auto better = [](const Load &l, const Load &m) {
+            return l.time(kTile128) + m.time(kTile128) <= l.time(kTile64) + m.time(kTile64) ? kTile128 : kTile64;
+        };
+        square_tiling = better(square, gram);
+        update_tiling = better(update, update);
+        const double g = gram.time(square_tiling), s = square.time(square_tiling), u = update.time(update_tiling);
+        pairs = g + u > 3.0 * s;
+        triples = shortest >= kTripleShort && 2.0 * (g + u) > 4.0 * s + square.time(square_tiling, 2);
+    }
+    int64_t pad() const { return square_tiling == kTile128 || update_tiling == kTile128 ? 128 : 64; }
+    int64_t part_bytes() const {
+        return std::max(partial_bytes(square_tiling), partial_bytes(update_tiling));
+    }
 };
 
 // A part of the list whose matrices go through the products together.
 struct Group {
     int32_t first = 0, last = 0;  // tensors [first, last)
-    int tile = 128;
     int64_t x_bytes = 0, a_bytes = 0;  // of one X (or X^T) array and of one square array
     int64_t block0 = 0, blocks = 0;    // 2048-element blocks
     int64_t flat0 = 0;                 // flat state index of its first element
@@ -106,8 +167,7 @@ struct Group {
 };
 
 bool is_small(const Shape &s) { return s.shorter() <= kSmallShort && s.longer() <= kSmallLong; }
-int tile_for(int64_t tiles128) { return large_tiles(tiles128) ? 128 : 64; }
-int tiling_of(int tile) { return tile == 128 ? kTile128 : kTile64; }
+int size_of(int tiling) { return tiling == kTile128 ? 128 : 64; }
 int64_t tiles_of(const Shape &s, int64_t tile) {
     return (pad_to(s.shorter(), tile) / tile) * (pad_to(s.longer(), tile) / tile);
 }
@@ -122,21 +182,21 @@ std::vector<Group> plan(const std::vector<Shape> &shapes) {
         g.first = k;
         g.block0 = block;
         g.flat0 = flat;
-        int64_t elements = 0, tiles128 = 0;
+        int64_t elements = 0;
         for (; k < n; ++k) {
             const int64_t t = shapes[k].numel() > 0 ? tiles_of(shapes[k], 128) : 0;
             if (elements > 0 && elements + t * 16384 > kGroupElements) break;
             elements += t * 16384;
-            if (!is_small(shapes[k])) tiles128 += t, g.size.add(shapes[k]);
+            if (t > 0 && !is_small(shapes[k])) g.size.add(shapes[k]);
             block += blocks_of(shapes[k].numel());
             flat += pad16(shapes[k].numel());
         }
         g.last = k;
         g.blocks = block - g.block0;
-        g.tile = tile_for(tiles128);
+        g.size.choose();
         for (int32_t i = g.first; i < g.last; ++i) {
             if (shapes[i].numel() == 0) continue;
-            const int64_t m = pad_to(shapes[i].shorter(), g.tile), l = pad_to(shapes[i].longer(), g.tile);
+            const int64_t m = pad_to(shapes[i].shorter(), g.size.pad()), l = pad_to(shapes[i].longer(), g.size.pad());
             g.x_bytes += 4 * m * l;
             g.a_bytes += 4 * m * m;
         }
@@ -148,16 +208,22 @@ std::vector<Group> plan(const std::vector<Shape> &shapes) {
 // The workspace a group needs: four X arrays, the square ones, the blocks' partial
 // sums and the matrices' sums.
 int64_t align256(int64_t n) { return pad_to(n, 256); }
+int64_t workspace_bytes(const Work &w, int64_t x_bytes, int64_t a_bytes, int64_t n_partials) {
+    return 4 * align256(x_bytes) + kSquares * align256(a_bytes) + 4 * kMaxSplit + kMaxPartials * w.part_bytes() +
+           align256(8 * n_partials);
+}
 int64_t group_bytes(const Group &g) {
-    return 4 * align256(g.x_bytes) + kSquares * align256(g.a_bytes) + align256(8 * g.blocks) + align256(8 * (g.last - g.first));
+    return workspace_bytes(g.size, g.x_bytes, g.a_bytes, g.blocks) + align256(8 * (g.last - g.first));
 }
 
 struct Workspace {
     MuonArrays f;
+    uint32_t *arrived;  // split tiles: counters and parts
+    float *parts;
     double *partials, *sums;
 };
 
-Workspace carve(char *base, int64_t x_bytes, int64_t a_bytes, int64_t n_partials) {
+Workspace carve(char *base, const Work &size, int64_t x_bytes, int64_t a_bytes, int64_t n_partials) {
     Workspace w;
     auto take = [&base](int64_t n) {
         char *p = base;
@@ -169,6 +235,8 @@ Workspace carve(char *base, int64_t x_bytes, int64_t a_bytes, int64_t n_partials
         w.f.xt[i] = take(x_bytes);
     }
     for (char *&p : w.f.square) p = take(a_bytes);
+    w.arrived = reinterpret_cast<uint32_t *>(take(4 * kMaxSplit));
+    w.parts = reinterpret_cast<float *>(take(kMaxPartials * size.part_bytes()));
     w.partials = reinterpret_cast<double *>(take(8 * n_partials));
     w.sums = reinterpret_cast<double *>(base);
     return w;
@@ -285,11 +353,14 @@ MuonSmallArgs small_args(const MuonWork &w, const void *u, bool u_bf16, const mu
 // What it costs in accuracy is that A' carries A's rounding, grown by a^2: two
 // iterations lose nothing that can be seen beside the rounding of X that they
 // save; three, at the start of a longer sequence, while |a_1 a_2| is at most
-// kPlainGrowth; four fail.  Factors held in single fp16 values are not put into runs.
+// kPlainGrowth and m at least kTripleShort (A's rounding errors add up to a
+// matrix of norm ~ m^(-1/2): of 3 x 5000, one direction over a noise of 0.1, the
+// result was off by 1.7e-4, by 6e-6 in plain fp32; from 256 rows on three are as good
+// as one at a time); four fail.  Factors held in single fp16 values are not put into runs.
 struct Run {
     int first, length;
 };
-std::vector<Run> runs_of(const muon_iteration &it, const int *forms, bool allowed) {
+std::vector<Run> runs_of(const muon_iteration &it, const int *forms, const Work &size) {
     auto a = [&](int k) {
         float c[3];
         coefficients_of(it, k, c);
@@ -299,12 +370,12 @@ std::vector<Run> runs_of(const muon_iteration &it, const int *forms, bool allowe
     while (split < it.steps && forms[split] == kSplit) ++split;
     std::vector<Run> runs;
     int k = 0;
-    if (allowed && split % 2 == 1) {  // pairs from the end, three iterations or one before them
-        const bool three = split >= 3 && it.steps > 3 && a(0) * a(1) <= kPlainGrowth && a(0) * a(1) * a(2) <= 64.0;
+    if (split % 2 == 1) {  // pairs from the end, three iterations or one before them
+        const bool three = size.triples && split >= 3 && it.steps > 3 && a(0) * a(1) <= kPlainGrowth && a(0) * a(1) * a(2) <= 64.0;
         runs.push_back(Run{0, three ? 3 : 1});
         k = runs[0].length;
     }
-    while (allowed && k + 1 < split) {
+    while (size.pairs && k + 1 < split) {
         if (a(k) * a(k + 1) <= 64.0) {  // an entry of P_2 P_1 has to stay below 256
             runs.push_back(Run{k, 2});
             k += 2;
@@ -317,46 +388,55 @@ std::vector<Run> runs_of(const muon_iteration &it, const int *forms, bool allowe
 }
 
 // The products of all iterations, X_0 and X_0^T being in f.x[0], f.xt[0].
-hipError_t run_products(int tiling, const MuonArrays &f, const MuonWork &square, const MuonWork &update, const Work &size,
+hipError_t run_products(const Workspace &w, const MuonWork &square, const MuonWork &update, const Work &size,
                         const muon_iteration &it, const int *forms, int last, const MuonGemmArgs &into, hipStream_t s) {
     hipError_t e = hipSuccess;
     int form = kSplit;
-    auto polynomial = [&](const char *a, char *p, int k) {
+    const MuonArrays &f = w.f;
+    auto launch = [&](int product, int out, MuonGemmArgs &g) {
         if (e != hipSuccess) return;
+        const bool is_square = product == kGram || product == kPolynomial || product == kCommuting;
+        const int tiling = is_square ? size.square_tiling : size.update_tiling;
+        const Load &load = product == kGram ? size.gram : (is_square ? size.square : size.update);
+        g.work = is_square ? square : update;
+        const Cut cut = load.cut(tiling, g.work.n_tiles, g.left2 ? 2 : 1, form);
+        g.work.n_whole = cut.whole;
+        g.work.parts = cut.parts;
+        g.work.partial = w.parts;
+        g.work.arrived = w.arrived;
+        e = launch_muon_product(tiling, product, form, out, g, s);
+    };
+    auto polynomial = [&](const char *a, char *p, int k) {
         float c[3];
         coefficients_of(it, k, c);
         MuonGemmArgs g{};
-        g.work = square;
         g.left = g.add = a;
         g.out = p;
         g.ca = c[0];
         g.cb = c[1];
         g.cc = c[2];
-        e = launch_muon_product(tiling, kPolynomial, form, form, g, s);
+        launch(kPolynomial, form, g);
     };
     auto commuting = [&](const char *left, const char *right, char *out, const char *left2 = nullptr,
                          const char *right2 = nullptr, char *out2 = nullptr) {
-        if (e != hipSuccess) return;
         MuonGemmArgs g{};
-        g.work = square;
         g.left = left;
         g.right = right;
         g.out = out;
         g.left2 = left2;
         g.right2 = right2;
         g.out2 = out2;
-        e = launch_muon_product(tiling, kCommuting, form, form, g, s);
+        launch(kCommuting, form, g);
     };
     char *const A = f.square[0], *const T = f.square[1], *const P = f.square[2], *const R = f.square[3],
                *const U = f.square[4];
     int cur = 0;
-    for (const Run &run : runs_of(it, forms, size.runs_pay())) {
+    for (const Run &run : runs_of(it, forms, size)) {
         form = forms[run.first];
         MuonGemmArgs g{};
-        g.work = square;
         g.left = f.x[cur];
         g.out = A;
-        if ((e = launch_muon_product(tiling, kGram, form, form, g, s)) != hipSuccess) return e;
+        launch(kGram, form, g);
         polynomial(A, P, run.first);
         const char *q = P;
         if (run.length >= 2) {
@@ -374,23 +454,20 @@ hipError_t run_products(int tiling, const MuonArrays &f, const MuonWork &square,
                 q = T;
             }
         }
-        if (e != hipSuccess) return e;
         const int next = run.first + run.length;
         g = next < it.steps ? MuonGemmArgs{} : into;
-        g.work = update;
         g.left = q;
         g.right = f.xt[cur];
         if (next < it.steps) {
             g.out = f.x[cur ^ 1];
             g.out_t = f.xt[cur ^ 1];
-            e = launch_muon_product(tiling, kUpdate, form, forms[next], g, s);
+            launch(kUpdate, forms[next], g);
             cur ^= 1;
         } else {
-            e = launch_muon_product(tiling, last, form, form, g, s);
+            launch(last, form, g);
         }
-        if (e != hipSuccess) return e;
     }
-    return hipSuccess;
+    return e;
 }
 
 }  // namespace
@@ -475,7 +552,8 @@ void build_tables(Group &g, const std::vector<Shape> &shapes) {
     std::stable_sort(order.begin(), order.end(),
                      [&](int32_t a, int32_t b) { return shapes[a].longer() > shapes[b].longer(); });
     uint64_t x_off = 0, a_off = 0;
-    const int T = g.tile;
+    const int64_t pad = g.size.pad();
+    const uint32_t S = size_of(g.size.square_tiling), U = size_of(g.size.update_tiling);
     for (int32_t k : order) {
         const Shape &s = shapes[k];
         MuonMat m{};
@@ -483,8 +561,8 @@ void build_tables(Group &g, const std::vector<Shape> &shapes) {
         m.a_off = a_off;
         m.u_off = (uint64_t)flats[k - g.first];
         m.u_ld = (uint64_t)s.cols;
-        m.mp = (uint32_t)pad_to(s.shorter(), T);
-        m.np = (uint32_t)pad_to(s.longer(), T);
+        m.mp = (uint32_t)pad_to(s.shorter(), pad);
+        m.np = (uint32_t)pad_to(s.longer(), pad);
         m.rows = (uint32_t)s.rows;
         m.cols = (uint32_t)s.cols;
         m.tall = s.rows > s.cols;
@@ -504,11 +582,11 @@ void build_tables(Group &g, const std::vector<Shape> &shapes) {
             g.small_long = std::max(g.small_long, s.longer());
             continue;
         }
-        const uint32_t mb = m.mp / T, nb = m.np / T;
+        const uint32_t sb = m.mp / S, mb = m.mp / U, nb = m.np / U;
         const uint32_t pr = (m.tall ? m.np : m.mp) / 64, pc = (m.tall ? m.mp : m.np) / 64;
         for (uint32_t a = 0; a < pr; ++a)
             for (uint32_t b = 0; b < pc; ++b) g.prep.push_back(MuonTile{i, (uint16_t)a, (uint16_t)b});
-        for (uint32_t a = 0; a < mb; ++a)
+        for (uint32_t a = 0; a < sb; ++a)
             for (uint32_t b = 0; b <= a; ++b) g.square.push_back(MuonTile{i, (uint16_t)a, (uint16_t)b});
         for (uint32_t a0 = 0; a0 < mb; a0 += 8)  // bands of 8 tile rows, as the kernel takes them
             for (uint32_t b = 0; b < nb; ++b)
@@ -764,7 +842,7 @@ int muon_step(muon_state *s, float *const *params, const void *const *grads, con
         int forms[MUON_MAX_STEPS];
         forms_of(hp->iteration, false, forms);
         for (const Group &g : s->groups) {
-            const Workspace w = carve(s->workspace, g.x_bytes, g.a_bytes, g.blocks);
+            const Workspace w = carve(s->workspace, g.size, g.x_bytes, g.a_bytes, g.blocks);
             MuonStepArgs a{};
             a.desc = s->d_desc + g.block0;
             a.tensors = tensors;
@@ -805,6 +883,7 @@ int muon_step(muon_state *s, float *const *params, const void *const *grads, con
             if ((e = launch_muon_norms(w.partials, g.d_ranges, w.sums, (uint32_t)g.mats.size(), stream)) != hipSuccess)
                 return hip_fail(e, "norm launch");
             MuonPrepArgs p{};
+            p.arrived = w.arrived;
             p.u = a.u;
             p.partials = w.sums;
             p.n_partials = 1;
@@ -814,7 +893,7 @@ int muon_step(muon_state *s, float *const *params, const void *const *grads, con
             if ((e = launch_muon_prep(false, forms[0], table_work(g, g.d_prep, g.prep.size()), p, stream)) !=
                 hipSuccess)
                 return hip_fail(e, "preparation launch");
-            if ((e = run_products(tiling_of(g.tile), w.f, table_work(g, g.d_square, g.square.size()),
+            if ((e = run_products(w, table_work(g, g.d_square, g.square.size()),
                                   table_work(g, g.d_update, g.update.size()), g.size, hp->iteration, forms, kLastParams, into,
                                   stream)) != hipSuccess)
                 return hip_fail(e, "product launch");
@@ -1077,8 +1156,8 @@ namespace {
 // How a batch is cut: `chunk` matrices go through the products together.
 struct BatchPlan {
     int64_t chunk = 1;
-    int tile = 128;
-    int64_t mb = 0, nb = 0;            // tiles along the short and the long side
+    Work size;                         // of a chunk
+    int64_t mp = 0, np = 0;            // padded sides
     int64_t x_bytes = 0, a_bytes = 0;  // per matrix
     int64_t n_partials = 1;            // per matrix
     int64_t bytes = 0;
@@ -1086,15 +1165,15 @@ struct BatchPlan {
 
 BatchPlan plan_batch(int64_t batch, const Shape &s) {
     BatchPlan p;
-    const int64_t tiles128 = tiles_of(s, 128);
-    p.chunk = std::max<int64_t>(1, std::min<int64_t>(batch, kGroupElements / (tiles128 * 16384)));
-    p.tile = tile_for(tiles128 * p.chunk);
-    p.mb = pad_to(s.shorter(), p.tile) / p.tile;
-    p.nb = pad_to(s.longer(), p.tile) / p.tile;
-    p.x_bytes = 4 * p.tile * p.tile * p.mb * p.nb;
-    p.a_bytes = 4 * p.tile * p.tile * p.mb * p.mb;
-    p.n_partials = std::min(kMaxPartials, tiles_of(s, 64));
-    p.bytes = 4 * align256(p.x_bytes * p.chunk) + kSquares * align256(p.a_bytes * p.chunk) + align256(8 * p.n_partials * p.chunk);
+    p.chunk = std::max<int64_t>(1, std::min<int64_t>(batch, kGroupElements / (tiles_of(s, 128) * 16384)));
+    p.size.add(s, (double)p.chunk);
+    p.size.choose();
+    p.mp = pad_to(s.shorter(), p.size.pad());
+    p.np = pad_to(s.longer(), p.size.pad());
+    p.x_bytes = 4 * p.mp * p.np;
+    p.a_bytes = 4 * p.mp * p.mp;
+    p.n_partials = std::min(kMaxSums, tiles_of(s, 64));
+    p.bytes = workspace_bytes(p.size, p.x_bytes * p.chunk, p.a_bytes * p.chunk, p.n_partials * p.chunk);
     return p;
 }
 
@@ -1170,10 +1249,10 @@ int muon_orthogonalize(const muon_matrices *mats, const void *x, void *out, cons
             return e == hipSuccess ? ADAM_OK : hip_fail(e, "launch");
         }
         const BatchPlan p = plan_batch(mats->batch, shape);
-        const Workspace w = carve(static_cast<char *>(workspace), p.x_bytes * p.chunk, p.a_bytes * p.chunk,
+        const Workspace w = carve(static_cast<char *>(workspace), p.size, p.x_bytes * p.chunk, p.a_bytes * p.chunk,
                                   p.n_partials * p.chunk);
-        work.one.mp = (uint32_t)(p.mb * p.tile);
-        work.one.np = (uint32_t)(p.nb * p.tile);
+        work.one.mp = (uint32_t)p.mp;
+        work.one.np = (uint32_t)p.np;
         work.x_stride = (uint64_t)p.x_bytes;
         work.a_stride = (uint64_t)p.a_bytes;
         work.norm_stride = (uint32_t)p.n_partials;
@@ -1191,20 +1270,28 @@ int muon_orthogonalize(const muon_matrices *mats, const void *x, void *out, cons
             if ((e = launch_muon_sums(xe == 2, with(p.n_partials), sums, (uint32_t)count, stream)) != hipSuccess)
                 return hip_fail(e, "sum launch");
             MuonPrepArgs prep{};
+            prep.arrived = w.arrived;
             prep.u = x;
             prep.partials = w.partials;
             prep.n_partials = (uint32_t)p.n_partials;
             prep.eps = (double)iteration->eps;
             prep.x = w.f.x[0];
             prep.xt = w.f.xt[0];
-            const int64_t sub = p.tile / 64;
-            if ((e = launch_muon_prep(xe == 2, forms[0], with(p.mb * p.nb * sub * sub), prep, stream)) != hipSuccess)
+            if ((e = launch_muon_prep(xe == 2, forms[0], with((p.mp / 64) * (p.np / 64)), prep, stream)) != hipSuccess)
                 return hip_fail(e, "preparation launch");
             MuonGemmArgs into{};
             into.o = out;
-            Work size;
-            size.add(shape, (double)count);
-            if ((e = run_products(tiling_of(p.tile), w.f, with(p.mb * (p.mb + 1) / 2), with(p.mb * p.nb), size, *iteration, forms,
+            Work size = p.size;
+            if (count != p.chunk) {  // the last chunk: its own counts, the tilings of the others
+                Work rest;
+                rest.add(shape, (double)count);
+                size.gram = rest.gram;
+                size.square = rest.square;
+                size.update = rest.update;
+            }
+            const int64_t sb = p.mp / size_of(size.square_tiling), ub = p.mp / size_of(size.update_tiling),
+                          lb = p.np / size_of(size.update_tiling);
+            if ((e = run_products(w, with(sb * (sb + 1) / 2), with(ub * lb), size, *iteration, forms,
                                   oe == 2 ? kLastBf16 : kLastF32, into, stream)) != hipSuccess)
                 return hip_fail(e, "product launch");
         }
