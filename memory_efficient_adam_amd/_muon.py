@@ -179,11 +179,13 @@ def muon_state_destroy(state):
 
 
 def _check_matrices(state, params, grads):
+    if len(params) == len(grads) == len(state.shapes):
+        for k, (p, g, shape) in enumerate(zip(params, grads, state.shapes)):
+            for t in (p, g):
+                if getattr(t, "shape", None) is not None and t.numel() == shape[0] * shape[1] and t.shape != shape:
+                    raise ValueError(f"tensor {k}: param/grad shape {tuple(t.shape)}, the state "
+                                     f"holds {shape}")
     B._check_step_tensors(state, params, grads)
-    for k, (p, g, shape) in enumerate(zip(params, grads, state.shapes)):
-        if tuple(p.shape) != shape or tuple(g.shape) != shape:
-            raise ValueError(f"tensor {k}: param/grad shape {tuple(p.shape)}/{tuple(g.shape)}, the "
-                             f"state holds {shape}")
 
 
 def muon_step(state, params, grads, *, lr, t, momentum=0.95, weight_decay=0.0, nesterov=True,

@@ -29,7 +29,7 @@ constexpr int64_t kGroupElements = int64_t(1) << 26;
 constexpr int64_t kMaxDim = int64_t(1) << 21;
 constexpr int64_t kMaxSums = 1024;
 constexpr double kPlainGrowth = 12.0;
-constexpr int64_t kTripleShort = 256;
+constexpr int64_t kPairShort = 256, kTripleShort = 512;
 constexpr float kDefaultCoefficients[3] = {3.4445f, -4.7750f, 2.0315f};
 
 int fail(int code, const std::string &msg) { return set_last_error(code, msg); }
@@ -140,7 +140,7 @@ struct Work {
         square_tiling = better(square, gram);
         update_tiling = better(update, update);
         const double g = gram.time(square_tiling), s = square.time(square_tiling), u = update.time(update_tiling);
-        pairs = g + u > 3.0 * s;
+        pairs = shortest >= kPairShort && g + u > 3.0 * s;
         triples = shortest >= kTripleShort && 2.0 * (g + u) > 4.0 * s + square.time(square_tiling, 2);
     }
     int64_t pad() const { return square_tiling == kTile128 || update_tiling == kTile128 ? 128 : 64; }
@@ -350,13 +350,15 @@ MuonSmallArgs small_args(const MuonWork &w, const void *u, bool u_bf16, const mu
 // polynomials in the run's first A = X X^T, so A' = P A P and X' = (P_2 P_1) X,
 // and a run of L costs 3 m^2 n + (4 L - 3) m^3 multiply-adds (symmetric results
 // counted by half) for the 3 L m^2 n + L m^3 of one iteration after the other.
-// What it costs in accuracy is that A' carries A's rounding, grown by a^2: two
-// iterations lose nothing that can be seen beside the rounding of X that they
-// save; three, at the start of a longer sequence, while |a_1 a_2| is at most
-// kPlainGrowth and m at least kTripleShort (A's rounding errors add up to a
-// matrix of norm ~ m^(-1/2): of 3 x 5000, one direction over a noise of 0.1, the
-// result was off by 1.7e-4, by 6e-6 in plain fp32; from 256 rows on three are as good
-// as one at a time); four fail.  Factors held in single fp16 values are not put into runs.
+// What it costs in accuracy is that A' carries A's rounding, grown by a^2, where
+// one iteration after the other forms A anew.  The rounding errors of m^2 entries
+// add up to a matrix of norm ~ m^(-1/2), so what counts is m: against plain fp32's
+// own error (rank m/16 over a noise of 0.1, in fp64) the result was off by
+// 1.1 to 1.25 times that with no runs; with runs by 4 times at 64 x 5000, 1.4 at
+// 256 x 4096, 0.9 at 600 x 5000, and by 30 times with three iterations at 3 x 5000.
+// So pairs are taken from kPairShort rows on, three iterations from kTripleShort
+// on, once, first, and while |a_1 a_2| is at most kPlainGrowth; four fail.
+// Factors held in single fp16 values are not put into runs.
 struct Run {
     int first, length;
 };

@@ -14,10 +14,11 @@ def triples(steps, coefficients):
 
 def iterate(u, steps=5, coefficients=None, eps=1e-7, dtype=torch.float64):
     """[X_0, .., X_steps] of one matrix (short side first)."""
-    x = u.to(dtype)
+    x = u.double()
     if x.shape[0] > x.shape[1]:
         x = x.T.contiguous()
-    x = x / (x.square().sum().sqrt() + float(torch.tensor(eps, dtype=torch.float32)))
+    # the norm in 64 bits also for an iteration in 32 (squares of 1e-30 vanish there)
+    x = (x / (x.square().sum().sqrt() + float(torch.tensor(eps, dtype=torch.float32)))).to(dtype)
     xs = [x]
     for a, b, c in triples(steps, coefficients):
         g = x @ x.T.contiguous()

@@ -249,3 +249,339 @@ def test_step_against_the_oracle_and_the_formula(storage, stochastic, gdt, neste
             err = float((p.double() - ref.exact[k]).norm())
             assert err <= total[k], (t, k, err, total[k])
     state.destroy()
+
+
+# ---------------------------------------------------------------- layouts, streams, graphs
+def test_orthogonalize_takes_strided_batches_and_writes_nothing_else():
+    for shape in ((4, 60, 90), (3, 200, 310), (2, 700, 129)):
+        b, r, c = shape
+        big = _matrix(5, (b, r + 3, c + 7))
+        x = big[:, 2:r + 2, 3:c + 3]  # not aligned to more than an element
+        dest = torch.full((b, r + 4, c + 5), 7.0, device="cuda")
+        out = dest[:, 1:r + 1, 4:c + 4]
+        before = big.clone()
+        assert ma.muon_orthogonalize(x, out=out) is out
+        assert torch.equal(out, ma.muon_orthogonalize(x.contiguous()))
+        assert torch.equal(big, before)
+        dest[:, 1:r + 1, 4:c + 4] = 7.0
+        assert bool((dest == 7.0).all())
+        half = torch.empty(shape, dtype=torch.bfloat16, device="cuda")
+        ma.muon_orthogonalize(x, out=half)  # fp32 in, bf16 out
+        _check(half, x.contiguous())
+        wide = ma.muon_orthogonalize(x.bfloat16(), out=torch.empty(shape, device="cuda"))  # bf16 in, fp32 out
+        _check(wide, x.bfloat16())
+
+
+def test_orthogonalize_in_place_broadcast_and_higher_batches():
+    x = _matrix(6, (2, 3, 150, 140))
+    want = ma.muon_orthogonalize(x)
+    assert torch.equal(ma.muon_orthogonalize(x[:, 1]), want[:, 1])
+    same = x[0, 0].expand(5, 150, 140)  # one matrix read five times
+    assert all(torch.equal(o, want[0, 0]) for o in ma.muon_orthogonalize(same))
+    assert ma.muon_orthogonalize(x, out=x) is x and torch.equal(x, want)
+    with pytest.raises(ma.AdamError, match="overlaps"):
+        flat = _matrix(6, (300, 140))
+        ma.muon_orthogonalize(flat[:200], out=flat[100:])
+
+
+def test_orthogonalize_batches_beyond_one_part():
+    # 2^26 elements go through the products at a time: two parts and a rest
+    x = _matrix(8, (1, 1024, 1100)).expand(130, 1024, 1100)
+    out = ma.muon_orthogonalize(x)
+    _check(out[:1], x[:1])
+    assert all(torch.equal(out[0], o) or float((out[0] - o).norm()) < 1e-5 * float(o.norm()) for o in out[1:])
+
+
+@pytest.mark.parametrize("shape", [(40, 70), (300, 300), (5, 600, 520), (2200, 2100)], ids=str)
+def test_zero_and_nonfinite_matrices(shape):
+    batch = 3
+    x = _matrix(2, (batch,) + shape[-2:])
+    good = ma.muon_orthogonalize(x)
+    x[1] = 0.0
+    out = ma.muon_orthogonalize(x)
+    assert bool((out[1] == 0).all())
+    for value in (float("nan"), float("inf"), float("-inf")):
+        x[1] = 0.0
+        x[1, -1, -1] = value
+        out = ma.muon_orthogonalize(x)
+        assert bool(out[1].isnan().all())
+        assert torch.equal(out[0], good[0]) and torch.equal(out[2], good[2])
+
+
+@pytest.mark.parametrize("size", [1e-30, 1e-10, 1e30], ids=str)
+def test_scales_of_the_gradient(size):
+    # squares that leave fp32's range; eps is small beside the norm
+    for shape in ((50, 60), (200, 333)):
+        x = _matrix(4, shape, size=size)
+        kw = dict(eps=1e-37)
+        _check(ma.muon_orthogonalize(x, **kw), x, **kw)
+
+
+def test_closed_forms():
+    # one direction, and a diagonal: the polynomial of each singular value
+    def poly(s, steps=5):
+        for a, b, c in muon_ref.triples(steps, None):
+            s = a * s + b * s ** 3 + c * s ** 5
+        return s
+    for shape in ((30, 50), (400, 260)):
+        u = torch.randn(shape[0], 1, generator=_gen(1), device="cuda", dtype=torch.float64)
+        v = torch.randn(1, shape[1], generator=_gen(2), device="cuda", dtype=torch.float64)
+        o = ma.muon_orthogonalize((u @ v).float())
+        want = poly(1.0) * (u / u.norm()) @ (v / v.norm())
+        # rounding u v^T to fp32 leaves up to 2^-24 of its norm outside the one
+        # direction, and X_0's two fp16 values 2^-23; singular values that small grow
+        # by the product of the a_k (484.9), the direction's own goes to poly(1)
+        growth = math.prod(abc[0] for abc in muon_ref.triples(5, None)) / abs(poly(1.0))
+        assert float((o.double() - want).norm() / want.norm()) < growth * (2.0 ** -24 + 2.0 ** -23)
+        n = min(shape)
+        s = torch.linspace(1.0, 0.01, n, device="cuda", dtype=torch.float64)
+        x = torch.zeros(shape, device="cuda", dtype=torch.float64)
+        x[range(n), range(n)] = s
+        o = ma.muon_orthogonalize(x.float())
+        want = torch.zeros_like(x)
+        want[range(n), range(n)] = poly(s / s.norm())
+        assert float((o.double() - want).norm() / want.norm()) < 2.0 ** -16
+
+
+def test_results_repeat_bit_for_bit_and_on_other_streams():
+    for shape in ((64, 300), (1000, 768), (2, 2048, 2048), (24, 600, 700)):
+        x = _matrix(9, shape)
+        want = ma.muon_orthogonalize(x)
+        for _ in range(3):
+            assert torch.equal(ma.muon_orthogonalize(x), want)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        got = ma.muon_orthogonalize(x, stream=side)
+        two = ma.muon_orthogonalize(x)  # at the same time, its own workspace
+        side.synchronize()
+        assert torch.equal(got, want) and torch.equal(two, want)
+        raw = ma.muon_orthogonalize(x, stream=side.cuda_stream)
+        side.synchronize()
+        assert torch.equal(raw, want)
+
+
+def test_orthogonalize_in_a_graph():
+    for shape in ((48, 80), (3, 500, 700), (2048, 2048)):
+        x = _matrix(1, shape)
+        out, ws = torch.empty_like(x), torch.empty(
+            max(1, ma.muon_orthogonalize_workspace_bytes(x.numel() // (shape[-1] * shape[-2]), *shape[-2:])),
+            dtype=torch.uint8, device="cuda")
+        ma.muon_orthogonalize(x, out=out, workspace=ws)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            ma.muon_orthogonalize(x, out=out, workspace=ws)
+        for k in range(4):
+            x.copy_(_matrix(20 + k, shape))
+            out.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, ma.muon_orthogonalize(x)), k
+
+
+# ---------------------------------------------------------------- states
+def _grads(t, shapes, dtype=torch.float32):
+    return [_matrix(100 * t + k, s).to(dtype) for k, s in enumerate(shapes)]
+
+
+RUN = [(300, 520), (64, 64), (700, 300), (33, 7), (520, 300)]
+
+
+@pytest.mark.parametrize("storage,stochastic", [("f32", False), ("bf16", False), ("q8", False), ("q8", True)])
+def test_checkpoint_resumes_bit_for_bit(storage, stochastic):
+    hp = dict(lr=1e-2, stochastic=stochastic, seed=5)
+    state = ma.muon_state_create(RUN, storage)
+    params = [torch.randn(*s, generator=_gen(k), device="cuda") * 0.02 for k, s in enumerate(RUN)]
+    for t in (1, 2):
+        ma.muon_step(state, params, _grads(t, RUN), t=t, **hp)
+    ma.muon_state_set_draw_index(state, [16 * 10 ** 6 * (k + 1) for k in range(len(RUN))])
+    blob = ma.muon_state_save(state)
+    other = ma.muon_state_load(blob)
+    assert other.shapes == RUN and other.storage == storage
+    assert ma.muon_state_get_draw_index(other) == ma.muon_state_get_draw_index(state)
+    copies = [p.clone() for p in params]
+    for t in (3, 4):
+        ma.muon_step(state, params, _grads(t, RUN), t=t, **hp)
+        ma.muon_step(other, copies, _grads(t, RUN), t=t, **hp)
+    assert all(torch.equal(a, b) for a, b in zip(params, copies))
+    assert np.array_equal(ma.muon_state_save(state), ma.muon_state_save(other))
+    bad = blob.copy()
+    bad[-1] ^= 1
+    with pytest.raises(ma.AdamError, match="checksum"):
+        ma.muon_state_load(bad)
+
+
+def test_shards_of_whole_matrices_draw_the_same_stream():
+    params = [torch.zeros(s, device="cuda") for s in RUN]
+    whole = ma.muon_state_create(RUN, "q8")
+    parts = [ma.muon_state_create(RUN[:2], "q8"), ma.muon_state_create(RUN[2:], "q8")]
+    first = ma.muon_state_get_draw_index(whole)
+    ma.muon_state_set_draw_index(parts[1], first[2:])
+    copies = [p.clone() for p in params]
+    for t in (1, 2, 3):
+        g = _grads(t, RUN)
+        hp = dict(lr=1e-2, t=t, stochastic=True, seed=8)
+        ma.muon_step(whole, params, g, **hp)
+        ma.muon_step(parts[0], copies[:2], g[:2], **hp)
+        ma.muon_step(parts[1], copies[2:], g[2:], **hp)
+    got = ma.muon_state_momentum(parts[0]) + ma.muon_state_momentum(parts[1])
+    assert all(torch.equal(a, b) for a, b in zip(ma.muon_state_momentum(whole), got))
+    # tiles are chosen for the whole list: the params agree to the orthogonalisation's error
+    for a, b in zip(params, copies):
+        assert float((a - b).norm()) <= 2e-5 * float(a.norm())
+
+
+def test_training_run_of_matrices_with_muon_and_the_rest_with_adam():
+    # the two steps as a program uses them together: matrices and their biases,
+    # states of both, a checkpoint of both in the middle
+    biases = [s[0] for s in RUN]
+    ref = Reference(RUN, "q8")
+    W = [p.clone() for p in ref.params]
+    b = [torch.zeros(n, device="cuda") for n in biases]
+    b_ref = [np.zeros(n, np.float32) for n in biases]
+    muon, adam = ma.muon_state_create(RUN, "q8", "bf16"), ma.adam_state_create(biases, "q8")
+    adam_ref = oracle.OracleState(biases, "q8")
+    total = [0.0] * len(RUN)
+    adam_hp = dict(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0)
+    for t in range(1, 6):
+        gW = _grads(t, RUN, torch.bfloat16)
+        gb = workloads.host_grads(77, biases, t)
+        ma.muon_step(muon, W, gW, t=t, lr=2e-3, weight_decay=0.05, stochastic=True, seed=3)
+        ma.adam_step(adam, b, [torch.from_numpy(g).cuda() for g in gb], t=t, **adam_hp)
+        slack = ref.step(gW, t, lr=2e-3, momentum=0.95, weight_decay=0.05, nesterov=True, scale="rms", stochastic=True, seed=3)
+        adam_ref.step(b_ref, gb, t=t, **adam_hp)
+        if t == 3:
+            muon, adam = ma.muon_state_load(ma.muon_state_save(muon)), ma.adam_state_load(ma.adam_state_save(adam))
+        _compare_state(muon, ref)
+        for k in range(len(RUN)):
+            total[k] += slack[k]
+            assert float((W[k].double() - ref.exact[k]).norm()) <= total[k], (t, k)
+            assert np.allclose(b[k].cpu().numpy(), b_ref[k], rtol=1e-5, atol=1e-9)
+
+
+def test_groups_of_a_long_list():
+    # more elements than go through the products at a time: every matrix as alone
+    shapes = [(1024, 4096)] * 18 + [(40, 30), (4096, 1024)]
+    state = ma.muon_state_create(shapes, "f32")
+    one = _matrix(3, (1024, 4096))
+    grads = [one] * 18 + [_matrix(4, (40, 30)), one.T.contiguous()]
+    params = [torch.zeros(s, device="cuda") for s in shapes]
+    ma.muon_step(state, params, grads, t=1, lr=1.0, momentum=0.0, nesterov=False, scale="none")
+    want = -muon_ref.orthogonalize(one)
+    for k, p in enumerate(params):
+        if k == 18:
+            continue
+        got = p if k < 18 else p.T
+        assert float((got.double() - want).norm() / want.norm()) < 1e-5, k
+    _check(-params[18], grads[18])
+
+
+def test_state_padding_and_parameters_beyond_a_matrix_stay():
+    shapes = [(33, 65), (130, 257)]
+    state = ma.muon_state_create(shapes, "f32")
+    flat = torch.full((130 * 257 + 64,), 3.0, device="cuda")
+    params = [torch.zeros(33, 65, device="cuda"), flat[:130 * 257].view(130, 257)]
+    junk = ma.muon_state_read(state, "m_f32")
+    junk.fill_(float("nan"))
+    junk[:33 * 65] = 0.0
+    at = (33 * 65 + 15) // 16 * 16
+    junk[at:at + 130 * 257] = 0.0  # NaN in the padding alone
+    ma.muon_state_write(state, "m_f32", junk)
+    grads = _grads(1, shapes)
+    ma.muon_step(state, params, grads, t=1, lr=1e-3)
+    assert all(bool(p.isfinite().all()) for p in params) and bool((flat[130 * 257:] == 3.0).all())
+    m = ma.muon_state_read(state, "m_f32")
+    assert bool((m[33 * 65:at] == 0).all()) and bool((m[at + 130 * 257:] == 0).all())
+
+
+def test_zero_gradients_and_a_nonfinite_one():
+    shapes = [(100, 200), (50, 60), (300, 100)]
+    state = ma.muon_state_create(shapes, "q8")
+    params = [torch.randn(*s, generator=_gen(k), device="cuda") for k, s in enumerate(shapes)]
+    before = [p.clone() for p in params]
+    ma.muon_step(state, params, [torch.zeros(s, device="cuda") for s in shapes], t=1, lr=0.5, weight_decay=0.0)
+    assert all(torch.equal(a, b) for a, b in zip(params, before))
+    grads = _grads(2, shapes)
+    grads[1][3, 4] = float("inf")
+    ma.muon_step(state, params, grads, t=2, lr=1e-3)
+    assert bool(params[1].isnan().all())
+    assert bool(params[0].isfinite().all()) and bool(params[2].isfinite().all())
+
+
+def test_a_step_on_a_side_stream_and_pointer_changes():
+    shapes = [(96, 130), (400, 333)]
+    a, b = (ma.muon_state_create(shapes, "bf16") for _ in range(2))
+    pa = [torch.zeros(s, device="cuda") for s in shapes]
+    pb = [p.clone() for p in pa]
+    side = torch.cuda.Stream()
+    for t in range(1, 12):  # more gradient sets than resident tables
+        g = _grads(t, shapes)
+        side.wait_stream(torch.cuda.current_stream())
+        ma.muon_step(a, pa, g, t=t, lr=1e-3)
+        ma.muon_step(b, pb, g, t=t, lr=1e-3, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(pa, pb))
+    got = ma.muon_state_momentum(b, stream=side)
+    side.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(got, ma.muon_state_momentum(a)))
+
+
+def test_step_refusals():
+    shapes = [(16, 32), (40, 8)]
+    state = ma.muon_state_create(shapes, "bf16")
+    p, g = [torch.zeros(s, device="cuda") for s in shapes], _grads(1, shapes)
+    ok = dict(lr=1e-3, t=1)
+    for bad, what in ((dict(t=0), "t must"), (dict(lr=-1.0), "lr"), (dict(lr=float("nan")), "lr"), (dict(momentum=1.0), "momentum"),
+                      (dict(weight_decay=-0.1), "weight_decay"), (dict(scale=7), "scale"), (dict(steps=0), "steps"),
+                      (dict(steps=17), "steps"), (dict(eps=0.0), "eps"), (dict(coefficients=(1.0, 2.0, 100.0)), "coefficient"),
+                      (dict(stochastic=True), "8-bit")):
+        with pytest.raises(ma.AdamError, match=what) as e:
+            ma.muon_step(state, p, g, **{**ok, **bad})
+        assert e.value.code == -1
+    with pytest.raises(ma.AdamError) as e:
+        ma.muon_step(state, p, g, expect=("q8", "f32"), **ok)
+    assert e.value.code == -2
+    flat = torch.zeros(16 * 32 + 1, device="cuda")
+    with pytest.raises(ma.AdamError) as e:
+        ma.muon_step(state, [flat[1:].view(16, 32), p[1]], g, **ok)
+    assert e.value.code == -3
+    twice = ma.muon_state_create([(16, 32)] * 2, "bf16")
+    with pytest.raises(ma.AdamError, match="same param"):
+        ma.muon_step(twice, [p[0], p[0]], [g[0], g[0]], **ok)
+    assert all(bool((x == 0).all()) for x in p)  # nothing ran
+    with pytest.raises(ma.AdamError):
+        ma.muon_state_read(state, "m_codes")
+    with pytest.raises(ma.AdamError):
+        ma.muon_state_read(state, "v_codes")
+    with pytest.raises(ValueError, match="bytes"):
+        ma.muon_state_write(state, "m_bf16", torch.zeros(3, device="cuda"))
+
+
+def test_step_refuses_to_be_captured():
+    shapes = [(64, 64)]
+    state = ma.muon_state_create(shapes, "f32")
+    p, g = [torch.zeros(64, 64, device="cuda")], _grads(1, shapes)
+    x = torch.zeros(8, device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(ma.AdamError, match="capturing"):
+            ma.muon_step(state, p, g, t=1, lr=1e-3)
+        x.add_(1.0)
+    for k in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert bool((x == k + 1).all()) and bool((p[0] == 0).all())
+
+
+def test_workspace_of_the_caller():
+    x = _matrix(1, (300, 400))
+    need = ma.muon_orthogonalize_workspace_bytes(1, 300, 400)
+    with pytest.raises(ma.AdamError, match="needed"):
+        ma.muon_orthogonalize(x, workspace=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ma.AdamError, match="256"):
+        ma.muon_orthogonalize(x, workspace=torch.empty(need + 8, dtype=torch.uint8, device="cuda")[8:])
+    guard = torch.full((need + 4096,), 77, dtype=torch.uint8, device="cuda")
+    out = ma.muon_orthogonalize(x, workspace=guard[:need])  # junk in the workspace, and nothing written behind it
+    assert torch.equal(out, ma.muon_orthogonalize(x)) and bool((guard[need:] == 77).all())
