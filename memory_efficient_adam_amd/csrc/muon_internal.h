@@ -72,8 +72,9 @@ struct MuonArrays {
     char *square[kSquares];  // A = X X^T, the polynomials, their products
 };
 
-// How one factor is held: split or plain slabs.
-enum MuonForm : int { kSplit = 0, kPlain = 1 };
+// How a product's factors are held: in split or plain slabs, or (kMixed, an
+// update) the left one split and the right one plain.
+enum MuonForm : int { kSplit = 0, kPlain = 1, kMixed = 2 };
 
 // The 256 CUs take tiles in rounds; the tiles of a last round that would leave
 // many of them idle are split.
@@ -97,6 +98,7 @@ struct MuonPrepArgs {
     uint32_t pad;
     double eps;
     char *x, *xt;
+    float *phi;  // raw form: X_0 = phi (x as written)
 };
 
 struct MuonGemmArgs {
@@ -106,6 +108,7 @@ struct MuonGemmArgs {
     char *out2;
     const char *add;           // A (polynomial only)
     char *out, *out_t;         // images written (out_t: X^T)
+    const float *phi;          // what a raw X_0 is still to be multiplied by (else NULL)
     float ca, cb, cc;          // polynomial coefficients
     // last product: where O goes
     const TensorRef *tensors;  // params (step), by MuonMat::index
@@ -160,7 +163,9 @@ hipError_t launch_muon_momentum(int storage, bool grad_bf16, bool stochastic, co
 hipError_t launch_muon_norms(const double *partials, const uint2 *ranges, double *sums, uint32_t n_mats,
                              hipStream_t s);
 hipError_t launch_muon_sums(bool bf16, const MuonWork &w, const MuonSumArgs &a, uint32_t n_mats, hipStream_t s);
-hipError_t launch_muon_prep(bool bf16, int form, const MuonWork &w, const MuonPrepArgs &a, hipStream_t s);
+// raw: bf16 input times a power of two, exact in plain slabs, with the rest of
+// the scale in phi
+hipError_t launch_muon_prep(bool bf16, bool raw, int form, const MuonWork &w, const MuonPrepArgs &a, hipStream_t s);
 
 enum MuonProduct : int { kGram, kPolynomial, kCommuting, kUpdate, kLastBf16, kLastF32, kLastParams };
 // The tiles of the products (rows and columns of the result, waves): the

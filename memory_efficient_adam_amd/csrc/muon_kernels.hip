@@ -155,11 +155,11 @@ __device__ __forceinline__ void banded(uint32_t t, uint32_t mb, uint32_t nb, uin
 // elements, for k a multiple of 4 (four elements lie side by side); remainders
 // (split form) are 1 KB on.
 template <int kForm>
-constexpr uint32_t slab_length() { return kForm == kSplit ? 32u : 64u; }
+constexpr uint32_t slab_length() { return kForm == kPlain ? 64u : 32u; }
 template <int kForm>
 __device__ __forceinline__ uint64_t image_pos(uint32_t r, uint32_t k, uint32_t length) {
     constexpr uint32_t kPer = slab_length<kForm>();
-    const uint32_t fragment = ((k % kPer) >> 4) * (kForm == kSplit ? 2u : 1u);
+    const uint32_t fragment = ((k % kPer) >> 4) * (kForm == kPlain ? 1u : 2u);
     return ((uint64_t)(r >> 5) * (length / kPer) + k / kPer) * 4096u + fragment * 1024u +
            ((r & 31u) + (((k >> 3) & 1u) << 5)) * 16u + (k & 7u) * 2u;
 }
@@ -174,9 +174,12 @@ struct Tiling {
     static constexpr int kWaves = D * A, kThreads = 64 * kWaves;
     static constexpr int kI = R / D / 32, kJ = C / A / 32;         // a wave's 32 x 32 blocks
     static constexpr int kStage = (R + C) * 128;                   // bytes of a slab of both factors
-    static constexpr int kLoads = kStage / 1024 / kWaves;          // 1 KB pieces a wave fetches per slab
+    // bytes of a slab of the right factor to 32 rows (mixed: half a plain slab,
+    // as long as a split one), and the 1 KB pieces a wave fetches per slab
+    static constexpr int right_bytes(int form) { return form == kMixed ? 2048 : 4096; }
+    static constexpr int loads(int form) { return (R / 32 * 4096 + C / 32 * right_bytes(form)) / 1024 / kWaves; }
     static constexpr int kPerSimd = W;                             // waves per SIMD it is compiled for
-    static_assert(kStage % (1024 * kWaves) == 0, "every wave fetches as much");
+    static_assert((R * 128 + C * 64) % (1024 * kWaves) == 0 && C * 64 % (1024 * kWaves) == 0, "every wave fetches as much");
 };
 
 // 16 bytes per lane from memory straight to LDS: lane i's go to base + 16 i.
@@ -194,49 +197,54 @@ __device__ __forceinline__ void wait_and_meet() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"i"(kLeft) : "memory");
 }
 
-template <class T>
+template <class T, int kForm>
 struct Sources {
-    const char *at[T::kLoads];  // this wave's pieces of the next slab
+    const char *at[T::loads(kForm)];  // this wave's pieces of the next slab
+    uint32_t step[T::loads(kForm)];   // to those of the slab after it
 };
+
+template <class T, int kForm>
+__device__ __forceinline__ void fetch(Sources<T, kForm> &src, char *stage, int wave, int lane) {
+#pragma unroll
+    for (int i = 0; i < T::loads(kForm); ++i) {
+        dma16(src.at[i] + lane * 16, stage + (wave * T::loads(kForm) + i) * 1024);
+        src.at[i] += src.step[i];
+    }
+}
 
 // rd and wr are different stages of LDS: without that promise the compiler
 // would wait for the fetches before every read.
 template <class T, int kForm>
 __device__ __forceinline__ void slab(f32x16 (&acc)[T::kI][T::kJ], const char *__restrict rd, char *__restrict wr,
-                                     Sources<T> &src, bool fetch, int wave, int lane) {
-    constexpr int kSteps = kForm == kSplit ? 2 : 4;
-    if (fetch) {
-#pragma unroll
-        for (int i = 0; i < T::kLoads; ++i) {
-            dma16(src.at[i] + lane * 16, wr + (wave * T::kLoads + i) * 1024);
-            src.at[i] += 4096;
-        }
-    }
+                                     Sources<T, kForm> &src, bool more, int wave, int lane) {
+    constexpr int kSteps = kForm == kPlain ? 4 : 2;
+    constexpr int kRight = T::right_bytes(kForm);
+    if (more) fetch<T, kForm>(src, wr, wave, lane);
     const char *left = rd + (wave / T::kAcross) * (T::kI * 4096) + lane * 16;
-    const char *right = rd + T::kRows * 128 + (wave % T::kAcross) * (T::kJ * 4096) + lane * 16;
+    const char *right = rd + T::kRows * 128 + (wave % T::kAcross) * (T::kJ * kRight) + lane * 16;
 #pragma unroll
     for (int k = 0; k < kSteps; ++k) {
         half8 l[T::kI], r[T::kJ], l2[T::kI], r2[T::kJ];
-        const int at = k * (kForm == kSplit ? 2048 : 1024);
+        const int at = k * (kForm == kPlain ? 1024 : 2048), at_r = k * (kForm == kSplit ? 2048 : 1024);
 #pragma unroll
         for (int i = 0; i < T::kI; ++i) {
             l[i] = *reinterpret_cast<const half8 *>(left + i * 4096 + at);
-            if constexpr (kForm == kSplit) l2[i] = *reinterpret_cast<const half8 *>(left + i * 4096 + at + kRemainder);
+            if constexpr (kForm != kPlain) l2[i] = *reinterpret_cast<const half8 *>(left + i * 4096 + at + kRemainder);
         }
 #pragma unroll
         for (int j = 0; j < T::kJ; ++j) {
-            r[j] = *reinterpret_cast<const half8 *>(right + j * 4096 + at);
-            if constexpr (kForm == kSplit) r2[j] = *reinterpret_cast<const half8 *>(right + j * 4096 + at + kRemainder);
+            r[j] = *reinterpret_cast<const half8 *>(right + j * kRight + at_r);
+            if constexpr (kForm == kSplit) r2[j] = *reinterpret_cast<const half8 *>(right + j * kRight + at_r + kRemainder);
         }
 #pragma unroll
         for (int i = 0; i < T::kI; ++i)
 #pragma unroll
             for (int j = 0; j < T::kJ; ++j) {
                 acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(l[i], r[j], acc[i][j], 0, 0, 0);
-                if constexpr (kForm == kSplit) {
+                if constexpr (kForm == kSplit)
                     acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(l[i], r2[j], acc[i][j], 0, 0, 0);
+                if constexpr (kForm != kPlain)
                     acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(l2[i], r[j], acc[i][j], 0, 0, 0);
-                }
             }
     }
 }
@@ -256,21 +264,20 @@ __device__ __forceinline__ void product(f32x16 (&sum)[T::kI][T::kJ], const char 
     constexpr int kS = T::kStages;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    Sources<T> src;
+    Sources<T, kForm> src;
 #pragma unroll
-    for (int i = 0; i < T::kLoads; ++i) {
-        const uint32_t piece = wave * T::kLoads + i, block = piece >> 2;
-        src.at[i] = (block < T::kRows / 32 ? left + block * left_block : right + (block - T::kRows / 32) * right_block) +
-                    (piece & 3u) * 1024u;
+    for (int i = 0; i < T::loads(kForm); ++i) {
+        // pieces: the left factor's, 4 to 32 rows, then the right one's, 4 or 2
+        constexpr uint32_t kLeft = T::kRows / 8, kTo = T::right_bytes(kForm) / 1024;
+        const uint32_t piece = wave * T::loads(kForm) + i, q = piece - kLeft;
+        const bool is_left = piece < kLeft;
+        src.at[i] = is_left ? left + (piece / 4u) * left_block + (piece % 4u) * 1024u
+                            : right + (q / kTo) * right_block + (q % kTo) * 1024u;
+        src.step[i] = is_left ? 4096u : (uint32_t)T::right_bytes(kForm);
     }
 #pragma unroll
     for (int s = 0; s < kS - 1; ++s)
-        if (s < (int)slabs)
-#pragma unroll
-            for (int i = 0; i < T::kLoads; ++i) {
-                dma16(src.at[i] + lane * 16, lds + s * T::kStage + (wave * T::kLoads + i) * 1024);
-                src.at[i] += 4096;
-            }
+        if (s < (int)slabs) fetch<T, kForm>(src, lds + s * T::kStage, wave, lane);
     f32x16 acc[T::kI][T::kJ];
 #pragma unroll
     for (int i = 0; i < T::kI; ++i)
@@ -281,7 +288,7 @@ __device__ __forceinline__ void product(f32x16 (&sum)[T::kI][T::kJ], const char 
         for (int u = 0; u < kS; ++u) {
             const uint32_t s = s0 + u;
             if (s >= slabs) break;
-            if (s + (kS - 2) < slabs) wait_and_meet<(kS - 2) * T::kLoads>();
+            if (s + (kS - 2) < slabs) wait_and_meet<(kS - 2) * T::loads(kForm)>();
             else wait_and_meet<0>();
             slab<T, kForm>(acc, lds + u * T::kStage, lds + ((u + kS - 1) % kS) * T::kStage, src, s + (kS - 1) < slabs, wave,
                            lane);
@@ -434,7 +441,9 @@ void muon_product_kernel(MuonGemmArgs a) {
         banded(t, m.mp / down, m.np / across, ti, tj);
     }
     const uint32_t k = kProduct == kGram ? m.np : m.mp;  // length of the products
-    const uint64_t block = (uint64_t)(k / slab_length<kIn>()) * 4096u;  // bytes of 32 rows of either factor
+    // bytes of 32 rows of either factor
+    const uint64_t block = (uint64_t)(k / slab_length<kIn>()) * 4096u;
+    const uint64_t right_block = kIn == kMixed ? (uint64_t)(k / 64u) * 4096u : block;
     const char *left, *right;
     uint32_t row0, col0;  // of the result
     if constexpr (kSquare) {
@@ -453,12 +462,14 @@ void muon_product_kernel(MuonGemmArgs a) {
         row0 = (swap ? tj : ti) * T::kRows;
         col0 = (swap ? ti : tj) * T::kCols;
         const char *p = a.left + m.a_off, *x = a.right + m.x_off;
+        static_assert(kIn != kMixed || kProduct == kUpdate, "no exchange of mixed factors");
         left = (swap ? x : p) + (row0 >> 5) * block;
-        right = (swap ? p : x) + (col0 >> 5) * block;
+        right = (swap ? p : x) + (col0 >> 5) * right_block;
     }
     const uint32_t slabs = k / slab_length<kIn>(), first = slabs * part / parts, last = slabs * (part + 1) / parts;
     f32x16 acc[T::kI][T::kJ];
-    product<T, kIn>(acc, left + (uint64_t)first * 4096u, block, right + (uint64_t)first * 4096u, block, last - first, lds);
+    product<T, kIn>(acc, left + (uint64_t)first * 4096u, block,
+                    right + (uint64_t)first * (uint32_t)T::right_bytes(kIn), right_block, last - first, lds);
 
     const uint32_t lane = threadIdx.x & 63u;
     const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
@@ -468,6 +479,8 @@ void muon_product_kernel(MuonGemmArgs a) {
     }
     row0 += (wave / T::kAcross) * (T::kI * 32);
     col0 += (wave % T::kAcross) * (T::kJ * 32);
+    // a raw X_0's factor is made up for here: once in an update, twice in X X^T
+    const float phi = (kProduct == kGram || kProduct == kUpdate) && a.phi ? a.phi[m.index] : 1.0f;
     float *param = nullptr;
     float step = 0.0f;
     if constexpr (kProduct == kLastParams) {
@@ -484,7 +497,7 @@ void muon_product_kernel(MuonGemmArgs a) {
             if constexpr (kSquare) {
                 char *out = (second ? a.out2 : a.out) + m.a_off;
                 if constexpr (kProduct == kGram) {
-                    v *= 1.0f / kScaleX;
+                    v *= phi * phi * (1.0f / kScaleX);
                 } else if constexpr (kProduct == kCommuting) {
                     v *= 1.0f / kScaleP;
                 } else {
@@ -511,7 +524,7 @@ void muon_product_kernel(MuonGemmArgs a) {
                 store_block<kOut, true>(v, out, r0, c0, m.mp, lane);
                 if (ti != tj) store_block<kOut, false>(v, out, r0, c0, m.mp, lane);
             } else if constexpr (kProduct == kUpdate) {
-                v *= 1.0f / kScaleP;
+                v *= phi * (1.0f / kScaleP);
                 store_block<kOut, false>(v, a.out + m.x_off, r0, c0, m.np, lane);
                 store_block<kOut, true>(v, a.out_t + m.x_off, r0, c0, m.mp, lane);
             } else {
@@ -832,7 +845,7 @@ __global__ __launch_bounds__(256) void muon_sums_kernel(MuonWork w, MuonSumArgs 
 
 // The images of X_0 and X_0^T, one 64 x 64 tile of the user's matrix a
 // workgroup.  A norm that is not finite makes all of X_0 NaN.
-template <bool kBf16, int kForm>
+template <bool kBf16, bool kRaw, int kForm>
 __global__ __launch_bounds__(256) void muon_prep_kernel(MuonWork w, MuonPrepArgs a) {
     __shared__ double s[4];
     __shared__ float y[64][65];
@@ -861,7 +874,14 @@ __global__ __launch_bounds__(256) void muon_prep_kernel(MuonWork w, MuonPrepArgs
     double part = 0.0;
     for (uint32_t i = threadIdx.x; i < a.n_partials; i += 256u) part += a.partials[m.norm + i];
     const double sum = block_sum(part, s);
-    const double inv = sum < __builtin_inf() ? (double)kScaleX / (sqrt(sum) + a.eps) : __builtin_nan("");
+    double inv = sum < __builtin_inf() ? (double)kScaleX / (sqrt(sum) + a.eps) : __builtin_nan("");
+    if constexpr (kRaw) {
+        // the power of two that brings the norm (and so every entry) to below
+        // 2^14: bf16's 8 bits are exact in fp16 down to 2^-27 of the norm
+        const double power = sum > 0.0 ? ldexp(1.0, 13 - ilogb(sqrt(sum))) : 1.0;
+        if (t == 0 && threadIdx.x == 0) a.phi[m.index] = sum > 0.0 ? (float)(inv / power) : 0.0f;
+        inv = sum < __builtin_inf() ? power : inv;
+    }
 #pragma unroll
     for (uint32_t i = 0; i < 16u; ++i) {
         const bool in = ti * 64u + r_in + 4u * i < m.rows && c < m.cols;
@@ -1107,14 +1127,17 @@ hipError_t launch_muon_sums(bool bf16, const MuonWork &w, const MuonSumArgs &a, 
     return hipGetLastError();
 }
 
-hipError_t launch_muon_prep(bool bf16, int form, const MuonWork &w, const MuonPrepArgs &a, hipStream_t s) {
+hipError_t launch_muon_prep(bool bf16, bool raw, int form, const MuonWork &w, const MuonPrepArgs &a, hipStream_t s) {
     const dim3 grid(w.n_tiles), block(256);
-    if (form == kSplit) {
-        if (bf16) muon_prep_kernel<true, kSplit><<<grid, block, 0, s>>>(w, a);
-        else muon_prep_kernel<false, kSplit><<<grid, block, 0, s>>>(w, a);
+    if (raw) {
+        if (!bf16 || form != kPlain) return hipErrorInvalidValue;
+        muon_prep_kernel<true, true, kPlain><<<grid, block, 0, s>>>(w, a);
+    } else if (form == kSplit) {
+        if (bf16) muon_prep_kernel<true, false, kSplit><<<grid, block, 0, s>>>(w, a);
+        else muon_prep_kernel<false, false, kSplit><<<grid, block, 0, s>>>(w, a);
     } else {
-        if (bf16) muon_prep_kernel<true, kPlain><<<grid, block, 0, s>>>(w, a);
-        else muon_prep_kernel<false, kPlain><<<grid, block, 0, s>>>(w, a);
+        if (bf16) muon_prep_kernel<true, false, kPlain><<<grid, block, 0, s>>>(w, a);
+        else muon_prep_kernel<false, false, kPlain><<<grid, block, 0, s>>>(w, a);
     }
     return hipGetLastError();
 }
@@ -1133,6 +1156,9 @@ static hipError_t product_of(int product, int in, int out, const MuonGemmArgs &a
     MUON_CASE(kCommuting, kSplit, kSplit)
     MUON_CASE(kUpdate, kSplit, kSplit)
     MUON_CASE(kUpdate, kSplit, kPlain)
+    MUON_CASE(kGram, kPlain, kSplit)
+    MUON_CASE(kUpdate, kMixed, kSplit)
+    MUON_CASE(kUpdate, kMixed, kPlain)
     MUON_CASE(kGram, kPlain, kPlain)
     MUON_CASE(kPolynomial, kPlain, kPlain)
     MUON_CASE(kUpdate, kPlain, kPlain)

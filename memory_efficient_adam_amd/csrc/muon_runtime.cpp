@@ -114,7 +114,7 @@ struct Load {
     }
     // plain slabs hold twice the elements
     Cut cut(int tiling, int64_t n_tiles, int64_t jobs, int form) const {
-        const double per = form == kSplit ? 1.0 : 2.0;
+        const double per = form == kPlain ? 2.0 : 1.0;
         return cut_tiles(tiling, n_tiles, jobs, slabs[tiling] / (double)std::max<int64_t>(1, tiles[tiling]) / per,
                          least / (int64_t)per);
     }
@@ -221,6 +221,7 @@ struct Workspace {
     uint32_t *arrived;  // split tiles: counters and parts
     float *parts;
     double *partials, *sums;
+    float *phi;
 };
 
 Workspace carve(char *base, const Work &size, int64_t x_bytes, int64_t a_bytes, int64_t n_partials) {
@@ -238,7 +239,8 @@ Workspace carve(char *base, const Work &size, int64_t x_bytes, int64_t a_bytes, 
     w.arrived = reinterpret_cast<uint32_t *>(take(4 * kMaxSplit));
     w.parts = reinterpret_cast<float *>(take(kMaxPartials * size.part_bytes()));
     w.partials = reinterpret_cast<double *>(take(8 * n_partials));
-    w.sums = reinterpret_cast<double *>(base);
+    w.sums = reinterpret_cast<double *>(base);  // step
+    w.phi = reinterpret_cast<float *>(base);    // orthogonalisation
     return w;
 }
 
@@ -389,8 +391,17 @@ std::vector<Run> runs_of(const muon_iteration &it, const int *forms, const Work 
     return runs;
 }
 
+// Whether a bf16 X_0 can be taken as it is: factors are split at first, and the
+// first run ends before the last iteration.
+bool raw_start(const muon_iteration &it, const int *forms, const Work &size) {
+    return forms[0] == kSplit && runs_of(it, forms, size)[0].length < it.steps;
+}
+
 // The products of all iterations, X_0 and X_0^T being in f.x[0], f.xt[0].
-hipError_t run_products(const Workspace &w, const MuonWork &square, const MuonWork &update, const Work &size,
+// raw: they are bf16 values times a power of two in plain slabs, and w.phi times
+// them is X_0: their own products need one partial product for three, and P X
+// two, in the first run, which is not the last (raw_start).
+hipError_t run_products(const Workspace &w, const MuonWork &square, const MuonWork &update, const Work &size, bool raw,
                         const muon_iteration &it, const int *forms, int last, const MuonGemmArgs &into, hipStream_t s) {
     hipError_t e = hipSuccess;
     int form = kSplit;
@@ -401,12 +412,13 @@ hipError_t run_products(const Workspace &w, const MuonWork &square, const MuonWo
         const int tiling = is_square ? size.square_tiling : size.update_tiling;
         const Load &load = product == kGram ? size.gram : (is_square ? size.square : size.update);
         g.work = is_square ? square : update;
-        const Cut cut = load.cut(tiling, g.work.n_tiles, g.left2 ? 2 : 1, form);
+        const int in = g.phi ? (product == kGram ? kPlain : kMixed) : form;
+        const Cut cut = load.cut(tiling, g.work.n_tiles, g.left2 ? 2 : 1, in);
         g.work.n_whole = cut.whole;
         g.work.parts = cut.parts;
         g.work.partial = w.parts;
         g.work.arrived = w.arrived;
-        e = launch_muon_product(tiling, product, form, out, g, s);
+        e = launch_muon_product(tiling, product, in, out, g, s);
     };
     auto polynomial = [&](const char *a, char *p, int k) {
         float c[3];
@@ -435,9 +447,11 @@ hipError_t run_products(const Workspace &w, const MuonWork &square, const MuonWo
     int cur = 0;
     for (const Run &run : runs_of(it, forms, size)) {
         form = forms[run.first];
+        const float *phi = raw && run.first == 0 ? w.phi : nullptr;
         MuonGemmArgs g{};
         g.left = f.x[cur];
         g.out = A;
+        g.phi = phi;
         launch(kGram, form, g);
         polynomial(A, P, run.first);
         const char *q = P;
@@ -463,6 +477,7 @@ hipError_t run_products(const Workspace &w, const MuonWork &square, const MuonWo
         if (next < it.steps) {
             g.out = f.x[cur ^ 1];
             g.out_t = f.xt[cur ^ 1];
+            g.phi = phi;
             launch(kUpdate, forms[next], g);
             cur ^= 1;
         } else {
@@ -892,11 +907,11 @@ int muon_step(muon_state *s, float *const *params, const void *const *grads, con
             p.eps = (double)hp->iteration.eps;
             p.x = w.f.x[0];
             p.xt = w.f.xt[0];
-            if ((e = launch_muon_prep(false, forms[0], table_work(g, g.d_prep, g.prep.size()), p, stream)) !=
+            if ((e = launch_muon_prep(false, false, forms[0], table_work(g, g.d_prep, g.prep.size()), p, stream)) !=
                 hipSuccess)
                 return hip_fail(e, "preparation launch");
             if ((e = run_products(w, table_work(g, g.d_square, g.square.size()),
-                                  table_work(g, g.d_update, g.update.size()), g.size, hp->iteration, forms, kLastParams, into,
+                                  table_work(g, g.d_update, g.update.size()), g.size, false, hp->iteration, forms, kLastParams, into,
                                   stream)) != hipSuccess)
                 return hip_fail(e, "product launch");
         }
@@ -1175,7 +1190,7 @@ BatchPlan plan_batch(int64_t batch, const Shape &s) {
     p.x_bytes = 4 * p.mp * p.np;
     p.a_bytes = 4 * p.mp * p.mp;
     p.n_partials = std::min(kMaxSums, tiles_of(s, 64));
-    p.bytes = workspace_bytes(p.size, p.x_bytes * p.chunk, p.a_bytes * p.chunk, p.n_partials * p.chunk);
+    p.bytes = workspace_bytes(p.size, p.x_bytes * p.chunk, p.a_bytes * p.chunk, p.n_partials * p.chunk) + align256(4 * p.chunk);
     return p;
 }
 
@@ -1279,7 +1294,9 @@ int muon_orthogonalize(const muon_matrices *mats, const void *x, void *out, cons
             prep.eps = (double)iteration->eps;
             prep.x = w.f.x[0];
             prep.xt = w.f.xt[0];
-            if ((e = launch_muon_prep(xe == 2, forms[0], with((p.mp / 64) * (p.np / 64)), prep, stream)) != hipSuccess)
+            prep.phi = w.phi;
+            const bool raw = xe == 2 && raw_start(*iteration, forms, p.size);
+            if ((e = launch_muon_prep(xe == 2, raw, raw ? kPlain : forms[0], with((p.mp / 64) * (p.np / 64)), prep, stream)) != hipSuccess)
                 return hip_fail(e, "preparation launch");
             MuonGemmArgs into{};
             into.o = out;
@@ -1293,7 +1310,7 @@ int muon_orthogonalize(const muon_matrices *mats, const void *x, void *out, cons
             }
             const int64_t sb = p.mp / size_of(size.square_tiling), ub = p.mp / size_of(size.update_tiling),
                           lb = p.np / size_of(size.update_tiling);
-            if ((e = run_products(w, with(sb * (sb + 1) / 2), with(ub * lb), size, *iteration, forms,
+            if ((e = run_products(w, with(sb * (sb + 1) / 2), with(ub * lb), size, raw, *iteration, forms,
                                   oe == 2 ? kLastBf16 : kLastF32, into, stream)) != hipSuccess)
                 return hip_fail(e, "product launch");
         }
