@@ -104,8 +104,6 @@ __device__ __forceinline__ uint32_t xcd_order(uint32_t id, uint32_t n) {
     return xcd * per + min(xcd, rest) + (id >> 3);
 }
 
-typedef const __attribute__((address_space(4))) MuonMat *ConstMatPtr;
-typedef const __attribute__((address_space(4))) MuonTile *ConstTilePtr;
 typedef const __attribute__((address_space(4))) BlockDesc *ConstDescPtr;
 typedef const __attribute__((address_space(4))) TensorRef *ConstTensorPtr;
 typedef const __attribute__((address_space(4))) uint64_t *ConstU64Ptr;
@@ -115,10 +113,14 @@ typedef const __attribute__((address_space(4))) uint64_t *ConstU64Ptr;
 __device__ __forceinline__ MuonMat find_mat(const MuonWork &w, uint32_t id, uint32_t &t) {
     MuonMat m;
     if (w.tiles) {
-        const ConstTilePtr e = (ConstTilePtr)w.tiles + id;
-        const ConstMatPtr p = (ConstMatPtr)w.mats + e->mat;
-        t = (uint32_t)e->ti | ((uint32_t)e->tj << 16);
-        __builtin_memcpy(&m, (const void *)p, sizeof(m));
+        // (word by word through the constant address space: scalar loads)
+        const uint64_t e = ((ConstU64Ptr)w.tiles)[id];
+        const ConstU64Ptr p = (ConstU64Ptr)w.mats + (uint32_t)e * (uint32_t)(sizeof(MuonMat) / 8);
+        t = (uint32_t)(e >> 32);
+        uint64_t words[sizeof(MuonMat) / 8];
+#pragma unroll
+        for (uint32_t i = 0; i < sizeof(MuonMat) / 8; ++i) words[i] = p[i];
+        __builtin_memcpy(&m, words, sizeof(m));
     } else {
         const uint32_t k = id / w.per_mat;
         t = id - k * w.per_mat;
@@ -321,25 +323,41 @@ __device__ __forceinline__ u32x2 quad_transpose(u32x2 d, uint32_t lane) {
     return (lane & 2u) ? u32x2{m1, e1} : u32x2{e0, m0};
 }
 
+// A store that goes on to memory at once instead of staying in the XCD's L2,
+// to be written back when the kernel ends: the factors are read next by
+// other XCDs (eight matrices of 500 x 600: 215 -> 201 us).
+__device__ __forceinline__ void store_through(char *at, u32x2 v) {
+    __hip_atomic_store(reinterpret_cast<uint64_t *>(at), __builtin_bit_cast(uint64_t, v), __ATOMIC_RELAXED,
+                       __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// Where in a block's piece of an image the four values 4 g .. 4 g + 3 of a
+// lane go, from the place of g = 0: along the rows (values of a column are
+// elements of the transposed image) or, after quad_transpose, down them.
+template <int kForm>
+constexpr uint32_t along(int g) { return (uint32_t)(g >> 1) * (kForm == kSplit ? 2048u : 1024u) + (uint32_t)(g & 1) * 512u; }
+constexpr uint32_t down(int g) { return (uint32_t)g * 128u; }
+
 // A 32 x 32 block of values, at rows r0.. and columns c0.., into an image whose
-// rows hold `length` elements: as it is, or (kTransposed) with rows and columns exchanged.
-template <int kForm, bool kTransposed>
-__device__ __forceinline__ void store_block(const f32x16 &v, char *image, uint32_t r0, uint32_t c0, uint32_t length, uint32_t lane) {
+// rows hold `length` elements and, transposed, into one with `length_t` (either may be NULL).
+template <int kForm>
+__device__ __forceinline__ void store_block(const f32x16 &v, char *image, uint32_t length, char *transposed, uint32_t length_t,
+                                            uint32_t r0, uint32_t c0, uint32_t lane) {
     const uint32_t r = r0 + 4u * (lane >> 5), c = c0 + (lane & 31u);
+    char *const at = image + image_pos<kForm>(r + (lane & 3u), c & ~3u, length);
+    char *const at_t = transposed + image_pos<kForm>(c, r, length_t);
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
         u32x2 h, l;
         split4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3], h, l);
-        char *at;
-        if constexpr (kTransposed) {
-            at = image + image_pos<kForm>(c, r + 8u * g, length);
-        } else {
-            h = quad_transpose(h, lane);
-            l = quad_transpose(l, lane);
-            at = image + image_pos<kForm>(r + 8u * g + (lane & 3u), c & ~3u, length);
+        if (transposed) {
+            store_through(at_t + along<kForm>(g), h);
+            if constexpr (kForm == kSplit) store_through(at_t + along<kForm>(g) + kRemainder, l);
         }
-        *reinterpret_cast<u32x2 *>(at) = h;
-        if constexpr (kForm == kSplit) *reinterpret_cast<u32x2 *>(at + kRemainder) = l;
+        if (image) {
+            store_through(at + down(g), quad_transpose(h, lane));
+            if constexpr (kForm == kSplit) store_through(at + down(g) + kRemainder, quad_transpose(l, lane));
+        }
     }
 }
 
@@ -504,9 +522,10 @@ void muon_product_kernel(MuonGemmArgs a) {
                     // A's block, read from its mirror image: four values down a column lie side by side
                     const float cb = a.cb * (kScaleP / kScaleX), cc = a.cc * (kScaleP / (kScaleX * kScaleX));
                     const float ca = a.ca * kScaleP;
+                    const char *const base = a.add + m.a_off + image_pos<kIn>(c, r, m.mp);
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
-                        const char *at = a.add + m.a_off + image_pos<kIn>(c, r + 8u * g, m.mp);
+                        const char *at = base + along<kIn>(g);
                         const u32x2 h = *reinterpret_cast<const u32x2 *>(at);
                         u32x2 l = {0u, 0u};
                         if constexpr (kIn == kSplit) l = *reinterpret_cast<const u32x2 *>(at + kRemainder);
@@ -521,12 +540,10 @@ void muon_product_kernel(MuonGemmArgs a) {
                         }
                     }
                 }
-                store_block<kOut, true>(v, out, r0, c0, m.mp, lane);
-                if (ti != tj) store_block<kOut, false>(v, out, r0, c0, m.mp, lane);
+                store_block<kOut>(v, ti != tj ? out : nullptr, m.mp, out, m.mp, r0, c0, lane);
             } else if constexpr (kProduct == kUpdate) {
                 v *= phi * (1.0f / kScaleP);
-                store_block<kOut, false>(v, a.out + m.x_off, r0, c0, m.np, lane);
-                store_block<kOut, true>(v, a.out_t + m.x_off, r0, c0, m.mp, lane);
+                store_block<kOut>(v, a.out + m.x_off, m.np, a.out_t + m.x_off, m.mp, r0, c0, lane);
             } else {
                 constexpr float kUnscale = 1.0f / (kScaleX * kScaleP);
                 float old[16];
