@@ -26,11 +26,15 @@
  * on the fp16 matrix units with fp32 sums: each factor is held as two fp16
  * values (high part and remainder, 22 bits; X and A scaled by 2^10, the
  * polynomial by 2^8) and three of the four partial products are summed, so
- * that O agrees with a computation in fp32 to fp32's own error.
+ * that O is about as far from the exact result as a computation in fp32 is
+ * (at most some four times as far, where that one loses almost nothing).
+ * Iterations of larger matrices may be taken two or three at a time, as one
+ * polynomial in the first one's A.
  * muon_orthogonalize to a bf16 output may hold the factors of the last
- * iterations (of larger matrices) in one fp16 value each: those from the first k on for which the
- * product of |a_k|, .., |a_steps| is at most 12 (by which their rounding,
- * 2^-12, can still grow), which keeps the error well below bf16's rounding.
+ * iterations (of larger matrices) in one fp16 value each: those from the first
+ * k on for which the product of |a_k|, .., |a_steps| is at most 12 (by which
+ * their rounding, 2^-12, can still grow), which keeps the error well below
+ * bf16's rounding.  bf16 input is taken exactly.
  * A matrix whose u is all zero gives O = 0; one with a NaN or an infinity
  * gives NaN in all of O (and in the params; the stored momentum of that
  * matrix is then unspecified).  Other matrices of the call are not affected.
@@ -105,9 +109,9 @@ typedef struct {
  *   for BF16, (1, 4) for Q8.
  * muon_state_workspace_bytes: the device workspace that a state of this list
  * holds beside it (the factors of the products, for a part of the list at a
- * time: 16 bytes per element of the largest part and 8 per element of its
+ * time: 16 bytes per element of the largest part and 20 per element of its
  * square factors, dimensions rounded up to tiles, and up to 64 MB for the
- *   parts of split products).
+ * parts of split products).
  * Pure host functions.  Return < 0 (an adam_status) on bad arguments:
  * n_tensors < 0, rows or cols NULL with n_tensors > 0, a dimension < 0 or
  * >= 2^21, rows*cols >= 2^32, layout NULL or invalid.
@@ -152,7 +156,8 @@ int muon_step(muon_state *s, float *const *params, const void *const *grads, con
  * to 16 entries (padding 0), in device memory dst, 16-byte aligned: float
  * for F32 and Q8 storage (codes times their scale), bf16 for BF16; nbytes
  * must be exactly that size.  Asynchronous on hip_stream.
- * Errors: EINVAL, EALIGN, EDEVICE.
+ * Errors: EINVAL (for muon_state_momentum also a call from a device other than
+ * the state's), EALIGN, EDEVICE.
  */
 int64_t muon_state_buffer_bytes(const muon_state *s, int32_t which);
 int muon_state_read(muon_state *s, int32_t which, void *dst, int64_t nbytes, void *hip_stream);
@@ -192,8 +197,8 @@ void muon_state_destroy(muon_state *s);
  *     with the same strides and type.
  *   workspace: device memory, 256-byte aligned, of at least
  *     muon_orthogonalize_workspace_bytes(batch, rows, cols), which may be 0
- *     (then NULL will do); written by the call.  Calls that share one must be ordered on the device; so must the
- *     replays of graphs that recorded one.
+ *     (then NULL will do); written by the call.  Calls that share one must be
+ *     ordered on the device; so must the replays of graphs that recorded one.
  * Errors (no work enqueued): EINVAL (NULL pointer with a non-empty batch, a
  * dimension < 0 or >= 2^21, rows*cols >= 2^32, batch >= 2^31, a stride
  * outside its domain, unknown dtype, an iteration outside its domain,

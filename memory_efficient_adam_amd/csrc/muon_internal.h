@@ -46,8 +46,8 @@ struct MuonTile {
 static_assert(sizeof(MuonTile) == 8, "tile descriptor is one 8-byte load");
 
 // Which matrices and tiles a launch covers: a table (tiles != NULL), or
-// `count` matrices alike, whose descriptors are `one` advanced by the
-// strides, with per_mat tiles each.
+// matrices alike, whose descriptors are `one` advanced by the strides, with
+// per_mat of the n_tiles tiles each.
 struct MuonWork {
     const MuonTile *tiles;
     const MuonMat *mats;
@@ -62,7 +62,6 @@ struct MuonWork {
     MuonMat one;
     uint64_t x_stride, a_stride, u_stride, o_stride;
     uint32_t norm_stride;
-    uint32_t pad;
 };
 
 // The factor arrays of one group of matrices.
@@ -95,7 +94,6 @@ struct MuonPrepArgs {
     const void *u;
     const double *partials;
     uint32_t n_partials;
-    uint32_t pad;
     double eps;
     char *x, *xt;
     float *phi;  // raw form: X_0 = phi (x as written)
@@ -121,6 +119,7 @@ struct MuonGemmArgs {
 // Whole orthogonalisations of matrices whose short side is at most kSmallShort
 // and long side at most kSmallLong, one workgroup a matrix.
 constexpr int64_t kSmallShort = 64, kSmallLong = 768;
+constexpr int64_t kSmallBatch = int64_t(1) << 22;  // matrices of a launch: it has less than 2^32 threads
 constexpr int kMaxIterations = 16;
 
 struct MuonSmallArgs {

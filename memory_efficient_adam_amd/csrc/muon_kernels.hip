@@ -252,8 +252,8 @@ __device__ __forceinline__ void slab(f32x16 (&acc)[T::kI][T::kJ], const char *__
 }
 
 // sum = left right^T over `slabs` slabs (left, right: the tile's first slab;
-// *_block: bytes from one 32-row block to the next), summed in runs of at
-// least kRun slabs: one sum that took every term of a long row in turn would
+// *_block: bytes from one 32-row block to the next), summed in runs of some
+// kRun slabs: one sum that took every term of a long row in turn would
 // lose more to fp32's rounding than the split factors do.  kStages - 1 slabs
 // are under way to LDS while the matrix cores work on one; at the barrier
 // before slab s, its fetches are done and every wave has read slab s - 1,
@@ -570,8 +570,8 @@ void muon_product_kernel(MuonGemmArgs a) {
 
 // ---------------------------------------------------------------- small matrices
 // A whole orthogonalisation in one workgroup of 8 waves, X staying in
-// registers.  (15 launches of the products take 70 us for a matrix of a few
-// KB; this takes one launch.)
+// registers, in one launch: 23 us for a bf16 matrix of 64 x 64 (one launch per
+// product, 69), 79 us for 96 of 64 x 768 (250).
 //
 // A wave holds blocks of 32 columns of X, block w + 8 b at wave w, as the
 // matrix cores give them: lane l holds column l % 32, rows 8 g + 4 (l / 32) + q
@@ -1187,14 +1187,17 @@ static hipError_t product_of(int product, int in, int out, const MuonGemmArgs &a
     return hipErrorInvalidValue;
 }
 
-// Eight waves hide more of the latency where a CU has one tile or two; with
-// many tiles the larger blocks of four waves read LDS less.  (us, 2 / 1
-// matrices of 4096^2 / 2048^2: P X 729 / 52 with four waves, 745 / 51 with
-// eight; X X^T 429 / 48 and 432 / 44.)
+// 128 x 128 tiles: eight waves hide more of the latency while a CU has one
+// tile; with more than one, two workgroups of four waves do, and their larger
+// blocks read LDS less.  (us with four / eight waves: 252 tiles, P of 12
+// matrices of 768^2 25.2 / 23.9 and X X^T 24.8 / 23.4; 432 tiles 39.5 / 39.5; 504 tiles, P of 24
+// of them 42.8 / 44.3, X X^T of 24 of 768 x 2304 102.8 / 116.2; 2048 tiles, P X of
+// two of 4096^2 729 / 745.  Three or four stages, or 128 x 256 tiles, were
+// slower in each.)  64 x 64 tiles have three stages: three workgroups to a CU.
 typedef Tiling<64, 64, 2, 2, 3, 3> Tiling64;
 typedef Tiling<128, 128, 2, 4, 2, 4> Tiling128;
 typedef Tiling<128, 128, 2, 2, 2, 2> Tiling128Many;
-constexpr uint32_t kManyTiles = 1024;
+constexpr uint32_t kManyTiles = 384;
 
 hipError_t launch_muon_product(int tiling, int product, int in, int out, const MuonGemmArgs &a, hipStream_t s) {
     if (tiling == kTile64) return product_of<Tiling64>(product, in, out, a, s);
@@ -1224,11 +1227,17 @@ hipError_t launch_muon_small(int64_t short_side, int64_t long_side, const MuonSm
 
 hipError_t launch_muon_decode(int storage, const BlockDesc *desc, uint32_t n_blocks, const void *m_state,
                               const float *m_scale, void *dst, hipStream_t s) {
-    const dim3 grid(n_blocks), block(256);
-    if (storage == kMuonBf16) muon_decode_kernel<kMuonBf16><<<grid, block, 0, s>>>(desc, m_state, m_scale, dst);
-    else if (storage == kMuonQ8) muon_decode_kernel<kMuonQ8><<<grid, block, 0, s>>>(desc, m_state, m_scale, dst);
-    else muon_decode_kernel<kMuonF32><<<grid, block, 0, s>>>(desc, m_state, m_scale, dst);
-    return hipGetLastError();
+    constexpr uint32_t kMost = 1u << 23;  // a launch has less than 2^32 threads
+    hipError_t e = hipSuccess;
+    for (uint32_t done = 0; done < n_blocks && e == hipSuccess; done += min(kMost, n_blocks - done)) {
+        const dim3 grid(min(kMost, n_blocks - done)), block(256);
+        const BlockDesc *d = desc + done;
+        if (storage == kMuonBf16) muon_decode_kernel<kMuonBf16><<<grid, block, 0, s>>>(d, m_state, m_scale, dst);
+        else if (storage == kMuonQ8) muon_decode_kernel<kMuonQ8><<<grid, block, 0, s>>>(d, m_state, m_scale, dst);
+        else muon_decode_kernel<kMuonF32><<<grid, block, 0, s>>>(d, m_state, m_scale, dst);
+        e = hipGetLastError();
+    }
+    return e;
 }
 
 }  // namespace adam_mi355x

@@ -27,7 +27,9 @@ constexpr int kStageSlots = 8;  // pinned staging buffers per state
 // elements: 1 GB of X, and some 4000 tiles of 128 x 128.
 constexpr int64_t kGroupElements = int64_t(1) << 26;
 constexpr int64_t kMaxDim = int64_t(1) << 21;
-constexpr int64_t kMaxSums = 1024;
+constexpr int64_t kMaxSums = 1024;  // workgroups that share a matrix's sum of squares
+// The growth of a rounding error up to which single fp16 factors and runs of
+// three iterations are taken, and the shortest side for runs (see runs_of).
 constexpr double kPlainGrowth = 12.0;
 constexpr int64_t kPairShort = 256, kTripleShort = 512;
 constexpr float kDefaultCoefficients[3] = {3.4445f, -4.7750f, 2.0315f};
@@ -144,8 +146,8 @@ struct Work {
         triples = shortest >= kTripleShort && 2.0 * (g + u) > 4.0 * s + square.time(square_tiling, 2);
     }
     int64_t pad() const { return square_tiling == kTile128 || update_tiling == kTile128 ? 128 : 64; }
-    int64_t part_bytes() const {
-        return std::max(partial_bytes(square_tiling), partial_bytes(update_tiling));
+    int64_t part_bytes() const {  // (small matrices have no tiles)
+        return update.tiles[0] == 0 ? 0 : std::max(partial_bytes(square_tiling), partial_bytes(update_tiling));
     }
 };
 
@@ -961,7 +963,13 @@ int muon_state_momentum(muon_state *s, void *dst, int64_t nbytes, void *hip_stre
         if (nbytes == 0) return ADAM_OK;
         if (!dst) return fail(ADAM_EINVAL, "NULL destination");
         if (reinterpret_cast<uintptr_t>(dst) & 15u) return fail(ADAM_EALIGN, "destination is not 16-byte aligned");
-        hipError_t e = launch_muon_decode(s->layout.storage, s->d_desc, (uint32_t)s->nblocks, s->m, s->m_scale, dst,
+        int dev = -1;
+        hipError_t e = hipGetDevice(&dev);
+        if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
+        if (dev != s->device)
+            return fail(ADAM_EINVAL, "state lives on device " + std::to_string(s->device) + ", current is " +
+                                         std::to_string(dev));
+        e = launch_muon_decode(s->layout.storage, s->d_desc, (uint32_t)s->nblocks, s->m, s->m_scale, dst,
                                           reinterpret_cast<hipStream_t>(hip_stream));
         return e == hipSuccess ? ADAM_OK : hip_fail(e, "decode launch");
     });
@@ -1259,11 +1267,16 @@ int muon_orthogonalize(const muon_matrices *mats, const void *x, void *out, cons
         hipError_t e;
         if (is_small(shape)) {
             work.per_mat = 1;
-            work.n_tiles = (uint32_t)mats->batch;
-            MuonSmallArgs small = small_args(work, x, xe == 2, *iteration, oe == 2 ? kLastBf16 : kLastF32);
-            small.o = out;
-            e = launch_muon_small(shape.shorter(), shape.longer(), small, stream);
-            return e == hipSuccess ? ADAM_OK : hip_fail(e, "launch");
+            for (int64_t first = 0; first < mats->batch; first += kSmallBatch) {
+                work.n_tiles = (uint32_t)std::min(kSmallBatch, mats->batch - first);
+                work.one.u_off = (uint64_t)(first * mats->x_batch_stride);
+                work.one.o_off = (uint64_t)(first * mats->out_batch_stride);
+                MuonSmallArgs small = small_args(work, x, xe == 2, *iteration, oe == 2 ? kLastBf16 : kLastF32);
+                small.o = out;
+                if ((e = launch_muon_small(shape.shorter(), shape.longer(), small, stream)) != hipSuccess)
+                    return hip_fail(e, "launch");
+            }
+            return ADAM_OK;
         }
         const BatchPlan p = plan_batch(mats->batch, shape);
         const Workspace w = carve(static_cast<char *>(workspace), p.size, p.x_bytes * p.chunk, p.a_bytes * p.chunk,

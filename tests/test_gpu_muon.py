@@ -292,6 +292,17 @@ def test_orthogonalize_batches_beyond_one_part():
     assert all(torch.equal(out[0], o) or float((out[0] - o).norm()) < 1e-5 * float(o.norm()) for o in out[1:])
 
 
+def test_orthogonalize_more_small_matrices_than_a_launch_has_workgroups():
+    # 2^32 threads are one too many for a launch of 512 a matrix
+    n = 2 ** 23 + 5
+    x = torch.ones(n, 1, 1, device="cuda")
+    x[1::2] = -2.0
+    x[5::7] = 0.0
+    out = ma.muon_orthogonalize(x)
+    assert torch.equal(out, ma.muon_orthogonalize(x[:14]).repeat(n // 14 + 1, 1, 1)[:n])
+    assert torch.equal(out[:, 0, 0].sign(), x[:, 0, 0].sign())
+
+
 @pytest.mark.parametrize("shape", [(40, 70), (300, 300), (5, 600, 520), (2200, 2100)], ids=str)
 def test_zero_and_nonfinite_matrices(shape):
     batch = 3
