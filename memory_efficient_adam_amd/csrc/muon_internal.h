@@ -62,6 +62,7 @@ struct MuonWork {
     MuonMat one;
     uint64_t x_stride, a_stride, u_stride, o_stride;
     uint32_t norm_stride;
+    uint32_t window;  // log2 of the workgroups among which each XCD gets a run of tiles
 };
 
 // The factor arrays of one group of matrices.

@@ -98,10 +98,12 @@ __device__ __forceinline__ double block_sum(double x, double *s) {
 
 // Consecutive tiles share factor rows, and workgroups are dealt to the 8 XCDs
 // (each with an L2 of its own) in turn: workgroup id takes the tile that
-// keeps each XCD on one run of consecutive tiles.
-__device__ __forceinline__ uint32_t xcd_order(uint32_t id, uint32_t n) {
-    const uint32_t xcd = id & 7u, per = n >> 3, rest = n & 7u;
-    return xcd * per + min(xcd, rest) + (id >> 3);
+// keeps each XCD on one run of consecutive tiles in each window of 2^window.
+__device__ __forceinline__ uint32_t xcd_order(uint32_t id, uint32_t n, uint32_t window) {
+    const uint32_t base = id >> window << window;
+    const uint32_t in = id - base, count = n - base >> window ? 1u << window : n - base;
+    const uint32_t xcd = in & 7u, per = count >> 3, rest = count & 7u;
+    return base + xcd * per + min(xcd, rest) + (in >> 3);
 }
 
 typedef const __attribute__((address_space(4))) BlockDesc *ConstDescPtr;
@@ -438,13 +440,13 @@ void muon_product_kernel(MuonGemmArgs a) {
     bool second = false;
     if (id < whole * jobs) {
         second = id >= whole;
-        id = xcd_order(second ? id - whole : id, whole);
+        id = xcd_order(second ? id - whole : id, whole, a.work.window);
     } else {
         parts = a.work.parts;
         const uint32_t rest = (a.work.n_tiles - whole) * parts;
         id -= whole * jobs;
         second = id >= rest;
-        id = xcd_order(second ? id - rest : id, rest);
+        id = xcd_order(second ? id - rest : id, rest, a.work.window);
         part = id % parts;
         id = whole + id / parts;
     }

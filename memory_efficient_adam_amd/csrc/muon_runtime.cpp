@@ -104,7 +104,7 @@ Cut cut_tiles(int tiling, int64_t tiles, int64_t jobs, double slabs, int64_t lea
 struct Load {
     int64_t tiles[2] = {0, 0};
     double slabs[2] = {0.0, 0.0};  // summed over tiles
-    int64_t least = kMaxDim;
+    int64_t least = kMaxDim, most = 0;  // in slabs, of a tile
     void add(double count, int64_t down, int64_t across, bool triangle, int64_t length) {
         for (int t = 0; t < 2; ++t) {
             const int64_t size = t == kTile128 ? 128 : 64, r = pad_to(down, size) / size, c = pad_to(across, size) / size;
@@ -113,6 +113,7 @@ struct Load {
             slabs[t] += (double)n * (double)pad_to(length, size) / 32.0;
         }
         least = std::min(least, length / 32);
+        most = std::max(most, length / 32);
     }
     // plain slabs hold twice the elements
     Cut cut(int tiling, int64_t n_tiles, int64_t jobs, int form) const {
@@ -120,6 +121,14 @@ struct Load {
         return cut_tiles(tiling, n_tiles, jobs, slabs[tiling] / (double)std::max<int64_t>(1, tiles[tiling]) / per,
                          least / (int64_t)per);
     }
+    // log2 of the workgroups among which each XCD gets a run of tiles.  Of long
+    // and short tiles every XCD is to have its share (a step of 12 encoder
+    // blocks' attention, X X^T over 768 and 2304: 1342 -> 1303 us).  Of very many
+    // alike the XCDs are kept near each other, so that they find each other's
+    // factors in the cache behind theirs (four matrices of 4096^2: 16425 -> 16237
+    // us).  Of fewer each gets one run (1296 tiles, 12 of 2304 x 768: 579
+    // us, 588 with windows of 1024).
+    uint32_t window(int tiling) const { return most > least ? 8u : (tiles[tiling] >= 2048 ? 10u : 31u); }
     double time(int tiling, int64_t jobs = 1) const { return cut(tiling, tiles[tiling], jobs, kSplit).time; }
 };
 
@@ -416,6 +425,7 @@ hipError_t run_products(const Workspace &w, const MuonWork &square, const MuonWo
         g.work = is_square ? square : update;
         const int in = g.phi ? (product == kGram ? kPlain : kMixed) : form;
         const Cut cut = load.cut(tiling, g.work.n_tiles, g.left2 ? 2 : 1, in);
+        g.work.window = load.window(tiling);
         g.work.n_whole = cut.whole;
         g.work.parts = cut.parts;
         g.work.partial = w.parts;
