@@ -96,6 +96,28 @@ def test_orthogonalize_steps_and_coefficients(steps, shape, dtype):
         _check(ma.muon_orthogonalize(x, **kw), x, **kw)
 
 
+# bf16 in and fp32 out, and the other way; runs, single fp16 values at the end, bf16 taken as it is
+@pytest.mark.parametrize("steps", [1, 2, 3, 5])
+@pytest.mark.parametrize("shape", [(40, 70), (129, 500), (6, 300, 900), (3, 1100, 520)], ids=str)
+def test_orthogonalize_from_one_type_to_another(steps, shape):
+    for dtype, out_dtype in ((torch.bfloat16, torch.float32), (torch.float32, torch.bfloat16)):
+        x = _matrix(20 + steps, shape).to(dtype)
+        out = torch.empty(shape, dtype=out_dtype, device="cuda")
+        _check(ma.muon_orthogonalize(x, out=out, steps=steps), x, steps=steps)
+
+
+# long and short products in one launch, several rounds of tiles, a rest that is split
+def test_step_of_many_matrices_of_unequal_length():
+    shapes = [(768, 2304)] * 13 + [(700, 768), (300, 2000), (64, 64)] * 7
+    grads = [_matrix(30 + k, s) for k, s in enumerate(shapes)]
+    params = [torch.zeros(s, device="cuda") for s in shapes]
+    state = ma.muon_state_create(shapes, "f32")
+    ma.muon_step(state, params, grads, t=1, lr=1.0, momentum=0.0, scale="none")
+    for p, g in zip(params, grads):
+        _check(-p, g)
+    state.destroy()
+
+
 # large first coefficients: no run of three, no plain factors before the end
 def test_orthogonalize_steep_coefficients():
     steep = [(8.28721, -23.5959, 17.3004), (4.1071, -2.9478, 0.5449), (3.9487, -2.9089, 0.5518),
@@ -369,6 +391,28 @@ def test_results_repeat_bit_for_bit_and_on_other_streams():
         raw = ma.muon_orthogonalize(x, stream=side.cuda_stream)
         side.synchronize()
         assert torch.equal(raw, want)
+
+
+def test_calls_under_way_at_once_on_two_streams():
+    # each with its own workspace and state; split tiles count arrivals in both
+    xs = [_matrix(40, (768, 1000)), _matrix(41, (2, 1100, 1300))]
+    want = [ma.muon_orthogonalize(x) for x in xs]
+    shapes = [(768, 1000), (500, 500), (33, 65)]
+    grads = [_matrix(42 + k, s) for k, s in enumerate(shapes)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    states = [ma.muon_state_create(shapes, "q8") for _ in streams]
+    params = [[torch.zeros(s, device="cuda") for s in shapes] for _ in streams]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for t in range(1, 6):
+        for i, stream in enumerate(streams):
+            got[i].append(ma.muon_orthogonalize(xs[i], stream=stream))
+            ma.muon_step(states[i], params[i], grads, t=t, lr=1e-2, stream=stream)
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(o, want[i]) for o in got[i])
+    assert all(torch.equal(a, b) for a, b in zip(*params))
+    assert all(torch.equal(a, b) for a, b in zip(*(ma.muon_state_momentum(s) for s in states)))
 
 
 def test_orthogonalize_in_a_graph():
