@@ -31,10 +31,9 @@
  * Iterations of larger matrices may be taken two or three at a time, as one
  * polynomial in the first one's A.
  * muon_orthogonalize to a bf16 output may hold the factors of the last
- * iterations (of larger matrices) in one fp16 value each: those from the first
- * k on for which the product of |a_k|, .., |a_steps| is at most 12 (by which
- * their rounding, 2^-12, can still grow), which keeps the error below bf16's
- * own rounding.  bf16 input is taken exactly.
+ * iterations in one fp16 value each: those from the first k on for which the
+ * product of |a_k|, .., |a_steps| is at most 12 (by which their rounding,
+ * 2^-12, can still grow), which keeps the error below bf16's own rounding.
  * A matrix whose u is all zero gives O = 0; one with a NaN or an infinity
  * gives NaN in all of O (and in the params; the stored momentum of that
  * matrix is then unspecified).  Other matrices of the call are not affected.

@@ -134,7 +134,7 @@ struct MuonSmallArgs {
     int32_t scale;
     int32_t product;           // kLastBf16, kLastF32, kLastParams
     int32_t u_bf16;
-    int32_t steps;
+    int32_t steps, split_steps;  // all iterations; those before factors are single fp16 values
     float coefficients[3 * kMaxIterations];
 };
 

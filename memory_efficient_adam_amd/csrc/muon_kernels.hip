@@ -101,7 +101,7 @@ __device__ __forceinline__ double block_sum(double x, double *s) {
 // keeps each XCD on one run of consecutive tiles in each window of 2^window.
 __device__ __forceinline__ uint32_t xcd_order(uint32_t id, uint32_t n, uint32_t window) {
     const uint32_t base = id >> window << window;
-    const uint32_t in = id - base, count = n - base >> window ? 1u << window : n - base;
+    const uint32_t in = id - base, count = ((n - base) >> window) ? 1u << window : n - base;
     const uint32_t xcd = in & 7u, per = count >> 3, rest = count & 7u;
     return base + xcd * per + min(xcd, rest) + (in >> 3);
 }
@@ -572,8 +572,10 @@ void muon_product_kernel(MuonGemmArgs a) {
 
 // ---------------------------------------------------------------- small matrices
 // A whole orthogonalisation in one workgroup of 8 waves, X staying in
-// registers, in one launch: 23 us for a bf16 matrix of 64 x 64 (one launch per
-// product, 69), 79 us for 96 of 64 x 768 (250).
+// registers, in one launch: 23 us for an fp32 matrix of 48 x 80 (one launch per
+// product, 69), 66 us for 96 of 64 x 768 in bf16 (250; and 82 with all
+// factors split: kPlainEnd holds those of the last iterations in single values, as
+// the larger matrices' products do).
 //
 // A wave holds blocks of 32 columns of X, block w + 8 b at wave w, as the
 // matrix cores give them: lane l holds column l % 32, rows 8 g + 4 (l / 32) + q
@@ -587,6 +589,11 @@ void muon_product_kernel(MuonGemmArgs a) {
 // which is what A = X X^T takes for both factors.  Nothing of X passes through
 // LDS; the price is that P X is computed twice.  A is summed over the waves in LDS.
 constexpr int kSmallWaves = 8;
+
+template <int kForm>
+struct FormOf {
+    static constexpr int value = kForm;
+};
 
 __device__ __forceinline__ uint32_t k_order(uint32_t j, uint32_t half) { return (j & 3u) + 4u * half + ((j & 4u) << 1); }
 
@@ -608,11 +615,14 @@ __device__ __forceinline__ u32x2 *small_quad(uint4 *image, uint32_t row, uint32_
 __device__ __forceinline__ f32x16 mfma(half8 a, half8 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
 }
-__device__ __forceinline__ f32x16 mfma_split(half8 ah, half8 al, half8 bh, half8 bl, f32x16 c) {
-    return mfma(al, bh, mfma(ah, bl, mfma(ah, bh, c)));
+// A product of factors in two fp16 values, or (kPlain) in their high parts alone.
+template <int kForm>
+__device__ __forceinline__ f32x16 mfma_form(half8 ah, half8 al, half8 bh, half8 bl, f32x16 c) {
+    if constexpr (kForm == kPlain) return mfma(ah, bh, c);
+    else return mfma(al, bh, mfma(ah, bl, mfma(ah, bh, c)));
 }
 
-template <int kRows, int kCols, bool kBf16>
+template <int kRows, int kCols, bool kBf16, bool kPlainEnd>
 __global__ __launch_bounds__(64 * kSmallWaves) void muon_small_kernel(MuonSmallArgs a) {
     constexpr int kSquare = kRows * (kRows + 1) / 2;  // 32 x 32 blocks of A on and below the diagonal
     constexpr int kSteps = 2 * kRows;                 // fragments along the rows of X
@@ -675,7 +685,9 @@ __global__ __launch_bounds__(64 * kSmallWaves) void muon_small_kernel(MuonSmallA
         }
     __syncthreads();
 
-    for (int it = 0; it < a.steps; ++it) {
+    // An iteration: X as `in` to X as `out`, then A and P of that.
+    auto iteration = [&](auto in, auto out, int it) {
+        constexpr int kIn = decltype(in)::value, kOut = decltype(out)::value;
         // X <- P X and, along the way, A = X X^T
         f32x16 acc[kSquare];
 #pragma unroll
@@ -690,7 +702,7 @@ __global__ __launch_bounds__(64 * kSmallWaves) void muon_small_kernel(MuonSmallA
                 f32x16 v = {};
 #pragma unroll
                 for (int s = 0; s < kSteps; ++s)
-                    v = mfma_split(xh[b][s], xl[b][s], small_frag(poly.hi, 32u * i + ln, 2u * s + half),
+                    v = mfma_form<kIn>(xh[b][s], xl[b][s], small_frag(poly.hi, 32u * i + ln, 2u * s + half),
                                    small_frag(poly.lo, 32u * i + ln, 2u * s + half), v);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
@@ -706,7 +718,7 @@ __global__ __launch_bounds__(64 * kSmallWaves) void muon_small_kernel(MuonSmallA
                 for (int j = 0; j <= i; ++j)
 #pragma unroll
                     for (int k = 0; k < 2; ++k)
-                        acc[i + j] = mfma_split(gh[i][k], gl[i][k], gh[j][k], gl[j][k], acc[i + j]);
+                        acc[i + j] = mfma_form<kOut>(gh[i][k], gl[i][k], gh[j][k], gl[j][k], acc[i + j]);
             if (it == 0) continue;  // P is still one
             f32x16 v[kRows];
 #pragma unroll
@@ -714,7 +726,7 @@ __global__ __launch_bounds__(64 * kSmallWaves) void muon_small_kernel(MuonSmallA
                 v[i] = f32x16{};
 #pragma unroll
                 for (int s = 0; s < kSteps; ++s)
-                    v[i] = mfma_split(small_frag(poly.hi, 32u * i + ln, 2u * s + half),
+                    v[i] = mfma_form<kIn>(small_frag(poly.hi, 32u * i + ln, 2u * s + half),
                                       small_frag(poly.lo, 32u * i + ln, 2u * s + half), xh[b][s], xl[b][s], v[i]);
             }
 #pragma unroll
@@ -751,10 +763,10 @@ __global__ __launch_bounds__(64 * kSmallWaves) void muon_small_kernel(MuonSmallA
             u32x2 h, l;
             split4(v[0], v[1], v[2], v[3], h, l);
             *small_quad(gram.hi, c, r) = h;
-            *small_quad(gram.lo, c, r) = l;
+            if constexpr (kOut == kSplit) *small_quad(gram.lo, c, r) = l;
             if (bi != bj) {
                 *small_quad(gram.hi, r + (lane & 3u), c & ~3u) = quad_transpose(h, lane);
-                *small_quad(gram.lo, r + (lane & 3u), c & ~3u) = quad_transpose(l, lane);
+                if constexpr (kOut == kSplit) *small_quad(gram.lo, r + (lane & 3u), c & ~3u) = quad_transpose(l, lane);
             }
         }
         __syncthreads();
@@ -765,7 +777,7 @@ __global__ __launch_bounds__(64 * kSmallWaves) void muon_small_kernel(MuonSmallA
 #pragma unroll
             for (int s = 0; s < kSteps; ++s) {
                 const uint32_t chunk = 2u * s + half;
-                p = mfma_split(small_frag(gram.hi, 32u * bi + ln, chunk), small_frag(gram.lo, 32u * bi + ln, chunk),
+                p = mfma_form<kOut>(small_frag(gram.hi, 32u * bi + ln, chunk), small_frag(gram.lo, 32u * bi + ln, chunk),
                                small_frag(gram.hi, 32u * bj + ln, chunk), small_frag(gram.lo, 32u * bj + ln, chunk), p);
             }
             const float ca = a.coefficients[3 * it] * kScaleP, cb = a.coefficients[3 * it + 1] * (kScaleP / kScaleX),
@@ -773,7 +785,9 @@ __global__ __launch_bounds__(64 * kSmallWaves) void muon_small_kernel(MuonSmallA
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
                 const uint32_t r = 32u * bi + 8u * g + 4u * half, c = 32u * bj + ln;
-                const u32x2 h = *small_quad(gram.hi, c, r), l = *small_quad(gram.lo, c, r);
+                const u32x2 h = *small_quad(gram.hi, c, r);
+                u32x2 l = {0u, 0u};
+                if constexpr (kOut == kSplit) l = *small_quad(gram.lo, c, r);
                 float x[4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
@@ -784,11 +798,21 @@ __global__ __launch_bounds__(64 * kSmallWaves) void muon_small_kernel(MuonSmallA
                     if (r + q == c) v += ca;
                     x[q] = v;
                 }
-                split4(x[0], x[1], x[2], x[3], *small_quad(poly.hi, c, r), *small_quad(poly.lo, c, r));
+                u32x2 ph, pl;
+                split4(x[0], x[1], x[2], x[3], ph, pl);
+                *small_quad(poly.hi, c, r) = ph;
+                if constexpr (kOut == kSplit) *small_quad(poly.lo, c, r) = pl;
             }
         }
         __syncthreads();
+    };
+    int it = 0;
+    for (; it < a.split_steps; ++it) iteration(FormOf<kSplit>{}, FormOf<kSplit>{}, it);
+    if constexpr (kPlainEnd) {
+        iteration(FormOf<kSplit>{}, FormOf<kPlain>{}, it);
+        for (++it; it < a.steps; ++it) iteration(FormOf<kPlain>{}, FormOf<kPlain>{}, it);
     }
+    constexpr int kForm = kPlainEnd ? kPlain : kSplit;
 
     // O = P X, lane = the user's column, so that a wave writes along rows
     float *param = nullptr;
@@ -808,7 +832,7 @@ __global__ __launch_bounds__(64 * kSmallWaves) void muon_small_kernel(MuonSmallA
             for (int s = 0; s < kSteps; ++s) {
                 const half8 ph = small_frag(poly.hi, 32u * i + ln, 2u * s + half);
                 const half8 pl = small_frag(poly.lo, 32u * i + ln, 2u * s + half);
-                v = m.tall ? mfma_split(xh[b][s], xl[b][s], ph, pl, v) : mfma_split(ph, pl, xh[b][s], xl[b][s], v);
+                v = m.tall ? mfma_form<kForm>(xh[b][s], xl[b][s], ph, pl, v) : mfma_form<kForm>(ph, pl, xh[b][s], xl[b][s], v);
             }
             const uint32_t r0 = (m.tall ? col0 : 32u * i) + 4u * half, c = m.tall ? 32u * i + ln : col0 + ln;
             float old[16];
@@ -1213,8 +1237,13 @@ hipError_t launch_muon_small(int64_t short_side, int64_t long_side, const MuonSm
     if (short_side > kSmallShort || cols < 1 || cols > 3) return hipErrorInvalidValue;
 #define MUON_SMALL(r, c)                                                    \
     if ((short_side <= 32) == (r == 1) && cols == c) {                      \
-        if (a.u_bf16) muon_small_kernel<r, c, true><<<grid, block, 0, s>>>(a);  \
-        else muon_small_kernel<r, c, false><<<grid, block, 0, s>>>(a);      \
+        if (a.split_steps < a.steps) {                                      \
+            if (a.u_bf16) muon_small_kernel<r, c, true, true><<<grid, block, 0, s>>>(a);  \
+            else muon_small_kernel<r, c, false, true><<<grid, block, 0, s>>>(a);          \
+        } else {                                                            \
+            if (a.u_bf16) muon_small_kernel<r, c, true, false><<<grid, block, 0, s>>>(a); \
+            else muon_small_kernel<r, c, false, false><<<grid, block, 0, s>>>(a);         \
+        }                                                                   \
         return hipGetLastError();                                           \
     }
     MUON_SMALL(1, 1)

@@ -355,6 +355,12 @@ MuonSmallArgs small_args(const MuonWork &w, const void *u, bool u_bf16, const mu
     a.eps = (double)it.eps;
     a.product = product;
     a.steps = it.steps;
+    a.split_steps = it.steps;
+    if (product == kLastBf16) {
+        int forms[MUON_MAX_STEPS];
+        forms_of(it, true, forms);
+        a.split_steps = (int32_t)(std::find(forms, forms + it.steps, (int)kPlain) - forms);
+    }
     for (int k = 0; k < it.steps; ++k) coefficients_of(it, k, a.coefficients + 3 * k);
     return a;
 }
