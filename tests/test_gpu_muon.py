@@ -350,6 +350,35 @@ def test_scales_of_the_gradient(size):
         _check(ma.muon_orthogonalize(x, **kw), x, **kw)
 
 
+@pytest.mark.parametrize("shape", [(33000, 34000), (34000, 33000), (70, 2 ** 21 - 1), (2 ** 21 - 1, 90)], ids=str)
+def test_matrices_beyond_32_bit_offsets(shape):
+    # one entry a row and column: each is its own singular value, the rest stays 0
+    m = min(shape)
+    if torch.cuda.mem_get_info()[0] < 60 * 2 ** 30:
+        pytest.skip("needs 60 GB")
+    g = _gen(12)
+    at = torch.randperm(max(shape) - 1, generator=g, device="cuda")[:m]
+    at[-1] = max(shape) - 1
+    i = torch.arange(m, device="cuda")
+    rows, cols = (i, at) if shape[0] < shape[1] else (at, i)
+    values = 0.5 + torch.rand(m, generator=g, device="cuda")
+    x = torch.zeros(shape, device="cuda")
+    x[rows, cols] = values
+    steps = [(3.4445, -4.7750, 2.0315)] * 2
+    out = ma.muon_orthogonalize(x, steps=2)
+    del x
+    s = values.double() / values.double().norm()
+    for a, b, c in muon_ref.triples(2, steps):
+        s = a * s + b * s ** 3 + c * s ** 5
+    got = out[rows, cols].double()
+    # an entry of 2^-13 and more has 22 bits in each factor, a smaller one an error of 2^-35
+    # in X_0, which the two iterations grow by 3.45 each
+    tol = 8 * 2.0 ** -22 * s.abs() + 12 * 2.0 ** -35
+    assert bool(((got - s).abs() <= tol).all()), float(((got - s).abs() / tol).max())
+    out[rows, cols] = 0.0
+    assert not bool(out.any())
+
+
 def test_closed_forms():
     # one direction, and a diagonal: the polynomial of each singular value
     def poly(s, steps=5):
