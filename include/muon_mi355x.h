@@ -29,11 +29,8 @@
  * that O is about as far from the exact result as a computation in fp32 is
  * (at most some four times as far, where that one loses almost nothing).
  * Iterations of larger matrices may be taken two or three at a time, as one
- * polynomial in the first one's A.
- * muon_orthogonalize to a bf16 output may hold the factors of the last
- * iterations in one fp16 value each: those from the first k on for which the
- * product of |a_k|, .., |a_steps| is at most 12 (by which their rounding,
- * 2^-12, can still grow), which keeps the error below bf16's own rounding.
+ * polynomial in the first one's A.  A bf16 output is the fp32 result rounded
+ * once, to nearest even.
  * A matrix whose u is all zero gives O = 0; one with a NaN or an infinity
  * gives NaN in all of O (and in the params; the stored momentum of that
  * matrix is then unspecified).  Other matrices of the call are not affected.

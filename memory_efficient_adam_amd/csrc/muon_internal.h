@@ -17,7 +17,8 @@ namespace adam_mi355x {
 // l % 32, elements 8 (l / 32) .. + 7 of the fragment's 16.
 //   split slabs (two fp16 values per element): 32 elements; fragments: high
 //     parts of the first 16, their remainders, the same of the second 16;
-//   plain slabs (one fp16 value per element): 64 elements, 16 per fragment.
+//   plain slabs (one fp16 value per element; an X_0 taken as its bf16 source
+//     has it): 64 elements, 16 per fragment.
 // So a slab goes to LDS as it is, is read there without bank conflicts, and
 // a wave's 32 x 32 block of a result is one contiguous piece of an image.
 // Dimensions are padded to multiples of the tile with zeros, which every
@@ -134,7 +135,7 @@ struct MuonSmallArgs {
     int32_t scale;
     int32_t product;           // kLastBf16, kLastF32, kLastParams
     int32_t u_bf16;
-    int32_t steps, split_steps;  // all iterations; those before factors are single fp16 values
+    int32_t steps;
     float coefficients[3 * kMaxIterations];
 };
 
@@ -163,8 +164,8 @@ hipError_t launch_muon_momentum(int storage, bool grad_bf16, bool stochastic, co
 hipError_t launch_muon_norms(const double *partials, const uint2 *ranges, double *sums, uint32_t n_mats,
                              hipStream_t s);
 hipError_t launch_muon_sums(bool bf16, const MuonWork &w, const MuonSumArgs &a, uint32_t n_mats, hipStream_t s);
-// raw: bf16 input times a power of two, exact in plain slabs, with the rest of
-// the scale in phi
+// raw: bf16 input times a power of two, exact in plain slabs (form kPlain), with
+// the rest of the scale in phi; else form is kSplit
 hipError_t launch_muon_prep(bool bf16, bool raw, int form, const MuonWork &w, const MuonPrepArgs &a, hipStream_t s);
 
 enum MuonProduct : int { kGram, kPolynomial, kCommuting, kUpdate, kLastBf16, kLastF32, kLastParams };
@@ -174,8 +175,9 @@ enum MuonProduct : int { kGram, kPolynomial, kCommuting, kUpdate, kLastBf16, kLa
 enum MuonTiling : int { kTile64, kTile128 };
 // Bytes of a split workgroup's sums.
 inline int64_t partial_bytes(int tiling) { return tiling == kTile128 ? 128 * 128 * 4 : 64 * 64 * 4; }
-// in: the form of the factors read; out: of the factor written
-hipError_t launch_muon_product(int tiling, int product, int in, int out, const MuonGemmArgs &a, hipStream_t s);
+// in: the form of the factors read (those written are split); jobs: 2 with a
+// second product (kCommuting), else 1
+hipError_t launch_muon_product(int tiling, int product, int in, int jobs, const MuonGemmArgs &a, hipStream_t s);
 
 // short_side, long_side: the largest of the launch's matrices
 hipError_t launch_muon_small(int64_t short_side, int64_t long_side, const MuonSmallArgs &a, hipStream_t s);

@@ -336,29 +336,27 @@ __device__ __forceinline__ void store_through(char *at, u32x2 v) {
 // Where in a block's piece of an image the four values 4 g .. 4 g + 3 of a
 // lane go, from the place of g = 0: along the rows (values of a column are
 // elements of the transposed image) or, after quad_transpose, down them.
-template <int kForm>
-constexpr uint32_t along(int g) { return (uint32_t)(g >> 1) * (kForm == kSplit ? 2048u : 1024u) + (uint32_t)(g & 1) * 512u; }
+constexpr uint32_t along(int g) { return (uint32_t)(g >> 1) * 2048u + (uint32_t)(g & 1) * 512u; }
 constexpr uint32_t down(int g) { return (uint32_t)g * 128u; }
 
-// A 32 x 32 block of values, at rows r0.. and columns c0.., into an image whose
+// A 32 x 32 block of values, at rows r0.. and columns c0.., into a split image whose
 // rows hold `length` elements and, transposed, into one with `length_t` (either may be NULL).
-template <int kForm>
 __device__ __forceinline__ void store_block(const f32x16 &v, char *image, uint32_t length, char *transposed, uint32_t length_t,
                                             uint32_t r0, uint32_t c0, uint32_t lane) {
     const uint32_t r = r0 + 4u * (lane >> 5), c = c0 + (lane & 31u);
-    char *const at = image + image_pos<kForm>(r + (lane & 3u), c & ~3u, length);
-    char *const at_t = transposed + image_pos<kForm>(c, r, length_t);
+    char *const at = image + image_pos<kSplit>(r + (lane & 3u), c & ~3u, length);
+    char *const at_t = transposed + image_pos<kSplit>(c, r, length_t);
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
         u32x2 h, l;
         split4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3], h, l);
         if (transposed) {
-            store_through(at_t + along<kForm>(g), h);
-            if constexpr (kForm == kSplit) store_through(at_t + along<kForm>(g) + kRemainder, l);
+            store_through(at_t + along(g), h);
+            store_through(at_t + along(g) + kRemainder, l);
         }
         if (image) {
             store_through(at + down(g), quad_transpose(h, lane));
-            if constexpr (kForm == kSplit) store_through(at + down(g) + kRemainder, quad_transpose(l, lane));
+            store_through(at + down(g) + kRemainder, quad_transpose(l, lane));
         }
     }
 }
@@ -420,13 +418,12 @@ __device__ __forceinline__ bool sum_parts(f32x16 (&acc)[T::kI][T::kJ], const Muo
 //   kGram:       A = X X^T                        tiles ti >= tj, stored at both places
 //   kPolynomial: P = a I + b A + c A A^T          the same
 //   kCommuting:  a product of two polynomials in one A (symmetric too), or
-//                two such products in one launch; one factor is a P, the
-//                other and the result are held alike
+//                two such products in one launch; one factor is a P
 //   kUpdate:     X' = P X, stored as X' and X'^T
 //   kLast..:     O = P X in the user's orientation (for a tall matrix the
 //                factors change places), rounded to the output's type, or
 //                applied to the params
-template <class T, int kProduct, int kIn, int kOut>
+template <class T, int kProduct, int kIn>
 __global__ __launch_bounds__(T::kThreads) __attribute__((amdgpu_waves_per_eu(T::kPerSimd)))
 void muon_product_kernel(MuonGemmArgs a) {
     __shared__ __attribute__((aligned(1024))) char lds[T::kStages * T::kStage];
@@ -524,13 +521,12 @@ void muon_product_kernel(MuonGemmArgs a) {
                     // A's block, read from its mirror image: four values down a column lie side by side
                     const float cb = a.cb * (kScaleP / kScaleX), cc = a.cc * (kScaleP / (kScaleX * kScaleX));
                     const float ca = a.ca * kScaleP;
-                    const char *const base = a.add + m.a_off + image_pos<kIn>(c, r, m.mp);
+                    const char *const base = a.add + m.a_off + image_pos<kSplit>(c, r, m.mp);
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
-                        const char *at = base + along<kIn>(g);
+                        const char *at = base + along(g);
                         const u32x2 h = *reinterpret_cast<const u32x2 *>(at);
-                        u32x2 l = {0u, 0u};
-                        if constexpr (kIn == kSplit) l = *reinterpret_cast<const u32x2 *>(at + kRemainder);
+                        const u32x2 l = *reinterpret_cast<const u32x2 *>(at + kRemainder);
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             const uint32_t hw = q < 2 ? h.x : h.y, lw = q < 2 ? l.x : l.y;
@@ -542,10 +538,10 @@ void muon_product_kernel(MuonGemmArgs a) {
                         }
                     }
                 }
-                store_block<kOut>(v, ti != tj ? out : nullptr, m.mp, out, m.mp, r0, c0, lane);
+                store_block(v, ti != tj ? out : nullptr, m.mp, out, m.mp, r0, c0, lane);
             } else if constexpr (kProduct == kUpdate) {
                 v *= phi * (1.0f / kScaleP);
-                store_block<kOut>(v, a.out + m.x_off, m.np, a.out_t + m.x_off, m.mp, r0, c0, lane);
+                store_block(v, a.out + m.x_off, m.np, a.out_t + m.x_off, m.mp, r0, c0, lane);
             } else {
                 constexpr float kUnscale = 1.0f / (kScaleX * kScaleP);
                 float old[16];
@@ -573,9 +569,7 @@ void muon_product_kernel(MuonGemmArgs a) {
 // ---------------------------------------------------------------- small matrices
 // A whole orthogonalisation in one workgroup of 8 waves, X staying in
 // registers, in one launch: 23 us for an fp32 matrix of 48 x 80 (one launch per
-// product, 69), 66 us for 96 of 64 x 768 in bf16 (250; and 82 with all
-// factors split: kPlainEnd holds those of the last iterations in single values, as
-// the larger matrices' products do).
+// product, 69), 82 us for 96 of 64 x 768 in bf16 (250).
 //
 // A wave holds blocks of 32 columns of X, block w + 8 b at wave w, as the
 // matrix cores give them: lane l holds column l % 32, rows 8 g + 4 (l / 32) + q
@@ -589,11 +583,6 @@ void muon_product_kernel(MuonGemmArgs a) {
 // which is what A = X X^T takes for both factors.  Nothing of X passes through
 // LDS; the price is that P X is computed twice.  A is summed over the waves in LDS.
 constexpr int kSmallWaves = 8;
-
-template <int kForm>
-struct FormOf {
-    static constexpr int value = kForm;
-};
 
 __device__ __forceinline__ uint32_t k_order(uint32_t j, uint32_t half) { return (j & 3u) + 4u * half + ((j & 4u) << 1); }
 
@@ -615,14 +604,12 @@ __device__ __forceinline__ u32x2 *small_quad(uint4 *image, uint32_t row, uint32_
 __device__ __forceinline__ f32x16 mfma(half8 a, half8 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
 }
-// A product of factors in two fp16 values, or (kPlain) in their high parts alone.
-template <int kForm>
-__device__ __forceinline__ f32x16 mfma_form(half8 ah, half8 al, half8 bh, half8 bl, f32x16 c) {
-    if constexpr (kForm == kPlain) return mfma(ah, bh, c);
-    else return mfma(al, bh, mfma(ah, bl, mfma(ah, bh, c)));
+// A product of factors in two fp16 values.
+__device__ __forceinline__ f32x16 mfma_split(half8 ah, half8 al, half8 bh, half8 bl, f32x16 c) {
+    return mfma(al, bh, mfma(ah, bl, mfma(ah, bh, c)));
 }
 
-template <int kRows, int kCols, bool kBf16, bool kPlainEnd>
+template <int kRows, int kCols, bool kBf16>
 __global__ __launch_bounds__(64 * kSmallWaves) void muon_small_kernel(MuonSmallArgs a) {
     constexpr int kSquare = kRows * (kRows + 1) / 2;  // 32 x 32 blocks of A on and below the diagonal
     constexpr int kSteps = 2 * kRows;                 // fragments along the rows of X
@@ -685,9 +672,7 @@ __global__ __launch_bounds__(64 * kSmallWaves) void muon_small_kernel(MuonSmallA
         }
     __syncthreads();
 
-    // An iteration: X as `in` to X as `out`, then A and P of that.
-    auto iteration = [&](auto in, auto out, int it) {
-        constexpr int kIn = decltype(in)::value, kOut = decltype(out)::value;
+    for (int it = 0; it < a.steps; ++it) {
         // X <- P X and, along the way, A = X X^T
         f32x16 acc[kSquare];
 #pragma unroll
@@ -702,7 +687,7 @@ __global__ __launch_bounds__(64 * kSmallWaves) void muon_small_kernel(MuonSmallA
                 f32x16 v = {};
 #pragma unroll
                 for (int s = 0; s < kSteps; ++s)
-                    v = mfma_form<kIn>(xh[b][s], xl[b][s], small_frag(poly.hi, 32u * i + ln, 2u * s + half),
+                    v = mfma_split(xh[b][s], xl[b][s], small_frag(poly.hi, 32u * i + ln, 2u * s + half),
                                    small_frag(poly.lo, 32u * i + ln, 2u * s + half), v);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
@@ -718,7 +703,7 @@ __global__ __launch_bounds__(64 * kSmallWaves) void muon_small_kernel(MuonSmallA
                 for (int j = 0; j <= i; ++j)
 #pragma unroll
                     for (int k = 0; k < 2; ++k)
-                        acc[i + j] = mfma_form<kOut>(gh[i][k], gl[i][k], gh[j][k], gl[j][k], acc[i + j]);
+                        acc[i + j] = mfma_split(gh[i][k], gl[i][k], gh[j][k], gl[j][k], acc[i + j]);
             if (it == 0) continue;  // P is still one
             f32x16 v[kRows];
 #pragma unroll
@@ -726,7 +711,7 @@ __global__ __launch_bounds__(64 * kSmallWaves) void muon_small_kernel(MuonSmallA
                 v[i] = f32x16{};
 #pragma unroll
                 for (int s = 0; s < kSteps; ++s)
-                    v[i] = mfma_form<kIn>(small_frag(poly.hi, 32u * i + ln, 2u * s + half),
+                    v[i] = mfma_split(small_frag(poly.hi, 32u * i + ln, 2u * s + half),
                                       small_frag(poly.lo, 32u * i + ln, 2u * s + half), xh[b][s], xl[b][s], v[i]);
             }
 #pragma unroll
@@ -763,10 +748,10 @@ __global__ __launch_bounds__(64 * kSmallWaves) void muon_small_kernel(MuonSmallA
             u32x2 h, l;
             split4(v[0], v[1], v[2], v[3], h, l);
             *small_quad(gram.hi, c, r) = h;
-            if constexpr (kOut == kSplit) *small_quad(gram.lo, c, r) = l;
+            *small_quad(gram.lo, c, r) = l;
             if (bi != bj) {
                 *small_quad(gram.hi, r + (lane & 3u), c & ~3u) = quad_transpose(h, lane);
-                if constexpr (kOut == kSplit) *small_quad(gram.lo, r + (lane & 3u), c & ~3u) = quad_transpose(l, lane);
+                *small_quad(gram.lo, r + (lane & 3u), c & ~3u) = quad_transpose(l, lane);
             }
         }
         __syncthreads();
@@ -777,7 +762,7 @@ __global__ __launch_bounds__(64 * kSmallWaves) void muon_small_kernel(MuonSmallA
 #pragma unroll
             for (int s = 0; s < kSteps; ++s) {
                 const uint32_t chunk = 2u * s + half;
-                p = mfma_form<kOut>(small_frag(gram.hi, 32u * bi + ln, chunk), small_frag(gram.lo, 32u * bi + ln, chunk),
+                p = mfma_split(small_frag(gram.hi, 32u * bi + ln, chunk), small_frag(gram.lo, 32u * bi + ln, chunk),
                                small_frag(gram.hi, 32u * bj + ln, chunk), small_frag(gram.lo, 32u * bj + ln, chunk), p);
             }
             const float ca = a.coefficients[3 * it] * kScaleP, cb = a.coefficients[3 * it + 1] * (kScaleP / kScaleX),
@@ -785,9 +770,7 @@ __global__ __launch_bounds__(64 * kSmallWaves) void muon_small_kernel(MuonSmallA
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
                 const uint32_t r = 32u * bi + 8u * g + 4u * half, c = 32u * bj + ln;
-                const u32x2 h = *small_quad(gram.hi, c, r);
-                u32x2 l = {0u, 0u};
-                if constexpr (kOut == kSplit) l = *small_quad(gram.lo, c, r);
+                const u32x2 h = *small_quad(gram.hi, c, r), l = *small_quad(gram.lo, c, r);
                 float x[4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
@@ -801,18 +784,11 @@ __global__ __launch_bounds__(64 * kSmallWaves) void muon_small_kernel(MuonSmallA
                 u32x2 ph, pl;
                 split4(x[0], x[1], x[2], x[3], ph, pl);
                 *small_quad(poly.hi, c, r) = ph;
-                if constexpr (kOut == kSplit) *small_quad(poly.lo, c, r) = pl;
+                *small_quad(poly.lo, c, r) = pl;
             }
         }
         __syncthreads();
-    };
-    int it = 0;
-    for (; it < a.split_steps; ++it) iteration(FormOf<kSplit>{}, FormOf<kSplit>{}, it);
-    if constexpr (kPlainEnd) {
-        iteration(FormOf<kSplit>{}, FormOf<kPlain>{}, it);
-        for (++it; it < a.steps; ++it) iteration(FormOf<kPlain>{}, FormOf<kPlain>{}, it);
     }
-    constexpr int kForm = kPlainEnd ? kPlain : kSplit;
 
     // O = P X, lane = the user's column, so that a wave writes along rows
     float *param = nullptr;
@@ -832,7 +808,7 @@ __global__ __launch_bounds__(64 * kSmallWaves) void muon_small_kernel(MuonSmallA
             for (int s = 0; s < kSteps; ++s) {
                 const half8 ph = small_frag(poly.hi, 32u * i + ln, 2u * s + half);
                 const half8 pl = small_frag(poly.lo, 32u * i + ln, 2u * s + half);
-                v = m.tall ? mfma_form<kForm>(xh[b][s], xl[b][s], ph, pl, v) : mfma_form<kForm>(ph, pl, xh[b][s], xl[b][s], v);
+                v = m.tall ? mfma_split(xh[b][s], xl[b][s], ph, pl, v) : mfma_split(ph, pl, xh[b][s], xl[b][s], v);
             }
             const uint32_t r0 = (m.tall ? col0 : 32u * i) + 4u * half, c = m.tall ? 32u * i + ln : col0 + ln;
             float old[16];
@@ -888,8 +864,9 @@ __global__ __launch_bounds__(256) void muon_sums_kernel(MuonWork w, MuonSumArgs 
 
 // The images of X_0 and X_0^T, one 64 x 64 tile of the user's matrix a
 // workgroup.  A norm that is not finite makes all of X_0 NaN.
-template <bool kBf16, bool kRaw, int kForm>
+template <bool kBf16, bool kRaw>
 __global__ __launch_bounds__(256) void muon_prep_kernel(MuonWork w, MuonPrepArgs a) {
+    constexpr int kForm = kRaw ? kPlain : kSplit;
     __shared__ double s[4];
     __shared__ float y[64][65];
     if (blockIdx.x == 0) a.arrived[threadIdx.x] = 0u;
@@ -1172,43 +1149,32 @@ hipError_t launch_muon_sums(bool bf16, const MuonWork &w, const MuonSumArgs &a, 
 
 hipError_t launch_muon_prep(bool bf16, bool raw, int form, const MuonWork &w, const MuonPrepArgs &a, hipStream_t s) {
     const dim3 grid(w.n_tiles), block(256);
-    if (raw) {
-        if (!bf16 || form != kPlain) return hipErrorInvalidValue;
-        muon_prep_kernel<true, true, kPlain><<<grid, block, 0, s>>>(w, a);
-    } else if (form == kSplit) {
-        if (bf16) muon_prep_kernel<true, false, kSplit><<<grid, block, 0, s>>>(w, a);
-        else muon_prep_kernel<false, false, kSplit><<<grid, block, 0, s>>>(w, a);
-    } else {
-        if (bf16) muon_prep_kernel<true, false, kPlain><<<grid, block, 0, s>>>(w, a);
-        else muon_prep_kernel<false, false, kPlain><<<grid, block, 0, s>>>(w, a);
-    }
+    if (form != (raw ? kPlain : kSplit) || (raw && !bf16)) return hipErrorInvalidValue;
+    if (raw) muon_prep_kernel<true, true><<<grid, block, 0, s>>>(w, a);
+    else if (bf16) muon_prep_kernel<true, false><<<grid, block, 0, s>>>(w, a);
+    else muon_prep_kernel<false, false><<<grid, block, 0, s>>>(w, a);
     return hipGetLastError();
 }
 
 template <class T>
-static hipError_t product_of(int product, int in, int out, const MuonGemmArgs &a, hipStream_t s) {
+static hipError_t product_of(int product, int in, int jobs, const MuonGemmArgs &a, hipStream_t s) {
     const uint32_t per_job = a.work.n_whole + (a.work.n_tiles - a.work.n_whole) * a.work.parts;
-    const dim3 grid(a.left2 ? 2 * per_job : per_job), block(T::kThreads);
-#define MUON_CASE(p, i, o)                                                       \
-    if (product == p && in == i && out == o) {                                   \
-        muon_product_kernel<T, p, i, o><<<grid, block, 0, s>>>(a);               \
+    const dim3 grid(jobs * per_job), block(T::kThreads);
+    if (jobs != (a.left2 ? 2 : 1)) return hipErrorInvalidValue;
+#define MUON_CASE(p, i)                                                          \
+    if (product == p && in == i) {                                               \
+        muon_product_kernel<T, p, i><<<grid, block, 0, s>>>(a);                  \
         return hipGetLastError();                                                \
     }
-    MUON_CASE(kGram, kSplit, kSplit)
-    MUON_CASE(kPolynomial, kSplit, kSplit)
-    MUON_CASE(kCommuting, kSplit, kSplit)
-    MUON_CASE(kUpdate, kSplit, kSplit)
-    MUON_CASE(kUpdate, kSplit, kPlain)
-    MUON_CASE(kGram, kPlain, kSplit)
-    MUON_CASE(kUpdate, kMixed, kSplit)
-    MUON_CASE(kUpdate, kMixed, kPlain)
-    MUON_CASE(kGram, kPlain, kPlain)
-    MUON_CASE(kPolynomial, kPlain, kPlain)
-    MUON_CASE(kUpdate, kPlain, kPlain)
-    MUON_CASE(kLastF32, kSplit, kSplit)
-    MUON_CASE(kLastBf16, kSplit, kSplit)
-    MUON_CASE(kLastBf16, kPlain, kPlain)
-    MUON_CASE(kLastParams, kSplit, kSplit)
+    MUON_CASE(kGram, kSplit)
+    MUON_CASE(kGram, kPlain)
+    MUON_CASE(kPolynomial, kSplit)
+    MUON_CASE(kCommuting, kSplit)
+    MUON_CASE(kUpdate, kSplit)
+    MUON_CASE(kUpdate, kMixed)
+    MUON_CASE(kLastF32, kSplit)
+    MUON_CASE(kLastBf16, kSplit)
+    MUON_CASE(kLastParams, kSplit)
 #undef MUON_CASE
     return hipErrorInvalidValue;
 }
@@ -1225,10 +1191,10 @@ typedef Tiling<128, 128, 2, 4, 2, 4> Tiling128;
 typedef Tiling<128, 128, 2, 2, 2, 2> Tiling128Many;
 constexpr uint32_t kManyTiles = 384;
 
-hipError_t launch_muon_product(int tiling, int product, int in, int out, const MuonGemmArgs &a, hipStream_t s) {
-    if (tiling == kTile64) return product_of<Tiling64>(product, in, out, a, s);
-    if (a.work.n_tiles >= kManyTiles) return product_of<Tiling128Many>(product, in, out, a, s);
-    return product_of<Tiling128>(product, in, out, a, s);
+hipError_t launch_muon_product(int tiling, int product, int in, int jobs, const MuonGemmArgs &a, hipStream_t s) {
+    if (tiling == kTile64) return product_of<Tiling64>(product, in, jobs, a, s);
+    if (a.work.n_tiles >= kManyTiles) return product_of<Tiling128Many>(product, in, jobs, a, s);
+    return product_of<Tiling128>(product, in, jobs, a, s);
 }
 
 hipError_t launch_muon_small(int64_t short_side, int64_t long_side, const MuonSmallArgs &a, hipStream_t s) {
@@ -1237,13 +1203,8 @@ hipError_t launch_muon_small(int64_t short_side, int64_t long_side, const MuonSm
     if (short_side > kSmallShort || cols < 1 || cols > 3) return hipErrorInvalidValue;
 #define MUON_SMALL(r, c)                                                    \
     if ((short_side <= 32) == (r == 1) && cols == c) {                      \
-        if (a.split_steps < a.steps) {                                      \
-            if (a.u_bf16) muon_small_kernel<r, c, true, true><<<grid, block, 0, s>>>(a);  \
-            else muon_small_kernel<r, c, false, true><<<grid, block, 0, s>>>(a);          \
-        } else {                                                            \
-            if (a.u_bf16) muon_small_kernel<r, c, true, false><<<grid, block, 0, s>>>(a); \
-            else muon_small_kernel<r, c, false, false><<<grid, block, 0, s>>>(a);         \
-        }                                                                   \
+        if (a.u_bf16) muon_small_kernel<r, c, true><<<grid, block, 0, s>>>(a);            \
+        else muon_small_kernel<r, c, false><<<grid, block, 0, s>>>(a);      \
         return hipGetLastError();                                           \
     }
     MUON_SMALL(1, 1)

@@ -28,9 +28,9 @@ constexpr int kStageSlots = 8;  // pinned staging buffers per state
 constexpr int64_t kGroupElements = int64_t(1) << 26;
 constexpr int64_t kMaxDim = int64_t(1) << 21;
 constexpr int64_t kMaxSums = 1024;  // workgroups that share a matrix's sum of squares
-// The growth of a rounding error up to which single fp16 factors and runs of
-// three iterations are taken, and the shortest side for runs (see runs_of).
-constexpr double kPlainGrowth = 12.0;
+// The growth of a rounding error up to which runs of three iterations are
+// taken, and the shortest side for runs (see runs_of).
+constexpr double kRunGrowth = 12.0;
 constexpr int64_t kPairShort = 256, kTripleShort = 512;
 constexpr float kDefaultCoefficients[3] = {3.4445f, -4.7750f, 2.0315f};
 
@@ -331,20 +331,10 @@ int check_draw_first(const std::vector<Shape> &shapes, const int64_t *first) {
 
 int64_t element_bytes(int32_t storage) { return storage == MUON_STORE_F32 ? 4 : (storage == MUON_STORE_BF16 ? 2 : 1); }
 
-// The coefficients of iteration k, and how the factors are held in it.
+// The coefficients of iteration k.
 void coefficients_of(const muon_iteration &it, int k, float c[3]) {
     const float *p = it.coefficients ? it.coefficients + 3 * k : kDefaultCoefficients;
     for (int i = 0; i < 3; ++i) c[i] = p[i];
-}
-void forms_of(const muon_iteration &it, bool plain_allowed, int forms[MUON_MAX_STEPS]) {
-    double growth = 1.0;
-    for (int k = it.steps - 1; k >= 0; --k) {
-        float c[3];
-        coefficients_of(it, k, c);
-        growth *= std::fabs((double)c[0]);
-        forms[k] = plain_allowed && growth <= kPlainGrowth ? kPlain : kSplit;
-        if (forms[k] == kSplit) plain_allowed = false;
-    }
 }
 
 MuonSmallArgs small_args(const MuonWork &w, const void *u, bool u_bf16, const muon_iteration &it, int product) {
@@ -355,12 +345,6 @@ MuonSmallArgs small_args(const MuonWork &w, const void *u, bool u_bf16, const mu
     a.eps = (double)it.eps;
     a.product = product;
     a.steps = it.steps;
-    a.split_steps = it.steps;
-    if (product == kLastBf16) {
-        int forms[MUON_MAX_STEPS];
-        forms_of(it, true, forms);
-        a.split_steps = (int32_t)(std::find(forms, forms + it.steps, (int)kPlain) - forms);
-    }
     for (int k = 0; k < it.steps; ++k) coefficients_of(it, k, a.coefficients + 3 * k);
     return a;
 }
@@ -376,27 +360,24 @@ MuonSmallArgs small_args(const MuonWork &w, const void *u, bool u_bf16, const mu
 // 1.1 to 1.25 times that with no runs; with runs by 4 times at 64 x 5000, 1.4 at
 // 256 x 4096, 0.9 at 600 x 5000, and by 30 times with three iterations at 3 x 5000.
 // So pairs are taken from kPairShort rows on, three iterations from kTripleShort
-// on, once, first, and while |a_1 a_2| is at most kPlainGrowth; four fail.
-// Factors held in single fp16 values are not put into runs.
+// on, once, first, and while |a_1 a_2| is at most kRunGrowth; four fail.
 struct Run {
     int first, length;
 };
-std::vector<Run> runs_of(const muon_iteration &it, const int *forms, const Work &size) {
+std::vector<Run> runs_of(const muon_iteration &it, const Work &size) {
     auto a = [&](int k) {
         float c[3];
         coefficients_of(it, k, c);
         return std::fabs((double)c[0]);
     };
-    int split = 0;
-    while (split < it.steps && forms[split] == kSplit) ++split;
     std::vector<Run> runs;
     int k = 0;
-    if (split % 2 == 1) {  // pairs from the end, three iterations or one before them
-        const bool three = size.triples && split >= 3 && it.steps > 3 && a(0) * a(1) <= kPlainGrowth && a(0) * a(1) * a(2) <= 64.0;
+    if (it.steps % 2 == 1) {  // pairs from the end, three iterations or one before them
+        const bool three = size.triples && it.steps > 3 && a(0) * a(1) <= kRunGrowth && a(0) * a(1) * a(2) <= 64.0;
         runs.push_back(Run{0, three ? 3 : 1});
         k = runs[0].length;
     }
-    while (size.pairs && k + 1 < split) {
+    while (size.pairs && k + 1 < it.steps) {
         if (a(k) * a(k + 1) <= 64.0) {  // an entry of P_2 P_1 has to stay below 256
             runs.push_back(Run{k, 2});
             k += 2;
@@ -408,35 +389,32 @@ std::vector<Run> runs_of(const muon_iteration &it, const int *forms, const Work 
     return runs;
 }
 
-// Whether a bf16 X_0 can be taken as it is: factors are split at first, and the
-// first run ends before the last iteration.
-bool raw_start(const muon_iteration &it, const int *forms, const Work &size) {
-    return forms[0] == kSplit && runs_of(it, forms, size)[0].length < it.steps;
-}
+// Whether a bf16 X_0 can be taken as it is: the first run ends before the last
+// iteration.
+bool raw_start(const muon_iteration &it, const Work &size) { return runs_of(it, size)[0].length < it.steps; }
 
 // The products of all iterations, X_0 and X_0^T being in f.x[0], f.xt[0].
 // raw: they are bf16 values times a power of two in plain slabs, and w.phi times
 // them is X_0: their own products need one partial product for three, and P X
 // two, in the first run, which is not the last (raw_start).
 hipError_t run_products(const Workspace &w, const MuonWork &square, const MuonWork &update, const Work &size, bool raw,
-                        const muon_iteration &it, const int *forms, int last, const MuonGemmArgs &into, hipStream_t s) {
+                        const muon_iteration &it, int last, const MuonGemmArgs &into, hipStream_t s) {
     hipError_t e = hipSuccess;
-    int form = kSplit;
     const MuonArrays &f = w.f;
-    auto launch = [&](int product, int out, MuonGemmArgs &g) {
+    auto launch = [&](int product, MuonGemmArgs &g) {
         if (e != hipSuccess) return;
         const bool is_square = product == kGram || product == kPolynomial || product == kCommuting;
         const int tiling = is_square ? size.square_tiling : size.update_tiling;
         const Load &load = product == kGram ? size.gram : (is_square ? size.square : size.update);
         g.work = is_square ? square : update;
-        const int in = g.phi ? (product == kGram ? kPlain : kMixed) : form;
-        const Cut cut = load.cut(tiling, g.work.n_tiles, g.left2 ? 2 : 1, in);
+        const int in = g.phi ? (product == kGram ? kPlain : kMixed) : kSplit, jobs = g.left2 ? 2 : 1;
+        const Cut cut = load.cut(tiling, g.work.n_tiles, jobs, in);
         g.work.window = load.window(tiling);
         g.work.n_whole = cut.whole;
         g.work.parts = cut.parts;
         g.work.partial = w.parts;
         g.work.arrived = w.arrived;
-        e = launch_muon_product(tiling, product, in, out, g, s);
+        e = launch_muon_product(tiling, product, in, jobs, g, s);
     };
     auto polynomial = [&](const char *a, char *p, int k) {
         float c[3];
@@ -447,7 +425,7 @@ hipError_t run_products(const Workspace &w, const MuonWork &square, const MuonWo
         g.ca = c[0];
         g.cb = c[1];
         g.cc = c[2];
-        launch(kPolynomial, form, g);
+        launch(kPolynomial, g);
     };
     auto commuting = [&](const char *left, const char *right, char *out, const char *left2 = nullptr,
                          const char *right2 = nullptr, char *out2 = nullptr) {
@@ -458,19 +436,18 @@ hipError_t run_products(const Workspace &w, const MuonWork &square, const MuonWo
         g.left2 = left2;
         g.right2 = right2;
         g.out2 = out2;
-        launch(kCommuting, form, g);
+        launch(kCommuting, g);
     };
     char *const A = f.square[0], *const T = f.square[1], *const P = f.square[2], *const R = f.square[3],
                *const U = f.square[4];
     int cur = 0;
-    for (const Run &run : runs_of(it, forms, size)) {
-        form = forms[run.first];
+    for (const Run &run : runs_of(it, size)) {
         const float *phi = raw && run.first == 0 ? w.phi : nullptr;
         MuonGemmArgs g{};
         g.left = f.x[cur];
         g.out = A;
         g.phi = phi;
-        launch(kGram, form, g);
+        launch(kGram, g);
         polynomial(A, P, run.first);
         const char *q = P;
         if (run.length >= 2) {
@@ -496,10 +473,10 @@ hipError_t run_products(const Workspace &w, const MuonWork &square, const MuonWo
             g.out = f.x[cur ^ 1];
             g.out_t = f.xt[cur ^ 1];
             g.phi = phi;
-            launch(kUpdate, forms[next], g);
+            launch(kUpdate, g);
             cur ^= 1;
         } else {
-            launch(last, form, g);
+            launch(last, g);
         }
     }
     return e;
@@ -874,8 +851,6 @@ int muon_step(muon_state *s, float *const *params, const void *const *grads, con
         TensorRef *tensors = nullptr;
         if ((rc = pointer_table(s, params, grads, stream, &tensors))) return rc;
 
-        int forms[MUON_MAX_STEPS];
-        forms_of(hp->iteration, false, forms);
         for (const Group &g : s->groups) {
             const Workspace w = carve(s->workspace, g.size, g.x_bytes, g.a_bytes, g.blocks);
             MuonStepArgs a{};
@@ -925,11 +900,11 @@ int muon_step(muon_state *s, float *const *params, const void *const *grads, con
             p.eps = (double)hp->iteration.eps;
             p.x = w.f.x[0];
             p.xt = w.f.xt[0];
-            if ((e = launch_muon_prep(false, false, forms[0], table_work(g, g.d_prep, g.prep.size()), p, stream)) !=
+            if ((e = launch_muon_prep(false, false, kSplit, table_work(g, g.d_prep, g.prep.size()), p, stream)) !=
                 hipSuccess)
                 return hip_fail(e, "preparation launch");
             if ((e = run_products(w, table_work(g, g.d_square, g.square.size()),
-                                  table_work(g, g.d_update, g.update.size()), g.size, false, hp->iteration, forms, kLastParams, into,
+                                  table_work(g, g.d_update, g.update.size()), g.size, false, hp->iteration, kLastParams, into,
                                   stream)) != hipSuccess)
                 return hip_fail(e, "product launch");
         }
@@ -1270,8 +1245,6 @@ int muon_orthogonalize(const muon_matrices *mats, const void *x, void *out, cons
         }
 
         hipStream_t stream = reinterpret_cast<hipStream_t>(hip_stream);
-        int forms[MUON_MAX_STEPS];
-        forms_of(*iteration, mats->out_dtype == ADAM_GRAD_BF16, forms);
         MuonWork work{};
         work.one.rows = (uint32_t)shape.rows;
         work.one.cols = (uint32_t)shape.cols;
@@ -1324,8 +1297,8 @@ int muon_orthogonalize(const muon_matrices *mats, const void *x, void *out, cons
             prep.x = w.f.x[0];
             prep.xt = w.f.xt[0];
             prep.phi = w.phi;
-            const bool raw = xe == 2 && raw_start(*iteration, forms, p.size);
-            if ((e = launch_muon_prep(xe == 2, raw, raw ? kPlain : forms[0], with((p.mp / 64) * (p.np / 64)), prep, stream)) != hipSuccess)
+            const bool raw = xe == 2 && raw_start(*iteration, p.size);
+            if ((e = launch_muon_prep(xe == 2, raw, raw ? kPlain : kSplit, with((p.mp / 64) * (p.np / 64)), prep, stream)) != hipSuccess)
                 return hip_fail(e, "preparation launch");
             MuonGemmArgs into{};
             into.o = out;
@@ -1339,7 +1312,7 @@ int muon_orthogonalize(const muon_matrices *mats, const void *x, void *out, cons
             }
             const int64_t sb = p.mp / size_of(size.square_tiling), ub = p.mp / size_of(size.update_tiling),
                           lb = p.np / size_of(size.update_tiling);
-            if ((e = run_products(w, with(sb * (sb + 1) / 2), with(ub * lb), size, raw, *iteration, forms,
+            if ((e = run_products(w, with(sb * (sb + 1) / 2), with(ub * lb), size, raw, *iteration,
                                   oe == 2 ? kLastBf16 : kLastF32, into, stream)) != hipSuccess)
                 return hip_fail(e, "product launch");
         }
