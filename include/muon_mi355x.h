@@ -25,9 +25,13 @@
  * with s by enum muon_scale.  The norm is summed in fp64.  The products run
  * on the fp16 matrix units with fp32 sums: each factor is held as two fp16
  * values (high part and remainder, 22 bits; X and A scaled by 2^10, the
- * polynomial by 2^8) and three of the four partial products are summed, so
- * that O is about as far from the exact result as a computation in fp32 is
- * (at most some four times as far, where that one loses almost nothing).
+ * polynomial by 2^8, remainders by 2^11 besides) and three of the four partial
+ * products are summed, so that O is about as far from the exact result as a
+ * computation in fp32 is (at most some six times as far, where that one loses
+ * almost nothing).  Entries of X below 2^-24, as one entry or column with nearly
+ * all of the norm leaves the others, have an error of 2^-46 instead of 22 bits,
+ * and below 2^-33 those of X_0 from a bf16 matrix one of 2^-40; the
+ * iterations may grow either by the product of the |a_k|.
  * Iterations of larger matrices may be taken two or three at a time, as one
  * polynomial in the first one's A.  A bf16 output is the fp32 result rounded
  * once, to nearest even.

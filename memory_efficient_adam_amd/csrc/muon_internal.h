@@ -15,8 +15,9 @@ namespace adam_mi355x {
 // rows; in each, slabs of 4 KB along the rows' elements; in each slab four
 // fragments of 1 KB, whose 16 bytes at position l are what lane l holds: row
 // l % 32, elements 8 (l / 32) .. + 7 of the fragment's 16.
-//   split slabs (two fp16 values per element): 32 elements; fragments: high
-//     parts of the first 16, their remainders, the same of the second 16;
+//   split slabs (two fp16 values per element, the remainder times 2^11): 32
+//     elements; fragments: high parts of the first 16, their remainders, the
+//     same of the second 16;
 //   plain slabs (one fp16 value per element; an X_0 taken as its bf16 source
 //     has it): 64 elements, 16 per fragment.
 // So a slab goes to LDS as it is, is read there without bank conflicts, and

@@ -4,12 +4,18 @@
 // The orthogonalisation is matrix products: per iteration A = X X^T,
 // P = a I + b A + c A^2 and X <- P X, with X short x long (m x n).  They run
 // on the fp16 matrix cores at fp32's accuracy: a factor is held as
-// hi + lo, two fp16 values (22 bits), and hi hi + hi lo + lo hi is summed in
-// fp32 (what is left out is below 2^-22 of the product).  Three fp16 products cost
-// a quarter of what the fp32 matrix instructions take for one.  The factors
-// are scaled by a power of two, so that no part of an entry that matters
-// falls below fp16's range (X and A by 2^10, P by 2^8: an entry of 2^-13 still
-// has all 22 bits, smaller ones an error of 2^-35).  A and P are symmetric:
+// hi + 2^-11 lo, two fp16 values (22 bits), and hi hi + 2^-11 (hi lo + lo hi) is
+// summed in fp32 (what is left out is below 2^-22 of the product).  Three fp16
+// products cost a quarter of what the fp32 matrix instructions take for one.
+// The factors are scaled by a power of two (X and A by 2^10, P by 2^8), and the
+// remainder by 2^11 once more, so that no part of an entry that matters falls
+// below fp16's range: an entry of X of 2^-24 still has all 22 bits, smaller ones
+// an error of 2^-46.  One entry or column that holds nearly all of a matrix's
+// norm leaves the others that small, and the iterations then grow them by the
+// product of the a_k (485): with remainders in the scale of the high parts
+// (errors of 2^-35 from 2^-13 down) such a matrix of 520 x 1600 was off by
+// 1e-5, the small entries by up to 7e-3 of themselves.  The price is a sum of
+// its own for the scaled products.  A and P are symmetric:
 // only tiles on and below the diagonal are computed, and stored twice.  The
 // term a X is a I in P, so that an update reads X once, as a factor.
 #include <hip/hip_runtime.h>
@@ -23,6 +29,7 @@ namespace {
 constexpr float kTiny = 0x1p-112f;  // smallest block maximum that is encoded (8-bit momentum)
 constexpr float kScaleX = 1024.0f;  // X and A are held times 2^10
 constexpr float kScaleP = 256.0f;   // P is held times 2^8
+constexpr float kScaleLo = 2048.0f, kUnscaleLo = 1.0f / kScaleLo;  // remainders are held times 2^11 besides
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
@@ -48,9 +55,10 @@ __device__ __forceinline__ float load_elem(const void *p, uint64_t i) {
         return static_cast<const float *>(p)[i];
 }
 
-// Two fp32 values as hi + lo each, packed: the sums hold 22 bits.  Pairs are
-// converted in one instruction (to nearest even), and a remainder y - hi
-// (exact) is one mixed-precision fma, which the compiler does not form by itself.
+// Two fp32 values as hi + 2^-11 lo each, packed: the sums hold 22 bits.  Pairs
+// are converted in one instruction (to nearest even), and a remainder y - hi
+// (exact, at most half of hi's last place: 2^11 times it stays in range) is one
+// mixed-precision fma, which the compiler does not form by itself.
 typedef _Float16 half2v __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ void split2(float y0, float y1, uint32_t &hi, uint32_t &lo) {
@@ -59,7 +67,7 @@ __device__ __forceinline__ void split2(float y0, float y1, uint32_t &hi, uint32_
     float r0, r1;
     asm("v_fma_mix_f32 %0, -%1, 1.0, %2 op_sel:[0,0,0] op_sel_hi:[1,0,0]" : "=v"(r0) : "v"(hi), "v"(y0));
     asm("v_fma_mix_f32 %0, -%1, 1.0, %2 op_sel:[1,0,0] op_sel_hi:[1,0,0]" : "=v"(r1) : "v"(hi), "v"(y1));
-    const half2v l = __builtin_convertvector((f32x2{r0, r1}), half2v);
+    const half2v l = __builtin_convertvector((f32x2{r0 * kScaleLo, r1 * kScaleLo}), half2v);
     lo = __builtin_bit_cast(uint32_t, l);
 }
 __device__ __forceinline__ void split4(float y0, float y1, float y2, float y3, u32x2 &hi, u32x2 &lo) {
@@ -81,6 +89,11 @@ __device__ __forceinline__ void split8(const float (&y)[8], half8 &hi, half8 &lo
     }
     hi = __builtin_bit_cast(half8, h);
     lo = __builtin_bit_cast(half8, l);
+}
+
+// The value that an entry's high part and remainder stand for.
+__device__ __forceinline__ float join(uint32_t hi, uint32_t lo) {
+    return fmaf((float)__builtin_bit_cast(_Float16, (uint16_t)lo), kUnscaleLo, (float)__builtin_bit_cast(_Float16, (uint16_t)hi));
 }
 
 // Sum over the workgroup's kWaves waves in a fixed order (s: kWaves doubles).
@@ -219,7 +232,7 @@ __device__ __forceinline__ void fetch(Sources<T, kForm> &src, char *stage, int w
 // rd and wr are different stages of LDS: without that promise the compiler
 // would wait for the fetches before every read.
 template <class T, int kForm>
-__device__ __forceinline__ void slab(f32x16 (&acc)[T::kI][T::kJ], const char *__restrict rd, char *__restrict wr,
+__device__ __forceinline__ void slab(f32x16 (&acc)[T::kI][T::kJ], f32x16 (&cross)[T::kI][T::kJ], const char *__restrict rd, char *__restrict wr,
                                      Sources<T, kForm> &src, bool more, int wave, int lane) {
     constexpr int kSteps = kForm == kPlain ? 4 : 2;
     constexpr int kRight = T::right_bytes(kForm);
@@ -246,9 +259,9 @@ __device__ __forceinline__ void slab(f32x16 (&acc)[T::kI][T::kJ], const char *__
             for (int j = 0; j < T::kJ; ++j) {
                 acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(l[i], r[j], acc[i][j], 0, 0, 0);
                 if constexpr (kForm == kSplit)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(l[i], r2[j], acc[i][j], 0, 0, 0);
+                    cross[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(l[i], r2[j], cross[i][j], 0, 0, 0);
                 if constexpr (kForm != kPlain)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(l2[i], r[j], acc[i][j], 0, 0, 0);
+                    cross[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(l2[i], r[j], cross[i][j], 0, 0, 0);
             }
     }
 }
@@ -256,7 +269,8 @@ __device__ __forceinline__ void slab(f32x16 (&acc)[T::kI][T::kJ], const char *__
 // sum = left right^T over `slabs` slabs (left, right: the tile's first slab;
 // *_block: bytes from one 32-row block to the next), summed in runs of some
 // kRun slabs: one sum that took every term of a long row in turn would
-// lose more to fp32's rounding than the split factors do.  kStages - 1 slabs
+// lose more to fp32's rounding than the split factors do.  (The products with
+// remainders, 2^-11 of the others, are one sum.)  kStages - 1 slabs
 // are under way to LDS while the matrix cores work on one; at the barrier
 // before slab s, its fetches are done and every wave has read slab s - 1,
 // whose place the next fetch takes.
@@ -282,11 +296,11 @@ __device__ __forceinline__ void product(f32x16 (&sum)[T::kI][T::kJ], const char 
 #pragma unroll
     for (int s = 0; s < kS - 1; ++s)
         if (s < (int)slabs) fetch<T, kForm>(src, lds + s * T::kStage, wave, lane);
-    f32x16 acc[T::kI][T::kJ];
+    f32x16 acc[T::kI][T::kJ], cross[T::kI][T::kJ];
 #pragma unroll
     for (int i = 0; i < T::kI; ++i)
 #pragma unroll
-        for (int j = 0; j < T::kJ; ++j) sum[i][j] = acc[i][j] = f32x16{};
+        for (int j = 0; j < T::kJ; ++j) sum[i][j] = acc[i][j] = cross[i][j] = f32x16{};
     for (uint32_t s0 = 0; s0 < slabs; s0 += kS) {
 #pragma unroll
         for (int u = 0; u < kS; ++u) {
@@ -294,7 +308,7 @@ __device__ __forceinline__ void product(f32x16 (&sum)[T::kI][T::kJ], const char 
             if (s >= slabs) break;
             if (s + (kS - 2) < slabs) wait_and_meet<(kS - 2) * T::loads(kForm)>();
             else wait_and_meet<0>();
-            slab<T, kForm>(acc, lds + u * T::kStage, lds + ((u + kS - 1) % kS) * T::kStage, src, s + (kS - 1) < slabs, wave,
+            slab<T, kForm>(acc, cross, lds + u * T::kStage, lds + ((u + kS - 1) % kS) * T::kStage, src, s + (kS - 1) < slabs, wave,
                            lane);
         }
         if (s0 % kRun + kS >= kRun || s0 + kS >= slabs) {
@@ -307,6 +321,13 @@ __device__ __forceinline__ void product(f32x16 (&sum)[T::kI][T::kJ], const char 
                 }
         }
     }
+    if constexpr (kForm != kPlain)
+#pragma unroll
+        for (int i = 0; i < T::kI; ++i)
+#pragma unroll
+            for (int j = 0; j < T::kJ; ++j)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) sum[i][j][e] = fmaf(cross[i][j][e], kUnscaleLo, sum[i][j][e]);
 }
 
 // Four values down the rows of one column per lane -> four along a row: a
@@ -530,8 +551,7 @@ void muon_product_kernel(MuonGemmArgs a) {
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             const uint32_t hw = q < 2 ? h.x : h.y, lw = q < 2 ? l.x : l.y;
-                            const float av = (float)__builtin_bit_cast(_Float16, (uint16_t)(hw >> (16 * (q & 1)))) +
-                                             (float)__builtin_bit_cast(_Float16, (uint16_t)(lw >> (16 * (q & 1))));
+                            const float av = join(hw >> (16 * (q & 1)), lw >> (16 * (q & 1)));
                             float x = fmaf(cb, av, cc * v[4 * g + q]);
                             if (r + 8u * g + q == c) x += ca;
                             v[4 * g + q] = x;
@@ -568,8 +588,8 @@ void muon_product_kernel(MuonGemmArgs a) {
 
 // ---------------------------------------------------------------- small matrices
 // A whole orthogonalisation in one workgroup of 8 waves, X staying in
-// registers, in one launch: 23 us for an fp32 matrix of 48 x 80 (one launch per
-// product, 69), 82 us for 96 of 64 x 768 in bf16 (250).
+// registers, in one launch: 25 us for an fp32 matrix of 48 x 80 (one launch per
+// product, 69), 85 us for 96 of 64 x 768 in bf16 (250).
 //
 // A wave holds blocks of 32 columns of X, block w + 8 b at wave w, as the
 // matrix cores give them: lane l holds column l % 32, rows 8 g + 4 (l / 32) + q
@@ -601,12 +621,36 @@ __device__ __forceinline__ u32x2 *small_quad(uint4 *image, uint32_t row, uint32_
     return reinterpret_cast<u32x2 *>(reinterpret_cast<char *>(image) + small_pos(row, 2u * s + (k4 & 1u)) + (k4 >> 1) * 8u);
 }
 
+// Values read from LDS before are read again rather than kept: P's fragments are
+// the same for every block of X, and holding them all would spill registers (96
+// matrices of 64 x 768: 121 us without, 85 with).
+__device__ __forceinline__ void forget_loads() { asm volatile("" ::: "memory"); }
+
 __device__ __forceinline__ f32x16 mfma(half8 a, half8 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
 }
-// A product of factors in two fp16 values.
-__device__ __forceinline__ f32x16 mfma_split(half8 ah, half8 al, half8 bh, half8 bl, f32x16 c) {
-    return mfma(al, bh, mfma(ah, bl, mfma(ah, bh, c)));
+// The part of a product that has the remainders of one factor, times 2^11.
+__device__ __forceinline__ f32x16 mfma_cross(half8 ah, half8 al, half8 bh, half8 bl, f32x16 c) {
+    return mfma(al, bh, mfma(ah, bl, c));
+}
+__device__ __forceinline__ void add_cross(f32x16 &v, const f32x16 &cross) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] = fmaf(cross[e], kUnscaleLo, v[e]);
+}
+// a[s] b[s] summed over kSteps fragments.
+template <int kSteps, class A, class B>
+__device__ __forceinline__ f32x16 product_of_fragments(const A &a, const B &b) {
+    f32x16 v = {}, cross = {};
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+        half8 ah, al, bh, bl;
+        a(s, ah, al);
+        b(s, bh, bl);
+        v = mfma(ah, bh, v);
+        cross = mfma_cross(ah, al, bh, bl, cross);
+    }
+    add_cross(v, cross);
+    return v;
 }
 
 template <int kRows, int kCols, bool kBf16>
@@ -672,6 +716,19 @@ __global__ __launch_bounds__(64 * kSmallWaves) void muon_small_kernel(MuonSmallA
         }
     __syncthreads();
 
+    // rows of a square matrix, and the wave's block b of X, as factors
+    auto square_rows = [&](const SmallSquare &m, uint32_t row) {
+        return [&m, row, half](int s, half8 &h, half8 &l) {
+            h = small_frag(m.hi, row, 2u * s + half);
+            l = small_frag(m.lo, row, 2u * s + half);
+        };
+    };
+    auto columns = [&](int b) {
+        return [&, b](int s, half8 &h, half8 &l) {
+            h = xh[b][s];
+            l = xl[b][s];
+        };
+    };
     for (int it = 0; it < a.steps; ++it) {
         // X <- P X and, along the way, A = X X^T
         f32x16 acc[kSquare];
@@ -681,14 +738,12 @@ __global__ __launch_bounds__(64 * kSmallWaves) void muon_small_kernel(MuonSmallA
         for (int b = 0; b < kCols; ++b) {
             const uint32_t col0 = 32u * (wave + kSmallWaves * b);
             if (col0 >= n) continue;
+            forget_loads();
             half8 gh[kRows][2], gl[kRows][2];
 #pragma unroll
             for (int i = 0; i < kRows; ++i) {
-                f32x16 v = {};
-#pragma unroll
-                for (int s = 0; s < kSteps; ++s)
-                    v = mfma_split(xh[b][s], xl[b][s], small_frag(poly.hi, 32u * i + ln, 2u * s + half),
-                                   small_frag(poly.lo, 32u * i + ln, 2u * s + half), v);
+                forget_loads();
+                const f32x16 v = product_of_fragments<kSteps>(columns(b), square_rows(poly, 32u * i + ln));
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     float y[8];
@@ -700,20 +755,20 @@ __global__ __launch_bounds__(64 * kSmallWaves) void muon_small_kernel(MuonSmallA
 #pragma unroll
             for (int i = 0; i < kRows; ++i)
 #pragma unroll
-                for (int j = 0; j <= i; ++j)
+                for (int j = 0; j <= i; ++j) {
+                    f32x16 cross = {};
 #pragma unroll
-                    for (int k = 0; k < 2; ++k)
-                        acc[i + j] = mfma_split(gh[i][k], gl[i][k], gh[j][k], gl[j][k], acc[i + j]);
+                    for (int k = 0; k < 2; ++k) {
+                        cross = mfma_cross(gh[i][k], gl[i][k], gh[j][k], gl[j][k], cross);
+                        acc[i + j] = mfma(gh[i][k], gh[j][k], acc[i + j]);
+                    }
+                    add_cross(acc[i + j], cross);
+                }
             if (it == 0) continue;  // P is still one
+            forget_loads();
             f32x16 v[kRows];
 #pragma unroll
-            for (int i = 0; i < kRows; ++i) {
-                v[i] = f32x16{};
-#pragma unroll
-                for (int s = 0; s < kSteps; ++s)
-                    v[i] = mfma_split(small_frag(poly.hi, 32u * i + ln, 2u * s + half),
-                                      small_frag(poly.lo, 32u * i + ln, 2u * s + half), xh[b][s], xl[b][s], v[i]);
-            }
+            for (int i = 0; i < kRows; ++i) v[i] = product_of_fragments<kSteps>(square_rows(poly, 32u * i + ln), columns(b));
 #pragma unroll
             for (int i = 0; i < kRows; ++i)
 #pragma unroll
@@ -758,13 +813,7 @@ __global__ __launch_bounds__(64 * kSmallWaves) void muon_small_kernel(MuonSmallA
         // P, one 32 x 32 block a wave, stored as its transpose (it is symmetric)
         if (wave < kRows * kRows) {
             const uint32_t bi = wave / kRows, bj = wave % kRows;
-            f32x16 p = {};
-#pragma unroll
-            for (int s = 0; s < kSteps; ++s) {
-                const uint32_t chunk = 2u * s + half;
-                p = mfma_split(small_frag(gram.hi, 32u * bi + ln, chunk), small_frag(gram.lo, 32u * bi + ln, chunk),
-                               small_frag(gram.hi, 32u * bj + ln, chunk), small_frag(gram.lo, 32u * bj + ln, chunk), p);
-            }
+            const f32x16 p = product_of_fragments<kSteps>(square_rows(gram, 32u * bi + ln), square_rows(gram, 32u * bj + ln));
             const float ca = a.coefficients[3 * it] * kScaleP, cb = a.coefficients[3 * it + 1] * (kScaleP / kScaleX),
                         cc = a.coefficients[3 * it + 2] * (kScaleP / (kScaleX * kScaleX));
 #pragma unroll
@@ -775,8 +824,7 @@ __global__ __launch_bounds__(64 * kSmallWaves) void muon_small_kernel(MuonSmallA
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     const uint32_t hw = q < 2 ? h.x : h.y, lw = q < 2 ? l.x : l.y;
-                    const float av = (float)__builtin_bit_cast(_Float16, (uint16_t)(hw >> (16 * (q & 1)))) +
-                                     (float)__builtin_bit_cast(_Float16, (uint16_t)(lw >> (16 * (q & 1))));
+                    const float av = join(hw >> (16 * (q & 1)), lw >> (16 * (q & 1)));
                     float v = fmaf(cb, av, cc * p[4 * g + q]);
                     if (r + q == c) v += ca;
                     x[q] = v;
@@ -803,13 +851,8 @@ __global__ __launch_bounds__(64 * kSmallWaves) void muon_small_kernel(MuonSmallA
         if (col0 >= n) continue;
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
-            f32x16 v = {};
-#pragma unroll
-            for (int s = 0; s < kSteps; ++s) {
-                const half8 ph = small_frag(poly.hi, 32u * i + ln, 2u * s + half);
-                const half8 pl = small_frag(poly.lo, 32u * i + ln, 2u * s + half);
-                v = m.tall ? mfma_split(xh[b][s], xl[b][s], ph, pl, v) : mfma_split(ph, pl, xh[b][s], xl[b][s], v);
-            }
+            const auto p = square_rows(poly, 32u * i + ln);
+            const f32x16 v = m.tall ? product_of_fragments<kSteps>(columns(b), p) : product_of_fragments<kSteps>(p, columns(b));
             const uint32_t r0 = (m.tall ? col0 : 32u * i) + 4u * half, c = m.tall ? 32u * i + ln : col0 + ln;
             float old[16];
             if (a.product == kLastParams) {  // all of the block's params at once, then the stores
@@ -897,8 +940,10 @@ __global__ __launch_bounds__(256) void muon_prep_kernel(MuonWork w, MuonPrepArgs
     double inv = sum < __builtin_inf() ? (double)kScaleX / (sqrt(sum) + a.eps) : __builtin_nan("");
     if constexpr (kRaw) {
         // the power of two that brings the norm (and so every entry) to below
-        // 2^14: bf16's 8 bits are exact in fp16 down to 2^-27 of the norm
-        const double power = sum > 0.0 ? ldexp(1.0, 13 - ilogb(sqrt(sum))) : 1.0;
+        // 2^16, of which the largest bf16 value is in fp16's range: bf16's 8 bits
+        // are exact down to 2^-33 of the norm, smaller entries have an error of
+        // at most 2^-40 of it
+        const double power = sum > 0.0 ? ldexp(1.0, 15 - ilogb(sqrt(sum))) : 1.0;
         if (t == 0 && threadIdx.x == 0) a.phi[m.index] = sum > 0.0 ? (float)(inv / power) : 0.0f;
         inv = sum < __builtin_inf() ? power : inv;
     }

@@ -67,3 +67,41 @@ def test_a_bf16_result_is_off_by_its_own_rounding(shape, kind, iteration):
         rounding = float((ref.bfloat16().double() - ref).norm()) / norm
         err = float((out.double() - ref).norm()) / norm
         assert err <= rounding + 2 * (8 * own + 2.0 ** -21), (str(dtype), err, rounding, own)
+
+
+@pytest.mark.parametrize("where", ["entry", "row", "column"])
+@pytest.mark.parametrize("shape", [(60, 90), (64, 700), (300, 30), (300, 500), (520, 1600), (1600, 520), (6, 300, 900)], ids=str)
+def test_one_entry_row_or_column_that_holds_nearly_all_of_the_norm(shape, where):
+    """The others are 1e-7 of it, and the iterations grow them by 485.
+
+    As a whole (fp32 result): the large direction's singular value goes 1, 0.70,
+    1.11, 0.72, 1.09; at slopes of 0.8 to 1.3 what an iteration adds is grown to
+    at most 1.5 times, in all 6.5 times one iteration's share, some 4 roundings
+    of 2^-23: 2^-18.1.  Apart from the large row and column: the rest grows
+    linearly by a each time, an iteration rounds X and P to 2^-23 each, drops
+    2^-24 in products with P and rounds sums, and |P| is up to 3 times a in
+    absolute sums along the large direction: 5 * 5 * 2^-23 * 3 = 9e-6; entries of
+    X_0 of 2.5e-9 have an error of at most 2^-46 besides, 5.7e-6 of them.  Both
+    are below 2^-16.  From a bf16 matrix, entries below 2^-33 = 0.047 * 2.5e-9, 3.7 in
+    a hundred, have an error of at most 2^-40 = 3.7e-4 * 2.5e-9: 7.1e-5 root mean square."""
+    x = torch.randn(shape, generator=_gen(3), device="cuda")
+    big = x.reshape(-1, *shape[-2:])
+    i, j = shape[-2] // 3, shape[-1] // 5
+    at = {"entry": (slice(None), i, j), "row": (slice(None), i), "column": (slice(None), slice(None), j)}[where]
+    big[at] = 1e7 if where == "entry" else big[at] * 1e7
+    for dtype in (torch.float32, torch.bfloat16):
+        y = big.to(dtype)
+        out = ma.muon_orthogonalize(y.reshape(shape), out=torch.empty(shape, device="cuda")).reshape(big.shape)
+        for got, one in zip(out.double(), y):
+            ref = muon_ref.orthogonalize(one)
+            own = float((muon_ref.orthogonalize(one, dtype=torch.float32).double() - ref).norm() / ref.norm())
+            err = float((got - ref).norm() / ref.norm())
+            assert err <= 8 * own + 2.0 ** -18, (str(dtype), err, own)
+            diff = got - ref
+            for t in (diff, ref):
+                if where != "column":
+                    t[i] = 0.0
+                if where != "row":
+                    t[:, j] = 0.0
+            rest = float(diff.norm() / ref.norm())
+            assert rest <= 2.0 ** -16 + (7.1e-5 if dtype == torch.bfloat16 else 0.0), (str(dtype), rest)
