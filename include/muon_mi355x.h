@@ -192,8 +192,10 @@ void muon_state_destroy(muon_state *s);
  * be recorded into a graph; a replay repeats the call as recorded).
  *   x, out: device memory of x_dtype and out_dtype (enum adam_grad_dtype);
  *     element (i, r, c) at i*batch_stride + r*row_stride + c elements, strides
- *     >= 0, row_stride >= cols; aligned to the element.  out's matrices may
- *     not overlap one another or x, except that out may be x itself
+ *     >= 0, row_stride >= cols; aligned to the element.  out's matrices lie one after the other
+ *     (batch_stride at least a matrix's extent) or side by side (all of them
+ *     within a row_stride, as the heads of a fused weight are), and not
+ *     between x's first and last element, except that out may be x itself
  *     with the same strides and type.
  *   workspace: device memory, 256-byte aligned, of at least
  *     muon_orthogonalize_workspace_bytes(batch, rows, cols), which may be 0
@@ -201,8 +203,8 @@ void muon_state_destroy(muon_state *s);
  *     ordered on the device; so must the replays of graphs that recorded one.
  * Errors (no work enqueued): EINVAL (NULL pointer with a non-empty batch, a
  * dimension < 0 or >= 2^21, rows*cols >= 2^32, batch >= 2^31, a stride
- * outside its domain, unknown dtype, an iteration outside its domain,
- * workspace too small), EALIGN; EDEVICE if a launch fails.
+ * outside its domain, out overlapping itself or x, unknown dtype, an iteration
+ * outside its domain, workspace too small), EALIGN; EDEVICE if a launch fails.
  */
 typedef struct {
     int64_t batch, rows, cols;

@@ -1231,8 +1231,12 @@ int muon_orthogonalize(const muon_matrices *mats, const void *x, void *out, cons
             return fail(ADAM_EALIGN, "x or out is not aligned to its element");
         if (reinterpret_cast<uintptr_t>(workspace) % 256) return fail(ADAM_EALIGN, "workspace is not 256-byte aligned");
         const int64_t out_span = (shape.rows - 1) * mats->out_row_stride + shape.cols;
-        if (mats->batch > 1 && mats->out_batch_stride < out_span)
-            return fail(ADAM_EINVAL, "out's matrices overlap: batch stride smaller than a matrix");
+        // one matrix after the other, or (heads of a fused weight) all their first rows
+        // beside each other, then all their second ones
+        const bool beside = mats->out_batch_stride >= shape.cols &&
+                            (mats->batch - 1) * mats->out_batch_stride + shape.cols <= mats->out_row_stride;
+        if (mats->batch > 1 && mats->out_batch_stride < out_span && !beside)
+            return fail(ADAM_EINVAL, "out's matrices overlap: they are neither one after the other nor side by side");
         const bool in_place = x == out && xe == oe && mats->x_row_stride == mats->out_row_stride &&
                               (mats->batch == 1 || mats->x_batch_stride == mats->out_batch_stride);
         if (!in_place) {

@@ -1,0 +1,26 @@
+"""Arguments of the Muon calls, and what the binding makes of them, where no GPU
+is needed: layouts of batches, workspaces, remembered tensors."""
+import pytest
+import torch
+
+import memory_efficient_adam_amd as ma
+from test_muon_host import X, _orth
+
+
+# the heads of a (rows, heads * d) weight: matrices of rows x d, d apart, rows heads * d apart
+HEADS = dict(batch=12, rows=100, cols=64, out_batch_stride=64, out_row_stride=12 * 64)
+
+
+# (the pointers are no memory: calls that are not refused have to end at a missing device)
+@pytest.mark.skipif(torch.cuda.device_count() > 0, reason="would launch on pointers that are no memory")
+def test_matrices_of_out_may_lie_side_by_side():
+    x = dict(x_batch_stride=64, x_row_stride=12 * 64)
+    assert _orth(**HEADS, **x) == -5
+    assert _orth(out=X, **HEADS, **x) == -5  # in place
+    assert _orth(**{**HEADS, "out_row_stride": 13 * 64}, **x) == -5
+    for over in (dict(out_batch_stride=63), dict(out_row_stride=12 * 64 - 1), dict(batch=13), dict(out_batch_stride=0)):
+        assert _orth(**{**HEADS, **over, **x}) == -1 and "overlap" in ma.adam_last_error(), over
+    # all of them count where x may not lie
+    last = X + 4 * (99 * 12 * 64 + 12 * 64)
+    assert _orth(out=last - 4, **HEADS, **x) == -1 and "overlaps" in ma.adam_last_error()
+    assert _orth(out=last, **HEADS, **x) == -5
