@@ -192,7 +192,8 @@ void muon_state_destroy(muon_state *s);
  * be recorded into a graph; a replay repeats the call as recorded).
  *   x, out: device memory of x_dtype and out_dtype (enum adam_grad_dtype);
  *     element (i, r, c) at i*batch_stride + r*row_stride + c elements, strides
- *     >= 0, row_stride >= cols; aligned to the element.  out's matrices lie one after the other
+ *     >= 0, row_stride >= cols; aligned to the element; the last element's
+ *     index is below 2^60.  out's matrices lie one after the other
  *     (batch_stride at least a matrix's extent) or side by side (all of them
  *     within a row_stride, as the heads of a fused weight are), and not
  *     between x's first and last element, except that out may be x itself

@@ -1216,7 +1216,7 @@ int muon_orthogonalize(const muon_matrices *mats, const void *x, void *out, cons
         const int64_t need = muon_orthogonalize_workspace_bytes(mats->batch, mats->rows, mats->cols);
         if (need < 0) return (int)need;
         const Shape shape{mats->rows, mats->cols};
-        constexpr int64_t kMaxStride = int64_t(1) << 40;
+        constexpr int64_t kMaxStride = int64_t(1) << 40, kMaxReach = int64_t(1) << 60;
         for (int64_t v : {mats->x_batch_stride, mats->x_row_stride, mats->out_batch_stride, mats->out_row_stride})
             if (v < 0 || v > kMaxStride) return fail(ADAM_EINVAL, "stride outside [0, 2^40]");
         if (mats->x_row_stride < shape.cols || mats->out_row_stride < shape.cols)
@@ -1230,7 +1230,16 @@ int muon_orthogonalize(const muon_matrices *mats, const void *x, void *out, cons
         if (reinterpret_cast<uintptr_t>(x) % xe || reinterpret_cast<uintptr_t>(out) % oe)
             return fail(ADAM_EALIGN, "x or out is not aligned to its element");
         if (reinterpret_cast<uintptr_t>(workspace) % 256) return fail(ADAM_EALIGN, "workspace is not 256-byte aligned");
+        // elements from the first of a matrix, and of all matrices, to the last
+        const int64_t x_span = (shape.rows - 1) * mats->x_row_stride + shape.cols;
         const int64_t out_span = (shape.rows - 1) * mats->out_row_stride + shape.cols;
+        int64_t x_all, out_all;
+        if (__builtin_mul_overflow(mats->batch - 1, mats->x_batch_stride, &x_all) ||
+            __builtin_mul_overflow(mats->batch - 1, mats->out_batch_stride, &out_all) || x_all >= kMaxReach - x_span ||
+            out_all >= kMaxReach - out_span)
+            return fail(ADAM_EINVAL, "strides reach beyond 2^60 elements");
+        x_all += x_span;
+        out_all += out_span;
         // one matrix after the other, or (heads of a fused weight) all their first rows
         // beside each other, then all their second ones
         const bool beside = mats->out_batch_stride >= shape.cols &&
@@ -1240,12 +1249,9 @@ int muon_orthogonalize(const muon_matrices *mats, const void *x, void *out, cons
         const bool in_place = x == out && xe == oe && mats->x_row_stride == mats->out_row_stride &&
                               (mats->batch == 1 || mats->x_batch_stride == mats->out_batch_stride);
         if (!in_place) {
-            const int64_t x_span = (shape.rows - 1) * mats->x_row_stride + shape.cols;
             const uintptr_t x0 = reinterpret_cast<uintptr_t>(x), o0 = reinterpret_cast<uintptr_t>(out);
-            const uintptr_t x1 = x0 + (uintptr_t)(((mats->batch - 1) * mats->x_batch_stride + x_span) * xe);
-            const uintptr_t o1 = o0 + (uintptr_t)(((mats->batch - 1) * mats->out_batch_stride + out_span) * oe);
             // interleaved views (one's rows between the other's) are refused too
-            if (x0 < o1 && o0 < x1) return fail(ADAM_EINVAL, "out overlaps x");
+            if (x0 < o0 + (uintptr_t)(out_all * oe) && o0 < x0 + (uintptr_t)(x_all * xe)) return fail(ADAM_EINVAL, "out overlaps x");
         }
 
         hipStream_t stream = reinterpret_cast<hipStream_t>(hip_stream);

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import memory_efficient_adam_amd as ma
-from test_muon_host import X, _orth
+from test_muon_host import OUT, X, _orth
 
 
 # the heads of a (rows, heads * d) weight: matrices of rows x d, d apart, rows heads * d apart
@@ -24,3 +24,15 @@ def test_matrices_of_out_may_lie_side_by_side():
     last = X + 4 * (99 * 12 * 64 + 12 * 64)
     assert _orth(out=last - 4, **HEADS, **x) == -1 and "overlaps" in ma.adam_last_error()
     assert _orth(out=last, **HEADS, **x) == -5
+
+
+def test_strides_whose_reach_does_not_fit_are_refused():
+    # (batch - 1) * stride is 2^62, 2^64 (0 in 64 bits) or more
+    for batch in (2 ** 20 + 1, 2 ** 22 + 1, 2 ** 24 + 1, 2 ** 31 - 1):
+        for name in ("x_batch_stride", "out_batch_stride"):
+            kw = {"batch": batch, "rows": 1, "cols": 8, "x_row_stride": 8, "out_row_stride": 8,
+                  "x_batch_stride": 8, "out_batch_stride": 8, name: 2 ** 40}
+            for out in (OUT, X + 2 ** 41):
+                assert _orth(out=out, **kw) == -1 and "reach" in ma.adam_last_error(), kw
+    kw = dict(batch=1, rows=2 ** 21 - 1, cols=8, out_row_stride=8)
+    assert _orth(x_row_stride=2 ** 40, **kw) == -1 and "reach" in ma.adam_last_error()
