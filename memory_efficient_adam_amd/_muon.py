@@ -3,6 +3,7 @@ include/muon_mi355x.h)."""
 import contextlib
 import ctypes
 import functools
+import math
 
 from . import _binding as B
 from ._binding import ADAM_BLOCK_SIZE, AdamError, _check, _stream, adam_last_error
@@ -330,6 +331,8 @@ def _matrices_of(name, shape, stride, dtype):
     if len(shape) < 2:
         raise ValueError(f"{name}: expected (..., rows, cols), got {shape}")
     rows, cols = shape[-2:]
+    if 0 in shape:  # nothing to read: any strides will do
+        return math.prod(shape[:-2]), rows, cols, rows * cols, cols, code
     batch, batch_stride = 1, 0
     for n, s in zip(reversed(shape[:-2]), reversed(stride[:-2])):
         if n == 1:
@@ -339,8 +342,6 @@ def _matrices_of(name, shape, stride, dtype):
         if batch == 1:
             batch_stride = s
         batch *= n
-    if batch * rows * cols == 0:
-        return batch, rows, cols, rows * cols, cols, code
     row_stride = stride[-2] if rows > 1 else cols
     if cols > 1 and stride[-1] != 1:
         raise ValueError(f"{name}: rows must be contiguous")

@@ -37,3 +37,10 @@ def test_heads_of_a_fused_weight_in_place_and_out_of_place(rows, heads, d, dtype
     for t, rest in ((dest, 5.0), (whole, before)):  # nothing else is written
         t[1:rows + 1, 4:4 + heads * d] = rest if isinstance(rest, float) else rest[1:rows + 1, 4:4 + heads * d]
         assert bool((t == rest).all())
+
+
+@pytest.mark.parametrize("shape", [(0, 3, 40, 50), (3, 0, 40, 50), (2, 0, 3, 40, 50), (3, 2, 0, 50), (3, 2, 40, 0)], ids=str)
+def test_empty_batches(shape):
+    x = torch.empty(shape, device="cuda")
+    assert ma.muon_orthogonalize(x).shape == x.shape
+    assert ma.muon_orthogonalize(x, out=x) is x

@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import memory_efficient_adam_amd as ma
+from memory_efficient_adam_amd import _muon as M
 from test_muon_host import OUT, X, _orth
 
 
@@ -36,3 +37,15 @@ def test_strides_whose_reach_does_not_fit_are_refused():
                 assert _orth(out=out, **kw) == -1 and "reach" in ma.adam_last_error(), kw
     kw = dict(batch=1, rows=2 ** 21 - 1, cols=8, out_row_stride=8)
     assert _orth(x_row_stride=2 ** 40, **kw) == -1 and "reach" in ma.adam_last_error()
+
+
+# ---------------------------------------------------------------- the binding
+@pytest.mark.parametrize("shape", [(0, 3, 40, 50), (3, 0, 40, 50), (2, 0, 3, 40, 50), (3, 2, 0, 50), (3, 2, 40, 0), (0, 0), (4, 0, 0)],
+                         ids=str)
+def test_empty_batches_of_any_arrangement_are_taken(shape):
+    for t in (torch.zeros(shape), torch.zeros(shape).transpose(0, -3) if len(shape) > 3 else torch.zeros(shape),
+              torch.zeros(shape).transpose(-1, -2)):
+        batch, rows, cols, batch_stride, row_stride, code = M._matrices_of("x", tuple(t.shape), t.stride(), t.dtype)
+        assert batch * rows * cols == 0 and (rows, cols) == tuple(t.shape[-2:]) and code == 0
+        assert batch == 0 or batch == t.shape[:-2].numel()
+        assert batch_stride >= 0 and row_stride >= cols  # as the library wants them
