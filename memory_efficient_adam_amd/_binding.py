@@ -154,7 +154,7 @@ def _check_step_tensors(state, params, grads):
 _CHECKED_SETS = 8  # tensor sets remembered per state (callers rotate gradient buffers)
 
 
-def _checked_pointers(state, params, grads, check=None):
+def _checked_pointers(state, params, grads, check=None, form=None):
     """Device pointer arrays (ctypes) of params and grads.  The full tensor
     checks (`check`; by default _check_step_tensors) run when the (params, grads) tensor objects and their data
     pointers are not among the last few sets checked on this state: a caller
@@ -163,7 +163,9 @@ def _checked_pointers(state, params, grads, check=None):
     instead of the checks (~1.5 us per tensor, which for a 150-tensor model
     outlast a step of the kernel and would leave the GPU waiting on the
     host), and reuses the set's pointer arrays.  The state holds the
-    remembered tensors until they are pushed out or destroy()."""
+    remembered tensors until they are pushed out or destroy().
+    form: what of the tensors has to be as it was besides (a function of
+    the list), for a step that their shapes matter to."""
     import torch
     check = check or _check_step_tensors
     ptr = torch.Tensor.data_ptr
@@ -174,15 +176,16 @@ def _checked_pointers(state, params, grads, check=None):
         check(state, params, grads)  # raises the precise error
         raise
     sets = state._checked
+    now = form and form([*params, *grads])
     for c in sets:
-        if (c[2] == pp and c[3] == gp and len(c[0]) == len(params) and len(c[1]) == len(grads)
+        if (c[2] == pp and c[3] == gp and c[6] == now and len(c[0]) == len(params) and len(c[1]) == len(grads)
                 and all(map(operator.is_, c[0], params)) and all(map(operator.is_, c[1], grads))):
             return c[4], c[5]
     check(state, params, grads)
     n = max(len(state.numels), 1)
     P = (ctypes.c_void_p * n)(*pp)
     G = (ctypes.c_void_p * n)(*gp)
-    sets.insert(0, (tuple(params), tuple(grads), pp, gp, P, G))
+    sets.insert(0, (tuple(params), tuple(grads), pp, gp, P, G, now))
     del sets[_CHECKED_SETS:]
     return P, G
 

@@ -189,6 +189,12 @@ def _check_matrices(state, params, grads):
     B._check_step_tensors(state, params, grads)
 
 
+def _form(tensors):
+    """What a tensor can change (by .data, t_(), resize_()) while it stays the same object
+    at the same address.  0.35 us a tensor."""
+    return [(t.shape, t.dtype, t.is_contiguous()) for t in tensors]
+
+
 def muon_step(state, params, grads, *, lr, t, momentum=0.95, weight_decay=0.0, nesterov=True,
               steps=5, coefficients=None, eps=1e-7, scale="rms", stochastic=False, seed=42,
               stream=None, expect=None):
@@ -198,7 +204,7 @@ def muon_step(state, params, grads, *, lr, t, momentum=0.95, weight_decay=0.0, n
     factor s ("none", "spectral", "rms").  coefficients: a triple, or one per
     iteration.  expect: (storage, grad_dtype[, block_size[, options]]) the
     caller believes the state has."""
-    P, G = B._checked_pointers(state, params, grads, _check_matrices)
+    P, G = B._checked_pointers(state, params, grads, _check_matrices, _form)
     if isinstance(scale, str) and scale not in MUON_SCALES:
         raise ValueError(f"scale must be one of {sorted(MUON_SCALES)}, got {scale!r}")
     hp = muon_hparams(lr, momentum, weight_decay,

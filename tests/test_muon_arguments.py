@@ -49,3 +49,30 @@ def test_empty_batches_of_any_arrangement_are_taken(shape):
         assert batch * rows * cols == 0 and (rows, cols) == tuple(t.shape[-2:]) and code == 0
         assert batch == 0 or batch == t.shape[:-2].numel()
         assert batch_stride >= 0 and row_stride >= cols  # as the library wants them
+
+
+def _remembering_state(monkeypatch, params, grads):
+    """A state that has checked these (host) tensors before, as one has on a device."""
+    st = M.MuonState(None, [tuple(p.shape) for p in params], M.muon_layout(2, 0, 2048, 0), device=0)
+    with monkeypatch.context() as m:
+        m.setattr(M, "_check_matrices", lambda *a: None)
+        with pytest.raises(ma.AdamError):  # reaches the library, which refuses the NULL state
+            ma.muon_step(st, params, grads, lr=1e-3, t=1, stream=0)
+    with pytest.raises(ma.AdamError):  # remembered
+        ma.muon_step(st, params, grads, lr=1e-3, t=2, stream=0)
+    return st
+
+
+@pytest.mark.parametrize("what,change", [
+    ("shape", lambda t: setattr(t, "data", t.data.view(6, 4))), ("contiguous", lambda t: t.t_()),
+    ("numel", lambda t: setattr(t, "data", t.data[:3])), ("dtype", lambda t: setattr(t, "data", t.data.view(torch.int32)))])
+@pytest.mark.parametrize("of", [0, 1], ids=["param", "grad"])
+def test_a_remembered_tensor_that_changed_its_form_is_checked_again(monkeypatch, what, change, of):
+    square = what == "contiguous"
+    sets = [[torch.zeros(6, 6) if square else torch.zeros(4, 6), torch.zeros(3, 2)] for _ in range(2)]
+    st = _remembering_state(monkeypatch, *sets)
+    at = sets[of][0].data_ptr()
+    change(sets[of][0])
+    assert sets[of][0].data_ptr() == at
+    with pytest.raises(ValueError, match=what):
+        ma.muon_step(st, *sets, lr=1e-3, t=3, stream=0)
