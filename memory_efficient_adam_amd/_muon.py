@@ -324,6 +324,12 @@ def _on(stream):
     return torch.cuda.stream(stream)
 
 
+def _has_tangent(t):
+    """Whether t is a dual tensor of the forward-mode level that is open, if one is."""
+    from torch.autograd import forward_ad
+    return forward_ad._current_level >= 0 and forward_ad.unpack_dual(t).tangent is not None
+
+
 _DTYPE_CODES = {"torch.float32": 0, "torch.bfloat16": 1}
 
 
@@ -368,7 +374,8 @@ def muon_orthogonalize(x, *, out=None, steps=5, coefficients=None, eps=1e-7, wor
     fp32 or bf16 (default: a new tensor of x's type; x itself for in place).
     workspace: a contiguous device tensor of at least
     muon_orthogonalize_workspace_bytes bytes that calls ordered on one stream may
-    share (default: allocated for the call).  No gradient is defined through it."""
+    share (default: allocated for the call).  No gradient is defined through it,
+    backward or forward: tensors that ask for one are refused."""
     import torch
     if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a torch tensor")
@@ -378,6 +385,9 @@ def muon_orthogonalize(x, *, out=None, steps=5, coefficients=None, eps=1e-7, wor
     if torch.is_grad_enabled() and (x.requires_grad or (out is not None and out.requires_grad)):
         raise ValueError("no gradient is defined through muon_orthogonalize: detach its input or "
                          "call it under torch.no_grad()")
+    if _has_tangent(x) or (out is not None and _has_tangent(out)):
+        raise ValueError("no forward-mode gradient is defined through muon_orthogonalize: pass the "
+                         "primal of a dual tensor")
     it = _iteration(steps, coefficients, eps)
     for name, t in (("x", x), ("out", out), ("workspace", workspace)):
         if t is None:

@@ -76,3 +76,20 @@ def test_a_remembered_tensor_that_changed_its_form_is_checked_again(monkeypatch,
     assert sets[of][0].data_ptr() == at
     with pytest.raises(ValueError, match=what):
         ma.muon_step(st, *sets, lr=1e-3, t=3, stream=0)
+
+
+def test_no_forward_mode_gradient_is_dropped_unremarked():
+    import torch.autograd.forward_ad as fwd
+    x = torch.ones(4, 5)
+    with fwd.dual_level():
+        dual = fwd.make_dual(x, torch.ones(4, 5))
+        for args in (dict(x=dual), dict(x=x, out=dual)):
+            with pytest.raises(ValueError, match="forward-mode"):
+                ma.muon_orthogonalize(**args)
+            with torch.no_grad(), pytest.raises(ValueError, match="forward-mode"):
+                ma.muon_orthogonalize(**args)
+        for plain in (x, fwd.unpack_dual(dual).primal):
+            with pytest.raises(ValueError, match="device"):  # the next check: a host tensor
+                ma.muon_orthogonalize(plain)
+    with pytest.raises(ValueError, match="forward-mode"):
+        torch.func.jvp(lambda t: ma.muon_orthogonalize(t), (x,), (x,))
