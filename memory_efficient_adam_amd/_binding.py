@@ -1,4 +1,5 @@
 """ctypes marshalling for libadam_mi355x.so (names follow include/adam_mi355x.h)."""
+import contextlib
 import ctypes
 import operator
 import os
@@ -199,6 +200,17 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+def _on(stream):
+    """torch's current stream set to `stream` (None: as it is), so that memory
+    allocated for a call belongs to the stream the call runs on."""
+    if stream is None:
+        return contextlib.nullcontext()
+    import torch
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream)
+    return torch.cuda.stream(stream)
+
+
 def adam_state_bytes(numels, storage, grad_dtype="f32", block_size=ADAM_BLOCK_SIZE,
                      amsgrad=False):
     n, arr = _numels(numels)
@@ -356,7 +368,8 @@ def adam_state_read(state, which, out=None, stream=None):
     nbytes = adam_state_buffer_bytes(state, which)
     if out is None:
         dt = getattr(torch, _BUF_DTYPES[which])
-        out = torch.empty(nbytes // dt.itemsize, dtype=dt, device="cuda")
+        with _on(stream):
+            out = torch.empty(nbytes // dt.itemsize, dtype=dt, device="cuda")
     elif out.numel() * out.element_size() != nbytes or not out.is_contiguous():
         raise ValueError(f"out must be a contiguous tensor of exactly {nbytes} bytes, got "
                          f"{out.numel() * out.element_size()} bytes")

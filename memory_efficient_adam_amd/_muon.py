@@ -1,12 +1,11 @@
 """ctypes marshalling for the Muon calls of libadam_mi355x.so (names follow
 include/muon_mi355x.h)."""
-import contextlib
 import ctypes
 import functools
 import math
 
 from . import _binding as B
-from ._binding import ADAM_BLOCK_SIZE, AdamError, _check, _stream, adam_last_error
+from ._binding import ADAM_BLOCK_SIZE, AdamError, _check, _on, _stream, adam_last_error
 
 MUON_STORAGES = {"bf16": 1, "q8": 2, "f32": 3}
 MUON_SCALES = {"none": 0, "spectral": 1, "rms": 2}
@@ -235,7 +234,8 @@ def muon_state_read(state, which, out=None, stream=None):
     nbytes = muon_state_buffer_bytes(state, which)
     if out is None:
         dt = getattr(torch, B._BUF_DTYPES[which])
-        out = torch.empty(nbytes // dt.itemsize, dtype=dt, device="cuda")
+        with _on(stream):
+            out = torch.empty(nbytes // dt.itemsize, dtype=dt, device="cuda")
     _exact_bytes("out", out, nbytes)
     _check(library().muon_state_read(state.handle, B.BUFFERS[which], out.data_ptr(), nbytes,
                                      _stream(stream)))
@@ -313,17 +313,6 @@ def muon_state_load(buf, stream=None):
 
 
 # ---------------------------------------------------------------- orthogonalisation
-def _on(stream):
-    """torch's current stream set to `stream` (None: as it is), so that memory
-    allocated for a call belongs to the stream the call runs on."""
-    if stream is None:
-        return contextlib.nullcontext()
-    import torch
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream)
-    return torch.cuda.stream(stream)
-
-
 def _has_tangent(t):
     """Whether t is a dual tensor of the forward-mode level that is open, if one is."""
     from torch.autograd import forward_ad

@@ -44,3 +44,33 @@ def test_empty_batches(shape):
     x = torch.empty(shape, device="cuda")
     assert ma.muon_orthogonalize(x).shape == x.shape
     assert ma.muon_orthogonalize(x, out=x) is x
+
+
+@pytest.mark.parametrize("kind", ["muon", "adam"])
+def test_a_buffer_read_on_a_side_stream_is_not_written_by_earlier_work(kind):
+    # memory given back to the current stream's allocator while fills of it are
+    # still queued there is no place for a copy that another stream makes now
+    side = torch.cuda.Stream()
+    if kind == "muon":
+        state, read = ma.muon_state_create([(1024, 1024)], "f32"), ma.muon_state_read
+        ma.muon_state_write(state, "m_f32", torch.full((1 << 20,), 3.0, device="cuda"))
+    else:
+        state, read = ma.adam_state_create([1 << 20], "q8_v_only"), ma.adam_state_read
+        ma.adam_state_write(state, "m_f32", torch.full((1 << 20,), 3.0, device="cuda"))
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    slow = torch.empty(1 << 28, device="cuda")
+    reused = torch.empty(1 << 20, device="cuda")
+    for _ in range(20):
+        slow.fill_(1.0)
+    reused.fill_(7.0)
+    del reused
+    got = read(state, "m_f32", stream=side)
+    torch.cuda.synchronize()
+    assert bool((got == 3.0).all())
+    raw = read(state, "m_f32", stream=side.cuda_stream)
+    side.synchronize()
+    zero = read(state, "m_f32", stream=0)
+    torch.cuda.synchronize()
+    assert torch.equal(raw, got) and torch.equal(zero, got)
+    state.destroy()
