@@ -188,6 +188,15 @@ def _check_matrices(state, params, grads):
     B._check_step_tensors(state, params, grads)
 
 
+def _launching_stream(stream):
+    """The stream, which has to be one of the current device: kernels run on the
+    stream's device, the pointers are this one's."""
+    device = getattr(stream, "device", None)  # None, and raw handles, have none
+    if device is not None and device.index != B._current_device():
+        raise ValueError(f"the stream is on {device}, the current device is cuda:{B._current_device()}")
+    return stream
+
+
 def _form(tensors):
     """What a tensor can change (by .data, t_(), resize_()) while it stays the same object
     at the same address.  0.35 us a tensor."""
@@ -213,7 +222,7 @@ def muon_step(state, params, grads, *, lr, t, momentum=0.95, weight_decay=0.0, n
     lay = state.layout if expect is None else _layout(*expect)
     _check(library().muon_step(state.handle, ctypes.cast(P, ctypes.c_void_p),
                                ctypes.cast(G, ctypes.c_void_p), ctypes.byref(hp),
-                               ctypes.byref(lay), _stream(stream)))
+                               ctypes.byref(lay), _stream(_launching_stream(stream))))
 
 
 def muon_state_buffer_bytes(state, which):
@@ -389,7 +398,7 @@ def muon_orthogonalize(x, *, out=None, steps=5, coefficients=None, eps=1e-7, wor
         if t is workspace and not t.is_contiguous():
             raise ValueError("workspace must be contiguous")
     need = muon_orthogonalize_workspace_bytes(batch, rows, cols)
-    with _on(stream):
+    with _on(_launching_stream(stream)):
         if out is None:
             out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
         if workspace is None and need > 0:

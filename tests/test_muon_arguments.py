@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import memory_efficient_adam_amd as ma
+from memory_efficient_adam_amd import _binding as B
 from memory_efficient_adam_amd import _muon as M
 from test_muon_host import OUT, X, _orth
 
@@ -93,3 +94,27 @@ def test_no_forward_mode_gradient_is_dropped_unremarked():
                 ma.muon_orthogonalize(plain)
     with pytest.raises(ValueError, match="forward-mode"):
         torch.func.jvp(lambda t: ma.muon_orthogonalize(t), (x,), (x,))
+
+
+class _StreamOf:
+    """What of a torch stream the binding looks at."""
+
+    def __init__(self, index):
+        self.device, self.cuda_stream = torch.device("cuda", index), 4096
+
+
+@pytest.mark.parametrize("call", ["step", "orthogonalize"])
+def test_a_stream_of_another_device_is_refused(monkeypatch, call):
+    monkeypatch.setattr(B, "_current_device", lambda: 0)
+    empty = M.MuonState(None, [(0, 5)], M.muon_layout(3, 0, 2048, 0), device=0)
+    none = [torch.zeros(0, 5)]
+    if call == "step":
+        with pytest.raises(ma.AdamError):  # the library refuses the NULL state
+            ma.muon_step(empty, none, none, lr=1e-3, t=1, stream=_StreamOf(0))
+        with pytest.raises(ValueError, match="stream is on cuda:1"):
+            ma.muon_step(empty, none, none, lr=1e-3, t=1, stream=_StreamOf(1))
+    else:
+        monkeypatch.setattr(torch.Tensor, "is_cuda", True)
+        monkeypatch.setattr(torch.Tensor, "get_device", lambda t: 0)
+        with pytest.raises(ValueError, match="stream is on cuda:1"):
+            ma.muon_orthogonalize(torch.zeros(70, 0, 5), stream=_StreamOf(1))
