@@ -200,12 +200,14 @@ void muon_state_destroy(muon_state *s);
  *     with the same strides and type.
  *   workspace: device memory, 256-byte aligned, of at least
  *     muon_orthogonalize_workspace_bytes(batch, rows, cols), which may be 0
- *     (then NULL will do); written by the call.  Calls that share one must be
- *     ordered on the device; so must the replays of graphs that recorded one.
+ *     (then NULL will do); written by the call, so neither x nor out lies in
+ *     those bytes.  Calls that share one must be ordered on the device; so must
+ *     the replays of graphs that recorded one.
  * Errors (no work enqueued): EINVAL (NULL pointer with a non-empty batch, a
  * dimension < 0 or >= 2^21, rows*cols >= 2^32, batch >= 2^31, a stride
  * outside its domain, out overlapping itself or x, unknown dtype, an iteration
- * outside its domain, workspace too small), EALIGN; EDEVICE if a launch fails.
+ * outside its domain, workspace too small or overlapping x or out), EALIGN;
+ * EDEVICE if a launch fails.
  */
 typedef struct {
     int64_t batch, rows, cols;

@@ -1248,11 +1248,14 @@ int muon_orthogonalize(const muon_matrices *mats, const void *x, void *out, cons
             return fail(ADAM_EINVAL, "out's matrices overlap: they are neither one after the other nor side by side");
         const bool in_place = x == out && xe == oe && mats->x_row_stride == mats->out_row_stride &&
                               (mats->batch == 1 || mats->x_batch_stride == mats->out_batch_stride);
-        if (!in_place) {
-            const uintptr_t x0 = reinterpret_cast<uintptr_t>(x), o0 = reinterpret_cast<uintptr_t>(out);
-            // interleaved views (one's rows between the other's) are refused too
-            if (x0 < o0 + (uintptr_t)(out_all * oe) && o0 < x0 + (uintptr_t)(x_all * xe)) return fail(ADAM_EINVAL, "out overlaps x");
-        }
+        // interleaved views (one's rows between the other's) are refused too
+        auto meet = [](const void *a, int64_t a_bytes, const void *b, int64_t b_bytes) {
+            const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+            return p < q + (uintptr_t)b_bytes && q < p + (uintptr_t)a_bytes;
+        };
+        if (!in_place && meet(x, x_all * xe, out, out_all * oe)) return fail(ADAM_EINVAL, "out overlaps x");
+        if (need > 0 && (meet(workspace, need, x, x_all * xe) || meet(workspace, need, out, out_all * oe)))
+            return fail(ADAM_EINVAL, "workspace overlaps x or out");
 
         hipStream_t stream = reinterpret_cast<hipStream_t>(hip_stream);
         MuonWork work{};

@@ -40,6 +40,27 @@ def test_strides_whose_reach_does_not_fit_are_refused():
     assert _orth(x_row_stride=2 ** 40, **kw) == -1 and "reach" in ma.adam_last_error()
 
 
+def test_a_workspace_that_holds_x_or_out_is_refused():
+    need = ma.muon_orthogonalize_workspace_bytes(2, 100, 80)
+    size = 4 * 2 * 8000
+    for ws in (X, X - need + 256, X + size // 256 * 256, OUT, OUT - need + 256, OUT + (size - 4) // 256 * 256):
+        assert _orth(ws=ws) == -1 and "workspace overlaps" in ma.adam_last_error(), hex(ws)
+    assert _orth(x=OUT, ws=OUT) == -1 and "workspace overlaps" in ma.adam_last_error()  # in place
+
+
+@pytest.mark.skipif(torch.cuda.device_count() > 0, reason="would launch on pointers that are no memory")
+def test_a_workspace_beside_x_and_out_is_taken():
+    need = ma.muon_orthogonalize_workspace_bytes(2, 100, 80)
+    size = 4 * 2 * 8000
+    assert need % 256 == 0 and size % 256 == 0
+    for ws in (X - need, X + size, OUT - need, OUT + size):
+        assert _orth(ws=ws) == -5, hex(ws)
+    # a workspace larger than needed may hold them behind its used part
+    assert _orth(ws=X - need, ws_bytes=1 << 40) == -5
+    # matrices that need none
+    assert _orth(rows=60, cols=80, ws=X, ws_bytes=1 << 30) == -5
+
+
 # ---------------------------------------------------------------- the binding
 @pytest.mark.parametrize("shape", [(0, 3, 40, 50), (3, 0, 40, 50), (2, 0, 3, 40, 50), (3, 2, 0, 50), (3, 2, 40, 0), (0, 0), (4, 0, 0)],
                          ids=str)
