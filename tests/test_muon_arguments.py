@@ -43,7 +43,7 @@ def test_strides_whose_reach_does_not_fit_are_refused():
 def test_a_workspace_that_holds_x_or_out_is_refused():
     need = ma.muon_orthogonalize_workspace_bytes(2, 100, 80)
     size = 4 * 2 * 8000
-    for ws in (X, X - need + 256, X + size // 256 * 256, OUT, OUT - need + 256, OUT + (size - 4) // 256 * 256):
+    for ws in (X, X - need + 256, X + (size - 4) // 256 * 256, OUT, OUT - need + 256, OUT + (size - 4) // 256 * 256):
         assert _orth(ws=ws) == -1 and "workspace overlaps" in ma.adam_last_error(), hex(ws)
     assert _orth(x=OUT, ws=OUT) == -1 and "workspace overlaps" in ma.adam_last_error()  # in place
 
