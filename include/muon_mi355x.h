@@ -109,9 +109,11 @@ typedef struct {
  *   for BF16, (1, 4) for Q8.
  * muon_state_workspace_bytes: the device workspace that a state of this list
  * holds beside it (the factors of the products, for a part of the list at a
- * time: 16 bytes per element of the largest part and 20 per element of its
- * square factors, dimensions rounded up to tiles, and up to 64 MB for the
- * parts of split products).
+ * time: 16 bytes per element of the largest part and 8, 16 or 20, as iterations
+ * are taken one, two or three at a time, per element of its square factors,
+ * dimensions rounded up to tiles, and up to 64 MB for the parts of split
+ * products; 4 bytes per element of matrices of up to 64 x 768, which
+ * take no factors in memory).
  * Pure host functions.  Return < 0 (an adam_status) on bad arguments:
  * n_tensors < 0, rows or cols NULL with n_tensors > 0, a dimension < 0 or
  * >= 2^21, rows*cols >= 2^32, layout NULL or invalid.

@@ -154,6 +154,8 @@ struct Work {
         pairs = shortest >= kPairShort && g + u > 3.0 * s;
         triples = shortest >= kTripleShort && 2.0 * (g + u) > 4.0 * s + square.time(square_tiling, 2);
     }
+    // Square arrays that its iterations use: A, P; in runs of two T, R too, of three U (run_products).
+    int squares() const { return triples ? kSquares : (pairs ? 4 : 2); }
     int64_t pad() const { return square_tiling == kTile128 || update_tiling == kTile128 ? 128 : 64; }
     int64_t part_bytes() const {  // (small matrices have no tiles)
         return update.tiles[0] == 0 ? 0 : std::max(partial_bytes(square_tiling), partial_bytes(update_tiling));
@@ -163,7 +165,8 @@ struct Work {
 // A part of the list whose matrices go through the products together.
 struct Group {
     int32_t first = 0, last = 0;  // tensors [first, last)
-    int64_t x_bytes = 0, a_bytes = 0;  // of one X (or X^T) array and of one square array
+    int64_t x_bytes = 0, a_bytes = 0;  // of one X (or X^T) array and of one square array (small matrices have none)
+    int64_t u_bytes = 0;               // of the update matrices
     int64_t block0 = 0, blocks = 0;    // 2048-element blocks
     int64_t flat0 = 0;                 // flat state index of its first element
     Work size;
@@ -195,10 +198,12 @@ std::vector<Group> plan(const std::vector<Shape> &shapes) {
         g.flat0 = flat;
         int64_t elements = 0;
         for (; k < n; ++k) {
-            const int64_t t = shapes[k].numel() > 0 ? tiles_of(shapes[k], 128) : 0;
-            if (elements > 0 && elements + t * 16384 > kGroupElements) break;
-            elements += t * 16384;
-            if (t > 0 && !is_small(shapes[k])) g.size.add(shapes[k]);
+            // (a small matrix takes its blocks of u alone)
+            const bool small = is_small(shapes[k]);
+            const int64_t more = small ? blocks_of(shapes[k].numel()) * kBlock : tiles_of(shapes[k], 128) * 16384;
+            if (elements > 0 && elements + more > kGroupElements) break;
+            elements += more;
+            if (!small && more > 0) g.size.add(shapes[k]);
             block += blocks_of(shapes[k].numel());
             flat += pad16(shapes[k].numel());
         }
@@ -206,7 +211,8 @@ std::vector<Group> plan(const std::vector<Shape> &shapes) {
         g.blocks = block - g.block0;
         g.size.choose();
         for (int32_t i = g.first; i < g.last; ++i) {
-            if (shapes[i].numel() == 0) continue;
+            g.u_bytes += 4 * pad16(shapes[i].numel());
+            if (shapes[i].numel() == 0 || is_small(shapes[i])) continue;
             const int64_t m = pad_to(shapes[i].shorter(), g.size.pad()), l = pad_to(shapes[i].longer(), g.size.pad());
             g.x_bytes += 4 * m * l;
             g.a_bytes += 4 * m * m;
@@ -216,15 +222,15 @@ std::vector<Group> plan(const std::vector<Shape> &shapes) {
     return groups;
 }
 
-// The workspace a group needs: four X arrays, the square ones, the blocks' partial
-// sums and the matrices' sums.
+// The workspace a group needs: four X arrays (u takes the place of the one that is
+// written last), the square ones, the blocks' partial sums and the matrices' sums.
 int64_t align256(int64_t n) { return pad_to(n, 256); }
-int64_t workspace_bytes(const Work &w, int64_t x_bytes, int64_t a_bytes, int64_t n_partials) {
-    return 4 * align256(x_bytes) + kSquares * align256(a_bytes) + 4 * kMaxSplit + kMaxPartials * w.part_bytes() +
-           align256(8 * n_partials);
+int64_t workspace_bytes(const Work &w, int64_t x_bytes, int64_t u_bytes, int64_t a_bytes, int64_t n_partials) {
+    return 3 * align256(x_bytes) + align256(std::max(x_bytes, u_bytes)) + w.squares() * align256(a_bytes) + 4 * kMaxSplit +
+           kMaxPartials * w.part_bytes() + align256(8 * n_partials);
 }
 int64_t group_bytes(const Group &g) {
-    return workspace_bytes(g.size, g.x_bytes, g.a_bytes, g.blocks) + align256(8 * (g.last - g.first));
+    return workspace_bytes(g.size, g.x_bytes, g.u_bytes, g.a_bytes, g.blocks) + align256(8 * (g.last - g.first));
 }
 
 struct Workspace {
@@ -235,18 +241,18 @@ struct Workspace {
     float *phi;
 };
 
-Workspace carve(char *base, const Work &size, int64_t x_bytes, int64_t a_bytes, int64_t n_partials) {
-    Workspace w;
+Workspace carve(char *base, const Work &size, int64_t x_bytes, int64_t u_bytes, int64_t a_bytes, int64_t n_partials) {
+    Workspace w{};
     auto take = [&base](int64_t n) {
         char *p = base;
         base += align256(n);
         return p;
     };
     for (int i = 0; i < 2; ++i) {
-        w.f.x[i] = take(x_bytes);
+        w.f.x[i] = take(i == 0 ? x_bytes : std::max(x_bytes, u_bytes));
         w.f.xt[i] = take(x_bytes);
     }
-    for (char *&p : w.f.square) p = take(a_bytes);
+    for (int i = 0; i < size.squares(); ++i) w.f.square[i] = take(a_bytes);
     w.arrived = reinterpret_cast<uint32_t *>(take(4 * kMaxSplit));
     w.parts = reinterpret_cast<float *>(take(kMaxPartials * size.part_bytes()));
     w.partials = reinterpret_cast<double *>(take(8 * n_partials));
@@ -438,7 +444,8 @@ hipError_t run_products(const Workspace &w, const MuonWork &square, const MuonWo
         g.out2 = out2;
         launch(kCommuting, g);
     };
-    char *const A = f.square[0], *const T = f.square[1], *const P = f.square[2], *const R = f.square[3],
+    // (T, R and U only where the runs' lengths ask for them: Work::squares)
+    char *const A = f.square[0], *const P = f.square[1], *const T = f.square[2], *const R = f.square[3],
                *const U = f.square[4];
     int cur = 0;
     for (const Run &run : runs_of(it, size)) {
@@ -583,8 +590,10 @@ void build_tables(Group &g, const std::vector<Shape> &shapes) {
         m.norm = i;
         m.scale_spectral = std::sqrt(std::max(1.0, (double)s.rows / (double)s.cols));
         m.scale_rms = 0.2 * std::sqrt((double)s.longer());
-        x_off += 4ull * m.mp * m.np;
-        a_off += 4ull * m.mp * m.mp;
+        if (!is_small(s)) {
+            x_off += 4ull * m.mp * m.np;
+            a_off += 4ull * m.mp * m.mp;
+        }
         g.mats.push_back(m);
         const int64_t b0 = firsts[k - g.first];
         g.ranges.push_back(uint2{(uint32_t)b0, (uint32_t)(b0 + blocks_of(s.numel()))});
@@ -852,7 +861,7 @@ int muon_step(muon_state *s, float *const *params, const void *const *grads, con
         if ((rc = pointer_table(s, params, grads, stream, &tensors))) return rc;
 
         for (const Group &g : s->groups) {
-            const Workspace w = carve(s->workspace, g.size, g.x_bytes, g.a_bytes, g.blocks);
+            const Workspace w = carve(s->workspace, g.size, g.x_bytes, g.u_bytes, g.a_bytes, g.blocks);
             MuonStepArgs a{};
             a.desc = s->d_desc + g.block0;
             a.tensors = tensors;
@@ -1189,7 +1198,7 @@ BatchPlan plan_batch(int64_t batch, const Shape &s) {
     p.x_bytes = 4 * p.mp * p.np;
     p.a_bytes = 4 * p.mp * p.mp;
     p.n_partials = std::min(kMaxSums, tiles_of(s, 64));
-    p.bytes = workspace_bytes(p.size, p.x_bytes * p.chunk, p.a_bytes * p.chunk, p.n_partials * p.chunk) + align256(4 * p.chunk);
+    p.bytes = workspace_bytes(p.size, p.x_bytes * p.chunk, 0, p.a_bytes * p.chunk, p.n_partials * p.chunk) + align256(4 * p.chunk);
     return p;
 }
 
@@ -1281,7 +1290,7 @@ int muon_orthogonalize(const muon_matrices *mats, const void *x, void *out, cons
             return ADAM_OK;
         }
         const BatchPlan p = plan_batch(mats->batch, shape);
-        const Workspace w = carve(static_cast<char *>(workspace), p.size, p.x_bytes * p.chunk, p.a_bytes * p.chunk,
+        const Workspace w = carve(static_cast<char *>(workspace), p.size, p.x_bytes * p.chunk, 0, p.a_bytes * p.chunk,
                                   p.n_partials * p.chunk);
         work.one.mp = (uint32_t)p.mp;
         work.one.np = (uint32_t)p.np;

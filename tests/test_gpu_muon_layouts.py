@@ -3,6 +3,7 @@ import pytest
 import torch
 
 import memory_efficient_adam_amd as ma
+import muon_ref
 
 pytestmark = pytest.mark.gpu
 
@@ -73,4 +74,24 @@ def test_a_buffer_read_on_a_side_stream_is_not_written_by_earlier_work(kind):
     zero = read(state, "m_f32", stream=0)
     torch.cuda.synchronize()
     assert torch.equal(raw, got) and torch.equal(zero, got)
+    state.destroy()
+
+
+@pytest.mark.parametrize("large", [[(70, 90)], [(300, 900)] * 2, [(768, 2304), (128, 4000)], [(600, 600)]], ids=str)
+def test_a_step_of_small_matrices_that_outweigh_the_large_ones(large):
+    # the updates of all of them stand where the large ones' factors come to be
+    shapes = [(64, 768)] * 20 + large + [(33, 65), (0, 5), (5, 0), (768, 64), (1, 1)] * 9 + [(700, 50)] * 30
+    grads = [1e-3 * _randn(k, *s) for k, s in enumerate(shapes)]
+    params = [torch.zeros(s, device="cuda") for s in shapes]
+    state = ma.muon_state_create(shapes, "f32")
+    for t in (1, 2):
+        for p in params:
+            p.zero_()
+        ma.muon_step(state, params, grads, t=t, lr=1.0, momentum=0.0, scale="none")
+        for k, (p, g) in enumerate(zip(params, grads)):
+            if g.numel() == 0:
+                continue
+            ref = muon_ref.orthogonalize(g)
+            own = float((muon_ref.orthogonalize(g, dtype=torch.float32).double() - ref).norm() / ref.norm())
+            assert float((-p.double() - ref).norm() / ref.norm()) <= 8 * own + 2.0 ** -21, (t, k, shapes[k])
     state.destroy()

@@ -139,3 +139,33 @@ def test_a_stream_of_another_device_is_refused(monkeypatch, call):
         monkeypatch.setattr(torch.Tensor, "get_device", lambda t: 0)
         with pytest.raises(ValueError, match="stream is on cuda:1"):
             ma.muon_orthogonalize(torch.zeros(70, 0, 5), stream=_StreamOf(1))
+
+
+# ---------------------------------------------------------------- workspaces
+def _workspace(shapes):
+    return ma.muon_state_workspace_bytes(shapes, "q8")
+
+
+@pytest.mark.parametrize("count,shape", [(4096, (64, 64)), (512, (16, 768)), (3000, (768, 3)), (20000, (1, 1))], ids=str)
+def test_small_matrices_take_a_workspace_of_their_updates_alone(count, shape):
+    n = shape[0] * shape[1]
+    # u, a partial sum a block, a sum a matrix, the counters, and rounding to 256 bytes
+    most = count * (4 * (n + 15 & ~15) + 8 * (-(-n // 2048)) + 8) + 1024 + 3 * 256
+    assert 4 * n * count <= _workspace([shape] * count) <= most
+    assert _workspace([shape] * count * 40) <= (1 << 28) + (1 << 26)  # 2^26 elements of u at a time
+
+
+def test_small_matrices_add_their_updates_to_a_list_and_no_factors():
+    large = [(1024, 1024)] * 4
+    assert _workspace(large + [(64, 768)] * 3) <= _workspace(large) + 4 * 3 * 64 * 768 + 4096
+    many = [(64, 768)] * 600
+    assert _workspace(large + many) <= _workspace(large) + _workspace(many)
+
+
+def test_square_factors_are_those_the_iterations_use():
+    n = 4096 * 4096
+    # no runs for square matrices: four arrays of X, A and P
+    assert _workspace([(4096, 4096)] * 4) <= 4 * n * (16 + 8) + (1 << 26) + (1 << 20)
+    # runs of three: five square arrays (long matrices, their Gram matrices are small)
+    wide = _workspace([(768, 7680)])
+    assert wide >= 16 * 768 * 7680 + 20 * 768 * 768
