@@ -279,8 +279,8 @@ int32_t adam_state_get_draw_index(const adam_state *s, int64_t *first_index, int
 int32_t adam_state_describe(const adam_state *s, adam_layout *layout, int64_t *numels,
                             int32_t max_tensors);
 
-/* Frees every buffer of the state (after synchronizing the device).
-   NULL is ignored. */
+/* Frees every buffer of the state (after synchronizing the device, so no
+   stream of the process may be capturing).  NULL is ignored. */
 void adam_state_destroy(adam_state *s);
 
 /*

@@ -185,7 +185,8 @@ int32_t muon_state_get_draw_index(const muon_state *s, int64_t *first_index, int
 int32_t muon_state_describe(const muon_state *s, muon_layout *layout, int64_t *rows, int64_t *cols,
                             int32_t max_tensors);
 
-/* Frees the state (after synchronizing the device).  NULL is ignored. */
+/* Frees the state (after synchronizing the device, so no stream of the process
+   may be capturing).  NULL is ignored. */
 void muon_state_destroy(muon_state *s);
 
 /*

@@ -3,6 +3,7 @@ import contextlib
 import ctypes
 import operator
 import os
+import sys
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libadam_mi355x.so")
@@ -221,8 +222,28 @@ def adam_state_bytes(numels, storage, grad_dtype="f32", block_size=ADAM_BLOCK_SI
     return int(rc)
 
 
+_waiting = []  # (function that frees it, handle) of states that went during a capture
+
+
+def _release(free=None, handle=None, waiting=_waiting, modules=sys.modules):
+    """Frees a state, and those that wait.  That synchronizes the device, which
+    would end a graph capture: a state that is destroyed, or that the
+    collector finds, while the current stream is capturing waits until the next
+    one is made or goes.  (The defaults outlive the module's globals, which may be gone when a
+    state is collected at exit.)"""
+    if handle:
+        waiting.append((free, handle))
+    cuda = getattr(modules.get("torch"), "cuda", None)
+    if not waiting or cuda is not None and cuda.is_initialized() and cuda.is_current_stream_capturing():
+        return
+    while waiting:
+        free, handle = waiting.pop()
+        free(handle)
+
+
 class AdamState:
-    """Owns one library state (freed on destroy() or garbage collection).
+    """Owns one library state (freed on destroy() or garbage collection; after a
+    graph capture, if that happens during one).
     device: the CUDA device index the state lives on (None: not recorded)."""
 
     def __init__(self, handle, numels, layout, device=None):
@@ -230,6 +251,9 @@ class AdamState:
         self.numels = list(numels)
         self.layout = layout
         self.device = device
+        # held here: globals may be gone when a state is collected at exit
+        self._free, self._release = (library().adam_state_destroy, _release) if handle else (None, None)
+        _release()
         # tensor sets (held) and pointers of recent checked adam_step calls
         self._checked = []
 
@@ -239,7 +263,7 @@ class AdamState:
     def destroy(self):
         self._checked = []
         if getattr(self, "handle", None):
-            library().adam_state_destroy(self.handle)
+            self._release(self._free, self.handle)
             self.handle = None
 
     @property

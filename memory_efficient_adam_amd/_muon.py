@@ -128,7 +128,8 @@ def muon_state_workspace_bytes(shapes, storage, grad_dtype="f32", block_size=ADA
 
 
 class MuonState:
-    """Owns one library state (freed on destroy() or garbage collection).
+    """Owns one library state (freed on destroy() or garbage collection; after a
+    graph capture, if that happens during one).
     device: the CUDA device index the state lives on (None: not recorded)."""
 
     def __init__(self, handle, shapes, layout, device=None):
@@ -137,7 +138,8 @@ class MuonState:
         self.layout = layout
         self.device = device
         # held here: globals may be gone when a state is collected at exit
-        self._free = library().muon_state_destroy if handle else None
+        self._free, self._release = (library().muon_state_destroy, B._release) if handle else (None, None)
+        B._release()
         self._checked = []  # tensor sets (held) and pointers of recent checked muon_step calls
 
     def _set_shapes(self, shapes):
@@ -155,7 +157,7 @@ class MuonState:
     def destroy(self):
         self._checked = []
         if getattr(self, "handle", None):
-            self._free(self.handle)
+            self._release(self._free, self.handle)
             self.handle = None
 
     @property

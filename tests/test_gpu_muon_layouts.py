@@ -1,9 +1,12 @@
 """GPU tests of the layouts, streams and workspaces that the Muon calls take."""
+import gc
+
 import pytest
 import torch
 
 import memory_efficient_adam_amd as ma
 import muon_ref
+from memory_efficient_adam_amd import _binding
 
 pytestmark = pytest.mark.gpu
 
@@ -95,3 +98,29 @@ def test_a_step_of_small_matrices_that_outweigh_the_large_ones(large):
             own = float((muon_ref.orthogonalize(g, dtype=torch.float32).double() - ref).norm() / ref.norm())
             assert float((-p.double() - ref).norm() / ref.norm()) <= 8 * own + 2.0 ** -21, (t, k, shapes[k])
     state.destroy()
+
+
+@pytest.mark.parametrize("kind", ["muon", "adam"])
+@pytest.mark.parametrize("how", ["destroyed", "collected"])
+def test_a_state_that_goes_during_a_capture_leaves_the_graph_whole(kind, how):
+    make = {"muon": lambda: ma.muon_state_create([(70, 80)], "q8"), "adam": lambda: ma.adam_state_create([5000], "q8")}[kind]
+    holder = [make()]
+    if how == "collected":  # only the cycle collector ends it, as one that an exception's frames hold
+        holder.append(holder)
+    x = torch.zeros(1000, device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        x.add_(1.0)
+        if how == "destroyed":
+            holder[0].destroy()
+        del holder
+        gc.collect()
+        x.add_(1.0)
+    for k in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert bool((x == 2.0 * (k + 1)).all())
+    assert len(_binding._waiting) == 1
+    make()  # another state frees it
+    assert not _binding._waiting
