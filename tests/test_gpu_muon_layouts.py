@@ -124,3 +124,24 @@ def test_a_state_that_goes_during_a_capture_leaves_the_graph_whole(kind, how):
     assert len(_binding._waiting) == 1
     make()  # another state frees it
     assert not _binding._waiting
+
+
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(40, 70), (300, 300), (600, 520), (520, 1600)], ids=str)
+def test_zero_and_nonfinite_bf16_matrices(shape, out_dtype):
+    # (large ones are taken as they are, with the rest of the norm beside them)
+    x = _randn(1, 4, *shape).bfloat16()
+    x[3] = 0.0
+    x[3, 0, 0] = 2.0 ** -133  # the least number
+    run = lambda: ma.muon_orthogonalize(x, out=torch.empty(4, *shape, dtype=out_dtype, device="cuda"), eps=1e-43)  # noqa: E731
+    good = run()
+    s = 1.0  # one entry: its own singular value
+    for _ in range(5):
+        s = 3.4445 * s - 4.7750 * s ** 3 + 2.0315 * s ** 5
+    assert abs(float(good[3, 0, 0]) - s) <= 2.0 ** -8 and int((good[3] != 0).sum()) == 1
+    for value in (0.0, float("nan"), float("inf"), float("-inf")):
+        x[1] = 0.0
+        x[1, -1, -1] = value
+        out = run()
+        assert bool((out[1] == 0).all() if value == 0.0 else out[1].isnan().all())
+        assert all(torch.equal(out[k], good[k]) for k in (0, 2, 3))
