@@ -157,8 +157,8 @@ class MuonState:
     def destroy(self):
         self._checked = []
         if getattr(self, "handle", None):
-            self._release(self._free, self.handle)
-            self.handle = None
+            handle, self.handle = self.handle, None
+            self._release(self._free, handle)
 
     @property
     def storage(self):

@@ -169,3 +169,47 @@ def test_square_factors_are_those_the_iterations_use():
     # runs of three: five square arrays (long matrices, their Gram matrices are small)
     wide = _workspace([(768, 7680)])
     assert wide >= 16 * 768 * 7680 + 20 * 768 * 768
+
+
+# ---------------------------------------------------------------- states that go
+class _Cuda:
+    """torch.cuda, as far as freeing a state asks it."""
+
+    def __init__(self):
+        self.cuda, self.capturing, self.initialized = self, False, True
+
+    def is_initialized(self):
+        return self.initialized
+
+    def is_current_stream_capturing(self):
+        if isinstance(self.capturing, Exception):
+            raise self.capturing
+        return self.capturing
+
+
+def test_states_that_go_during_a_capture_are_freed_once_after_it():
+    cuda, freed, waiting = _Cuda(), [], []
+    release = lambda *a: B._release(*a, waiting=waiting, modules={"torch": cuda})  # noqa: E731
+    for make in (lambda: M.MuonState(None, [(3, 4)], None), lambda: B.AdamState(None, [12], None)):
+        states = [make() for _ in range(4)]
+        for k, st in enumerate(states):
+            st.handle, st._free, st._release = k + 1, freed.append, release
+        states[0].destroy()
+        assert freed == [1] and not waiting
+        cuda.capturing = True
+        states[1].destroy()
+        release()
+        assert freed == [1] and len(waiting) == 1
+        cuda.capturing = RuntimeError("the query failed")  # nothing is known of a capture
+        with pytest.raises(RuntimeError):
+            states[2].destroy()
+        cuda.capturing = False
+        states[3].destroy()
+        for st in states:
+            st.destroy()
+        assert sorted(freed) == [1, 2, 3, 4] and not waiting
+        freed.clear()
+    cuda.initialized, cuda.capturing = False, True  # no capture by torch without its runtime
+    release(freed.append, 9)
+    B._release(freed.append, 10, waiting=waiting, modules={})
+    assert freed == [9, 10]
