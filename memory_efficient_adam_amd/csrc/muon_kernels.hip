@@ -1227,10 +1227,12 @@ static hipError_t product_of(int product, int in, int jobs, const MuonGemmArgs &
 // 128 x 128 tiles: eight waves hide more of the latency while a CU has one
 // tile; with more than one, two workgroups of four waves do, and their larger
 // blocks read LDS less.  (us with four / eight waves: 252 tiles, P of 12
-// matrices of 768^2 25.2 / 23.9 and X X^T 24.8 / 23.4; 432 tiles 39.5 / 39.5; 504 tiles, P of 24
-// of them 42.8 / 44.3, X X^T of 24 of 768 x 2304 102.8 / 116.2; 2048 tiles, P X of
-// two of 4096^2 729 / 745.  Three or four stages, or 128 x 256 tiles, were
-// slower in each.)  64 x 64 tiles have three stages: three workgroups to a CU.
+// matrices of 768^2 26.5 / 24.9 and X X^T 25.0 / 23.5; 432 tiles 38.6 / 39.6; 504 tiles, P of 24
+// of them 43.0 / 43.8, X X^T of 24 of 768 x 2304 110 / 116; 2048 tiles, P X of four
+// of 2048 x 4096 400 / 421; 4096 tiles, P X of four of 4096^2 1506 / 1538; but 2592
+// tiles, P X of 24 of 768 x 2304, 240 / 232.  Three stages were slower in
+// each but for 252 tiles, where they made no difference; four, and 128 x 256
+// tiles, were slower when remainders had no sums of their own.)  64 x 64 tiles have three stages: three workgroups to a CU.
 typedef Tiling<64, 64, 2, 2, 3, 3> Tiling64;
 typedef Tiling<128, 128, 2, 4, 2, 4> Tiling128;
 typedef Tiling<128, 128, 2, 2, 2, 2> Tiling128Many;
