@@ -44,7 +44,7 @@
  * AMSGrad maximum draws one Philox call per 8 elements: half (i mod 2) of
  * word (i / 2) mod 4 at counter (i / 8 + 2^63, t) for draw index i) and
  * pins |x| >= A to qmax; a block with A < 2^-112 stores zero codes and
- * scale 0.  The AMSGrad maximum is stored as v is: bf16, or uint8 codes
+ * scale 0.  The AMSGrad maximum is stored as v is: bf16, fp32, or uint8 codes
  * with their own per-block scale.
  *
  * State layout (device memory owned by the library): tensor k's segment has
@@ -88,7 +88,11 @@ enum adam_status {
 enum adam_storage {
     ADAM_STORE_BF16 = 1,     /* m, v: bf16 (round to nearest even) */
     ADAM_STORE_Q8 = 2,       /* m: int8 [-127,127], v: uint8, fp32 scale per block each */
-    ADAM_STORE_Q8_V_ONLY = 3 /* m: fp32, v: uint8 + fp32 scale per block */
+    ADAM_STORE_Q8_V_ONLY = 3, /* m: fp32, v: uint8 + fp32 scale per block */
+    /* m, v: fp32, nothing rounded for storage.  For tensors whose gradients are too uneven for
+     * 8 bits, embedding tables above all (Dettmers et al., "8-bit Optimizers via
+     * Block-wise Quantization", 2021, keep their states in 32 bits). */
+    ADAM_STORE_F32 = 4
 };
 
 enum adam_grad_dtype { ADAM_GRAD_F32 = 0, ADAM_GRAD_BF16 = 1 };
@@ -114,11 +118,13 @@ enum adam_buffer {
     ADAM_BUF_V_SCALE = 3, /* float[blocks]             (Q8, Q8_V_ONLY) */
     ADAM_BUF_M_BF16 = 4,  /* uint16[padded elements]   (BF16) */
     ADAM_BUF_V_BF16 = 5,  /* uint16[padded elements]   (BF16) */
-    ADAM_BUF_M_F32 = 6,   /* float[padded elements]    (Q8_V_ONLY) */
+    ADAM_BUF_M_F32 = 6,   /* float[padded elements]    (Q8_V_ONLY, F32) */
     ADAM_BUF_VMAX_CODES = 7, /* uint8[padded elements] (Q8, Q8_V_ONLY with AMSGRAD) */
     ADAM_BUF_VMAX_SCALE = 8, /* float[blocks]          (Q8, Q8_V_ONLY with AMSGRAD) */
     ADAM_BUF_VMAX_BF16 = 9,  /* uint16[padded elements] (BF16 with AMSGRAD) */
-    ADAM_BUF_COUNT = 10      /* number of buffer ids */
+    ADAM_BUF_V_F32 = 10,     /* float[padded elements]  (F32) */
+    ADAM_BUF_VMAX_F32 = 11,  /* float[padded elements]  (F32 with AMSGRAD) */
+    ADAM_BUF_COUNT = 12      /* number of buffer ids */
 };
 
 enum adam_options {
@@ -150,8 +156,8 @@ typedef struct {
 /*
  * Bytes of optimizer state for a tensor list, without allocating:
  *   sum_k pad16(numel_k) * e + blocks * s, with (e, s) = (4, 0) for BF16,
- *   (2, 8) for Q8 and (5, 4) for Q8_V_ONLY; ADAM_OPT_AMSGRAD adds (2, 0)
- *   for BF16 and (1, 4) for the 8-bit modes.
+ *   (2, 8) for Q8, (5, 4) for Q8_V_ONLY and (8, 0) for F32; ADAM_OPT_AMSGRAD
+ *   adds (2, 0) for BF16, (1, 4) for the 8-bit modes and (4, 0) for F32.
  * The per-block descriptor table (16 bytes per block) and the per-tensor
  * pointer table (16 bytes per tensor) are bookkeeping, not counted.
  * Memory accounting follows the 8-bit Adam page (GetMemoryUsage).
@@ -191,7 +197,7 @@ int adam_state_create(adam_state **out, int32_t n_tensors, const int64_t *numels
  *   from the layout given at create returns EMODE (no work enqueued).
  * Errors (no work enqueued): EINVAL (NULL state/params/grads/hp/expect,
  * hyperparameter outside its domain, unknown flag bits, reserved != 0,
- * STOCHASTIC, PERCENTILE or STATIC_SCALES with BF16 storage, call from a
+ * STOCHASTIC, PERCENTILE or STATIC_SCALES with BF16 or F32 storage, call from a
  * device other than the one the state was created on, hip_stream in HIP
  * graph capture: a captured launch would replay this call's t and
  * hyperparameters with a pointer table that later calls may re-use), EMODE,
@@ -295,7 +301,8 @@ void adam_state_destroy(adam_state *s);
  * hip_stream, before the step kernel.
  *   numels, layout: the tensor list and layout, as for adam_state_create.
  *   params, grads: as for adam_step.
- *   state: ADAM_BUF_COUNT device pointers indexed by enum adam_buffer; the
+ *   state: ADAM_BUF_COUNT device pointers indexed by enum adam_buffer (an array
+ *     that ends with the layout's last buffer will do); the
  *     entries of the buffers the layout has (see adam_state_read) must point
  *     at caller-owned device memory of exactly the sizes a state of this
  *     tensor list would have (padded elements = sum of pad16(numel); blocks =

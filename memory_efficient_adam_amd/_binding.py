@@ -9,10 +9,11 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libadam_mi355x.so")
 
 ADAM_BLOCK_SIZE = 2048
-STORAGES = {"bf16": 1, "q8": 2, "q8_v_only": 3}
+STORAGES = {"bf16": 1, "q8": 2, "q8_v_only": 3, "f32": 4}
 GRAD_DTYPES = {"f32": 0, "bf16": 1}
 BUFFERS = {"m_codes": 0, "v_codes": 1, "m_scale": 2, "v_scale": 3, "m_bf16": 4,
-           "v_bf16": 5, "m_f32": 6, "vmax_codes": 7, "vmax_scale": 8, "vmax_bf16": 9}
+           "v_bf16": 5, "m_f32": 6, "vmax_codes": 7, "vmax_scale": 8, "vmax_bf16": 9,
+           "v_f32": 10, "vmax_f32": 11}
 OPT_AMSGRAD = 1
 _F_DECOUPLED, _F_STOCHASTIC, _F_PERCENTILE, _F_STATIC_SCALES = 1, 2, 4, 8
 _STATUS = {0: "ADAM_OK", -1: "ADAM_EINVAL", -2: "ADAM_EMODE", -3: "ADAM_EALIGN",
@@ -326,10 +327,11 @@ def state_buffer_sizes(numels, storage, amsgrad=False):
     sizes = {"bf16": {"m_bf16": 2 * padded, "v_bf16": 2 * padded},
              "q8": {"m_codes": padded, "v_codes": padded, "m_scale": 4 * blocks,
                     "v_scale": 4 * blocks},
-             "q8_v_only": {"v_codes": padded, "v_scale": 4 * blocks, "m_f32": 4 * padded}}[storage]
+             "q8_v_only": {"v_codes": padded, "v_scale": 4 * blocks, "m_f32": 4 * padded},
+             "f32": {"m_f32": 4 * padded, "v_f32": 4 * padded}}[storage]
     if amsgrad:
-        sizes.update({"vmax_bf16": 2 * padded} if storage == "bf16"
-                     else {"vmax_codes": padded, "vmax_scale": 4 * blocks})
+        sizes.update({"bf16": {"vmax_bf16": 2 * padded}, "f32": {"vmax_f32": 4 * padded}}.get(
+            storage, {"vmax_codes": padded, "vmax_scale": 4 * blocks}))
     return sizes
 
 
@@ -382,7 +384,8 @@ def adam_state_buffer_bytes(state, which):
 
 _BUF_DTYPES = {"m_codes": "int8", "v_codes": "uint8", "m_scale": "float32",
                "v_scale": "float32", "m_bf16": "int16", "v_bf16": "int16", "m_f32": "float32",
-               "vmax_codes": "uint8", "vmax_scale": "float32", "vmax_bf16": "int16"}
+               "vmax_codes": "uint8", "vmax_scale": "float32", "vmax_bf16": "int16",
+               "v_f32": "float32", "vmax_f32": "float32"}
 
 
 def adam_state_read(state, which, out=None, stream=None):

@@ -32,18 +32,18 @@ struct TensorRef {
 };
 static_assert(sizeof(TensorRef) == 16, "pointer pair is one 16-byte load");
 
-enum Storage : int { kStoreBf16 = 1, kStoreQ8 = 2, kStoreQ8VOnly = 3 };
+enum Storage : int { kStoreBf16 = 1, kStoreQ8 = 2, kStoreQ8VOnly = 3, kStoreF32 = 4 };
 
 // Kernel arguments for one step (passed by value in the kernarg segment).
 struct StepArgs {
     const BlockDesc *desc;
     const TensorRef *tensors;
     void *m_state;   // bf16 / int8 codes / fp32, per storage mode
-    void *v_state;   // bf16 / uint8 codes
+    void *v_state;   // bf16 / uint8 codes / fp32
     float *m_scale;  // per block (Q8)
     float *v_scale;  // per block (Q8, Q8_V_ONLY)
     const uint64_t *draw_first;  // per tensor: stochastic-rounding draw index of element 0
-    void *w_state;   // AMSGrad running max of v: bf16 / uint8 codes (else NULL)
+    void *w_state;   // AMSGrad running max of v, stored as v is (else NULL)
     float *w_scale;  // its per-block scale (8-bit storage with AMSGrad)
     float step;      // lr / (1 - beta1^t)
     float ibc2;      // 1 / sqrt(1 - beta2^t)

@@ -7,9 +7,10 @@
 // statistic, walks down the top values (of the lanes' top-4 lists, or of
 // per-wave lists when v is the only 8-bit moment) or an LDS radix select;
 // skipped for a moment whose static scale is already set), requantizes and
-// writes params, moments and the new scales once.  With AMSGrad the running
+// writes params, moments and the new scales once (bf16 and fp32 moments have
+// no statistic).  With AMSGrad the running
 // maximum of v travels the same way as v.  The step is a streaming map over
-// HBM (14-20 bytes per parameter, ~1.5 flop/byte), so there is no MFMA work; what matters is
+// HBM (14-36 bytes per parameter, ~1.5 flop/byte), so there is no MFMA work; what matters is
 // coalesced 16-byte loads, enough bytes in flight per CU and a VALU budget
 // of roughly 100 instructions per element at the bandwidth target.
 //
@@ -858,17 +859,41 @@ __device__ __forceinline__ BlockCtx load_ctx(const StepArgs &a, uint32_t idx) {
     return c;
 }
 
+// 8-bit codes with a scale per block (v, and m too in kStoreQ8).
+constexpr bool quantizes(int store) { return store == kStoreQ8 || store == kStoreQ8VOnly; }
+
+// Words a thread holds of one moment: bf16 pairs, four codes, or fp32 values.
+constexpr int moment_words(int store, bool is_m) {
+    if (store == kStoreBf16) return kItems / 2;
+    if (store == kStoreF32 || (is_m && store == kStoreQ8VOnly)) return kItems;
+    return kGroups;
+}
+
 // Raw (undecoded) per-thread data of one block, as loaded.  w: the AMSGrad
 // running maximum of v, stored as v is (unused without kAms).
 template <int kStore, bool kGradBf16, bool kAms>
 struct BlockRegs {
     float p[kItems];
     uint32_t g[kGradBf16 ? kItems / 2 : kItems];  // fp32 bits, or bf16 pairs
-    uint32_t m[kStore == kStoreBf16 ? kItems / 2 : (kStore == kStoreQ8 ? kGroups : kItems)];
-    uint32_t v[kStore == kStoreBf16 ? kItems / 2 : kGroups];
-    uint32_t w[!kAms ? 1 : (kStore == kStoreBf16 ? kItems / 2 : kGroups)];
+    uint32_t m[moment_words(kStore, true)];
+    uint32_t v[moment_words(kStore, false)];
+    uint32_t w[!kAms ? 1 : moment_words(kStore, false)];
     float Am, Av, Aw;  // stored scales of the 8-bit moments
 };
+
+// Four fp32 state values from `from`, or zeros; the first `live` of them are
+// the tensor's, the others (its padding) zero as well.
+template <bool kFull>
+__device__ __forceinline__ void load_state_f32(const float *from, bool in, int32_t live, uint32_t *r) {
+    f32x4 x = {0.f, 0.f, 0.f, 0.f};
+    if (in) x = ld_f32x4(from);
+    r[0] = __float_as_uint(x.x); r[1] = __float_as_uint(x.y);
+    r[2] = __float_as_uint(x.z); r[3] = __float_as_uint(x.w);
+    if constexpr (!kFull) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) r[k] &= (uint32_t)((int32_t)(k - live) >> 31);
+    }
+}
 
 // Issues every load of one block.  kFull: the block has 2048 live elements,
 // so all loads are unconditional 16/8/4-byte vector loads (no branches: the
@@ -880,8 +905,8 @@ __device__ __forceinline__ void load_data(const StepArgs &a, const BlockCtx &c,
                                           BlockRegs<kStore, kGradBf16, kAms> &r) {
     const int tid = kFull ? (int)threadIdx.x : local_tid();  // the ragged path: see local_tid
     r.Am = kStore == kStoreQ8 ? a.m_scale[c.slot] : 0.0f;
-    r.Av = kStore != kStoreBf16 ? a.v_scale[c.slot] : 0.0f;
-    r.Aw = kAms && kStore != kStoreBf16 ? a.w_scale[c.slot] : 0.0f;
+    r.Av = quantizes(kStore) ? a.v_scale[c.slot] : 0.0f;
+    r.Aw = kAms && quantizes(kStore) ? a.w_scale[c.slot] : 0.0f;
 #pragma unroll
     for (int j = 0; j < kGroups; ++j) {
         const uint32_t e0 = j * (kThreads * 4) + 4 * tid;
@@ -940,20 +965,18 @@ __device__ __forceinline__ void load_data(const StepArgs &a, const BlockCtx &c,
                 if (in) hw = ld_u32x2(reinterpret_cast<const uint16_t *>(a.w_state) + s);
                 r.w[2 * j] = hw.x & keep16lo; r.w[2 * j + 1] = hw.y & keep16hi;
             }
+        } else if constexpr (kStore == kStoreF32) {
+            load_state_f32<kFull>(reinterpret_cast<const float *>(a.m_state) + s, in, live, r.m + 4 * j);
+            load_state_f32<kFull>(reinterpret_cast<const float *>(a.v_state) + s, in, live, r.v + 4 * j);
+            if constexpr (kAms)
+                load_state_f32<kFull>(reinterpret_cast<const float *>(a.w_state) + s, in, live, r.w + 4 * j);
         } else {
             r.v[j] = in ? ld_u32(reinterpret_cast<const uint8_t *>(a.v_state) + s) & keep8 : 0u;
             if constexpr (kAms) r.w[j] = in ? ld_u32(reinterpret_cast<const uint8_t *>(a.w_state) + s) & keep8 : 0u;
             if constexpr (kStore == kStoreQ8) {
                 r.m[j] = in ? ld_u32(reinterpret_cast<const int8_t *>(a.m_state) + s) & keep8 : 0u;
             } else {
-                f32x4 mf = {0.f, 0.f, 0.f, 0.f};
-                if (in) mf = ld_f32x4(reinterpret_cast<const float *>(a.m_state) + s);
-                r.m[4 * j + 0] = __float_as_uint(mf.x); r.m[4 * j + 1] = __float_as_uint(mf.y);
-                r.m[4 * j + 2] = __float_as_uint(mf.z); r.m[4 * j + 3] = __float_as_uint(mf.w);
-                if constexpr (!kFull) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) r.m[4 * j + k] &= (uint32_t)((int32_t)(k - live) >> 31);
-                }
+                load_state_f32<kFull>(reinterpret_cast<const float *>(a.m_state) + s, in, live, r.m + 4 * j);
             }
         }
     }
@@ -1076,6 +1099,10 @@ __device__ __forceinline__ void process_block(const StepArgs &a, const BlockCtx 
             mo[i] = bf16_to_f32((r.m[i / 2] >> (16 * (i & 1))) & 0xFFFFu);
             vo[i] = bf16_to_f32((r.v[i / 2] >> (16 * (i & 1))) & 0xFFFFu);
             if constexpr (kAms) wo[i] = bf16_to_f32((r.w[i / 2] >> (16 * (i & 1))) & 0xFFFFu);
+        } else if constexpr (kStore == kStoreF32) {
+            mo[i] = __uint_as_float(r.m[i]);
+            vo[i] = __uint_as_float(r.v[i]);
+            if constexpr (kAms) wo[i] = __uint_as_float(r.w[i]);
         } else {
             vo[i] = ((float)((r.v[i / 4] >> (8 * (i & 3))) & 0xFFu) * Rv) * r.Av;
             if constexpr (kAms) wo[i] = ((float)((r.w[i / 4] >> (8 * (i & 3))) & 0xFFu) * Rv) * r.Aw;
@@ -1169,6 +1196,19 @@ __device__ __forceinline__ void process_block(const StepArgs &a, const BlockCtx 
                                       f32_to_bf16(wo[4 * j + 2]) | (f32_to_bf16(wo[4 * j + 3]) << 16)};
                     st_u32x2(reinterpret_cast<uint16_t *>(a.w_state) + s, hw);
                 }
+            }
+        }
+    } else if constexpr (kStore == kStoreF32) {
+#pragma unroll
+        for (int j = 0; j < kGroups; ++j) {
+            const uint32_t e0 = j * (kThreads * 4) + 4 * tid;
+            if (kFull || e0 < c.npad) {
+                const size_t s = c.gidx + e0;
+                const int b = 4 * j;
+                st_f32x4(reinterpret_cast<float *>(a.m_state) + s, f32x4{mo[b], mo[b + 1], mo[b + 2], mo[b + 3]});
+                st_f32x4(reinterpret_cast<float *>(a.v_state) + s, f32x4{vo[b], vo[b + 1], vo[b + 2], vo[b + 3]});
+                if constexpr (kAms)
+                    st_f32x4(reinterpret_cast<float *>(a.w_state) + s, f32x4{wo[b], wo[b + 1], wo[b + 2], wo[b + 3]});
             }
         }
     } else {
@@ -1436,6 +1476,9 @@ adam_step_kernel(StepArgs a) {
 // variants with little compute per block stream fastest with few workgroups
 // resident per CU; their launch reserves LDS it does not use (CU LDS is 160
 // KiB).  Measured per variant: bf16 moments (no block statistic) at most 3;
+// fp32 moments, whose blocks bring the most bytes, at most 2 (three decoder blocks
+// of width 2048, fp32 gradients: 722 us, 744 at 3, 751 at 4, 770 uncapped; two
+// tables with AMSGrad and bf16 gradients: 646 us, 649 at 3, 658 at 4, 674 uncapped);
 // 8-bit with the block maximum and nearest rounding at most 4 (GPT-1.3B
 // shaped set with bf16 gradients +7% over uncapped, ViT-Base with fp32
 // gradients unchanged); fp32 m + 8-bit v with the percentile walk and
@@ -1450,6 +1493,9 @@ adam_step_kernel(StepArgs a) {
 constexpr int kCuLdsBytes = 160 * 1024;
 #ifndef ADAM_BF16_RESIDENT_PER_CU
 #define ADAM_BF16_RESIDENT_PER_CU 3
+#endif
+#ifndef ADAM_F32_RESIDENT_PER_CU
+#define ADAM_F32_RESIDENT_PER_CU 2
 #endif
 #ifndef ADAM_Q8_NEAREST_RESIDENT_PER_CU
 #define ADAM_Q8_NEAREST_RESIDENT_PER_CU 4
@@ -1470,6 +1516,7 @@ hipError_t launch_one(const StepArgs &a, hipStream_t stream) {
     constexpr bool kLight = !kSR && (kPct == kPctNone || (kPct == kPctTop && kStore == kStoreQ8VOnly && !kAms));
     constexpr bool kSrBf16g = kSR && kGradBf16 && !kAms && kPct == kPctNone;
     constexpr int kResident = kStore == kStoreBf16 ? ADAM_BF16_RESIDENT_PER_CU
+                              : kStore == kStoreF32 ? ADAM_F32_RESIDENT_PER_CU
                               : kLight             ? ADAM_Q8_NEAREST_RESIDENT_PER_CU
                               : kSrBf16g           ? ADAM_Q8_SR_BF16G_RESIDENT_PER_CU
                                                    : ADAM_Q8_RESIDENT_PER_CU;
@@ -1513,6 +1560,9 @@ hipError_t launch_storage(const Variant &v, const StepArgs &a, hipStream_t strea
     case kStoreBf16:
         return v.grad_bf16 ? launch_one<kStoreBf16, true, false, kPctNone, false, kAms>(a, stream)
                            : launch_one<kStoreBf16, false, false, kPctNone, false, kAms>(a, stream);
+    case kStoreF32:
+        return v.grad_bf16 ? launch_one<kStoreF32, true, false, kPctNone, false, kAms>(a, stream)
+                           : launch_one<kStoreF32, false, false, kPctNone, false, kAms>(a, stream);
     case kStoreQ8:
         return v.grad_bf16 ? launch_q<kStoreQ8, true, kAms>(v, a, stream)
                            : launch_q<kStoreQ8, false, kAms>(v, a, stream);

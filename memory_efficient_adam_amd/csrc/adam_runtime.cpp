@@ -56,10 +56,10 @@ struct adam_state {
     bool stage_pending[kStageSlots] = {};
     int next_stage = 0;
     void *m = nullptr;                   // bf16 / int8 / fp32 first moment
-    void *v = nullptr;                   // bf16 / uint8 second moment
+    void *v = nullptr;                   // bf16 / uint8 / fp32 second moment
     float *m_scale = nullptr;
     float *v_scale = nullptr;
-    void *w = nullptr;                   // AMSGrad running max of v: bf16 / uint8
+    void *w = nullptr;                   // AMSGrad running max of v: bf16 / uint8 / fp32
     float *w_scale = nullptr;
 };
 
@@ -93,7 +93,8 @@ int64_t blocks_of(int64_t n) { return (n + kBlock - 1) / kBlock; }
 
 int check_layout(const adam_layout *l) {
     if (!l) return fail(ADAM_EINVAL, "layout is NULL");
-    if (l->storage != ADAM_STORE_BF16 && l->storage != ADAM_STORE_Q8 && l->storage != ADAM_STORE_Q8_V_ONLY)
+    if (l->storage != ADAM_STORE_BF16 && l->storage != ADAM_STORE_Q8 && l->storage != ADAM_STORE_Q8_V_ONLY &&
+        l->storage != ADAM_STORE_F32)
         return fail(ADAM_EINVAL, "unknown storage mode " + std::to_string(l->storage));
     if (l->grad_dtype != ADAM_GRAD_F32 && l->grad_dtype != ADAM_GRAD_BF16)
         return fail(ADAM_EINVAL, "unknown grad dtype " + std::to_string(l->grad_dtype));
@@ -115,16 +116,24 @@ int check_numels(int32_t n_tensors, const int64_t *numels) {
 
 bool amsgrad(const adam_layout &l) { return (l.options & ADAM_OPT_AMSGRAD) != 0; }
 
+// 8-bit codes with a scale per block (v, and m too in ADAM_STORE_Q8)
+bool quantizes(int32_t storage) { return storage == ADAM_STORE_Q8 || storage == ADAM_STORE_Q8_V_ONLY; }
+
+// bytes of a stored entry of m, and of v and its AMSGrad maximum
+int64_t m_entry_bytes(int32_t storage) {
+    return storage == ADAM_STORE_BF16 ? 2 : (storage == ADAM_STORE_Q8 ? 1 : 4);
+}
+int64_t v_entry_bytes(int32_t storage) {
+    return storage == ADAM_STORE_BF16 ? 2 : (storage == ADAM_STORE_F32 ? 4 : 1);
+}
+
 // (bytes per padded element, bytes per block) of a layout's state
 void storage_costs(const adam_layout &l, int64_t &per_elem, int64_t &per_block) {
-    switch (l.storage) {
-    case ADAM_STORE_BF16: per_elem = 4; per_block = 0; break;
-    case ADAM_STORE_Q8: per_elem = 2; per_block = 8; break;
-    default: per_elem = 5; per_block = 4; break;
-    }
+    per_elem = m_entry_bytes(l.storage) + v_entry_bytes(l.storage);
+    per_block = l.storage == ADAM_STORE_Q8 ? 8 : (l.storage == ADAM_STORE_Q8_V_ONLY ? 4 : 0);
     if (amsgrad(l)) {  // the running maximum is stored as v is
-        per_elem += l.storage == ADAM_STORE_BF16 ? 2 : 1;
-        per_block += l.storage == ADAM_STORE_BF16 ? 0 : 4;
+        per_elem += v_entry_bytes(l.storage);
+        per_block += quantizes(l.storage) ? 4 : 0;
     }
 }
 
@@ -144,7 +153,7 @@ int check_hparams(const adam_hparams *hp, int32_t storage) {
     if (hp->reserved != 0) return fail(ADAM_EINVAL, "reserved must be 0");
     if ((hp->flags & ADAM_F_PERCENTILE) && !(hp->percentile >= 0.0f && hp->percentile <= 100.0f))
         return fail(ADAM_EINVAL, "percentile must be in [0, 100]");
-    if (storage == ADAM_STORE_BF16 && (hp->flags & (ADAM_F_STOCHASTIC | ADAM_F_PERCENTILE | ADAM_F_STATIC_SCALES)))
+    if (!quantizes(storage) && (hp->flags & (ADAM_F_STOCHASTIC | ADAM_F_PERCENTILE | ADAM_F_STATIC_SCALES)))
         return fail(ADAM_EINVAL, "stochastic rounding, percentile and static scales apply to 8-bit storage only");
     return ADAM_OK;
 }
@@ -215,21 +224,25 @@ BufferView buffer_of(const adam_state *s, int32_t which) {
     const bool ams = amsgrad(s->layout);
     switch (which) {
     case ADAM_BUF_M_CODES: return st == ADAM_STORE_Q8 ? BufferView{s->m, s->padded} : BufferView{nullptr, -1};
-    case ADAM_BUF_V_CODES: return st != ADAM_STORE_BF16 ? BufferView{s->v, s->padded} : BufferView{nullptr, -1};
+    case ADAM_BUF_V_CODES: return quantizes(st) ? BufferView{s->v, s->padded} : BufferView{nullptr, -1};
     case ADAM_BUF_M_SCALE:
         return st == ADAM_STORE_Q8 ? BufferView{s->m_scale, 4 * s->nblocks} : BufferView{nullptr, -1};
     case ADAM_BUF_V_SCALE:
-        return st != ADAM_STORE_BF16 ? BufferView{s->v_scale, 4 * s->nblocks} : BufferView{nullptr, -1};
+        return quantizes(st) ? BufferView{s->v_scale, 4 * s->nblocks} : BufferView{nullptr, -1};
     case ADAM_BUF_M_BF16: return st == ADAM_STORE_BF16 ? BufferView{s->m, 2 * s->padded} : BufferView{nullptr, -1};
     case ADAM_BUF_V_BF16: return st == ADAM_STORE_BF16 ? BufferView{s->v, 2 * s->padded} : BufferView{nullptr, -1};
     case ADAM_BUF_M_F32:
-        return st == ADAM_STORE_Q8_V_ONLY ? BufferView{s->m, 4 * s->padded} : BufferView{nullptr, -1};
+        return st == ADAM_STORE_Q8_V_ONLY || st == ADAM_STORE_F32 ? BufferView{s->m, 4 * s->padded}
+                                                                  : BufferView{nullptr, -1};
     case ADAM_BUF_VMAX_CODES:
-        return ams && st != ADAM_STORE_BF16 ? BufferView{s->w, s->padded} : BufferView{nullptr, -1};
+        return ams && quantizes(st) ? BufferView{s->w, s->padded} : BufferView{nullptr, -1};
     case ADAM_BUF_VMAX_SCALE:
-        return ams && st != ADAM_STORE_BF16 ? BufferView{s->w_scale, 4 * s->nblocks} : BufferView{nullptr, -1};
+        return ams && quantizes(st) ? BufferView{s->w_scale, 4 * s->nblocks} : BufferView{nullptr, -1};
     case ADAM_BUF_VMAX_BF16:
         return ams && st == ADAM_STORE_BF16 ? BufferView{s->w, 2 * s->padded} : BufferView{nullptr, -1};
+    case ADAM_BUF_V_F32: return st == ADAM_STORE_F32 ? BufferView{s->v, 4 * s->padded} : BufferView{nullptr, -1};
+    case ADAM_BUF_VMAX_F32:
+        return ams && st == ADAM_STORE_F32 ? BufferView{s->w, 4 * s->padded} : BufferView{nullptr, -1};
     default: return BufferView{nullptr, -1};
     }
 }
@@ -335,8 +348,7 @@ int adam_state_create(adam_state **out, int32_t n_tensors, const int64_t *numels
 
         hipStream_t stream = reinterpret_cast<hipStream_t>(hip_stream);
         const int32_t st = layout->storage;
-        const int64_t m_bytes = st == ADAM_STORE_BF16 ? 2 * s->padded : (st == ADAM_STORE_Q8 ? s->padded : 4 * s->padded);
-        const int64_t v_bytes = st == ADAM_STORE_BF16 ? 2 * s->padded : s->padded;
+        const int64_t m_bytes = m_entry_bytes(st) * s->padded, v_bytes = v_entry_bytes(st) * s->padded;
         if ((rc = alloc_zeroed(&s->m, m_bytes, stream)) || (rc = alloc_zeroed(&s->v, v_bytes, stream))) {
             release(s);
             return rc;
@@ -345,13 +357,13 @@ int adam_state_create(adam_state **out, int32_t n_tensors, const int64_t *numels
             release(s);
             return rc;
         }
-        if (st != ADAM_STORE_BF16 && (rc = alloc_zeroed((void **)&s->v_scale, 4 * s->nblocks, stream))) {
+        if (quantizes(st) && (rc = alloc_zeroed((void **)&s->v_scale, 4 * s->nblocks, stream))) {
             release(s);
             return rc;
         }
         if (amsgrad(*layout) &&
-            ((rc = alloc_zeroed(&s->w, st == ADAM_STORE_BF16 ? 2 * s->padded : s->padded, stream)) ||
-             (st != ADAM_STORE_BF16 && (rc = alloc_zeroed((void **)&s->w_scale, 4 * s->nblocks, stream))))) {
+            ((rc = alloc_zeroed(&s->w, v_bytes, stream)) ||
+             (quantizes(st) && (rc = alloc_zeroed((void **)&s->w_scale, 4 * s->nblocks, stream))))) {
             release(s);
             return rc;
         }
@@ -441,11 +453,14 @@ std::vector<int32_t> buffers_of(const adam_layout &l) {
     switch (l.storage) {
     case ADAM_STORE_BF16: b = {ADAM_BUF_M_BF16, ADAM_BUF_V_BF16}; break;
     case ADAM_STORE_Q8: b = {ADAM_BUF_M_CODES, ADAM_BUF_V_CODES, ADAM_BUF_M_SCALE, ADAM_BUF_V_SCALE}; break;
+    case ADAM_STORE_F32: b = {ADAM_BUF_M_F32, ADAM_BUF_V_F32}; break;
     default: b = {ADAM_BUF_V_CODES, ADAM_BUF_V_SCALE, ADAM_BUF_M_F32}; break;
     }
     if (amsgrad(l)) {
         if (l.storage == ADAM_STORE_BF16) {
             b.push_back(ADAM_BUF_VMAX_BF16);
+        } else if (l.storage == ADAM_STORE_F32) {
+            b.push_back(ADAM_BUF_VMAX_F32);
         } else {
             b.push_back(ADAM_BUF_VMAX_CODES);
             b.push_back(ADAM_BUF_VMAX_SCALE);
@@ -864,11 +879,14 @@ int adam_step_noalloc(int32_t n_tensors, const int64_t *numels, const adam_layou
         const int32_t st = layout->storage;
         const bool ams = amsgrad(*layout);
         a.m_state = state[st == ADAM_STORE_BF16 ? ADAM_BUF_M_BF16 : (st == ADAM_STORE_Q8 ? ADAM_BUF_M_CODES : ADAM_BUF_M_F32)];
-        a.v_state = state[st == ADAM_STORE_BF16 ? ADAM_BUF_V_BF16 : ADAM_BUF_V_CODES];
+        a.v_state = state[st == ADAM_STORE_BF16 ? ADAM_BUF_V_BF16 : (st == ADAM_STORE_F32 ? ADAM_BUF_V_F32 : ADAM_BUF_V_CODES)];
         a.m_scale = st == ADAM_STORE_Q8 ? static_cast<float *>(state[ADAM_BUF_M_SCALE]) : nullptr;
-        a.v_scale = st != ADAM_STORE_BF16 ? static_cast<float *>(state[ADAM_BUF_V_SCALE]) : nullptr;
-        a.w_state = ams ? state[st == ADAM_STORE_BF16 ? ADAM_BUF_VMAX_BF16 : ADAM_BUF_VMAX_CODES] : nullptr;
-        a.w_scale = ams && st != ADAM_STORE_BF16 ? static_cast<float *>(state[ADAM_BUF_VMAX_SCALE]) : nullptr;
+        a.v_scale = quantizes(st) ? static_cast<float *>(state[ADAM_BUF_V_SCALE]) : nullptr;
+        a.w_state = ams ? state[st == ADAM_STORE_BF16  ? ADAM_BUF_VMAX_BF16
+                                : st == ADAM_STORE_F32 ? ADAM_BUF_VMAX_F32
+                                                       : ADAM_BUF_VMAX_CODES]
+                        : nullptr;
+        a.w_scale = ams && quantizes(st) ? static_cast<float *>(state[ADAM_BUF_VMAX_SCALE]) : nullptr;
         fill_scalars(a, hp);
         a.n_full = (uint32_t)n_full;
         a.n_all = (uint32_t)nblocks;
