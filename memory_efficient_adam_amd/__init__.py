@@ -1,8 +1,9 @@
-"""MI355X-native compressed-moment Adam/AdamW step, and the Muon step with its
-Newton-Schulz orthogonalisation for 2-D weights.
+"""MI355X-native compressed-moment Adam/AdamW step, the Muon step with its
+Newton-Schulz orthogonalisation for 2-D weights, and an embedding table's
+lookup, gradient and step of rows.
 
-Thin Python binding over ``libadam_mi355x.so`` (C ABI in
-``include/adam_mi355x.h`` and ``include/muon_mi355x.h``): the functions below carry the C names and only
+Thin Python binding over ``libadam_mi355x.so`` (C ABI in ``include/adam_mi355x.h``,
+``include/muon_mi355x.h`` and ``include/embedding_mi355x.h``): the functions below carry the C names and only
 marshal arguments (torch tensors -> device pointers, the caller's current
 HIP stream).  Every step of the update runs in the library's HIP kernels;
 there is no CPU or PyTorch fallback -- if the library is not built, the
@@ -34,6 +35,12 @@ from ._binding import (  # noqa: F401
     library,
     library_path,
     state_buffer_sizes,
+)
+from ._embedding import (  # noqa: F401
+    embedding_adam_step,
+    embedding_gradient,
+    embedding_gradient_workspace_bytes,
+    embedding_lookup,
 )
 from ._muon import (  # noqa: F401
     MUON_SCALES,

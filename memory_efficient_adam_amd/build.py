@@ -1,4 +1,4 @@
-"""Builds libadam_mi355x.so (the Adam and Muon steps) and libadam_stream_probe.so (the
+"""Builds libadam_mi355x.so (the Adam and Muon steps, the embedding operations) and libadam_stream_probe.so (the
 stream probe, a measurement kernel the step does not use) in-tree with hipcc
 for gfx950.
 
@@ -14,7 +14,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIBRARY = os.path.join(HERE, "libadam_mi355x.so")
-SOURCES = [os.path.join(CSRC, f) for f in ("adam_kernels.hip", "adam_runtime.cpp", "muon_kernels.hip",
+SOURCES = [os.path.join(CSRC, f) for f in ("adam_kernels.hip", "adam_runtime.cpp", "embedding_kernels.hip",
+                                           "embedding_runtime.cpp", "muon_kernels.hip",
                                            "muon_runtime.cpp")]
 PROBE_LIBRARY = os.path.join(HERE, "libadam_stream_probe.so")
 PROBE_SOURCES = [os.path.join(CSRC, "stream_probe.hip")]

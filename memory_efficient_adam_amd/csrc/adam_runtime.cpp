@@ -276,6 +276,9 @@ void fill_scalars(StepArgs &a, const adam_hparams *hp) {
 }  // namespace
 
 int adam_mi355x::set_last_error(int code, const std::string &msg) { return fail(code, msg); }
+int adam_mi355x::check_adam_layout(const adam_layout *l) { return check_layout(l); }
+int adam_mi355x::check_adam_hparams(const adam_hparams *hp, int32_t storage) { return check_hparams(hp, storage); }
+void adam_mi355x::adam_scalars(StepArgs &a, const adam_hparams *hp) { fill_scalars(a, hp); }
 
 extern "C" {
 

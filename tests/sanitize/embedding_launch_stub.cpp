@@ -1,0 +1,9 @@
+// Host-only build of the embedding runtime (see launch_stub.cpp): nothing is launched.
+#include "embedding_internal.h"
+
+namespace adam_mi355x {
+hipError_t launch_lookup(bool, bool, const LookupArgs &, hipStream_t) { return hipErrorInvalidValue; }
+hipError_t launch_group(const GroupArgs &, hipStream_t) { return hipErrorInvalidValue; }
+hipError_t launch_sums(bool, bool, Goal, const SumArgs &, hipStream_t) { return hipErrorInvalidValue; }
+hipError_t launch_joins(bool, Goal, const SumArgs &, hipStream_t) { return hipErrorInvalidValue; }
+}  // namespace adam_mi355x
