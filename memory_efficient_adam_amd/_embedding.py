@@ -1,10 +1,14 @@
 """ctypes marshalling for the embedding calls of libadam_mi355x.so (names follow
-include/embedding_mi355x.h)."""
+include/embedding_mi355x.h).
+
+The calls on few tokens take some 4 us on the GPU, so what a call derives from its
+tensors' sizes, strides and types (the C call's shape, its checks, the workspace's
+size) is remembered by exactly those, in _lookup_form and _gradient_form."""
 import ctypes
 import functools
 
 from . import _binding as B
-from ._binding import AdamError, _check, _on, _stream, adam_last_error
+from ._binding import AdamError, _check, _on, adam_last_error
 from ._muon import _has_tangent, _launching_stream
 
 
@@ -49,7 +53,6 @@ def _dtype(name, dtype, codes=_DTYPES):
     return code
 
 
-@functools.lru_cache(maxsize=256)
 def _row_stride(name, shape, stride):
     """Elements between the rows of a tensor (.., cols) whose rows are contiguous
     and whose other dimensions have one stride between rows."""
@@ -69,11 +72,11 @@ def _row_stride(name, shape, stride):
     return between if count > 1 else shape[-1]
 
 
-def _check_tensors(**tensors):
-    """Tensors of the current device (None: not given)."""
+def _check_tensors(*named):
+    """Tensors of the current device, as (name, tensor) pairs (None: not given)."""
     import torch
     current = B._current_device()
-    for name, t in tensors.items():
+    for name, t in named:
         if t is None:
             continue
         if not isinstance(t, torch.Tensor):
@@ -84,41 +87,52 @@ def _check_tensors(**tensors):
             raise ValueError(f"{name} is on {t.device}, the current device is cuda:{current}")
 
 
-def _check_no_gradient(what, **tensors):
+def _check_no_gradient(what, *named):
     import torch
-    for name, t in tensors.items():
+    for name, t in named:
         if t is None:
             continue
-        if torch.is_grad_enabled() and t.requires_grad:
+        if t.requires_grad and torch.is_grad_enabled():
             raise ValueError(f"no gradient is defined through {what}: detach {name} or call it under torch.no_grad()")
         if _has_tangent(t):
             raise ValueError(f"no forward-mode gradient is defined through {what}: pass the primal of {name}")
 
 
-def _table_of(name, t):
-    if t.dim() != 2:
-        raise ValueError(f"{name}: expected (rows, cols), got {tuple(t.shape)}")
-    return _dtype(name, t.dtype), _row_stride(name, tuple(t.shape), t.stride())
-
-
-def _shape_of(rows, cols, tokens, table_stride, value_stride, table_dtype, value_dtype, scale):
-    return embedding_shape(rows, cols, tokens.numel(), table_stride, value_stride, table_dtype, value_dtype,
-                           _dtype("tokens", tokens.dtype, _TOKEN_DTYPES), float(scale))
+def _current_stream(device):
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device)
 
 
 # ---------------------------------------------------------------- lookup
-def _lookup(table, tokens, scale, dtype, out, stream):
+@functools.lru_cache(maxsize=512)
+def _lookup_form(table_shape, table_stride, table_dtype, token_shape, token_dtype, out_shape, out_stride, out_dtype, scale):
+    """The C call's shape.  out_stride: None for a new tensor's."""
+    if len(table_shape) != 2:
+        raise ValueError(f"table: expected (rows, cols), got {tuple(table_shape)}")
+    rows, cols = table_shape
+    want = tuple(token_shape) + (cols,)
+    if out_stride is not None and tuple(out_shape) != want:
+        raise ValueError(f"out must have the shape {want} and, if one is given, dtype")
+    count = 1
+    for n in token_shape:
+        count *= n
+    return embedding_shape(rows, cols, count, _row_stride("table", table_shape, table_stride),
+                           cols if out_stride is None else _row_stride("out", out_shape, out_stride),
+                           _dtype("table", table_dtype), _dtype("dtype", out_dtype),
+                           _dtype("tokens", token_dtype, _TOKEN_DTYPES), scale)
+
+
+def _lookup(table, tokens, scale, dtype, out):
     import torch
-    rows, cols = table.shape
-    table_code, table_stride = _table_of("table", table)
-    with _on(_launching_stream(stream)):
-        tokens = tokens.contiguous()
-        if out is None:
-            out = torch.empty(tokens.shape + (cols,), dtype=dtype, device=table.device)
-        shape = _shape_of(rows, cols, tokens, table_stride, _row_stride("out", tuple(out.shape), out.stride()),
-                          table_code, _dtype("out", out.dtype), scale)
-        _check(library().embedding_lookup(ctypes.byref(shape), table.data_ptr(), tokens.data_ptr(), out.data_ptr(),
-                                          _stream(None)))
+    if out is None:
+        shape = _lookup_form(table.shape, table.stride(), table.dtype, tokens.shape, tokens.dtype, None, None, dtype, scale)
+        out = torch.empty((*tokens.shape, table.shape[1]), dtype=dtype, device=table.device)
+    else:
+        shape = _lookup_form(table.shape, table.stride(), table.dtype, tokens.shape, tokens.dtype, out.shape, out.stride(),
+                             dtype, scale)
+    tokens = tokens.contiguous()
+    _check(library().embedding_lookup(shape, table.data_ptr(), tokens.data_ptr(), out.data_ptr(),
+                                      _current_stream(table.get_device())))
     return out
 
 
@@ -129,17 +143,17 @@ def _function():
 
     class Lookup(torch.autograd.Function):
         @staticmethod
-        def forward(ctx, table, tokens, scale, dtype, stream):
+        def forward(ctx, table, tokens, scale, dtype):
             ctx.save_for_backward(tokens)
             ctx.rows, ctx.scale, ctx.dtype = table.shape[0], scale, table.dtype
-            return _lookup(table, tokens, scale, dtype, None, stream)
+            return _lookup(table, tokens, scale, dtype, None)
 
         @staticmethod
         @once_differentiable
         def backward(ctx, grad):
             tokens, = ctx.saved_tensors
             return embedding_gradient(grad.contiguous(), tokens, ctx.rows, scale=ctx.scale,
-                                      dtype=ctx.dtype), None, None, None, None
+                                      dtype=ctx.dtype), None, None, None
     return Lookup
 
 
@@ -151,29 +165,29 @@ def embedding_lookup(table, tokens, *, scale=1.0, dtype=None, out=None, stream=N
     a gradient it gets the dense one of embedding_gradient (in a backward pass; in neither a
     graph capture nor forward mode, and with no out)."""
     import torch
-    _check_tensors(table=table, tokens=tokens, out=out)
-    _table_of("table", table)
-    if out is not None and (out.shape != tokens.shape + table.shape[1:] or dtype not in (None, out.dtype)):
-        raise ValueError(f"out must have the shape {tuple(tokens.shape + table.shape[1:])} and, if one is given, dtype")
-    dtype = dtype or table.dtype
-    _dtype("dtype", dtype)
-    _dtype("tokens", tokens.dtype, _TOKEN_DTYPES)
+    _check_tensors(("table", table), ("tokens", tokens), ("out", out))
+    if out is not None and dtype not in (None, out.dtype):
+        raise ValueError(f"out has dtype {out.dtype}, not {dtype}")
+    dtype = out.dtype if out is not None else dtype or table.dtype
     if _has_tangent(table):
         raise ValueError("no forward-mode gradient is defined through embedding_lookup: pass the primal of table")
-    if torch.is_grad_enabled() and (table.requires_grad or (out is not None and out.requires_grad)):
+    _launching_stream(stream)
+    if (table.requires_grad or (out is not None and out.requires_grad)) and torch.is_grad_enabled():
         if out is not None:
             raise ValueError("no gradient is defined through out: detach table and out, or call it under torch.no_grad()")
         if torch.cuda.is_current_stream_capturing():
             raise ValueError("a lookup with a gradient cannot be captured: record embedding_lookup under "
                              "torch.no_grad(), and embedding_gradient")
-        _launching_stream(stream)
         with _on(stream):
-            return _function().apply(table, tokens, scale, dtype, None)
-    return _lookup(table, tokens, scale, dtype, out, stream)
+            return _function().apply(table, tokens, float(scale), dtype)
+    if stream is None:
+        return _lookup(table, tokens, float(scale), dtype, out)
+    with _on(stream):
+        return _lookup(table, tokens, float(scale), dtype, out)
 
 
 # ---------------------------------------------------------------- gradient
-@functools.lru_cache(maxsize=256)
+@functools.lru_cache(maxsize=512)
 def embedding_gradient_workspace_bytes(tokens, rows, cols):
     n = library().embedding_gradient_workspace_bytes(tokens, rows, cols)
     if n < 0:
@@ -181,21 +195,34 @@ def embedding_gradient_workspace_bytes(tokens, rows, cols):
     return int(n)
 
 
-def _check_grad(grad, tokens):
-    if grad.dim() != tokens.dim() + 1 or grad.shape[:-1] != tokens.shape:
-        raise ValueError(f"grad must have tokens' shape and one dimension more, got {tuple(grad.shape)} for "
-                         f"{tuple(tokens.shape)}")
-    return _dtype("grad", grad.dtype), _row_stride("grad", tuple(grad.shape), grad.stride())
+@functools.lru_cache(maxsize=512)
+def _gradient_form(grad_shape, grad_stride, grad_dtype, token_shape, token_dtype, rows, out_shape, out_stride, out_dtype,
+                   scale):
+    """The C call's shape and the bytes of its workspace.  out_stride: None for a new
+    tensor's."""
+    if len(grad_shape) != len(token_shape) + 1 or grad_shape[:-1] != token_shape:
+        raise ValueError(f"grad must have tokens' shape and one dimension more, got {tuple(grad_shape)} for "
+                         f"{tuple(token_shape)}")
+    cols = grad_shape[-1]
+    if out_stride is not None and tuple(out_shape) != (rows, cols):
+        raise ValueError(f"out must have the shape {(rows, cols)} and, if one is given, dtype")
+    count = 1
+    for n in token_shape:
+        count *= n
+    shape = embedding_shape(rows, cols, count, cols if out_stride is None else _row_stride("out", out_shape, out_stride),
+                            _row_stride("grad", grad_shape, grad_stride), _dtype("dtype", out_dtype),
+                            _dtype("grad", grad_dtype), _dtype("tokens", token_dtype, _TOKEN_DTYPES), scale)
+    return shape, embedding_gradient_workspace_bytes(count, rows, cols)
 
 
 def _workspace(workspace, need, device):
-    """(address, bytes, what holds it) of the workspace of a call on the current stream."""
+    """What holds the workspace of a call on the current stream, and its bytes."""
     import torch
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    elif not workspace.is_contiguous():
+        return torch.empty(need, dtype=torch.uint8, device=device), need
+    if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+    return workspace, workspace.numel() * workspace.element_size()
 
 
 def embedding_gradient(grad, tokens, rows, *, scale=1.0, dtype=None, out=None, accumulate=False, workspace=None,
@@ -208,32 +235,40 @@ def embedding_gradient(grad, tokens, rows, *, scale=1.0, dtype=None, out=None, a
     embedding_gradient_workspace_bytes(tokens, rows, cols) bytes that calls ordered on
     one stream may share (default: allocated for the call)."""
     import torch
-    _check_tensors(grad=grad, tokens=tokens, out=out, workspace=workspace)
-    _check_no_gradient("embedding_gradient", grad=grad, out=out)
-    code, stride = _check_grad(grad, tokens)
-    rows, cols = int(rows), grad.shape[-1]
+    _check_tensors(("grad", grad), ("tokens", tokens), ("out", out), ("workspace", workspace))
+    _check_no_gradient("embedding_gradient", ("grad", grad), ("out", out))
+    rows = int(rows)
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
         if rows < 0:
             raise ValueError(f"rows must not be negative, got {rows}")
-        _dtype("dtype", dtype or torch.float32)
-    elif tuple(out.shape) != (rows, cols) or dtype not in (None, out.dtype):
-        raise ValueError(f"out must have the shape {(rows, cols)} and, if one is given, dtype")
-    need = embedding_gradient_workspace_bytes(tokens.numel(), rows, cols)
+        dtype = dtype or torch.float32
+        form = _gradient_form(grad.shape, grad.stride(), grad.dtype, tokens.shape, tokens.dtype, rows, None, None, dtype,
+                              float(scale))
+    else:
+        if dtype not in (None, out.dtype):
+            raise ValueError(f"out has dtype {out.dtype}, not {dtype}")
+        form = _gradient_form(grad.shape, grad.stride(), grad.dtype, tokens.shape, tokens.dtype, rows, out.shape,
+                              out.stride(), out.dtype, float(scale))
+    shape, need = form
     with _on(_launching_stream(stream)):
         tokens = tokens.contiguous()
         if out is None:
-            out = torch.empty(rows, cols, dtype=dtype or torch.float32, device=grad.device)
-        out_code, out_stride = _table_of("out", out)
-        shape = _shape_of(rows, cols, tokens, out_stride, stride, out_code, code, scale)
-        at, nbytes, _held = _workspace(workspace, need, grad.device)
-        _check(library().embedding_gradient(ctypes.byref(shape), grad.data_ptr(), tokens.data_ptr(), out.data_ptr(),
-                                            int(bool(accumulate)), at, nbytes, _stream(None)))
+            out = torch.empty((rows, grad.shape[-1]), dtype=dtype, device=grad.device)
+        workspace, nbytes = _workspace(workspace, need, grad.device)
+        _check(library().embedding_gradient(shape, grad.data_ptr(), tokens.data_ptr(), out.data_ptr(),
+                                            1 if accumulate else 0, workspace.data_ptr(), nbytes,
+                                            _current_stream(grad.get_device())))
     return out
 
 
 # ---------------------------------------------------------------- step
+@functools.lru_cache(maxsize=64)
+def _buffer_sizes(numel, amsgrad):
+    return B.state_buffer_sizes([numel], "f32", amsgrad)
+
+
 def embedding_adam_step(table, grad, tokens, buffers, *, amsgrad=False, scale=1.0, lr, beta1, beta2, eps, weight_decay,
                         t, decoupled=True, workspace=None, stream=None):
     """The Adam/AdamW step with fp32 moments on the rows of table that tokens name, its
@@ -243,31 +278,30 @@ def embedding_adam_step(table, grad, tokens, buffers, *, amsgrad=False, scale=1.
     (state_buffer_sizes([rows * cols], "f32", amsgrad); zeros for a new state), on which
     either kind of step may be taken."""
     import torch
-    _check_tensors(table=table, grad=grad, tokens=tokens, workspace=workspace)
-    _check_no_gradient("embedding_adam_step", grad=grad)
-    code, stride = _check_grad(grad, tokens)
+    _check_tensors(("table", table), ("grad", grad), ("tokens", tokens), ("workspace", workspace))
+    _check_no_gradient("embedding_adam_step", ("grad", grad))
     if table.dim() != 2 or table.dtype != torch.float32 or not table.is_contiguous():
         raise ValueError("table must be a contiguous fp32 tensor (rows, cols)")
     rows, cols = table.shape
-    if grad.shape[-1] != cols:
-        raise ValueError(f"grad has {grad.shape[-1]} columns, the table {cols}")
-    want = B.state_buffer_sizes([rows * cols], "f32", amsgrad)
-    if set(buffers) != set(want):
+    if grad.dim() == 0 or grad.shape[-1] != cols:
+        raise ValueError(f"grad must have {cols} columns as the table has, got {tuple(grad.shape)}")
+    shape, need = _gradient_form(grad.shape, grad.stride(), grad.dtype, tokens.shape, tokens.dtype, rows, table.shape,
+                                 (cols, 1), table.dtype, float(scale))
+    want = _buffer_sizes(rows * cols, bool(amsgrad))
+    if buffers.keys() != want.keys():
         raise ValueError(f"buffers must be exactly {sorted(want)}, got {sorted(buffers)}")
     state = (ctypes.c_void_p * len(B.BUFFERS))()
-    _check_tensors(**{f"buffer {name}": b for name, b in buffers.items()})
     for name, nbytes in want.items():
         b = buffers[name]
+        _check_tensors((f"buffer {name}", b))
         if b.numel() * b.element_size() != nbytes or not b.is_contiguous():
             raise ValueError(f"buffer {name}: must be a contiguous tensor of {nbytes} bytes")
         state[B.BUFFERS[name]] = b.data_ptr()
-    need = embedding_gradient_workspace_bytes(tokens.numel(), rows, cols)
     hp = B._hparams(lr, beta1, beta2, eps, weight_decay, t, decoupled, False, None, 0, False)
-    layout = B._layout("f32", code, options=B.OPT_AMSGRAD if amsgrad else 0)
+    layout = B.adam_layout(B.STORAGES["f32"], shape.value_dtype, B.ADAM_BLOCK_SIZE, B.OPT_AMSGRAD if amsgrad else 0)
     with _on(_launching_stream(stream)):
         tokens = tokens.contiguous()
-        shape = _shape_of(rows, cols, tokens, cols, stride, 0, code, scale)
-        at, nbytes, _held = _workspace(workspace, need, table.device)
-        _check(library().embedding_adam_step(ctypes.byref(shape), table.data_ptr(), grad.data_ptr(), tokens.data_ptr(),
-                                             ctypes.cast(state, ctypes.c_void_p), ctypes.byref(hp),
-                                             ctypes.byref(layout), at, nbytes, _stream(None)))
+        workspace, nbytes = _workspace(workspace, need, table.device)
+        _check(library().embedding_adam_step(shape, table.data_ptr(), grad.data_ptr(), tokens.data_ptr(),
+                                             ctypes.addressof(state), hp, layout, workspace.data_ptr(), nbytes,
+                                             _current_stream(table.get_device())))

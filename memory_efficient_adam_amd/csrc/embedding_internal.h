@@ -22,9 +22,11 @@ struct LookupArgs {
 hipError_t launch_lookup(bool table_bf16, bool out_bf16, const LookupArgs &a, hipStream_t stream);
 
 // ---------------------------------------------------------------- grouping
-// The tokens' positions grouped by row.  Row r is in bucket r % kBuckets; a
-// workgroup a bucket.  Within a bucket a position's key is r / kBuckets, taken
-// kDigitBits bits at a time.
+// The tokens' positions grouped by row, in the rows' order.  Row r is in bucket
+// r >> bucket_bits, a workgroup a bucket; a bucket's rows are sorted by kDigitBits
+// bits at a time.  (Rows in order, not spread over the buckets: what is
+// read and written of the table then lies together, DRAM pages and translations
+// serve more of it.)
 constexpr uint32_t kBuckets = 256;
 constexpr uint32_t kDigitBits = 10;
 constexpr uint32_t kNoRow = 0xFFFFFFFFu;
@@ -33,14 +35,13 @@ struct GroupArgs {
     const void *tokens;
     uint32_t tokens_n, rows;
     uint32_t wide;
-    uint32_t passes, bits;  // digits of a key, and bits of each
-    uint32_t *keys[2];      // rows, grouped: [0] the result, [1] between passes (if there are several)
-    uint32_t *order[2];     // and the positions they came from
-    uint32_t *total;        // positions that name a row
-    // rows that no token names, zeroed (NULL: not)
-    void *zero;
-    uint64_t zero_stride;  // bytes
-    uint64_t zero_bytes;   // of a row
+    uint32_t bucket_bits;   // at most kBuckets buckets
+    uint32_t passes, bits;  // digits of a bucket's rows, and bits of each
+    uint32_t *keys[2];      // the positions' rows: [0] the result (kNoRow behind the last), [1] between passes
+    uint32_t *order[2];     // and the positions themselves
+    uint32_t *arrivals;     // counters of the sums, set to zero
+    uint64_t arrivals_n;
+    uint8_t *named;         // of each row, whether a token names it (NULL: not wanted)
 };
 hipError_t launch_group(const GroupArgs &a, hipStream_t stream);
 
@@ -48,22 +49,23 @@ hipError_t launch_group(const GroupArgs &a, hipStream_t stream);
 // What becomes of a row's sum.
 enum Goal : int { kWrite = 0, kAdd = 1, kAdam = 2, kAdamMax = 3 };
 
-// Positions are taken in windows of kWindow: a run of one row's positions
-// that crosses a window's end leaves a partial sum in each window.
-constexpr uint32_t kWindow = 64;
+// Positions are taken in windows of 32 or 64: of a run of one row's positions
+// that crosses a window's end, each window's piece is summed for itself first.
 
 struct SumArgs {
-    const uint32_t *keys, *order, *total;
+    const uint32_t *keys, *order;
+    uint32_t tokens_n, rows;
     const void *grad;
     uint64_t grad_stride;  // elements
     uint32_t cols;
-    uint32_t portion;  // positions a wave starts runs in (a power of two up to kWindow)
-    uint32_t slices;   // column slices of a row
-    uint32_t windows;
-    uint64_t units;    // waves' worth of work: portions * slices
+    uint32_t window, windows;  // positions of a window, and how many windows
+    uint32_t slices;   // of a row
     float scale;
+    uint32_t sum_groups;   // workgroups that sum; those behind them zero rows (kWrite)
+    const uint8_t *named;
     float *partials;   // two rows a window: of the run that began before it, of the one that began in it
     uint64_t partial_stride;
+    uint32_t *arrivals;  // of each slice: two counters a window, and one for the run that begins in it
     void *out;         // the table's gradient, or the table
     uint64_t out_stride;
     // the step
@@ -71,10 +73,14 @@ struct SumArgs {
     float step, ibc2, decay, omb1, omb2, beta1, beta2, eps, wd;
     uint32_t l2, fast_ok;
 };
-// Columns a wave takes of a row: 256 or 512.
-constexpr uint32_t slice_cols(uint32_t cols) { return cols <= 256 ? 256 : 512; }
+// Columns that a wave takes of a row, in groups of 256.
+constexpr int kSmallGroups = 1;
+constexpr int large_groups(int goal) { return goal >= kAdam ? 1 : 2; }
 hipError_t launch_sums(bool grad_bf16, bool out_bf16, Goal goal, const SumArgs &a, hipStream_t stream);
-// the runs that crossed windows, from their partial sums
-hipError_t launch_joins(bool out_bf16, Goal goal, const SumArgs &a, hipStream_t stream);
+
+// Up to this many tokens need no grouping.
+constexpr uint32_t kDirectTokens = 512;
+hipError_t launch_direct(bool grad_bf16, bool out_bf16, Goal goal, const SumArgs &a, const void *tokens, bool wide,
+                         hipStream_t stream);
 
 }  // namespace adam_mi355x

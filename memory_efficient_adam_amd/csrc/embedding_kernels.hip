@@ -22,6 +22,7 @@ namespace {
 // global memory takes.
 typedef float f32x4e __attribute__((ext_vector_type(4), aligned(4)));
 typedef uint16_t u16x4e __attribute__((ext_vector_type(4), aligned(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef uint16_t u16x8e __attribute__((ext_vector_type(8), aligned(2)));
 
 __device__ __forceinline__ float widen(float x) { return x; }
@@ -29,28 +30,36 @@ __device__ __forceinline__ float widen(uint16_t x) { return bf16_to_f32(x); }
 __device__ __forceinline__ void narrow(float x, float &out) { out = x; }
 __device__ __forceinline__ void narrow(float x, uint16_t &out) { out = (uint16_t)f32_to_bf16(x); }
 
+template <int kN> struct Int { static constexpr int value = kN; };
+
 template <class T> struct Vec4;
 template <> struct Vec4<float> { typedef f32x4e type; };
 template <> struct Vec4<uint16_t> { typedef u16x4e type; };
 
-// Four columns of a row from p, the first n of which exist (n may be 0 or
-// less, or more than 4): others are zero.
-template <bool kStream, class T>
-__device__ __forceinline__ f32x4 load4(const T *p, int32_t n) {
-    f32x4 r = {0.f, 0.f, 0.f, 0.f};
-    if (n >= 4) {
-        typename Vec4<T>::type x;
-        if constexpr (kStream) x = __builtin_nontemporal_load(reinterpret_cast<const typename Vec4<T>::type *>(p));
-        else x = *reinterpret_cast<const typename Vec4<T>::type *>(p);
+// Four columns of a row as they are stored.  Loading and widening are apart:
+// what follows a load in its branch waits for it there, and with it for every
+// load before, so a widening in the branch would let one load be under way at a time.
+template <class T>
+struct Four {
+    typename Vec4<T>::type x;
+
+    // from p, the first n of which exist (n may be 0 or less, or more than 4): others are zero
+    template <bool kStream>
+    __device__ __forceinline__ void load(const T *p, int32_t n) {
+        x = typename Vec4<T>::type{};
+        if (n >= 4) {
+            if constexpr (kStream) x = __builtin_nontemporal_load(reinterpret_cast<const typename Vec4<T>::type *>(p));
+            else x = *reinterpret_cast<const typename Vec4<T>::type *>(p);
+        } else if (n > 0) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) r[k] = widen((T)x[k]);
-    } else {
-#pragma unroll
-        for (int k = 0; k < 3; ++k)
-            if (k < n) r[k] = widen(p[k]);
+            for (int k = 0; k < 3; ++k)
+                if (k < n) x[k] = p[k];
+        }
     }
-    return r;
-}
+    __device__ __forceinline__ f32x4 wide() const {
+        return f32x4{widen((T)x[0]), widen((T)x[1]), widen((T)x[2]), widen((T)x[3])};
+    }
+};
 
 template <class T>
 __device__ __forceinline__ void store4(T *p, f32x4 r, int32_t n) {
@@ -73,17 +82,10 @@ __device__ __forceinline__ void store4(T *p, f32x4 r, int32_t n) {
     }
 }
 
-// The row a token names, or kNoRow.
-template <bool kWide>
-__device__ __forceinline__ uint32_t row_of(const void *tokens, uint32_t i, uint32_t rows) {
-    if constexpr (kWide) {
-        const uint64_t t = reinterpret_cast<const uint64_t *>(tokens)[i];
-        return t < rows ? (uint32_t)t : kNoRow;
-    } else {
-        const uint32_t t = reinterpret_cast<const uint32_t *>(tokens)[i];  // negative ones are 2^31 and more
-        return t < rows ? t : kNoRow;
-    }
-}
+// The row that a token names, or kNoRow.
+__device__ __forceinline__ uint32_t row_of(uint64_t token, uint32_t rows) { return token < rows ? (uint32_t)token : kNoRow; }
+// (negative ones are 2^31 and more)
+__device__ __forceinline__ uint32_t row_of(uint32_t token, uint32_t rows) { return token < rows ? token : kNoRow; }
 
 __device__ __forceinline__ uint32_t uniform_u32(uint32_t x) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)x); }
 __device__ __forceinline__ uint32_t lane_u32(uint32_t x, uint32_t lane) {
@@ -93,93 +95,137 @@ __device__ __forceinline__ uint32_t lane_u32(uint32_t x, uint32_t lane) {
 // ---------------------------------------------------------------- lookup
 constexpr int kLookupThreads = 256;
 
-template <class T, class O, bool kWide>
+template <class T, class O, class Token>
 __global__ void __launch_bounds__(kLookupThreads) lookup_kernel(LookupArgs a, uint32_t slices, uint64_t units) {
     const uint32_t lane = threadIdx.x & 63u;
     for (uint64_t u = (uint64_t)blockIdx.x * 4 + (threadIdx.x >> 6); u < units; u += (uint64_t)gridDim.x * 4) {
         const uint32_t i = uniform_u32((uint32_t)(u / slices));
         const uint32_t c0 = uniform_u32((uint32_t)(u % slices)) * 512 + lane * 4;
-        const uint32_t row = uniform_u32(row_of<kWide>(a.tokens, i, a.rows));
+        const uint32_t row = uniform_u32(row_of(reinterpret_cast<const Token *>(a.tokens)[i], a.rows));
         const T *from = reinterpret_cast<const T *>(a.table) + (uint64_t)row * a.table_stride;
         O *to = reinterpret_cast<O *>(a.out) + (uint64_t)i * a.out_stride;
-        f32x4 x[2] = {};
-        if (row != kNoRow) {
+        const int32_t left = (int32_t)(a.cols - c0);
+        Four<T> x[2];
 #pragma unroll
-            for (int g = 0; g < 2; ++g) x[g] = load4<false>(from + c0 + 256 * g, (int32_t)(a.cols - c0) - 256 * g);
+        for (int g = 0; g < 2; ++g) x[g].template load<false>(from + c0 + 256 * g, row != kNoRow ? left - 256 * g : 0);
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            // 0 for padding, whatever the scale
+            const f32x4 one = row != kNoRow ? x[g].wide() * a.scale : f32x4{0.f, 0.f, 0.f, 0.f};
+            store4(to + c0 + 256 * g, one, left - 256 * g);
         }
-#pragma unroll
-        for (int g = 0; g < 2; ++g) store4(to + c0 + 256 * g, x[g] * a.scale, (int32_t)(a.cols - c0) - 256 * g);
+    }
+}
+
+// Zeroes the rows [r0, r1) of a table that are not `named`, by a workgroup: rows one
+// after the other, so that the workgroups in flight write one stretch of memory.
+template <class O, class Named>
+__device__ __forceinline__ void zero_rows(O *table, uint64_t stride, uint32_t cols, uint64_t r0, uint64_t r1, uint32_t threads,
+                                          Named named) {
+    constexpr uint32_t kPer = 16 / sizeof(O);
+    for (uint64_t r = r0; r < r1; ++r) {
+        if (named(r)) continue;
+        O *const row = table + r * stride;
+        const uint32_t whole = cols / kPer;
+        for (uint32_t c = threadIdx.x; c < whole; c += threads) *reinterpret_cast<u16x8e *>(row + c * (uint64_t)kPer) = u16x8e{};
+        const uint32_t rest = whole * kPer + threadIdx.x;
+        if (rest < cols) row[rest] = O(0);
     }
 }
 
 // ---------------------------------------------------------------- grouping
 constexpr int kGroupThreads = 1024, kGroupWaves = 16;
-constexpr uint32_t kGroupBlock = 256;  // positions a wave takes at a time, four a lane
-constexpr uint32_t kMaxBins = 1u << kDigitBits;
+constexpr int kHeld = 16;  // tokens that a lane has under way at a time
+constexpr uint32_t kGroupChunk = kGroupThreads * kHeld;
+constexpr uint32_t kListed = 512;  // positions of its bucket that a wave keeps: those of half a chunk at most
 
-// One workgroup a bucket: it reads every token and keeps those of its rows.
-// Reading all tokens 256 times costs 8 bytes x 256 a token from the caches, and
-// saves the passes over memory (with a launch each) of a sort by tiles.  The positions are
-// placed by counting: each wave counts its own positions by digit, the counts
-// become places by a sum over digits and waves, and each wave goes
-// through the same positions again and places them.  Lanes with one digit are
-// ranked by ballots, not by the order in which atomics arrive, so the result is
-// always the same.
-template <bool kWide>
+// Orders a wave's LDS stores before its loads of what other lanes stored.
+__device__ __forceinline__ void wave_lds_fence() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
+// One workgroup a bucket: it reads every token and keeps the positions of its
+// rows.  Reading all tokens 256 times costs 8 bytes x 256 a token from the
+// caches, and saves the passes over memory (with a launch each) of a sort by
+// tiles.  The positions are placed by counting: each wave lists its own (in
+// LDS; where they are too many it finds them again later) and counts them by digit,
+// the counts become places by a sum over digits and waves, and each wave
+// places its list, 64 positions at a time.  Lanes with one digit are ranked by
+// ballots, not by the order in which atomics arrive, so the result is always
+// the same.
+template <class Token>
 __global__ void __launch_bounds__(kGroupThreads) group_kernel(GroupArgs a) {
-    extern __shared__ uint32_t counts[];  // [kGroupWaves][bins]
+    extern __shared__ uint2 shared[];  // [kGroupWaves][kListed] {row, position}, then counts [kGroupWaves][bins]
     __shared__ uint32_t wave_sums[kGroupWaves];
     __shared__ uint32_t below_sum;
-    __shared__ uint32_t named[kMaxBins / 32];  // bitmap of rows that a token names
     const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = uniform_u32(tid >> 6), bucket = blockIdx.x;
     const uint32_t bins = 1u << a.bits;
-    uint32_t *mine = counts + wave * bins;
+    uint32_t *const counts = reinterpret_cast<uint32_t *>(shared + kGroupWaves * kListed), *const mine = counts + wave * bins;
+    uint2 *const list = shared + wave * kListed;
     uint32_t base = 0, len = a.tokens_n;
     if (tid == 0) below_sum = 0;
+    for (uint64_t i = bucket * kGroupThreads + tid; i < a.arrivals_n; i += kBuckets * kGroupThreads) a.arrivals[i] = 0;
     for (uint32_t pass = 0; pass < a.passes; ++pass) {
-        const uint32_t shift = 8 + pass * kDigitBits, to = (a.passes - 1 - pass) & 1u;
+        const uint32_t shift = pass * kDigitBits, to = (a.passes - 1 - pass) & 1u;
         const uint32_t *keys_in = a.keys[to ^ 1u], *order_in = a.order[to ^ 1u];
-        for (uint32_t i = tid; i < kGroupWaves * bins; i += kGroupThreads) counts[i] = 0;
-        __syncthreads();
-        // the keys of this wave's positions from block `b` on; in the first pass kNoRow
-        // for the other buckets' ones
-        uint32_t below = 0;
-        auto fetch = [&](uint32_t b, uint32_t (&key)[4], bool count) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t i = b * kGroupBlock + j * 64 + lane;
-                key[j] = kNoRow;
-                if (i < len) key[j] = pass == 0 ? row_of<kWide>(a.tokens, i, a.rows) : keys_in[base + i];
-            }
+        const uint32_t chunks = len / kGroupChunk + (len % kGroupChunk != 0);
+        uint32_t below = 0, listed = 0;
+        // the rows of this thread's positions of a chunk; in the first pass kNoRow for
+        // the other buckets' ones, with `below` counting those of earlier buckets
+        auto fetch = [&](uint32_t chunk, uint32_t (&key)[kHeld]) {
+            const uint32_t i0 = chunk * kGroupChunk + tid;
             if (pass == 0) {
+                Token token[kHeld];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint32_t in = key[j] & (kBuckets - 1);
-                    if (count) below += key[j] != kNoRow && in < bucket ? 1u : 0u;
+                for (int j = 0; j < kHeld; ++j)
+                    token[j] = reinterpret_cast<const Token *>(a.tokens)[min(i0 + j * kGroupThreads, len - 1)];
+#pragma unroll
+                for (int j = 0; j < kHeld; ++j) {
+                    key[j] = i0 + j * kGroupThreads < len ? row_of(token[j], a.rows) : kNoRow;
+                    const uint32_t in = key[j] >> a.bucket_bits;
+                    below += key[j] != kNoRow && in < bucket ? 1u : 0u;
                     if (in != bucket) key[j] = kNoRow;
                 }
+            } else {
+#pragma unroll
+                for (int j = 0; j < kHeld; ++j) key[j] = keys_in[base + min(i0 + j * kGroupThreads, len - 1)];
+#pragma unroll
+                for (int j = 0; j < kHeld; ++j)
+                    if (i0 + j * kGroupThreads >= len) key[j] = kNoRow;
             }
         };
-        const uint32_t blocks = len / kGroupBlock + (len % kGroupBlock != 0);
-        for (uint32_t b = wave; b < blocks; b += kGroupWaves) {
-            uint32_t key[4];
-            fetch(b, key, true);
+        auto digit_of = [&](uint32_t key) { return (key >> shift) & (bins - 1); };
+        // the positions of key[j] behind the `listed` ones
+        auto append = [&](uint32_t key, uint32_t i, bool count) {
+            const uint64_t have = __ballot(key != kNoRow);
+            if (have == 0) return;
+            if (key != kNoRow) {
+                const uint32_t at = listed + (uint32_t)__popcll(have & ((1ull << lane) - 1));
+                if (at < kListed) list[at] = uint2{key, i};
+                if (count) atomicAdd(mine + digit_of(key), 1u);
+            }
+            listed += (uint32_t)__popcll(have);
+        };
+        for (uint32_t i = tid; i < kGroupWaves * bins; i += kGroupThreads) counts[i] = 0;
+        __syncthreads();
+        for (uint32_t c = 0; c < chunks; ++c) {
+            uint32_t key[kHeld];
+            fetch(c, key);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (key[j] != kNoRow) atomicAdd(mine + ((key[j] >> shift) & (bins - 1)), 1u);
+            for (int j = 0; j < kHeld; ++j) append(key[j], c * kGroupChunk + j * kGroupThreads + tid, true);
         }
         if (pass == 0) {
             for (int s = 32; s > 0; s >>= 1) below += __shfl_xor(below, s);
             if (lane == 0) atomicAdd(&below_sum, below);
         }
         __syncthreads();
-        // counts to places
-        uint32_t digit_total = 0;
+        // counts to places: thread d has digit d's of every wave
+        uint32_t held[kGroupWaves], digit_total = 0;
         if (tid < bins) {
 #pragma unroll
+            for (int w = 0; w < kGroupWaves; ++w) held[w] = counts[w * bins + tid];
+#pragma unroll
             for (int w = 0; w < kGroupWaves; ++w) {
-                const uint32_t c = counts[w * bins + tid];
-                counts[w * bins + tid] = digit_total;
+                const uint32_t c = held[w];
+                held[w] = digit_total;
                 digit_total += c;
             }
         }
@@ -189,10 +235,9 @@ __global__ void __launch_bounds__(kGroupThreads) group_kernel(GroupArgs a) {
             if (lane >= (uint32_t)s) incl += x;
         }
         if (lane == 63) wave_sums[wave] = incl;
-        const uint64_t any = __ballot(digit_total != 0);
-        if (pass == 0 && lane < 2) named[2 * wave + lane] = (uint32_t)(any >> (32 * lane));
         __syncthreads();
         uint32_t before = 0, all = 0;
+#pragma unroll
         for (int w = 0; w < kGroupWaves; ++w) {
             const uint32_t s = wave_sums[w];
             before += w < (int)wave ? s : 0u;
@@ -202,69 +247,68 @@ __global__ void __launch_bounds__(kGroupThreads) group_kernel(GroupArgs a) {
         const uint32_t first = base + before + incl - digit_total;
         if (tid < bins) {
 #pragma unroll
-            for (int w = 0; w < kGroupWaves; ++w) counts[w * bins + tid] += first;
+            for (int w = 0; w < kGroupWaves; ++w) counts[w * bins + tid] = held[w] + first;
         }
         __syncthreads();
         // places
-        for (uint32_t b = wave; b < blocks; b += kGroupWaves) {
-            uint32_t key[4];
-            fetch(b, key, false);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint64_t same = __ballot(key[j] != kNoRow);
-                if (same == 0) continue;
-                const uint32_t digit = (key[j] >> shift) & (bins - 1);
+        auto place_list = [&]() {
+            for (uint32_t k0 = 0; k0 < listed; k0 += 64) {
+                const uint2 one = k0 + lane < listed ? list[k0 + lane] : uint2{kNoRow, 0};
+                const uint32_t digit = digit_of(one.x);
+                uint64_t same = __ballot(one.x != kNoRow);
                 for (uint32_t k = 0; k < a.bits; ++k) {
                     const uint64_t set = __ballot((digit >> k) & 1u);
                     same &= (digit >> k) & 1u ? set : ~set;
                 }
-                if (key[j] != kNoRow) {
+                if (one.x != kNoRow) {
                     const uint32_t leader = (uint32_t)__builtin_ctzll(same);
-                    const uint32_t rank = (uint32_t)__popcll(same & ((1ull << lane) - 1));
                     uint32_t place = 0;
                     if (lane == leader) place = atomicAdd(mine + digit, (uint32_t)__popcll(same));
-                    place = __shfl(place, (int)leader) + rank;
-                    const uint32_t i = b * kGroupBlock + j * 64 + lane;
+                    place = __shfl(place, (int)leader) + (uint32_t)__popcll(same & ((1ull << lane) - 1));
                     if (place < a.tokens_n) {  // always, unless tokens change under the call
-                        a.keys[to][place] = key[j];
-                        a.order[to][place] = pass == 0 ? i : order_in[base + i];
+                        a.keys[to][place] = one.x;
+                        a.order[to][place] = pass == 0 ? one.y : order_in[base + one.y];
                     }
+                }
+            }
+        };
+        if (listed <= kListed) {
+            place_list();
+        } else {
+            for (uint32_t c = 0; c < chunks; ++c) {
+                uint32_t key[kHeld];
+                fetch(c, key);
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    listed = 0;
+#pragma unroll
+                    for (int j = half * kHeld / 2; j < (half + 1) * kHeld / 2; ++j)
+                        append(key[j], c * kGroupChunk + j * kGroupThreads + tid, false);
+                    wave_lds_fence();
+                    place_list();
+                    wave_lds_fence();
                 }
             }
         }
         if (pass == 0) len = all;
         __syncthreads();
     }
-    if (bucket == kBuckets - 1 && tid == 0) *a.total = base + len;
-    if (!a.zero) return;
-    // the bucket's rows that no token names
-    const uint32_t rows = a.rows > bucket ? (a.rows - bucket - 1) / kBuckets + 1 : 0;
-    for (uint32_t r0 = 0; r0 < rows; r0 += kMaxBins) {
-        if (a.passes > 1) {
-            for (uint32_t i = tid; i < kMaxBins / 32; i += kGroupThreads) named[i] = 0;
-            __syncthreads();
-            for (uint32_t i = tid; i < len; i += kGroupThreads) {
-                const uint32_t r = a.keys[0][base + i] / kBuckets;
-                if (r >= r0 && r - r0 < kMaxBins) atomicOr(&named[(r - r0) / 32], 1u << (r % 32));
-            }
-            __syncthreads();
-        }
-        const uint32_t n = min(kMaxBins, rows - r0);
-        for (uint32_t k = wave; k < n; k += kGroupWaves) {
-            if ((uniform_u32(named[k / 32]) >> (k % 32)) & 1u) continue;
-            char *row = reinterpret_cast<char *>(a.zero) + (uint64_t)((r0 + k) * (uint64_t)kBuckets + bucket) * a.zero_stride;
-            const uint64_t fours = a.zero_bytes / 16;
-            for (uint64_t c = lane; c < fours; c += 64)
-                __builtin_nontemporal_store(u16x8e{}, reinterpret_cast<u16x8e *>(row) + c);
-            const uint64_t rest = fours * 16 + lane * 2;
-            if (rest < a.zero_bytes) __builtin_nontemporal_store((uint16_t)0, reinterpret_cast<uint16_t *>(row + rest));
-        }
-        if (a.passes > 1) __syncthreads();
-    }
+    // positions that name no row come last
+    if (bucket == kBuckets - 1)
+        for (uint32_t i = base + len + tid; i < a.tokens_n; i += kGroupThreads) a.keys[0][i] = kNoRow;
+    if (!a.named) return;
+    // which of the bucket's rows a token names
+    const uint64_t bucket0 = (uint64_t)bucket << a.bucket_bits;
+    const uint32_t rows = a.rows > bucket0 ? (uint32_t)min((uint64_t)a.rows - bucket0, 1ull << a.bucket_bits) : 0u;
+    for (uint32_t r = tid; r < rows; r += kGroupThreads) a.named[bucket0 + r] = 0;
+    __syncthreads();
+    for (uint32_t i = tid; i < len; i += kGroupThreads) a.named[a.keys[0][base + i]] = 1;
 }
 
 // ---------------------------------------------------------------- sums
 constexpr int kSumThreads = 256;
+constexpr uint32_t kZeroRows = 8;  // rows that a workgroup zeroes
+constexpr uint32_t kFan = 16;  // pieces of a run that are added up together
 
 // The update of four elements, adam_step's operations in its order (see there for
 // the ranges of the short sequences).  n: how many of them exist.
@@ -297,170 +341,402 @@ __device__ __forceinline__ void update4(const SumArgs &a, f32x4 &p, f32x4 g, f32
     }
 }
 
-// A row's whole sum: written, added, or taken as the step's gradient.
+// What a row's whole sum meets: nothing, the value it is added to, or the
+// step's params and state, loaded before the sum so that both are under way
+// together.
 template <class O, Goal kGoal, int kG>
-__device__ __forceinline__ void finish(const SumArgs &a, uint32_t row, uint32_t c0, const f32x4 (&sum)[kG]) {
-    O *to = reinterpret_cast<O *>(a.out) + (uint64_t)row * a.out_stride + c0;
-    const int32_t left = (int32_t)(a.cols - c0);
-    if constexpr (kGoal == kWrite) {
-#pragma unroll
-        for (int g = 0; g < kG; ++g) store4(to + 256 * g, sum[g] * a.scale, left - 256 * g);
-    } else if constexpr (kGoal == kAdd) {
-        f32x4 old[kG];
-#pragma unroll
-        for (int g = 0; g < kG; ++g) old[g] = load4<true>(to + 256 * g, left - 256 * g);
-#pragma unroll
-        for (int g = 0; g < kG; ++g) store4(to + 256 * g, old[g] + sum[g] * a.scale, left - 256 * g);
-    } else {
-        constexpr bool kMax = kGoal == kAdamMax;
+struct Target {
+    Four<O> p[kG];
+    Four<float> m[kG], v[kG], w[kG];
+
+    __device__ __forceinline__ void load(const SumArgs &a, uint32_t row, uint32_t c0) {
+        if constexpr (kGoal == kWrite) return;
+        const int32_t left = (int32_t)(a.cols - c0);
+        const O *from = reinterpret_cast<const O *>(a.out) + (uint64_t)row * a.out_stride + c0;
         const uint64_t s = (uint64_t)row * a.cols + c0;
-        f32x4 p[kG], m[kG], v[kG], w[kG];
 #pragma unroll
         for (int g = 0; g < kG; ++g) {
-            p[g] = load4<true>(to + 256 * g, left - 256 * g);
-            m[g] = load4<true>(a.m + s + 256 * g, left - 256 * g);
-            v[g] = load4<true>(a.v + s + 256 * g, left - 256 * g);
-            if constexpr (kMax) w[g] = load4<true>(a.w + s + 256 * g, left - 256 * g);
-        }
-#pragma unroll
-        for (int g = 0; g < kG; ++g) {
-            update4<kMax>(a, p[g], sum[g] * a.scale, m[g], v[g], w[g], left - 256 * g);
-            store4(to + 256 * g, p[g], left - 256 * g);
-            store4(a.m + s + 256 * g, m[g], left - 256 * g);
-            store4(a.v + s + 256 * g, v[g], left - 256 * g);
-            if constexpr (kMax) store4(a.w + s + 256 * g, w[g], left - 256 * g);
+            p[g].template load<true>(from + 256 * g, left - 256 * g);
+            if constexpr (kGoal >= kAdam) {
+                m[g].template load<true>(a.m + s + 256 * g, left - 256 * g);
+                v[g].template load<true>(a.v + s + 256 * g, left - 256 * g);
+            }
+            if constexpr (kGoal == kAdamMax) w[g].template load<true>(a.w + s + 256 * g, left - 256 * g);
         }
     }
-}
 
-// A wave takes the runs (of one row's positions) that begin in its portion of a
-// window, in one slice of columns.  A run that crosses the window's end counts
-// as beginning again in the next one, and leaves partial sums.
-template <class T, class O, Goal kGoal, int kG>
-__global__ void __launch_bounds__(kSumThreads) sum_kernel(SumArgs a) {
-    const uint32_t lane = threadIdx.x & 63u, total = *a.total;
-    for (uint64_t u = (uint64_t)blockIdx.x * 4 + uniform_u32(threadIdx.x >> 6); u < a.units; u += (uint64_t)gridDim.x * 4) {
-        const uint32_t first = uniform_u32((uint32_t)(u / a.slices)) * a.portion;
-        const uint32_t c0 = uniform_u32((uint32_t)(u % a.slices)) * (256 * kG) + lane * 4;
-        if (first >= total) break;
-        const uint32_t w0 = first & ~(kWindow - 1), pos = w0 + lane;
-        const uint32_t live = min(kWindow, total - w0);
-        const bool in = lane < live;
-        const uint32_t key = in ? a.keys[pos] : kNoRow, from = in ? a.order[pos] : 0u;
-        const uint32_t last = w0 > 0 ? a.keys[w0 - 1] : kNoRow;
-        const uint32_t next = total - w0 > kWindow ? a.keys[w0 + kWindow] : kNoRow;
-        const uint32_t prev = __shfl_up(key, 1);
-        const uint64_t heads = __ballot(in && (lane == 0 || key != prev));
-        const bool continued = uniform_u32(key) == last;  // the window's first run began before it
-        const uint32_t stop = min(first - w0 + a.portion, live);
+    __device__ __forceinline__ void finish(const SumArgs &a, uint32_t row, uint32_t c0, const f32x4 (&sum)[kG]) {
         const int32_t left = (int32_t)(a.cols - c0);
-        const uint64_t mine = heads >> (first - w0);
-        uint32_t h = mine ? first - w0 + (uint32_t)__builtin_ctzll(mine) : kWindow;
-        while (h < stop) {
-            const uint64_t after = h + 1 < kWindow ? heads >> (h + 1) : 0;
-            const uint32_t e = after ? h + 1 + (uint32_t)__builtin_ctzll(after) : live;
-            const uint32_t row = lane_u32(key, h);
-            f32x4 sum[kG] = {};
-            auto fetch = [&](uint32_t k, f32x4 (&x)[kG]) {
-                const T *p = reinterpret_cast<const T *>(a.grad) + (uint64_t)lane_u32(from, k) * a.grad_stride + c0;
+        O *to = reinterpret_cast<O *>(a.out) + (uint64_t)row * a.out_stride + c0;
+        const uint64_t s = (uint64_t)row * a.cols + c0;
 #pragma unroll
-                for (int g = 0; g < kG; ++g) x[g] = load4<true>(p + 256 * g, left - 256 * g);
-            };
-            uint32_t k = h;
-            for (; k + 4 <= e; k += 4) {
-                f32x4 x[4][kG];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) fetch(k + j, x[j]);
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                    for (int g = 0; g < kG; ++g) sum[g] += x[j][g];
-            }
-            for (; k < e; ++k) {
-                f32x4 x[kG];
-                fetch(k, x);
-#pragma unroll
-                for (int g = 0; g < kG; ++g) sum[g] += x[g];
-            }
-            const bool began = !(h == 0 && continued), ends = !(e == kWindow && next == row);
-            if (began && ends) {
-                finish<O, kGoal, kG>(a, row, c0, sum);
+        for (int g = 0; g < kG; ++g) {
+            const f32x4 one = sum[g] * a.scale;
+            if constexpr (kGoal == kWrite) {
+                store4(to + 256 * g, one, left - 256 * g);
+            } else if constexpr (kGoal == kAdd) {
+                store4(to + 256 * g, p[g].wide() + one, left - 256 * g);
             } else {
-                float *to = a.partials + ((uint64_t)(w0 / kWindow) * 2 + (began ? 1 : 0)) * a.partial_stride + c0;
-#pragma unroll
-                for (int g = 0; g < kG; ++g) store4(to + 256 * g, sum[g], left - 256 * g);
+                f32x4 ps = p[g].wide(), ms = m[g].wide(), vs = v[g].wide(), ws = {};
+                if constexpr (kGoal == kAdamMax) ws = w[g].wide();
+                update4<kGoal == kAdamMax>(a, ps, one, ms, vs, ws, left - 256 * g);
+                store4(to + 256 * g, ps, left - 256 * g);
+                store4(a.m + s + 256 * g, ms, left - 256 * g);
+                store4(a.v + s + 256 * g, vs, left - 256 * g);
+                if constexpr (kGoal == kAdamMax) store4(a.w + s + 256 * g, ws, left - 256 * g);
             }
-            h = after ? e : kWindow;
         }
+    }
+};
+
+// sum += the rows at(k) + c0 for k in [from, to), the loads of up to kDeep rows
+// under way together (as many batches of kDeep, then at most one each of 8, 4, 2 and 1).
+template <int kDeep, int kG, class T, class At>
+__device__ __forceinline__ void add_rows(f32x4 (&sum)[kG], uint32_t from, uint32_t to, int32_t left, At at) {
+    auto batch = [&](auto size) {
+        constexpr int kN = decltype(size)::value;
+        Four<T> x[kN][kG];
+#pragma unroll
+        for (int j = 0; j < kN; ++j) {
+            const T *p = at(from + j);
+#pragma unroll
+            for (int g = 0; g < kG; ++g) x[j][g].template load<true>(p + 256 * g, left - 256 * g);
+        }
+#pragma unroll
+        for (int j = 0; j < kN; ++j)
+#pragma unroll
+            for (int g = 0; g < kG; ++g) sum[g] += x[j][g].wide();
+        from += kN;
+    };
+    while (to - from >= (uint32_t)kDeep) batch(Int<kDeep>());
+    if constexpr (kDeep > 8)
+        if (to - from >= 8) batch(Int<8>());
+    if constexpr (kDeep > 4)
+        if (to - from >= 4) batch(Int<4>());
+    if (to - from >= 2) batch(Int<2>());
+    if (to - from >= 1) batch(Int<1>());
+}
+
+// Partial sums go to memory and come from it past the XCDs' own caches, by
+// device-scope atomic accesses of 8 bytes (a lane's four columns, padding included).
+__device__ __forceinline__ void put_partial(float *at, f32x4 x, int32_t n) {
+    if (n <= 0) return;
+    uint64_t *to = reinterpret_cast<uint64_t *>(at);
+    __hip_atomic_store(to, __builtin_bit_cast(uint64_t, (f32x2{x[0], x[1]})), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __hip_atomic_store(to + 1, __builtin_bit_cast(uint64_t, (f32x2{x[2], x[3]})), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ f32x4 get_partial(const float *at, int32_t n) {
+    if (n <= 0) return f32x4{0.f, 0.f, 0.f, 0.f};
+    const uint64_t *from = reinterpret_cast<const uint64_t *>(at);
+    const f32x2 x = __builtin_bit_cast(f32x2, __hip_atomic_load(from, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+    const f32x2 y = __builtin_bit_cast(f32x2, __hip_atomic_load(from + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+    return f32x4{x[0], x[1], y[0], y[1]};
+}
+
+// Leaves a partial sum in slot `mine` and counts it in at *arrivals; true for
+// the wave that comes last of n, which then has their sum, slot_at(0) first,
+// slot_at(n - 1) last.
+template <int kG, class Slot>
+__device__ __forceinline__ bool meet(const SumArgs &a, f32x4 (&sum)[kG], uint64_t mine, uint32_t n, Slot slot_at,
+                                     uint32_t *arrivals, uint32_t c0) {
+    const int32_t left = (int32_t)(a.cols - c0);
+    float *const partials = a.partials + c0;
+#pragma unroll
+    for (int g = 0; g < kG; ++g) put_partial(partials + mine * a.partial_stride + 256 * g, sum[g], left - 256 * g);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // in memory before it is counted
+    uint32_t before = 0;
+    if ((threadIdx.x & 63u) == 0)
+        before = __hip_atomic_fetch_add(arrivals, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (uniform_u32(before) + 1 != n) return false;
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int g = 0; g < kG; ++g) sum[g] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (uint32_t k = 0; k < n; k += 4) {
+        f32x4 x[4][kG];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float *from = partials + slot_at(min(k + j, n - 1)) * a.partial_stride;
+#pragma unroll
+            for (int g = 0; g < kG; ++g) x[j][g] = get_partial(from + 256 * g, left - 256 * g);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int g = 0; g < kG; ++g)
+                if (k + j < n) sum[g] += x[j][g];
+    }
+    return true;
+}
+
+// A workgroup takes a window of 4 kPer positions, each wave kPer of them, in one
+// slice of the columns.  Of the runs (of one row's positions) in the window
+//   - those that lie in one wave's positions are summed by it, kBatch positions at a
+//     time: their loads, and those of the rows that runs end on (params and state, which
+//     come from memory in some 2 us under load), are all issued before the first is used;
+//   - a run over several waves' positions is summed by the wave that it begins
+//     in, from the others' sums of their first rows (in LDS);
+//   - of a run over several windows each leaves a partial sum in memory, and the wave
+//     that comes last adds them up in the order of the windows (kFan at a time,
+//     then those sums).  No wave waits for another workgroup.
+template <class T, class O, Goal kGoal, int kG, int kPer>
+__global__ void __launch_bounds__(kSumThreads) sum_kernel(SumArgs a) {
+    constexpr uint32_t kWin = 4 * kPer;
+    constexpr int kBatch = kGoal >= kAdam && kPer == 16 ? 2 : 4, kDeep = 16 / kG * 2 / (int)sizeof(T);
+    __shared__ f32x4 leads[4][kG][64];  // what each wave has of a run that began before its positions
+    const uint32_t lane = threadIdx.x & 63u, wave = uniform_u32(threadIdx.x >> 6);
+    if constexpr (kGoal == kWrite) {
+        if (blockIdx.x >= a.sum_groups) {
+            // the workgroups behind zero the rows that no token names, while the sums wait for memory
+            for (uint64_t r0 = (uint64_t)(blockIdx.x - a.sum_groups) * kZeroRows; r0 < a.rows;
+                 r0 += (uint64_t)(gridDim.x - a.sum_groups) * kZeroRows) {
+                const uint64_t named = *reinterpret_cast<const uint64_t *>(a.named + r0);  // a byte a row
+                zero_rows(reinterpret_cast<O *>(a.out), a.out_stride, a.cols, r0, min(r0 + kZeroRows, (uint64_t)a.rows), kSumThreads,
+                          [&](uint64_t r) { return ((named >> (8 * (r - r0))) & 1u) != 0; });
+            }
+            return;
+        }
+    }
+    // workgroups go to the 8 XCDs in turn: an XCD has all of a window's slices
+    const uint64_t units = (a.windows + 7) / 8 * (uint64_t)a.slices * 8;
+    for (uint64_t u = blockIdx.x; u < units; u += a.sum_groups) {
+        const uint64_t window64 = u / 8 / a.slices * 8 + u % 8;
+        if (window64 >= a.windows) continue;
+        const uint32_t slice = (uint32_t)(u / 8 % a.slices);
+        const uint32_t window = (uint32_t)window64, w0 = window * kWin, end = a.tokens_n - 1;
+        // all of them loaded together, at clamped places
+        const uint32_t key_at = a.keys[min(w0 + lane, end)], from = a.order[min(w0 + lane, end)];
+        const uint32_t last_at = a.keys[w0 > 0 ? w0 - 1 : 0], next_at = a.keys[min(w0 + kWin, end)];
+        const uint32_t key = lane < kWin && lane <= end - w0 ? key_at : kNoRow;
+        const uint32_t live = (uint32_t)__popcll(__ballot(key != kNoRow));
+        if (live == 0) continue;  // padding
+        const uint32_t above = __shfl_up(key, 1), prev = lane > 0 ? above : (w0 > 0 ? last_at : kNoRow);
+        const uint64_t heads = __ballot(key != kNoRow && key != prev);  // where runs begin
+        const uint32_t next = end - w0 >= kWin ? uniform_u32(next_at) : kNoRow;
+        // where the run at position h ends in the window
+        auto end_of = [&](uint32_t h) {
+            const uint64_t after = h + 1 < kWin ? heads >> (h + 1) : 0;
+            return after ? h + 1 + (uint32_t)__builtin_ctzll(after) : live;
+        };
+        // this wave's positions [q0, qe): [q0, body) of a run that began before, then whole runs, and [tail, qe) of one that goes on
+        const uint32_t q0 = min(wave * kPer, live), qe = min(q0 + kPer, live);
+        const uint64_t in_mine = qe > q0 ? (heads >> q0) & (~0ull >> (64 - (qe - q0))) : 0;
+        const uint32_t body = in_mine ? q0 + (uint32_t)__builtin_ctzll(in_mine) : qe;
+        uint32_t tail = qe;
+        if (in_mine) {
+            const uint32_t h = q0 + 63u - (uint32_t)__builtin_clzll(in_mine), e = end_of(h);
+            if (e > qe || (e == kWin && lane_u32(key, h) == next)) tail = h;
+        }
+        auto row_of_key = [&](uint32_t k) { return lane_u32(key, k); };
+        const uint32_t c0 = slice * (256 * kG) + lane * 4;
+        const int32_t left = (int32_t)(a.cols - c0);
+        auto row_at = [&](uint32_t k) {
+            return reinterpret_cast<const T *>(a.grad) + (uint64_t)lane_u32(from, k) * a.grad_stride + c0;
+        };
+        f32x4 sum[kG] = {};
+        if (body > q0) {
+            add_rows<kDeep, kG, T>(sum, q0, body, left, row_at);
+#pragma unroll
+            for (int g = 0; g < kG; ++g) leads[wave][g][lane] = sum[g];
+        }
+        for (uint32_t k = body; k < tail; k += kBatch) {
+            Four<T> x[kBatch][kG];
+            Target<O, kGoal, kG> target[kBatch];
+            uint32_t closes = 0;  // positions that a run ends at
+#pragma unroll
+            for (uint32_t j = 0; j < kBatch; ++j) {
+                if (k + j >= tail) continue;
+                const T *p = row_at(k + j);
+#pragma unroll
+                for (int g = 0; g < kG; ++g) x[j][g].template load<true>(p + 256 * g, left - 256 * g);
+                if (k + j + 1 == live || ((heads >> (k + j + 1)) & 1u)) {  // (k + j + 1 == 64 only where it is live)
+                    closes |= 1u << j;
+                    target[j].load(a, row_of_key(k + j), c0);
+                }
+            }
+#pragma unroll
+            for (uint32_t j = 0; j < kBatch; ++j) {
+                if (k + j >= tail) continue;
+                const bool begins = (heads >> (k + j)) & 1u;
+#pragma unroll
+                for (int g = 0; g < kG; ++g) {
+                    const f32x4 one = x[j][g].wide();
+                    sum[g] = begins ? one : sum[g] + one;
+                }
+                if ((closes >> j) & 1u) target[j].finish(a, row_of_key(k + j), c0, sum);
+            }
+        }
+        // the run that goes on behind the wave's positions; in the first wave also the one that began before the window
+        Target<O, kGoal, kG> target;
+        const bool goes_on = tail < qe, crosses = goes_on && end_of(tail) == kWin && next == row_of_key(tail);
+        if (goes_on) {
+            if (!crosses) target.load(a, row_of_key(tail), c0);
+#pragma unroll
+            for (int g = 0; g < kG; ++g) sum[g] = f32x4{0.f, 0.f, 0.f, 0.f};
+            add_rows<kDeep, kG, T>(sum, tail, qe, left, row_at);
+        }
+        __syncthreads();
+        for (uint32_t k = 0; k < 2; ++k) {
+            if (!(k == 0 ? goes_on : wave == 0 && body > 0)) continue;
+            // k = 0: from this wave's sum; 1: from the first wave's lead
+            const uint32_t h = k == 0 ? tail : 0, e = k == 0 ? end_of(h) : (body < qe ? body : end_of(qe - 1)), row = row_of_key(h);
+            for (uint32_t w = k == 0 ? wave + 1 : 0; w * kPer < e; ++w) {
+#pragma unroll
+                for (int g = 0; g < kG; ++g) sum[g] = (k == 1 && w == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : sum[g]) + leads[w][g][lane];
+            }
+            bool all_in = true;
+            if (k == 1 || crosses) {
+                // the windows that the run has before this one and after it
+                uint32_t earlier = 0, later = 0;
+                while (k == 1 && window > earlier) {
+                    const uint32_t w = window - earlier;
+                    const uint64_t all = __ballot(w > lane && a.keys[(w > lane ? w - lane : 1) * kWin - 1] == row);
+                    const uint32_t got = ~all ? (uint32_t)__builtin_ctzll(~all) : 64u;
+                    earlier += got;
+                    if (got < 64) break;
+                }
+                while (e == kWin && next == row) {
+                    const uint64_t at = (uint64_t)w0 + (uint64_t)(later + 1 + lane) * kWin;
+                    const uint64_t all = __ballot(at <= end && a.keys[at <= end ? at : end] == row);
+                    const uint32_t got = ~all ? (uint32_t)__builtin_ctzll(~all) : 64u;
+                    later += got;
+                    if (got < 64) break;
+                }
+                const uint32_t start = window - earlier, pieces = earlier + 1 + later;
+                const uint32_t fan = earlier / kFan, fans = (pieces + kFan - 1) / kFan;
+                // the slot of a piece: its window's second where the run began there, else its first
+                auto slot_of = [&](uint32_t piece) { return (uint64_t)(start + piece) * 2 + (piece == 0 ? 1 : 0); };
+                uint32_t *const counters = a.arrivals + (uint64_t)slice * a.windows * 3;
+                all_in = meet<kG>(a, sum, slot_of(earlier), min(kFan, pieces - fan * kFan),
+                                  [&](uint32_t i) { return slot_of(fan * kFan + i); }, counters + slot_of(fan * kFan), c0);
+                if (all_in && fans > 1)
+                    all_in = meet<kG>(a, sum, slot_of(fan * kFan), fans, [&](uint32_t i) { return slot_of(i * kFan); },
+                                      counters + (uint64_t)a.windows * 2 + start, c0);
+                if (all_in) target.load(a, row, c0);
+            }
+            if (all_in) target.finish(a, row, c0, sum);
+        }
+        __syncthreads();
     }
 }
 
-// The run that crosses the end of a window and began in it: its partial sums
-// are the window's second, and the first of each window that it goes on into.
-// A workgroup a window and slice; its waves take a quarter of the windows each.
-template <class O, Goal kGoal, int kG>
-__global__ void __launch_bounds__(kSumThreads) join_kernel(SumArgs a) {
-    __shared__ f32x4 parts[3][kG][64];
-    const uint32_t lane = threadIdx.x & 63u, wave = uniform_u32(threadIdx.x >> 6), total = *a.total;
-    for (uint64_t u = blockIdx.x; u < (uint64_t)a.windows * a.slices; u += gridDim.x) {
-        const uint32_t window = uniform_u32((uint32_t)(u / a.slices));
-        const uint32_t end = (window + 1) * kWindow;
-        if (end >= total) break;
-        const uint32_t row = a.keys[end];
-        if (a.keys[end - 1] != row) continue;
-        if (window > 0 && a.keys[window * kWindow - 1] == row) continue;  // began before
-        // windows that the run goes on into
-        uint32_t more = 1;
-        for (;;) {
-            const uint64_t at = (uint64_t)end + (uint64_t)(more + lane) * kWindow;
-            const uint64_t same = __ballot(at < total && a.keys[at < total ? at : 0] == row);
-            const uint32_t got = ~same ? (uint32_t)__builtin_ctzll(~same) : 64u;
-            more += got;
-            if (got < 64) break;
+// ---------------------------------------------------------------- few tokens
+constexpr int kDirectThreads = (int)kDirectTokens, kDirectWaves = kDirectThreads / 64;
+
+// Up to kDirectTokens tokens in one launch and without a workspace: a workgroup a
+// position (and, of few tokens, a share of the columns), which looks through all
+// tokens for its row's.  The first position of a row has the row's sum: its waves
+// share the slices of the columns, and where there are fewer of those the
+// positions.  Where the whole gradient is written, the workgroups behind zero the rows that no
+// token names, by the same look.
+template <class Token, class T, class O, Goal kGoal>
+__global__ void __launch_bounds__(kDirectThreads) direct_kernel(SumArgs a, const void *tokens, uint32_t zero_rows_each) {
+    constexpr int kDeep = 32 / (int)sizeof(T);
+    __shared__ uint64_t masks[kDirectWaves];
+    __shared__ uint32_t list[kDirectTokens];
+    __shared__ f32x4 parts[kDirectWaves][64];
+    const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = uniform_u32(tid >> 6), n = a.tokens_n;
+    const uint32_t i = blockIdx.x < n ? blockIdx.x : 0;
+    const Token *const all = reinterpret_cast<const Token *>(tokens);
+    // (tokens_n is 0 only where there are rows to zero)
+    const Token my_token = n > 0 ? all[min(tid, n - 1)] : (Token)0, the_token = n > 0 ? all[i] : (Token)0;
+    const uint32_t my_row = tid < n ? row_of(my_token, a.rows) : kNoRow;
+    if constexpr (kGoal == kWrite) {
+        if (blockIdx.x >= n) {
+            uint32_t *const named = list;  // a bitmap
+            if (blockIdx.y > 0) return;
+            const uint64_t r0 = (uint64_t)(blockIdx.x - n) * zero_rows_each;
+            if (tid < kDirectTokens / 32) named[tid] = 0;
+            __syncthreads();
+            if (my_row != kNoRow && my_row >= r0 && my_row - r0 < zero_rows_each)
+                atomicOr(&named[(my_row - r0) / 32], 1u << ((my_row - r0) % 32));
+            __syncthreads();
+            zero_rows(reinterpret_cast<O *>(a.out), a.out_stride, a.cols, r0, min(r0 + zero_rows_each, (uint64_t)a.rows), kDirectThreads,
+                      [&](uint64_t r) { return (named[(r - r0) / 32] >> ((r - r0) % 32)) & 1u; });
+            return;
         }
-        const uint32_t c0 = uniform_u32((uint32_t)(u % a.slices)) * (256 * kG) + lane * 4;
+    }
+    const uint32_t row = uniform_u32(row_of(the_token, a.rows));
+    if (row == kNoRow) return;
+    const uint64_t same = __ballot(my_row == row);
+    if (lane == 0) masks[wave] = same;
+    __syncthreads();
+    uint32_t count = 0, before = 0, earlier = 0;  // positions of the row: all, in earlier waves, before i
+#pragma unroll
+    for (uint32_t w = 0; w < kDirectWaves; ++w) {
+        const uint64_t m = masks[w];
+        const uint32_t c = (uint32_t)__popcll(m);
+        count += c;
+        before += w < wave ? c : 0u;
+        earlier += w < i / 64 ? c : (w == i / 64 ? (uint32_t)__popcll(m & ((1ull << (i % 64)) - 1)) : 0u);
+    }
+    if (uniform_u32(earlier) != 0) return;
+    if (my_row == row) list[before + (uint32_t)__popcll(same & ((1ull << lane) - 1))] = tid;
+    __syncthreads();
+    count = uniform_u32(count);
+    // this workgroup's slices [s0, s1)
+    const uint32_t per = (a.slices + gridDim.y - 1) / gridDim.y, s0 = min(a.slices, blockIdx.y * per), s1 = min(a.slices, s0 + per);
+    const uint32_t at_once = min(max(s1 - s0, 1u), (uint32_t)kDirectWaves), shares = kDirectWaves / at_once;
+    const uint32_t share = wave / at_once, each = (count + shares - 1) / shares;
+    if (count == 1 && share > 0) return;
+    for (uint32_t slice = s0 + wave % at_once; slice < s1; slice += at_once) {  // (once, unless shares is 1)
+        const uint32_t c0 = slice * 256 + lane * 4;
         const int32_t left = (int32_t)(a.cols - c0);
-        f32x4 sum[kG] = {};
-        auto add = [&](uint64_t slot) {
-            const float *p = a.partials + slot * a.partial_stride + c0;
-#pragma unroll
-            for (int g = 0; g < kG; ++g) sum[g] += load4<false>(p + 256 * g, left - 256 * g);
-        };
-        if (wave == 0) add((uint64_t)window * 2 + 1);
-        const uint32_t quarter = (more + 3) / 4, k1 = min(more, (wave + 1) * quarter);
-        for (uint32_t k = wave * quarter; k < k1; ++k) add((uint64_t)(window + 1 + k) * 2);
-        if (wave > 0) {
-#pragma unroll
-            for (int g = 0; g < kG; ++g) parts[wave - 1][g][lane] = sum[g];
+        Target<O, kGoal, 1> target;
+        if (share == 0) target.load(a, row, c0);
+        f32x4 sum[1] = {};
+        if (share < shares)
+            add_rows<kDeep, 1, T>(sum, min(count, share * each), min(count, (share + 1) * each), left, [&](uint32_t k) {
+                return reinterpret_cast<const T *>(a.grad) + (uint64_t)uniform_u32(list[k]) * a.grad_stride + c0;
+            });
+        if (shares > 1 && count > 1) {
+            parts[wave][lane] = sum[0];
+            __syncthreads();
+            if (share == 0)
+                for (uint32_t k = 1; k < shares; ++k) sum[0] += parts[wave + k * at_once][lane];
         }
-        __syncthreads();
-        if (wave == 0) {
-            for (int k = 0; k < 3; ++k)
-#pragma unroll
-                for (int g = 0; g < kG; ++g) sum[g] += parts[k][g][lane];
-            finish<O, kGoal, kG>(a, row, c0, sum);
-        }
-        __syncthreads();
+        if (share == 0) target.finish(a, row, c0, sum);
     }
 }
 
 constexpr uint64_t kMaxGrid = (1u << 24) - 1;  // grid.x * 256 work-items < 2^32
-uint32_t grid_of(uint64_t workgroups) { return (uint32_t)std::min<uint64_t>(workgroups, kMaxGrid); }
+uint32_t grid_of(uint64_t workgroups, uint64_t most = kMaxGrid) { return (uint32_t)std::min<uint64_t>(workgroups, most); }
 
 template <class T, class O, Goal kGoal>
 hipError_t launch_sums_of(const SumArgs &a, hipStream_t stream) {
-    const dim3 grid(grid_of((a.units + 3) / 4));
-    if (slice_cols(a.cols) == 256) hipLaunchKernelGGL((sum_kernel<T, O, kGoal, 1>), grid, dim3(kSumThreads), 0, stream, a);
-    else hipLaunchKernelGGL((sum_kernel<T, O, kGoal, 2>), grid, dim3(kSumThreads), 0, stream, a);
+    SumArgs b = a;
+    b.sum_groups = grid_of((a.windows + 7) / 8 * (uint64_t)a.slices * 8, kMaxGrid / 2);
+    const uint32_t zeros = kGoal == kWrite ? grid_of((a.rows + (uint64_t)kZeroRows - 1) / kZeroRows, kMaxGrid / 2) : 0u;
+    const dim3 grid(b.sum_groups + zeros), block(kSumThreads);
+    if (a.window == 32) hipLaunchKernelGGL((sum_kernel<T, O, kGoal, kSmallGroups, 8>), grid, block, 0, stream, b);
+    else hipLaunchKernelGGL((sum_kernel<T, O, kGoal, large_groups(kGoal), 16>), grid, block, 0, stream, b);
     return hipGetLastError();
 }
 
-template <class O, Goal kGoal>
-hipError_t launch_joins_of(const SumArgs &a, hipStream_t stream) {
-    const dim3 grid(grid_of((uint64_t)a.windows * a.slices));
-    if (slice_cols(a.cols) == 256) hipLaunchKernelGGL((join_kernel<O, kGoal, 1>), grid, dim3(kSumThreads), 0, stream, a);
-    else hipLaunchKernelGGL((join_kernel<O, kGoal, 2>), grid, dim3(kSumThreads), 0, stream, a);
+template <class T, class O, Goal kGoal>
+hipError_t launch_direct_of(const SumArgs &a, const void *tokens, bool wide, hipStream_t stream) {
+    // the rows to zero: 64 KB and more a workgroup, over some 1024 of them, but no more rows than its bitmap has
+    const uint64_t each64 = std::max<uint64_t>(a.rows / 1024 + 1, 65536 / std::max<uint64_t>(a.cols * sizeof(O), 1));
+    const uint32_t each = (uint32_t)std::min<uint64_t>(each64, kDirectTokens);
+    const uint32_t zeros = kGoal == kWrite ? (a.rows + each - 1) / each : 0u;
+    const uint32_t split = a.tokens_n == 0 ? 1u : std::min(a.slices, std::max(1u, 1024u / a.tokens_n));
+    const dim3 grid(a.tokens_n + zeros, split), block(kDirectThreads);
+    if (wide) hipLaunchKernelGGL((direct_kernel<uint64_t, T, O, kGoal>), grid, block, 0, stream, a, tokens, each);
+    else hipLaunchKernelGGL((direct_kernel<uint32_t, T, O, kGoal>), grid, block, 0, stream, a, tokens, each);
     return hipGetLastError();
+}
+
+template <class T> struct Type { typedef T type; };
+
+// launch(gradient's type, result's type, goal) for the forms that there are.
+template <class Launch>
+hipError_t by_types(bool grad_bf16, bool out_bf16, Goal goal, Launch launch) {
+    auto with = [&](auto o, auto g) { return grad_bf16 ? launch(Type<uint16_t>(), o, g) : launch(Type<float>(), o, g); };
+    switch (goal) {
+    case kWrite: return out_bf16 ? with(Type<uint16_t>(), Int<kWrite>()) : with(Type<float>(), Int<kWrite>());
+    case kAdd: return out_bf16 ? with(Type<uint16_t>(), Int<kAdd>()) : with(Type<float>(), Int<kAdd>());
+    case kAdam: return with(Type<float>(), Int<kAdam>());
+    default: return with(Type<float>(), Int<kAdamMax>());
+    }
 }
 
 template <class T, class O>
@@ -468,8 +744,8 @@ hipError_t launch_lookup_of(const LookupArgs &a, hipStream_t stream) {
     const uint32_t slices = (a.cols + 511) / 512;
     const uint64_t units = (uint64_t)a.tokens_n * slices;
     const dim3 grid(grid_of((units + 3) / 4));
-    if (a.wide) hipLaunchKernelGGL((lookup_kernel<T, O, true>), grid, dim3(kLookupThreads), 0, stream, a, slices, units);
-    else hipLaunchKernelGGL((lookup_kernel<T, O, false>), grid, dim3(kLookupThreads), 0, stream, a, slices, units);
+    if (a.wide) hipLaunchKernelGGL((lookup_kernel<T, O, uint64_t>), grid, dim3(kLookupThreads), 0, stream, a, slices, units);
+    else hipLaunchKernelGGL((lookup_kernel<T, O, uint32_t>), grid, dim3(kLookupThreads), 0, stream, a, slices, units);
     return hipGetLastError();
 }
 
@@ -482,39 +758,24 @@ hipError_t launch_lookup(bool table_bf16, bool out_bf16, const LookupArgs &a, hi
 }
 
 hipError_t launch_group(const GroupArgs &a, hipStream_t stream) {
-    const size_t lds = (size_t)kGroupWaves * 4u << a.bits;
-    if (a.wide) hipLaunchKernelGGL(group_kernel<true>, dim3(kBuckets), dim3(kGroupThreads), lds, stream, a);
-    else hipLaunchKernelGGL(group_kernel<false>, dim3(kBuckets), dim3(kGroupThreads), lds, stream, a);
+    const size_t lds = (size_t)kGroupWaves * (kListed * sizeof(uint2) + (4u << a.bits));
+    if (a.wide) hipLaunchKernelGGL(group_kernel<uint64_t>, dim3(kBuckets), dim3(kGroupThreads), lds, stream, a);
+    else hipLaunchKernelGGL(group_kernel<uint32_t>, dim3(kBuckets), dim3(kGroupThreads), lds, stream, a);
     return hipGetLastError();
 }
 
 hipError_t launch_sums(bool grad_bf16, bool out_bf16, Goal goal, const SumArgs &a, hipStream_t stream) {
-    switch (goal) {
-    case kWrite:
-        if (grad_bf16)
-            return out_bf16 ? launch_sums_of<uint16_t, uint16_t, kWrite>(a, stream)
-                            : launch_sums_of<uint16_t, float, kWrite>(a, stream);
-        return out_bf16 ? launch_sums_of<float, uint16_t, kWrite>(a, stream) : launch_sums_of<float, float, kWrite>(a, stream);
-    case kAdd:
-        if (grad_bf16)
-            return out_bf16 ? launch_sums_of<uint16_t, uint16_t, kAdd>(a, stream)
-                            : launch_sums_of<uint16_t, float, kAdd>(a, stream);
-        return out_bf16 ? launch_sums_of<float, uint16_t, kAdd>(a, stream) : launch_sums_of<float, float, kAdd>(a, stream);
-    case kAdam:
-        return grad_bf16 ? launch_sums_of<uint16_t, float, kAdam>(a, stream) : launch_sums_of<float, float, kAdam>(a, stream);
-    default:
-        return grad_bf16 ? launch_sums_of<uint16_t, float, kAdamMax>(a, stream)
-                         : launch_sums_of<float, float, kAdamMax>(a, stream);
-    }
+    return by_types(grad_bf16, out_bf16, goal, [&](auto t, auto o, auto g) {
+        return launch_sums_of<typename decltype(t)::type, typename decltype(o)::type, (Goal)decltype(g)::value>(a, stream);
+    });
 }
 
-hipError_t launch_joins(bool out_bf16, Goal goal, const SumArgs &a, hipStream_t stream) {
-    switch (goal) {
-    case kWrite: return out_bf16 ? launch_joins_of<uint16_t, kWrite>(a, stream) : launch_joins_of<float, kWrite>(a, stream);
-    case kAdd: return out_bf16 ? launch_joins_of<uint16_t, kAdd>(a, stream) : launch_joins_of<float, kAdd>(a, stream);
-    case kAdam: return launch_joins_of<float, kAdam>(a, stream);
-    default: return launch_joins_of<float, kAdamMax>(a, stream);
-    }
+hipError_t launch_direct(bool grad_bf16, bool out_bf16, Goal goal, const SumArgs &a, const void *tokens, bool wide,
+                         hipStream_t stream) {
+    return by_types(grad_bf16, out_bf16, goal, [&](auto t, auto o, auto g) {
+        return launch_direct_of<typename decltype(t)::type, typename decltype(o)::type, (Goal)decltype(g)::value>(a, tokens, wide,
+                                                                                                               stream);
+    });
 }
 
 }  // namespace adam_mi355x

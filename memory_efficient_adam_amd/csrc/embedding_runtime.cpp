@@ -84,28 +84,37 @@ int64_t token_bytes(const embedding_shape *s) { return s->token_dtype == EMBEDDI
 Span token_span(const embedding_shape *s, const void *tokens) { return Span{tokens, s->tokens * token_bytes(s)}; }
 
 // ---------------------------------------------------------------- gradient
+// Up to this many tokens windows of 32 positions and slices of 256 columns give more
+// waves something to do; of more tokens larger ones leave fewer partial sums and longer
+// accesses.
+constexpr int64_t kSmallTokens = 8192;
+
 struct Plan {
-    uint32_t passes, bits;
-    int64_t windows;
-    int64_t keys[2], order[2], partials, bytes;  // offsets in the workspace; total at 0
+    bool direct;  // in one launch, without a workspace
+    uint32_t bucket_bits, passes, bits;
+    int64_t window, windows, arrivals_n;
+    int64_t arrivals, keys[2], order[2], named, partials, bytes;  // offsets in the workspace, and its size
 };
 
 Plan plan_gradient(int64_t tokens, int64_t rows, int64_t cols) {
     Plan p{};
-    const int64_t keys = std::max<int64_t>(1, ceil_div(rows, kBuckets));  // of a bucket
-    uint32_t bits = 0;
-    while ((int64_t(1) << bits) < keys) ++bits;
-    p.passes = std::max<uint32_t>(1, (bits + kDigitBits - 1) / kDigitBits);
-    p.bits = p.passes == 1 ? bits : kDigitBits;
-    p.windows = ceil_div(tokens, kWindow);
-    int64_t at = 256;
+    p.direct = tokens <= kDirectTokens;
+    if (p.direct) return p;
+    while ((int64_t(kBuckets) << p.bucket_bits) < rows) ++p.bucket_bits;
+    p.passes = std::max<uint32_t>(1, (p.bucket_bits + kDigitBits - 1) / kDigitBits);
+    p.bits = p.passes == 1 ? p.bucket_bits : kDigitBits;
+    p.window = tokens <= kSmallTokens ? 32 : 64;
+    p.windows = ceil_div(tokens, p.window);
+    p.arrivals_n = 3 * p.windows * ceil_div(cols, 256);
+    int64_t at = align256(4 * p.arrivals_n);
     for (uint32_t k = 0; k < (p.passes > 1 ? 2u : 1u); ++k) {
         p.keys[k] = at;
         p.order[k] = at + align256(4 * tokens);
         at = p.order[k] + align256(4 * tokens);
     }
-    p.partials = at;
-    p.bytes = at + align256(2 * p.windows * ((cols + 3) / 4 * 16));
+    p.named = at;
+    p.partials = at + align256(rows);
+    p.bytes = p.partials + align256(2 * p.windows * ((cols + 3) / 4 * 16));
     return p;
 }
 
@@ -129,54 +138,55 @@ int check_gradient(const embedding_shape *s, const void *grad, const void *token
     return ADAM_OK;
 }
 
-SumArgs sum_args(const embedding_shape *s, const Plan &p, const void *grad, void *table, char *ws) {
+SumArgs sum_args(const embedding_shape *s, const Plan &p, Goal goal, const void *grad, void *table, char *ws) {
     SumArgs a{};
-    a.keys = reinterpret_cast<uint32_t *>(ws + p.keys[0]);
-    a.order = reinterpret_cast<uint32_t *>(ws + p.order[0]);
-    a.total = reinterpret_cast<uint32_t *>(ws);
+    a.tokens_n = (uint32_t)s->tokens;
+    a.rows = (uint32_t)s->rows;
     a.grad = grad;
     a.grad_stride = (uint64_t)s->value_stride;
     a.cols = (uint32_t)s->cols;
-    a.slices = (uint32_t)ceil_div(s->cols, slice_cols(a.cols));
-    a.windows = (uint32_t)p.windows;
-    // enough waves to fill the card, and no more positions a wave than that leaves
-    a.portion = 16;
-    while (a.portion > 2 && ceil_div(s->tokens, a.portion) * a.slices < 8192) a.portion /= 2;
-    a.units = (uint64_t)ceil_div(s->tokens, a.portion) * a.slices;
+    a.slices = (uint32_t)ceil_div(s->cols, 256 * (p.direct || p.window == 32 ? kSmallGroups : large_groups(goal)));
     a.scale = s->scale;
-    a.partials = reinterpret_cast<float *>(ws + p.partials);
-    a.partial_stride = ((uint64_t)s->cols + 3) / 4 * 4;
     a.out = table;
     a.out_stride = (uint64_t)s->table_stride;
+    if (p.direct) return a;
+    a.keys = reinterpret_cast<uint32_t *>(ws + p.keys[0]);
+    a.order = reinterpret_cast<uint32_t *>(ws + p.order[0]);
+    a.window = (uint32_t)p.window;
+    a.windows = (uint32_t)p.windows;
+    a.named = reinterpret_cast<uint8_t *>(ws + p.named);
+    a.partials = reinterpret_cast<float *>(ws + p.partials);
+    a.partial_stride = ((uint64_t)s->cols + 3) / 4 * 4;
+    a.arrivals = reinterpret_cast<uint32_t *>(ws + p.arrivals);
     return a;
 }
 
 int run_gradient(const embedding_shape *s, const Plan &p, const void *tokens, char *ws, const SumArgs &a, Goal goal,
                  hipStream_t stream) {
+    const bool grad_bf16 = s->value_dtype == ADAM_GRAD_BF16, out_bf16 = s->table_dtype == ADAM_GRAD_BF16;
+    const bool wide = s->token_dtype == EMBEDDING_TOKENS_I64;
+    hipError_t e;
+    if (p.direct) {
+        e = launch_direct(grad_bf16, out_bf16, goal, a, tokens, wide, stream);
+        return e == hipSuccess ? ADAM_OK : hip_fail(e, "launch of the sums");
+    }
     GroupArgs g{};
     g.tokens = tokens;
-    g.tokens_n = (uint32_t)s->tokens;
-    g.rows = (uint32_t)s->rows;
-    g.wide = s->token_dtype == EMBEDDING_TOKENS_I64;
+    g.tokens_n = a.tokens_n;
+    g.rows = a.rows;
+    g.wide = wide;
+    g.bucket_bits = p.bucket_bits;
     g.passes = p.passes;
     g.bits = p.bits;
     for (int k = 0; k < 2; ++k) {
         g.keys[k] = reinterpret_cast<uint32_t *>(ws + p.keys[k]);
         g.order[k] = reinterpret_cast<uint32_t *>(ws + p.order[k]);
     }
-    g.total = reinterpret_cast<uint32_t *>(ws);
-    if (goal == kWrite) {
-        g.zero = a.out;
-        g.zero_stride = a.out_stride * (uint64_t)element_bytes(s->table_dtype);
-        g.zero_bytes = (uint64_t)s->cols * (uint64_t)element_bytes(s->table_dtype);
-    }
-    hipError_t e = launch_group(g, stream);
-    if (e != hipSuccess) return hip_fail(e, "launch of the grouping");
-    if (s->tokens == 0) return ADAM_OK;
-    const bool grad_bf16 = s->value_dtype == ADAM_GRAD_BF16, out_bf16 = s->table_dtype == ADAM_GRAD_BF16;
+    g.arrivals = a.arrivals;
+    g.arrivals_n = (uint64_t)p.arrivals_n;
+    g.named = goal == kWrite ? reinterpret_cast<uint8_t *>(ws + p.named) : nullptr;
+    if ((e = launch_group(g, stream)) != hipSuccess) return hip_fail(e, "launch of the grouping");
     if ((e = launch_sums(grad_bf16, out_bf16, goal, a, stream)) != hipSuccess) return hip_fail(e, "launch of the sums");
-    if (p.windows > 1 && (e = launch_joins(out_bf16, goal, a, stream)) != hipSuccess)
-        return hip_fail(e, "launch of the joins");
     return ADAM_OK;
 }
 
@@ -230,7 +240,8 @@ int embedding_gradient(const embedding_shape *shape, const void *grad, const voi
         const Plan p = plan_gradient(shape->tokens, shape->rows, shape->cols);
         if (int rc = check_gradient(shape, grad, tokens, table_grad, workspace, workspace_bytes, p.bytes)) return rc;
         char *ws = static_cast<char *>(workspace);
-        return run_gradient(shape, p, tokens, ws, sum_args(shape, p, grad, table_grad, ws), accumulate ? kAdd : kWrite,
+        const Goal goal = accumulate ? kAdd : kWrite;
+        return run_gradient(shape, p, tokens, ws, sum_args(shape, p, goal, grad, table_grad, ws), goal,
                             reinterpret_cast<hipStream_t>(hip_stream));
     });
 }
@@ -270,7 +281,8 @@ int embedding_adam_step(const embedding_shape *shape, float *table, const void *
                 if (meet(one, Span{state[buffers[j]], bytes})) return fail(ADAM_EINVAL, "state buffers overlap");
         }
         char *ws = static_cast<char *>(workspace);
-        SumArgs a = sum_args(shape, p, grad, table, ws);
+        const Goal goal = ams ? kAdamMax : kAdam;
+        SumArgs a = sum_args(shape, p, goal, grad, table, ws);
         StepArgs scalars{};
         adam_scalars(scalars, hp);
         a.m = static_cast<float *>(state[ADAM_BUF_M_F32]);
@@ -287,7 +299,7 @@ int embedding_adam_step(const embedding_shape *shape, float *table, const void *
         a.wd = scalars.wd;
         a.l2 = scalars.l2;
         a.fast_ok = scalars.fast_ok;
-        return run_gradient(shape, p, tokens, ws, a, ams ? kAdamMax : kAdam, reinterpret_cast<hipStream_t>(hip_stream));
+        return run_gradient(shape, p, tokens, ws, a, goal, reinterpret_cast<hipStream_t>(hip_stream));
     });
 }
 

@@ -78,6 +78,11 @@ SIZES = [
     (5000, 300, 520, "spread"), (4500, 5, 130, "same"), (9000, 33, 64, "two"), (4097, 70001, 36, "flat"),
     (20000, 1000, 96, "spread"), (3000, 131073, 17, "flat"), (3000, 262144, 16, "flat"), (3000, 262145, 16, "flat"),
     (2000, 300007, 9, "ends"),
+    # around the numbers of tokens from which another way is taken
+    (512, 60, 300, "spread"), (513, 60, 300, "spread"), (512, 1, 2100, "same"), (513, 1, 1030, "same"),
+    (8192, 100, 257, "spread"), (8193, 100, 257, "spread"), (16384, 50, 4, "spread"), (16385, 50, 4, "flat"),
+    # runs over more windows than are added up at once, and over more than 64 times 16 of them
+    (20000, 1, 9, "same"), (70001, 2, 5, "two"), (140000, 2, 4, "two"),
 ]
 
 
