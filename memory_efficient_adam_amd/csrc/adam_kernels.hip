@@ -935,7 +935,14 @@ __device__ __forceinline__ void load_data(const StepArgs &a, const BlockCtx &c,
             if constexpr (kStore == kStoreQ8) {
                 r.m[j] = in ? ld_u32(reinterpret_cast<const int8_t *>(a.m_state) + s) & keep8 : 0u;
             } else {
-                load_state_f32<kFull>(reinterpret_cast<const float *>(a.m_state) + s, in, live, r.m + 4 * j);
+                f32x4 mf = {0.f, 0.f, 0.f, 0.f};
+                if (in) mf = ld_f32x4(reinterpret_cast<const float *>(a.m_state) + s);
+                r.m[4 * j + 0] = __float_as_uint(mf.x); r.m[4 * j + 1] = __float_as_uint(mf.y);
+                r.m[4 * j + 2] = __float_as_uint(mf.z); r.m[4 * j + 3] = __float_as_uint(mf.w);
+                if constexpr (!kFull) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) r.m[4 * j + k] &= (uint32_t)((int32_t)(k - live) >> 31);
+                }
             }
         }
     }
