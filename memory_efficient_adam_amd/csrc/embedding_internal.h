@@ -78,8 +78,13 @@ constexpr int kSmallGroups = 1;
 constexpr int large_groups(int goal) { return goal >= kAdam ? 1 : 2; }
 hipError_t launch_sums(bool grad_bf16, bool out_bf16, Goal goal, const SumArgs &a, hipStream_t stream);
 
-// Up to this many tokens need no grouping.
-constexpr uint32_t kDirectTokens = 512;
+// Up to this many tokens need no grouping: each position looks through all of them, in
+// time that grows with their square.  us for a bf16 gradient of 2048 columns and tokens as
+// frequent as words are, this way / by groups: 1024 tokens 6.8 / 17, added to a
+// table, 10 / 22 as a step; 2048 tokens 12.5 / 19 and 17 / 27; 4096 tokens 24 / 22 and 31 / 39.
+// All of one row: 1024 tokens 16 / 17, 2048 tokens 33 / 19, 4096 tokens 67 / 25.
+constexpr uint32_t kDirectTokens = 2048;
+constexpr uint32_t kFewTokens = 1024;  // threads look at two tokens each, not at four (0.4 us)
 hipError_t launch_direct(bool grad_bf16, bool out_bf16, Goal goal, const SumArgs &a, const void *tokens, bool wide,
                          hipStream_t stream);
 

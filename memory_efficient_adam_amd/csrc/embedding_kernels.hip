@@ -504,9 +504,10 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(SumArgs a) {
         const uint32_t slice = (uint32_t)(u / 8 % a.slices);
         const uint32_t window = (uint32_t)window64, w0 = window * kWin, end = a.tokens_n - 1;
         // all of them loaded together, at clamped places
-        const uint32_t key_at = a.keys[min(w0 + lane, end)], from = a.order[min(w0 + lane, end)];
+        // (order and keys in bounds even where tokens changed under the call)
+        const uint32_t key_at = a.keys[min(w0 + lane, end)], from = min(a.order[min(w0 + lane, end)], end);
         const uint32_t last_at = a.keys[w0 > 0 ? w0 - 1 : 0], next_at = a.keys[min(w0 + kWin, end)];
-        const uint32_t key = lane < kWin && lane <= end - w0 ? key_at : kNoRow;
+        const uint32_t key = lane < kWin && lane <= end - w0 && key_at < a.rows ? key_at : kNoRow;
         const uint32_t live = (uint32_t)__popcll(__ballot(key != kNoRow));
         if (live == 0) continue;  // padding
         const uint32_t above = __shfl_up(key, 1), prev = lane > 0 ? above : (w0 > 0 ? last_at : kNoRow);
@@ -620,35 +621,45 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(SumArgs a) {
 }
 
 // ---------------------------------------------------------------- few tokens
-constexpr int kDirectThreads = (int)kDirectTokens, kDirectWaves = kDirectThreads / 64;
+constexpr int kDirectThreads = 512, kDirectWaves = kDirectThreads / 64;
 
 // Up to kDirectTokens tokens in one launch and without a workspace: a workgroup a
 // position (and, of few tokens, a share of the columns), which looks through all
-// tokens for its row's.  The first position of a row has the row's sum: its waves
-// share the slices of the columns, and where there are fewer of those the
-// positions.  Where the whole gradient is written, the workgroups behind zero the rows that no
-// token names, by the same look.
-template <class Token, class T, class O, Goal kGoal>
-__global__ void __launch_bounds__(kDirectThreads) direct_kernel(SumArgs a, const void *tokens, uint32_t zero_rows_each) {
+// tokens for its row's.  The workgroups of a row's positions share the slices of its
+// columns, each of them the positions of a slice among its waves, so that a row
+// that many tokens name has many workgroups.  Where the whole gradient is written, the workgroups
+// behind zero the rows that no token names, by the same look.
+// kLooks: tokens that a thread looks at.
+template <class Token, class T, class O, Goal kGoal, uint32_t kLooks>
+__global__ void __launch_bounds__(kDirectThreads) direct_kernel(SumArgs a, const void *tokens, uint32_t splits, uint32_t zero_rows_each) {
     constexpr int kDeep = 32 / (int)sizeof(T);
-    __shared__ uint64_t masks[kDirectWaves];
-    __shared__ uint32_t list[kDirectTokens];
+    constexpr uint32_t kTokens = kLooks * kDirectThreads, kWords = kTokens / 64;
+    __shared__ uint64_t masks[kWords];
+    __shared__ uint32_t list[kTokens];
     __shared__ f32x4 parts[kDirectWaves][64];
     const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = uniform_u32(tid >> 6), n = a.tokens_n;
-    const uint32_t i = blockIdx.x < n ? blockIdx.x : 0;
+    const bool zeroes = blockIdx.x >= n * splits;
+    const uint32_t i = zeroes ? 0 : blockIdx.x / splits, split = zeroes ? 0 : blockIdx.x % splits;
     const Token *const all = reinterpret_cast<const Token *>(tokens);
-    // (tokens_n is 0 only where there are rows to zero)
-    const Token my_token = n > 0 ? all[min(tid, n - 1)] : (Token)0, the_token = n > 0 ? all[i] : (Token)0;
-    const uint32_t my_row = tid < n ? row_of(my_token, a.rows) : kNoRow;
+    Token token[kLooks], the_token = 0;
+    if (n > 0) {  // (it is 0 only where there are rows to zero)
+#pragma unroll
+        for (uint32_t k = 0; k < kLooks; ++k) token[k] = all[min(k * kDirectThreads + tid, n - 1)];
+        the_token = all[i];
+    }
+    auto row_at = [&](uint32_t k) { return k * kDirectThreads + tid < n ? row_of(token[k], a.rows) : kNoRow; };
     if constexpr (kGoal == kWrite) {
-        if (blockIdx.x >= n) {
+        if (zeroes) {
             uint32_t *const named = list;  // a bitmap
-            if (blockIdx.y > 0) return;
-            const uint64_t r0 = (uint64_t)(blockIdx.x - n) * zero_rows_each;
-            if (tid < kDirectTokens / 32) named[tid] = 0;
+            const uint64_t r0 = (uint64_t)(blockIdx.x - n * splits) * zero_rows_each;
+            if (tid < kTokens / 32) named[tid] = 0;
             __syncthreads();
-            if (my_row != kNoRow && my_row >= r0 && my_row - r0 < zero_rows_each)
-                atomicOr(&named[(my_row - r0) / 32], 1u << ((my_row - r0) % 32));
+#pragma unroll
+            for (uint32_t k = 0; k < kLooks; ++k) {
+                const uint32_t row = row_at(k);
+                if (row != kNoRow && row >= r0 && row - r0 < zero_rows_each)
+                    atomicOr(&named[(row - r0) / 32], 1u << ((row - r0) % 32));
+            }
             __syncthreads();
             zero_rows(reinterpret_cast<O *>(a.out), a.out_stride, a.cols, r0, min(r0 + zero_rows_each, (uint64_t)a.rows), kDirectThreads,
                       [&](uint64_t r) { return (named[(r - r0) / 32] >> ((r - r0) % 32)) & 1u; });
@@ -657,42 +668,52 @@ __global__ void __launch_bounds__(kDirectThreads) direct_kernel(SumArgs a, const
     }
     const uint32_t row = uniform_u32(row_of(the_token, a.rows));
     if (row == kNoRow) return;
-    const uint64_t same = __ballot(my_row == row);
-    if (lane == 0) masks[wave] = same;
-    __syncthreads();
-    uint32_t count = 0, before = 0, earlier = 0;  // positions of the row: all, in earlier waves, before i
+    uint64_t same[kLooks];
 #pragma unroll
-    for (uint32_t w = 0; w < kDirectWaves; ++w) {
-        const uint64_t m = masks[w];
-        const uint32_t c = (uint32_t)__popcll(m);
-        count += c;
-        before += w < wave ? c : 0u;
-        earlier += w < i / 64 ? c : (w == i / 64 ? (uint32_t)__popcll(m & ((1ull << (i % 64)) - 1)) : 0u);
+    for (uint32_t k = 0; k < kLooks; ++k) {
+        same[k] = __ballot(row_at(k) == row);
+        if (lane == 0) masks[k * kDirectWaves + wave] = same[k];
     }
-    if (uniform_u32(earlier) != 0) return;
-    if (my_row == row) list[before + (uint32_t)__popcll(same & ((1ull << lane) - 1))] = tid;
     __syncthreads();
-    count = uniform_u32(count);
-    // this workgroup's slices [s0, s1)
-    const uint32_t per = (a.slices + gridDim.y - 1) / gridDim.y, s0 = min(a.slices, blockIdx.y * per), s1 = min(a.slices, s0 + per);
-    const uint32_t at_once = min(max(s1 - s0, 1u), (uint32_t)kDirectWaves), shares = kDirectWaves / at_once;
+    // the row's positions: how many, and how many before this workgroup's and before each of this wave's words
+    const uint64_t word = lane < kWords ? masks[lane] : 0;
+    uint32_t incl = (uint32_t)__popcll(word);
+#pragma unroll
+    for (uint32_t s = 1; s < kWords; s <<= 1) {
+        const uint32_t x = __shfl_up(incl, s);
+        if (lane >= s) incl += x;
+    }
+    const uint32_t excl = incl - (uint32_t)__popcll(word);
+    const uint32_t count = lane_u32(incl, kWords - 1);
+    const uint32_t rank = lane_u32(excl + (uint32_t)__popcll(word & ((1ull << (i % 64)) - 1)), i / 64);
+    // this workgroup's slices: s0 + rank, s0 + rank + helpers, .. of the split's [s0, s1)
+    const uint32_t per = (a.slices + splits - 1) / splits, s0 = min(a.slices, split * per), s1 = min(a.slices, s0 + per);
+    const uint32_t helpers = min(count, s1 - s0);
+    if (rank >= helpers) return;
+#pragma unroll
+    for (uint32_t k = 0; k < kLooks; ++k)
+        if ((same[k] >> lane) & 1u)
+            list[lane_u32(excl, k * kDirectWaves + wave) + (uint32_t)__popcll(same[k] & ((1ull << lane) - 1))] = k * kDirectThreads + tid;
+    __syncthreads();
+    const uint32_t have = (s1 - s0 - rank + helpers - 1) / helpers;  // slices, >= 1
+    const uint32_t at_once = min(have, (uint32_t)kDirectWaves), shares = kDirectWaves / at_once;
     const uint32_t share = wave / at_once, each = (count + shares - 1) / shares;
     if (count == 1 && share > 0) return;
-    for (uint32_t slice = s0 + wave % at_once; slice < s1; slice += at_once) {  // (once, unless shares is 1)
-        const uint32_t c0 = slice * 256 + lane * 4;
+    for (uint32_t k = wave % at_once; k < have; k += at_once) {  // (once, unless shares is 1)
+        const uint32_t c0 = (s0 + rank + k * helpers) * 256 + lane * 4;
         const int32_t left = (int32_t)(a.cols - c0);
         Target<O, kGoal, 1> target;
         if (share == 0) target.load(a, row, c0);
         f32x4 sum[1] = {};
         if (share < shares)
-            add_rows<kDeep, 1, T>(sum, min(count, share * each), min(count, (share + 1) * each), left, [&](uint32_t k) {
-                return reinterpret_cast<const T *>(a.grad) + (uint64_t)uniform_u32(list[k]) * a.grad_stride + c0;
+            add_rows<kDeep, 1, T>(sum, min(count, share * each), min(count, (share + 1) * each), left, [&](uint32_t p) {
+                return reinterpret_cast<const T *>(a.grad) + (uint64_t)uniform_u32(list[p]) * a.grad_stride + c0;
             });
         if (shares > 1 && count > 1) {
             parts[wave][lane] = sum[0];
             __syncthreads();
             if (share == 0)
-                for (uint32_t k = 1; k < shares; ++k) sum[0] += parts[wave + k * at_once][lane];
+                for (uint32_t p = 1; p < shares; ++p) sum[0] += parts[wave + p * at_once][lane];
         }
         if (share == 0) target.finish(a, row, c0, sum);
     }
@@ -716,12 +737,16 @@ template <class T, class O, Goal kGoal>
 hipError_t launch_direct_of(const SumArgs &a, const void *tokens, bool wide, hipStream_t stream) {
     // the rows to zero: 64 KB and more a workgroup, over some 1024 of them, but no more rows than its bitmap has
     const uint64_t each64 = std::max<uint64_t>(a.rows / 1024 + 1, 65536 / std::max<uint64_t>(a.cols * sizeof(O), 1));
-    const uint32_t each = (uint32_t)std::min<uint64_t>(each64, kDirectTokens);
+    const uint32_t each = (uint32_t)std::min<uint64_t>(each64, kFewTokens);
     const uint32_t zeros = kGoal == kWrite ? (a.rows + each - 1) / each : 0u;
-    const uint32_t split = a.tokens_n == 0 ? 1u : std::min(a.slices, std::max(1u, 1024u / a.tokens_n));
-    const dim3 grid(a.tokens_n + zeros, split), block(kDirectThreads);
-    if (wide) hipLaunchKernelGGL((direct_kernel<uint64_t, T, O, kGoal>), grid, block, 0, stream, a, tokens, each);
-    else hipLaunchKernelGGL((direct_kernel<uint32_t, T, O, kGoal>), grid, block, 0, stream, a, tokens, each);
+    const uint32_t splits = a.tokens_n == 0 ? 1u : std::min(a.slices, std::max(1u, 1024u / a.tokens_n));
+    const dim3 grid(a.tokens_n * splits + zeros), block(kDirectThreads);
+    constexpr uint32_t kFew = kFewTokens / kDirectThreads, kMore = kDirectTokens / kDirectThreads;
+    const bool few = a.tokens_n <= kFewTokens;
+    if (wide && few) hipLaunchKernelGGL((direct_kernel<uint64_t, T, O, kGoal, kFew>), grid, block, 0, stream, a, tokens, splits, each);
+    else if (wide) hipLaunchKernelGGL((direct_kernel<uint64_t, T, O, kGoal, kMore>), grid, block, 0, stream, a, tokens, splits, each);
+    else if (few) hipLaunchKernelGGL((direct_kernel<uint32_t, T, O, kGoal, kFew>), grid, block, 0, stream, a, tokens, splits, each);
+    else hipLaunchKernelGGL((direct_kernel<uint32_t, T, O, kGoal, kMore>), grid, block, 0, stream, a, tokens, splits, each);
     return hipGetLastError();
 }
 

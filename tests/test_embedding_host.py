@@ -22,7 +22,7 @@ without_gpu = pytest.mark.skipif(torch.cuda.device_count() > 0, reason="would la
 
 
 def _shape(**kw):
-    s = dict(rows=100, cols=40, tokens=600, table_stride=40, value_stride=40, table_dtype=0, value_dtype=0, token_dtype=1,
+    s = dict(rows=100, cols=40, tokens=3000, table_stride=40, value_stride=40, table_dtype=0, value_dtype=0, token_dtype=1,
              scale=1.0)
     s.update(kw)
     if "cols" in kw:
@@ -65,8 +65,8 @@ def test_exports_and_struct():
 def test_workspace_bytes():
     w = ma.embedding_gradient_workspace_bytes
     assert w(0, 0, 5) == 0 and w(5, 5, 0) == 0
-    assert w(1, 5, 7) == w(512, 2 ** 31 - 1, 2 ** 31 - 1) == 0  # few tokens need none
-    for tokens, rows, cols in ((513, 1, 1), (8192, 1000, 7), (8193, 1000, 7), (16384, 50304, 2048), (5000, 2 ** 31 - 1, 3)):
+    assert w(1, 5, 7) == w(2048, 2 ** 31 - 1, 2 ** 31 - 1) == 0  # few tokens need none
+    for tokens, rows, cols in ((2049, 1, 1), (8192, 1000, 7), (8193, 1000, 7), (16384, 50304, 2048), (5000, 2 ** 31 - 1, 3)):
         n = w(tokens, rows, cols)
         # keys and positions, twice for more rows than 2^18; a byte a row; two fp32 rows and three counters a window of 32 or 64
         windows = -(-tokens // (32 if tokens <= 8192 else 64))
@@ -112,26 +112,26 @@ def test_pointers_that_are_missing_or_unaligned():
 
 
 def test_the_workspace_has_to_suffice():
-    need = ma.embedding_gradient_workspace_bytes(600, 100, 40)
+    need = ma.embedding_gradient_workspace_bytes(3000, 100, 40)
     assert _gradient(ws_bytes=need - 1) == -1 and str(need) in ma.adam_last_error()
     assert _step(ws_bytes=need - 1) == -1 and str(need) in ma.adam_last_error()
 
 
 @without_gpu
 def test_few_tokens_need_no_workspace():
-    assert _gradient(ws=None, ws_bytes=0, tokens=512) == _step(ws=None, ws_bytes=0, tokens=512) == -5
-    assert _gradient(ws=TABLE, ws_bytes=0, tokens=512) == -5  # not looked at
+    assert _gradient(ws=None, ws_bytes=0, tokens=2048) == _step(ws=None, ws_bytes=0, tokens=2048) == -5
+    assert _gradient(ws=TABLE, ws_bytes=0, tokens=2048) == -5  # not looked at
 
 
 def test_what_is_written_meets_nothing_else():
-    table, values, tokens = 100 * 40 * 4, 600 * 40 * 4, 600 * 8
+    table, values, tokens = 100 * 40 * 4, 3000 * 40 * 4, 3000 * 8
     for out in (TABLE, TABLE + table - 4, TABLE - values + 4, TOKENS, TOKENS + tokens - 4, TOKENS - values + 4):
         assert _lookup(out=out) == -1 and "overlaps" in ma.adam_last_error(), hex(out)
     for out in (VALUES, VALUES + values - 4, VALUES - table + 4, TOKENS, TOKENS - table + 4):
         assert _gradient(table=out) == -1 and "overlaps" in ma.adam_last_error(), hex(out)
     for out in (VALUES, VALUES + values - 16, VALUES - table + 16, TOKENS, TOKENS - table + 16):
         assert _step(table=out) == -1 and "overlaps" in ma.adam_last_error(), hex(out)
-    need = ma.embedding_gradient_workspace_bytes(600, 100, 40)
+    need = ma.embedding_gradient_workspace_bytes(3000, 100, 40)
     for ws in (TABLE, TABLE - need + 256, TABLE + (table - 4) // 256 * 256, VALUES, TOKENS):
         assert _gradient(ws=ws) == -1 and "workspace" in ma.adam_last_error(), hex(ws)
         assert _step(ws=ws) == -1 and "workspace" in ma.adam_last_error(), hex(ws)
@@ -163,7 +163,7 @@ def test_arguments_of_the_step():
 
 @without_gpu
 def test_calls_that_are_not_refused_reach_the_device():
-    table, values = 100 * 40 * 4, 600 * 40 * 4
+    table, values = 100 * 40 * 4, 3000 * 40 * 4
     assert _lookup() == _gradient() == _step() == -5
     assert _lookup(out=TABLE + table) == _lookup(out=TABLE - values) == -5
     assert _gradient(value_stride=0) == _gradient(value_stride=1000, table_stride=77) == -5

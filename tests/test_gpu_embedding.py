@@ -79,7 +79,8 @@ SIZES = [
     (20000, 1000, 96, "spread"), (3000, 131073, 17, "flat"), (3000, 262144, 16, "flat"), (3000, 262145, 16, "flat"),
     (2000, 300007, 9, "ends"),
     # around the numbers of tokens from which another way is taken
-    (512, 60, 300, "spread"), (513, 60, 300, "spread"), (512, 1, 2100, "same"), (513, 1, 1030, "same"),
+    (1024, 60, 300, "spread"), (1025, 60, 300, "spread"), (2048, 60, 300, "spread"), (2049, 60, 300, "spread"),
+    (512, 1, 2100, "same"), (2048, 1, 2100, "same"), (1024, 3, 4500, "two"), (2049, 1, 1030, "same"), (7, 2, 5000, "two"),
     (8192, 100, 257, "spread"), (8193, 100, 257, "spread"), (16384, 50, 4, "spread"), (16385, 50, 4, "flat"),
     # runs over more windows than are added up at once, and over more than 64 times 16 of them
     (20000, 1, 9, "same"), (70001, 2, 5, "two"), (140000, 2, 4, "two"),
