@@ -87,6 +87,10 @@ __device__ __forceinline__ uint32_t row_of(uint64_t token, uint32_t rows) { retu
 // (negative ones are 2^31 and more)
 __device__ __forceinline__ uint32_t row_of(uint32_t token, uint32_t rows) { return token < rows ? token : kNoRow; }
 
+// The token, or 2^32 - 1 where it does not fit 32 bits.
+__device__ __forceinline__ uint32_t low_word(uint64_t token) { return (uint32_t)(token >> 32) == 0 ? (uint32_t)token : kNoRow; }
+__device__ __forceinline__ uint32_t low_word(uint32_t token) { return token; }
+
 __device__ __forceinline__ uint32_t uniform_u32(uint32_t x) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)x); }
 __device__ __forceinline__ uint32_t lane_u32(uint32_t x, uint32_t lane) {
     return (uint32_t)__builtin_amdgcn_readlane((int)x, (int)lane);
@@ -161,6 +165,8 @@ __global__ void __launch_bounds__(kGroupThreads) group_kernel(GroupArgs a) {
     uint32_t *const counts = reinterpret_cast<uint32_t *>(shared + kGroupWaves * kListed), *const mine = counts + wave * bins;
     uint2 *const list = shared + wave * kListed;
     uint32_t base = 0, len = a.tokens_n;
+    // the bucket's rows are [bucket0, bucket0 + width); rows below `limit` are those of earlier buckets
+    const uint32_t bucket0 = bucket << a.bucket_bits, limit = min(bucket0, a.rows), width = min(a.rows - limit, 1u << a.bucket_bits);
     if (tid == 0) below_sum = 0;
     for (uint64_t i = bucket * kGroupThreads + tid; i < a.arrivals_n; i += kBuckets * kGroupThreads) a.arrivals[i] = 0;
     for (uint32_t pass = 0; pass < a.passes; ++pass) {
@@ -168,8 +174,8 @@ __global__ void __launch_bounds__(kGroupThreads) group_kernel(GroupArgs a) {
         const uint32_t *keys_in = a.keys[to ^ 1u], *order_in = a.order[to ^ 1u];
         const uint32_t chunks = len / kGroupChunk + (len % kGroupChunk != 0);
         uint32_t below = 0, listed = 0;
-        // the rows of this thread's positions of a chunk; in the first pass kNoRow for
-        // the other buckets' ones, with `below` counting those of earlier buckets
+        // The rows at this thread's positions of a chunk.  A row in another bucket, or
+        // none, is 2^32 - 1 or beyond the bucket's rows either way.
         auto fetch = [&](uint32_t chunk, uint32_t (&key)[kHeld]) {
             const uint32_t i0 = chunk * kGroupChunk + tid;
             if (pass == 0) {
@@ -178,31 +184,28 @@ __global__ void __launch_bounds__(kGroupThreads) group_kernel(GroupArgs a) {
                 for (int j = 0; j < kHeld; ++j)
                     token[j] = reinterpret_cast<const Token *>(a.tokens)[min(i0 + j * kGroupThreads, len - 1)];
 #pragma unroll
-                for (int j = 0; j < kHeld; ++j) {
-                    key[j] = i0 + j * kGroupThreads < len ? row_of(token[j], a.rows) : kNoRow;
-                    const uint32_t in = key[j] >> a.bucket_bits;
-                    below += key[j] != kNoRow && in < bucket ? 1u : 0u;
-                    if (in != bucket) key[j] = kNoRow;
-                }
+                for (int j = 0; j < kHeld; ++j) key[j] = low_word(token[j]);
             } else {
 #pragma unroll
                 for (int j = 0; j < kHeld; ++j) key[j] = keys_in[base + min(i0 + j * kGroupThreads, len - 1)];
-#pragma unroll
-                for (int j = 0; j < kHeld; ++j)
-                    if (i0 + j * kGroupThreads >= len) key[j] = kNoRow;
             }
+#pragma unroll
+            for (int j = 0; j < kHeld; ++j)
+                if (i0 + j * kGroupThreads >= len) key[j] = kNoRow;
         };
         auto digit_of = [&](uint32_t key) { return (key >> shift) & (bins - 1); };
-        // the positions of key[j] behind the `listed` ones
+        // the bucket's positions of these are listed behind the `listed` ones
         auto append = [&](uint32_t key, uint32_t i, bool count) {
-            const uint64_t have = __ballot(key != kNoRow);
-            if (have == 0) return;
-            if (key != kNoRow) {
-                const uint32_t at = listed + (uint32_t)__popcll(have & ((1ull << lane) - 1));
+            const bool have = key - bucket0 < width;
+            const uint64_t all = __ballot(have);
+            if (count && pass == 0) below += (uint32_t)__popcll(__ballot(key < limit));
+            if (all == 0) return;
+            if (have) {
+                const uint32_t at = listed + (uint32_t)__popcll(all & ((1ull << lane) - 1));
                 if (at < kListed) list[at] = uint2{key, i};
                 if (count) atomicAdd(mine + digit_of(key), 1u);
             }
-            listed += (uint32_t)__popcll(have);
+            listed += (uint32_t)__popcll(all);
         };
         for (uint32_t i = tid; i < kGroupWaves * bins; i += kGroupThreads) counts[i] = 0;
         __syncthreads();
@@ -212,10 +215,7 @@ __global__ void __launch_bounds__(kGroupThreads) group_kernel(GroupArgs a) {
 #pragma unroll
             for (int j = 0; j < kHeld; ++j) append(key[j], c * kGroupChunk + j * kGroupThreads + tid, true);
         }
-        if (pass == 0) {
-            for (int s = 32; s > 0; s >>= 1) below += __shfl_xor(below, s);
-            if (lane == 0) atomicAdd(&below_sum, below);
-        }
+        if (pass == 0 && lane == 0) atomicAdd(&below_sum, below);
         __syncthreads();
         // counts to places: thread d has digit d's of every wave
         uint32_t held[kGroupWaves], digit_total = 0;
@@ -298,9 +298,7 @@ __global__ void __launch_bounds__(kGroupThreads) group_kernel(GroupArgs a) {
         for (uint32_t i = base + len + tid; i < a.tokens_n; i += kGroupThreads) a.keys[0][i] = kNoRow;
     if (!a.named) return;
     // which of the bucket's rows a token names
-    const uint64_t bucket0 = (uint64_t)bucket << a.bucket_bits;
-    const uint32_t rows = a.rows > bucket0 ? (uint32_t)min((uint64_t)a.rows - bucket0, 1ull << a.bucket_bits) : 0u;
-    for (uint32_t r = tid; r < rows; r += kGroupThreads) a.named[bucket0 + r] = 0;
+    for (uint32_t r = tid; r < width; r += kGroupThreads) a.named[(uint64_t)bucket0 + r] = 0;
     __syncthreads();
     for (uint32_t i = tid; i < len; i += kGroupThreads) a.named[a.keys[0][base + i]] = 1;
 }
