@@ -36,7 +36,7 @@ sys.path.insert(0, ROOT)
 
 HBM_PEAK_GBS = 8000.0
 KERNEL_SOURCES = [os.path.join(ROOT, "memory_efficient_adam_amd", "csrc", f)
-                  for f in ("adam_kernels.hip", "adam_internal.h")]
+                  for f in ("adam_kernels.hip", "adam_internal.h", "adam_element.h")]
 TRAFFIC_FILE = os.path.join(ROOT, "profiles", "hbm_traffic.json")
 
 # algorithmic bytes per parameter (read + write) and per block (scales)
