@@ -59,7 +59,7 @@ struct SumArgs {
     uint64_t grad_stride;  // elements
     uint32_t cols;
     uint32_t window, windows;  // positions of a window, and how many windows
-    uint32_t slices;   // of a row
+    uint32_t slices;   // of a row, 256 columns each
     float scale;
     uint32_t sum_groups;   // workgroups that sum; those behind them zero rows (kWrite)
     const uint8_t *named;
@@ -73,9 +73,6 @@ struct SumArgs {
     float step, ibc2, decay, omb1, omb2, beta1, beta2, eps, wd;
     uint32_t l2, fast_ok;
 };
-// Columns that a wave takes of a row, in groups of 256.
-constexpr int kSmallGroups = 1;
-constexpr int large_groups(int goal) { return goal >= kAdam ? 1 : 2; }
 hipError_t launch_sums(bool grad_bf16, bool out_bf16, Goal goal, const SumArgs &a, hipStream_t stream);
 
 // Up to this many tokens need no grouping: each position looks through all of them, in

@@ -342,68 +342,55 @@ __device__ __forceinline__ void update4(const SumArgs &a, f32x4 &p, f32x4 g, f32
 // What a row's whole sum meets: nothing, the value it is added to, or the
 // step's params and state, loaded before the sum so that both are under way
 // together.
-template <class O, Goal kGoal, int kG>
+template <class O, Goal kGoal>
 struct Target {
-    Four<O> p[kG];
-    Four<float> m[kG], v[kG], w[kG];
+    Four<O> p;
+    Four<float> m, v, w;
 
     __device__ __forceinline__ void load(const SumArgs &a, uint32_t row, uint32_t c0) {
         if constexpr (kGoal == kWrite) return;
         const int32_t left = (int32_t)(a.cols - c0);
-        const O *from = reinterpret_cast<const O *>(a.out) + (uint64_t)row * a.out_stride + c0;
         const uint64_t s = (uint64_t)row * a.cols + c0;
-#pragma unroll
-        for (int g = 0; g < kG; ++g) {
-            p[g].template load<true>(from + 256 * g, left - 256 * g);
-            if constexpr (kGoal >= kAdam) {
-                m[g].template load<true>(a.m + s + 256 * g, left - 256 * g);
-                v[g].template load<true>(a.v + s + 256 * g, left - 256 * g);
-            }
-            if constexpr (kGoal == kAdamMax) w[g].template load<true>(a.w + s + 256 * g, left - 256 * g);
+        p.template load<true>(reinterpret_cast<const O *>(a.out) + (uint64_t)row * a.out_stride + c0, left);
+        if constexpr (kGoal >= kAdam) {
+            m.template load<true>(a.m + s, left);
+            v.template load<true>(a.v + s, left);
         }
+        if constexpr (kGoal == kAdamMax) w.template load<true>(a.w + s, left);
     }
 
-    __device__ __forceinline__ void finish(const SumArgs &a, uint32_t row, uint32_t c0, const f32x4 (&sum)[kG]) {
+    __device__ __forceinline__ void finish(const SumArgs &a, uint32_t row, uint32_t c0, f32x4 sum) {
         const int32_t left = (int32_t)(a.cols - c0);
         O *to = reinterpret_cast<O *>(a.out) + (uint64_t)row * a.out_stride + c0;
         const uint64_t s = (uint64_t)row * a.cols + c0;
-#pragma unroll
-        for (int g = 0; g < kG; ++g) {
-            const f32x4 one = sum[g] * a.scale;
-            if constexpr (kGoal == kWrite) {
-                store4(to + 256 * g, one, left - 256 * g);
-            } else if constexpr (kGoal == kAdd) {
-                store4(to + 256 * g, p[g].wide() + one, left - 256 * g);
-            } else {
-                f32x4 ps = p[g].wide(), ms = m[g].wide(), vs = v[g].wide(), ws = {};
-                if constexpr (kGoal == kAdamMax) ws = w[g].wide();
-                update4<kGoal == kAdamMax>(a, ps, one, ms, vs, ws, left - 256 * g);
-                store4(to + 256 * g, ps, left - 256 * g);
-                store4(a.m + s + 256 * g, ms, left - 256 * g);
-                store4(a.v + s + 256 * g, vs, left - 256 * g);
-                if constexpr (kGoal == kAdamMax) store4(a.w + s + 256 * g, ws, left - 256 * g);
-            }
+        const f32x4 one = sum * a.scale;
+        if constexpr (kGoal == kWrite) {
+            store4(to, one, left);
+        } else if constexpr (kGoal == kAdd) {
+            store4(to, p.wide() + one, left);
+        } else {
+            f32x4 ps = p.wide(), ms = m.wide(), vs = v.wide(), ws = {};
+            if constexpr (kGoal == kAdamMax) ws = w.wide();
+            update4<kGoal == kAdamMax>(a, ps, one, ms, vs, ws, left);
+            store4(to, ps, left);
+            store4(a.m + s, ms, left);
+            store4(a.v + s, vs, left);
+            if constexpr (kGoal == kAdamMax) store4(a.w + s, ws, left);
         }
     }
 };
 
 // sum += the rows at(k) + c0 for k in [from, to), the loads of up to kDeep rows
 // under way together (as many batches of kDeep, then at most one each of 8, 4, 2 and 1).
-template <int kDeep, int kG, class T, class At>
-__device__ __forceinline__ void add_rows(f32x4 (&sum)[kG], uint32_t from, uint32_t to, int32_t left, At at) {
+template <int kDeep, class T, class At>
+__device__ __forceinline__ void add_rows(f32x4 &sum, uint32_t from, uint32_t to, int32_t left, At at) {
     auto batch = [&](auto size) {
         constexpr int kN = decltype(size)::value;
-        Four<T> x[kN][kG];
+        Four<T> x[kN];
 #pragma unroll
-        for (int j = 0; j < kN; ++j) {
-            const T *p = at(from + j);
+        for (int j = 0; j < kN; ++j) x[j].template load<true>(at(from + j), left);
 #pragma unroll
-            for (int g = 0; g < kG; ++g) x[j][g].template load<true>(p + 256 * g, left - 256 * g);
-        }
-#pragma unroll
-        for (int j = 0; j < kN; ++j)
-#pragma unroll
-            for (int g = 0; g < kG; ++g) sum[g] += x[j][g].wide();
+        for (int j = 0; j < kN; ++j) sum += x[j].wide();
         from += kN;
     };
     while (to - from >= (uint32_t)kDeep) batch(Int<kDeep>());
@@ -434,34 +421,26 @@ __device__ __forceinline__ f32x4 get_partial(const float *at, int32_t n) {
 // Leaves a partial sum in slot `mine` and counts it in at *arrivals; true for
 // the wave that comes last of n, which then has their sum, slot_at(0) first,
 // slot_at(n - 1) last.
-template <int kG, class Slot>
-__device__ __forceinline__ bool meet(const SumArgs &a, f32x4 (&sum)[kG], uint64_t mine, uint32_t n, Slot slot_at,
+template <class Slot>
+__device__ __forceinline__ bool meet(const SumArgs &a, f32x4 &sum, uint64_t mine, uint32_t n, Slot slot_at,
                                      uint32_t *arrivals, uint32_t c0) {
     const int32_t left = (int32_t)(a.cols - c0);
     float *const partials = a.partials + c0;
-#pragma unroll
-    for (int g = 0; g < kG; ++g) put_partial(partials + mine * a.partial_stride + 256 * g, sum[g], left - 256 * g);
+    put_partial(partials + mine * a.partial_stride, sum, left);
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // in memory before it is counted
     uint32_t before = 0;
     if ((threadIdx.x & 63u) == 0)
         before = __hip_atomic_fetch_add(arrivals, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     if (uniform_u32(before) + 1 != n) return false;
     asm volatile("" ::: "memory");
-#pragma unroll
-    for (int g = 0; g < kG; ++g) sum[g] = f32x4{0.f, 0.f, 0.f, 0.f};
+    sum = f32x4{0.f, 0.f, 0.f, 0.f};
     for (uint32_t k = 0; k < n; k += 4) {
-        f32x4 x[4][kG];
+        f32x4 x[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float *from = partials + slot_at(min(k + j, n - 1)) * a.partial_stride;
-#pragma unroll
-            for (int g = 0; g < kG; ++g) x[j][g] = get_partial(from + 256 * g, left - 256 * g);
-        }
+        for (int j = 0; j < 4; ++j) x[j] = get_partial(partials + slot_at(min(k + j, n - 1)) * a.partial_stride, left);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int g = 0; g < kG; ++g)
-                if (k + j < n) sum[g] += x[j][g];
+            if (k + j < n) sum += x[j];
     }
     return true;
 }
@@ -476,11 +455,11 @@ __device__ __forceinline__ bool meet(const SumArgs &a, f32x4 (&sum)[kG], uint64_
 //   - of a run over several windows each leaves a partial sum in memory, and the wave
 //     that comes last adds them up in the order of the windows (kFan at a time,
 //     then those sums).  No wave waits for another workgroup.
-template <class T, class O, Goal kGoal, int kG, int kPer>
+template <class T, class O, Goal kGoal, int kPer>
 __global__ void __launch_bounds__(kSumThreads) sum_kernel(SumArgs a) {
     constexpr uint32_t kWin = 4 * kPer;
-    constexpr int kBatch = kGoal >= kAdam && kPer == 16 ? 2 : 4, kDeep = 16 / kG * 2 / (int)sizeof(T);
-    __shared__ f32x4 leads[4][kG][64];  // what each wave has of a run that began before its positions
+    constexpr int kBatch = 4, kDeep = 32 / (int)sizeof(T);
+    __shared__ f32x4 leads[4][64];  // what each wave has of a run that began before its positions
     const uint32_t lane = threadIdx.x & 63u, wave = uniform_u32(threadIdx.x >> 6);
     if constexpr (kGoal == kWrite) {
         if (blockIdx.x >= a.sum_groups) {
@@ -526,27 +505,24 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(SumArgs a) {
             if (e > qe || (e == kWin && lane_u32(key, h) == next)) tail = h;
         }
         auto row_of_key = [&](uint32_t k) { return lane_u32(key, k); };
-        const uint32_t c0 = slice * (256 * kG) + lane * 4;
+        const uint32_t c0 = slice * 256 + lane * 4;
         const int32_t left = (int32_t)(a.cols - c0);
         auto row_at = [&](uint32_t k) {
             return reinterpret_cast<const T *>(a.grad) + (uint64_t)lane_u32(from, k) * a.grad_stride + c0;
         };
-        f32x4 sum[kG] = {};
+        f32x4 sum = {};
         if (body > q0) {
-            add_rows<kDeep, kG, T>(sum, q0, body, left, row_at);
-#pragma unroll
-            for (int g = 0; g < kG; ++g) leads[wave][g][lane] = sum[g];
+            add_rows<kDeep, T>(sum, q0, body, left, row_at);
+            leads[wave][lane] = sum;
         }
         for (uint32_t k = body; k < tail; k += kBatch) {
-            Four<T> x[kBatch][kG];
-            Target<O, kGoal, kG> target[kBatch];
+            Four<T> x[kBatch];
+            Target<O, kGoal> target[kBatch];
             uint32_t closes = 0;  // positions that a run ends at
 #pragma unroll
             for (uint32_t j = 0; j < kBatch; ++j) {
                 if (k + j >= tail) continue;
-                const T *p = row_at(k + j);
-#pragma unroll
-                for (int g = 0; g < kG; ++g) x[j][g].template load<true>(p + 256 * g, left - 256 * g);
+                x[j].template load<true>(row_at(k + j), left);
                 if (k + j + 1 == live || ((heads >> (k + j + 1)) & 1u)) {  // (k + j + 1 == 64 only where it is live)
                     closes |= 1u << j;
                     target[j].load(a, row_of_key(k + j), c0);
@@ -555,33 +531,26 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(SumArgs a) {
 #pragma unroll
             for (uint32_t j = 0; j < kBatch; ++j) {
                 if (k + j >= tail) continue;
-                const bool begins = (heads >> (k + j)) & 1u;
-#pragma unroll
-                for (int g = 0; g < kG; ++g) {
-                    const f32x4 one = x[j][g].wide();
-                    sum[g] = begins ? one : sum[g] + one;
-                }
+                const f32x4 one = x[j].wide();
+                sum = (heads >> (k + j)) & 1u ? one : sum + one;
                 if ((closes >> j) & 1u) target[j].finish(a, row_of_key(k + j), c0, sum);
             }
         }
         // the run that goes on behind the wave's positions; in the first wave also the one that began before the window
-        Target<O, kGoal, kG> target;
+        Target<O, kGoal> target;
         const bool goes_on = tail < qe, crosses = goes_on && end_of(tail) == kWin && next == row_of_key(tail);
         if (goes_on) {
             if (!crosses) target.load(a, row_of_key(tail), c0);
-#pragma unroll
-            for (int g = 0; g < kG; ++g) sum[g] = f32x4{0.f, 0.f, 0.f, 0.f};
-            add_rows<kDeep, kG, T>(sum, tail, qe, left, row_at);
+            sum = f32x4{0.f, 0.f, 0.f, 0.f};
+            add_rows<kDeep, T>(sum, tail, qe, left, row_at);
         }
         __syncthreads();
         for (uint32_t k = 0; k < 2; ++k) {
             if (!(k == 0 ? goes_on : wave == 0 && body > 0)) continue;
             // k = 0: from this wave's sum; 1: from the first wave's lead
             const uint32_t h = k == 0 ? tail : 0, e = k == 0 ? end_of(h) : (body < qe ? body : end_of(qe - 1)), row = row_of_key(h);
-            for (uint32_t w = k == 0 ? wave + 1 : 0; w * kPer < e; ++w) {
-#pragma unroll
-                for (int g = 0; g < kG; ++g) sum[g] = (k == 1 && w == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : sum[g]) + leads[w][g][lane];
-            }
+            if (k == 1) sum = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (uint32_t w = k == 0 ? wave + 1 : 0; w * kPer < e; ++w) sum += leads[w][lane];
             bool all_in = true;
             if (k == 1 || crosses) {
                 // the windows that the run has before this one and after it
@@ -605,11 +574,11 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(SumArgs a) {
                 // the slot of a piece: its window's second where the run began there, else its first
                 auto slot_of = [&](uint32_t piece) { return (uint64_t)(start + piece) * 2 + (piece == 0 ? 1 : 0); };
                 uint32_t *const counters = a.arrivals + (uint64_t)slice * a.windows * 3;
-                all_in = meet<kG>(a, sum, slot_of(earlier), min(kFan, pieces - fan * kFan),
-                                  [&](uint32_t i) { return slot_of(fan * kFan + i); }, counters + slot_of(fan * kFan), c0);
+                all_in = meet(a, sum, slot_of(earlier), min(kFan, pieces - fan * kFan),
+                              [&](uint32_t i) { return slot_of(fan * kFan + i); }, counters + slot_of(fan * kFan), c0);
                 if (all_in && fans > 1)
-                    all_in = meet<kG>(a, sum, slot_of(fan * kFan), fans, [&](uint32_t i) { return slot_of(i * kFan); },
-                                      counters + (uint64_t)a.windows * 2 + start, c0);
+                    all_in = meet(a, sum, slot_of(fan * kFan), fans, [&](uint32_t i) { return slot_of(i * kFan); },
+                                  counters + (uint64_t)a.windows * 2 + start, c0);
                 if (all_in) target.load(a, row, c0);
             }
             if (all_in) target.finish(a, row, c0, sum);
@@ -700,18 +669,18 @@ __global__ void __launch_bounds__(kDirectThreads) direct_kernel(SumArgs a, const
     for (uint32_t k = wave % at_once; k < have; k += at_once) {  // (once, unless shares is 1)
         const uint32_t c0 = (s0 + rank + k * helpers) * 256 + lane * 4;
         const int32_t left = (int32_t)(a.cols - c0);
-        Target<O, kGoal, 1> target;
+        Target<O, kGoal> target;
         if (share == 0) target.load(a, row, c0);
-        f32x4 sum[1] = {};
+        f32x4 sum = {};
         if (share < shares)
-            add_rows<kDeep, 1, T>(sum, min(count, share * each), min(count, (share + 1) * each), left, [&](uint32_t p) {
+            add_rows<kDeep, T>(sum, min(count, share * each), min(count, (share + 1) * each), left, [&](uint32_t p) {
                 return reinterpret_cast<const T *>(a.grad) + (uint64_t)uniform_u32(list[p]) * a.grad_stride + c0;
             });
         if (shares > 1 && count > 1) {
-            parts[wave][lane] = sum[0];
+            parts[wave][lane] = sum;
             __syncthreads();
             if (share == 0)
-                for (uint32_t p = 1; p < shares; ++p) sum[0] += parts[wave + p * at_once][lane];
+                for (uint32_t p = 1; p < shares; ++p) sum += parts[wave + p * at_once][lane];
         }
         if (share == 0) target.finish(a, row, c0, sum);
     }
@@ -726,8 +695,8 @@ hipError_t launch_sums_of(const SumArgs &a, hipStream_t stream) {
     b.sum_groups = grid_of((a.windows + 7) / 8 * (uint64_t)a.slices * 8, kMaxGrid / 2);
     const uint32_t zeros = kGoal == kWrite ? grid_of((a.rows + (uint64_t)kZeroRows - 1) / kZeroRows, kMaxGrid / 2) : 0u;
     const dim3 grid(b.sum_groups + zeros), block(kSumThreads);
-    if (a.window == 32) hipLaunchKernelGGL((sum_kernel<T, O, kGoal, kSmallGroups, 8>), grid, block, 0, stream, b);
-    else hipLaunchKernelGGL((sum_kernel<T, O, kGoal, large_groups(kGoal), 16>), grid, block, 0, stream, b);
+    if (a.window == 32) hipLaunchKernelGGL((sum_kernel<T, O, kGoal, 8>), grid, block, 0, stream, b);
+    else hipLaunchKernelGGL((sum_kernel<T, O, kGoal, 16>), grid, block, 0, stream, b);
     return hipGetLastError();
 }
 

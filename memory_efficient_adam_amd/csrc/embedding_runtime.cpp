@@ -145,7 +145,7 @@ SumArgs sum_args(const embedding_shape *s, const Plan &p, Goal goal, const void 
     a.grad = grad;
     a.grad_stride = (uint64_t)s->value_stride;
     a.cols = (uint32_t)s->cols;
-    a.slices = (uint32_t)ceil_div(s->cols, 256 * (p.direct || p.window == 32 ? kSmallGroups : large_groups(goal)));
+    a.slices = (uint32_t)ceil_div(s->cols, 256);
     a.scale = s->scale;
     a.out = table;
     a.out_stride = (uint64_t)s->table_stride;
