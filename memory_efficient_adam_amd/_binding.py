@@ -1,6 +1,7 @@
 """ctypes marshalling for libadam_mi355x.so (names follow include/adam_mi355x.h)."""
 import contextlib
 import ctypes
+import functools
 import operator
 import os
 import sys
@@ -130,14 +131,15 @@ def _check_step_tensors(state, params, grads):
     n = len(state.numels)
     if len(params) != n or len(grads) != n:
         raise ValueError(f"expected {n} params and grads, got {len(params)} and {len(grads)}")
-    gdts = _GRAD_TORCH_DTYPES[state.layout.grad_dtype]
+    f32, gdts = torch.float32, [getattr(torch, d) for d in _GRAD_TORCH_DTYPES[state.layout.grad_dtype]]
     for k, (p, g, want) in enumerate(zip(params, grads, state.numels)):
         if not isinstance(p, torch.Tensor) or not isinstance(g, torch.Tensor):
             raise TypeError(f"tensor {k}: params and grads must be torch tensors")
-        if p.dtype != torch.float32:
+        if p.dtype != f32:
             raise ValueError(f"param {k}: dtype {p.dtype}, expected torch.float32")
-        if str(g.dtype).replace("torch.", "") not in gdts:
-            raise ValueError(f"grad {k}: dtype {g.dtype}, expected one of {gdts} for this layout")
+        if g.dtype not in gdts:
+            raise ValueError(f"grad {k}: dtype {g.dtype}, expected one of "
+                             f"{_GRAD_TORCH_DTYPES[state.layout.grad_dtype]} for this layout")
         if p.numel() != want or g.numel() != want:
             raise ValueError(f"tensor {k}: param/grad numel {p.numel()}/{g.numel()}, the state "
                              f"holds {want}")
@@ -322,8 +324,13 @@ def state_buffer_sizes(numels, storage, amsgrad=False):
     """{buffer name: bytes} of every state buffer a layout has, for caller-owned
     state (adam_step_noalloc): padded elements = sum of pad16(numel), blocks =
     sum of ceil(numel / 2048), as include/adam_mi355x.h lays them out."""
-    padded = sum((int(n) + 15) // 16 * 16 for n in numels)
-    blocks = sum(-(-int(n) // ADAM_BLOCK_SIZE) for n in numels)
+    return dict(_buffer_sizes(tuple([int(n) for n in numels]), storage, bool(amsgrad)))
+
+
+@functools.lru_cache(maxsize=64)
+def _buffer_sizes(numels, storage, amsgrad):
+    padded = sum((n + 15) // 16 * 16 for n in numels)
+    blocks = sum(-(-n // ADAM_BLOCK_SIZE) for n in numels)
     sizes = {"bf16": {"m_bf16": 2 * padded, "v_bf16": 2 * padded},
              "q8": {"m_codes": padded, "v_codes": padded, "m_scale": 4 * blocks,
                     "v_scale": 4 * blocks},
@@ -344,10 +351,10 @@ def adam_step_noalloc(params, grads, buffers, *, storage, grad_dtype="f32", amsg
     tensor of exactly that many bytes (zeros for a new state).  The library
     allocates nothing; its tables live in a fixed device array (calls that
     overlap on one GPU race on it)."""
-    numels = [int(p.numel()) for p in params]
+    numels = tuple([p.numel() for p in params])
     lay = _layout(storage, grad_dtype, ADAM_BLOCK_SIZE, OPT_AMSGRAD if amsgrad else 0)
     _check_step_tensors(AdamState(None, numels, lay), params, grads)
-    want = state_buffer_sizes(numels, storage, amsgrad)
+    want = _buffer_sizes(numels, storage, bool(amsgrad))
     if set(buffers) != set(want):
         raise ValueError(f"buffers must be exactly {sorted(want)}, got {sorted(buffers)}")
     S = (ctypes.c_void_p * len(BUFFERS))()
