@@ -99,6 +99,12 @@ __device__ __forceinline__ uint32_t lane_u32(uint32_t x, uint32_t lane) {
 // ---------------------------------------------------------------- lookup
 constexpr int kLookupThreads = 256;
 
+// out_i = scale table[x_i].  A wave a token and 512 columns: two loads of each lane are
+// under way, and a workgroup's four waves are at four places of the table.  Bound by
+// memory: 16384 tokens of 50304 x 2048, fp32 to bf16: 116 MB (rows named twice come
+// from the caches) in 23 us, 5.0 TB/s, where a large copy reaches 4.9; by the launch
+// for a few tokens (8 tokens: 3 us).
+
 template <class T, class O, class Token>
 __global__ void __launch_bounds__(kLookupThreads) lookup_kernel(LookupArgs a, uint32_t slices, uint64_t units) {
     const uint32_t lane = threadIdx.x & 63u;
@@ -155,6 +161,13 @@ __device__ __forceinline__ void wave_lds_fence() { asm volatile("s_waitcnt lgkmc
 // places its list, 64 positions at a time.  Lanes with one digit are ranked by
 // ballots, not by the order in which atomics arrive, so the result is always
 // the same.
+//
+// What bounds it are the loads of the tokens through each CU's cache: 9 us for 16384 tokens
+// of 64 bits, 21 to 23 for 65536, against 80 to 450 us of the sums behind it.  256 buckets, one a CU:
+// with 128 the whole call on narrow rows takes 1 to 4% more and with 64 3 to 13%, though the
+// XCDs' caches then serve half and a quarter as much; and the largest table whose
+// rows one digit tells apart, 262144 rows, becomes smaller (5 us and more for a
+// second digit).
 template <class Token>
 __global__ void __launch_bounds__(kGroupThreads) group_kernel(GroupArgs a) {
     extern __shared__ uint2 shared[];  // [kGroupWaves][kListed] {row, position}, then counts [kGroupWaves][bins]
@@ -300,7 +313,10 @@ __global__ void __launch_bounds__(kGroupThreads) group_kernel(GroupArgs a) {
     // which of the bucket's rows a token names
     for (uint32_t r = tid; r < width; r += kGroupThreads) a.named[(uint64_t)bucket0 + r] = 0;
     __syncthreads();
-    for (uint32_t i = tid; i < len; i += kGroupThreads) a.named[a.keys[0][base + i]] = 1;
+    for (uint32_t i = tid; i < len; i += kGroupThreads) {
+        const uint32_t row = a.keys[0][base + i];
+        if (row < a.rows) a.named[row] = 1;  // always, unless tokens change under the call
+    }
 }
 
 // ---------------------------------------------------------------- sums
@@ -446,7 +462,7 @@ __device__ __forceinline__ bool meet(const SumArgs &a, f32x4 &sum, uint64_t mine
 }
 
 // A workgroup takes a window of 4 kPer positions, each wave kPer of them, in one
-// slice of the columns.  Of the runs (of one row's positions) in the window
+// slice of 256 columns (512 columns a wave took 0 to 4% more).  Of the runs (of one row's positions) in the window
 //   - those that lie in one wave's positions are summed by it, kBatch positions at a
 //     time: their loads, and those of the rows that runs end on (params and state, which
 //     come from memory in some 2 us under load), are all issued before the first is used;
@@ -455,6 +471,12 @@ __device__ __forceinline__ bool meet(const SumArgs &a, f32x4 &sum, uint64_t mine
 //   - of a run over several windows each leaves a partial sum in memory, and the wave
 //     that comes last adds them up in the order of the windows (kFan at a time,
 //     then those sums).  No wave waits for another workgroup.
+// Bound by memory: for 65536 tokens of 32000 x 4096 (bf16 gradient, words' frequencies, a
+// tenth padding) 900 MB in 180 us when added to a table (5.0 TB/s), 2150 MB in 450 us as
+// an AMSGrad step (4.8 TB/s; the params and three arrays of state lie in four
+// places); for 16384 tokens of 50304 x 2048, 360 MB in 80 us as a step (4.5 TB/s, since the XCDs
+// start some us apart and the last windows run alone).  Batches of four positions:
+// two take 0 to 3% more.
 template <class T, class O, Goal kGoal, int kPer>
 __global__ void __launch_bounds__(kSumThreads) sum_kernel(SumArgs a) {
     constexpr uint32_t kWin = 4 * kPer;
@@ -597,6 +619,8 @@ constexpr int kDirectThreads = 512, kDirectWaves = kDirectThreads / 64;
 // that many tokens name has many workgroups.  Where the whole gradient is written, the workgroups
 // behind zero the rows that no token names, by the same look.
 // kLooks: tokens that a thread looks at.
+// Chains of dependent loads (tokens, the gradient's rows and the table's side) bound it,
+// not bytes: 8 us for 333 tokens of 1000 x 771, written, and for 500 of 32000 x 770 as a step.
 template <class Token, class T, class O, Goal kGoal, uint32_t kLooks>
 __global__ void __launch_bounds__(kDirectThreads) direct_kernel(SumArgs a, const void *tokens, uint32_t splits, uint32_t zero_rows_each) {
     constexpr int kDeep = 32 / (int)sizeof(T);

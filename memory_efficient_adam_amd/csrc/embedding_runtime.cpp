@@ -84,9 +84,11 @@ int64_t token_bytes(const embedding_shape *s) { return s->token_dtype == EMBEDDI
 Span token_span(const embedding_shape *s, const void *tokens) { return Span{tokens, s->tokens * token_bytes(s)}; }
 
 // ---------------------------------------------------------------- gradient
-// Up to this many tokens windows of 32 positions and slices of 256 columns give more
-// waves something to do; of more tokens larger ones leave fewer partial sums and longer
-// accesses.
+// Windows of 32 positions up to this many tokens, which gives more waves something to
+// do; of 64 beyond, which leaves fewer partial sums.  us for a bf16 gradient and 32000 x 4096,
+// 32 / 64: 8192 tokens as frequent as words are, as a step 94 / 100, added to a table 49 / 48,
+// all rows alike 165 / 168 and 67 / 69; 32768 tokens 258 / 251 and 148 / 128, all rows
+// alike 443 / 461 and 188 / 187.
 constexpr int64_t kSmallTokens = 8192;
 
 struct Plan {
