@@ -151,6 +151,8 @@ def _function():
         @staticmethod
         @once_differentiable
         def backward(ctx, grad):
+            if torch.cuda.is_current_stream_capturing():
+                raise ValueError("the backward pass of an eager lookup cannot be captured: record embedding_gradient")
             tokens, = ctx.saved_tensors
             return embedding_gradient(grad.contiguous(), tokens, ctx.rows, scale=ctx.scale,
                                       dtype=ctx.dtype), None, None, None
@@ -162,8 +164,8 @@ def embedding_lookup(table, tokens, *, scale=1.0, dtype=None, out=None, stream=N
     (padding).  table: (rows, cols), fp32 or bf16, rows contiguous; tokens: int32 or
     int64, any shape.  dtype: the result's (default: the table's).  out: a
     tensor of tokens' shape + (cols,) to write instead of a new one.  If the table asks for
-    a gradient it gets the dense one of embedding_gradient (in a backward pass; in neither a
-    graph capture nor forward mode, and with no out)."""
+    a gradient it gets the dense one of embedding_gradient (in a backward pass; neither the lookup
+    nor that pass in a graph capture, not in forward mode, and with no out)."""
     import torch
     _check_tensors(("table", table), ("tokens", tokens), ("out", out))
     if out is not None and dtype not in (None, out.dtype):

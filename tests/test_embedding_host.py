@@ -200,6 +200,11 @@ def test_binding_refuses_host_tensors_and_others():
         B._current_device = B_current
 
 
+def test_a_captured_backward_pass_is_refused(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    _raises(ValueError, "cannot be captured", E._function().backward, None, torch.zeros(3, 4))
+
+
 def test_binding_checks_of_layouts():
     # the shape rules need no device
     assert E._row_stride("x", (3, 4), (4, 1)) == 4 and E._row_stride("x", (3, 4), (9, 1)) == 9
