@@ -11,6 +11,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "adam_element.h"
 #include "embedding_internal.h"
@@ -87,9 +88,11 @@ __device__ __forceinline__ uint32_t row_of(uint64_t token, uint32_t rows) { retu
 // (negative ones are 2^31 and more)
 __device__ __forceinline__ uint32_t row_of(uint32_t token, uint32_t rows) { return token < rows ? token : kNoRow; }
 
-// The token, or 2^32 - 1 where it does not fit 32 bits.
-__device__ __forceinline__ uint32_t low_word(uint64_t token) { return (uint32_t)(token >> 32) == 0 ? (uint32_t)token : kNoRow; }
+// A token in two words.
+__device__ __forceinline__ uint32_t low_word(uint64_t token) { return (uint32_t)token; }
 __device__ __forceinline__ uint32_t low_word(uint32_t token) { return token; }
+__device__ __forceinline__ uint32_t high_word(uint64_t token) { return (uint32_t)(token >> 32); }
+__device__ __forceinline__ uint32_t high_word(uint32_t) { return 0; }
 
 __device__ __forceinline__ uint32_t uniform_u32(uint32_t x) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)x); }
 __device__ __forceinline__ uint32_t lane_u32(uint32_t x, uint32_t lane) {
@@ -145,9 +148,9 @@ __device__ __forceinline__ void zero_rows(O *table, uint64_t stride, uint32_t co
 
 // ---------------------------------------------------------------- grouping
 constexpr int kGroupThreads = 1024, kGroupWaves = 16;
-constexpr int kHeld = 16;  // tokens that a lane has under way at a time
+constexpr int kHeld = 8;  // tokens that a lane has under way at a time (16: 0.4 to 1.5 us more, 4: 0.5 us less for 2304 and more for 65536)
 constexpr uint32_t kGroupChunk = kGroupThreads * kHeld;
-constexpr uint32_t kListed = 512;  // positions of its bucket that a wave keeps: those of half a chunk at most
+constexpr uint32_t kListed = 64 * kHeld;  // positions of its bucket that a wave keeps: those of a chunk at most
 
 // Orders a wave's LDS stores before its loads of what other lanes stored.
 __device__ __forceinline__ void wave_lds_fence() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
@@ -162,8 +165,8 @@ __device__ __forceinline__ void wave_lds_fence() { asm volatile("s_waitcnt lgkmc
 // ballots, not by the order in which atomics arrive, so the result is always
 // the same.
 //
-// What bounds it are the loads of the tokens through each CU's cache: 9 us for 16384 tokens
-// of 64 bits, 21 to 23 for 65536, against 80 to 450 us of the sums behind it.  256 buckets, one a CU:
+// What bounds it is the latency of the tokens' loads in each CU: 9 us for 16384 tokens
+// of 64 bits, 21 for 65536, against 80 to 450 us of the sums behind it.  256 buckets, one a CU:
 // with 128 the whole call on narrow rows takes 1 to 4% more and with 64 3 to 13%, though the
 // XCDs' caches then serve half and a quarter as much; and the largest table whose
 // rows one digit tells apart, 262144 rows, becomes smaller (5 us and more for a
@@ -187,46 +190,46 @@ __global__ void __launch_bounds__(kGroupThreads) group_kernel(GroupArgs a) {
         const uint32_t *keys_in = a.keys[to ^ 1u], *order_in = a.order[to ^ 1u];
         const uint32_t chunks = len / kGroupChunk + (len % kGroupChunk != 0);
         uint32_t below = 0, listed = 0;
-        // The rows at this thread's positions of a chunk.  A row in another bucket, or
-        // none, is 2^32 - 1 or beyond the bucket's rows either way.
-        auto fetch = [&](uint32_t chunk, uint32_t (&key)[kHeld]) {
-            const uint32_t i0 = chunk * kGroupChunk + tid;
-            if (pass == 0) {
-                Token token[kHeld];
+        auto digit_of = [&](uint32_t key) { return (key >> shift) & (bins - 1); };
+        // The bucket's positions in the chunk of `in` from c0 on are listed behind the `listed`
+        // ones and, the first time, counted.  A CU looks at every token, so instructions count: a chunk
+        // that is not the last is loaded without clamping, and a token's words are compared apart (7% of
+        // a call on 65536 tokens of 32 bits and narrow rows, 1% of one on 64 bits).
+        auto visit = [&](const auto *in, uint32_t c0, bool count) {
+            typedef std::remove_cv_t<std::remove_pointer_t<decltype(in)>> Key;
+            Key key[kHeld];
+            if (len - c0 >= kGroupChunk) {
 #pragma unroll
-                for (int j = 0; j < kHeld; ++j)
-                    token[j] = reinterpret_cast<const Token *>(a.tokens)[min(i0 + j * kGroupThreads, len - 1)];
-#pragma unroll
-                for (int j = 0; j < kHeld; ++j) key[j] = low_word(token[j]);
+                for (int j = 0; j < kHeld; ++j) key[j] = (in + c0 + j * kGroupThreads)[tid];
             } else {
 #pragma unroll
-                for (int j = 0; j < kHeld; ++j) key[j] = keys_in[base + min(i0 + j * kGroupThreads, len - 1)];
+                for (int j = 0; j < kHeld; ++j) key[j] = in[min(c0 + j * kGroupThreads + tid, len - 1)];
+#pragma unroll
+                for (int j = 0; j < kHeld; ++j)
+                    if (c0 + j * kGroupThreads + tid >= len) key[j] = ~Key(0);  // names no row
             }
 #pragma unroll
-            for (int j = 0; j < kHeld; ++j)
-                if (i0 + j * kGroupThreads >= len) key[j] = kNoRow;
-        };
-        auto digit_of = [&](uint32_t key) { return (key >> shift) & (bins - 1); };
-        // the bucket's positions of these are listed behind the `listed` ones
-        auto append = [&](uint32_t key, uint32_t i, bool count) {
-            const bool have = key - bucket0 < width;
-            const uint64_t all = __ballot(have);
-            if (count && pass == 0) below += (uint32_t)__popcll(__ballot(key < limit));
-            if (all == 0) return;
-            if (have) {
-                const uint32_t at = listed + (uint32_t)__popcll(all & ((1ull << lane) - 1));
-                if (at < kListed) list[at] = uint2{key, i};
-                if (count) atomicAdd(mine + digit_of(key), 1u);
+            for (int j = 0; j < kHeld; ++j) {
+                const uint32_t low = low_word(key[j]);
+                uint32_t high = high_word(key[j]);
+                if constexpr (sizeof(Key) == 8) asm("" : "+v"(high));  // compared as a word, not with the low one
+                const bool fits = high == 0, have = fits && low - bucket0 < width;
+                const uint64_t all = __builtin_amdgcn_ballot_w64(have);
+                if (count) below += (uint32_t)__popcll(__builtin_amdgcn_ballot_w64(fits && low < limit));
+                if (all == 0) continue;
+                if (have) {
+                    const uint32_t at = listed + (uint32_t)__popcll(all & ((1ull << lane) - 1));
+                    if (at < kListed) list[at] = uint2{low, c0 + j * kGroupThreads + tid};
+                    if (count) atomicAdd(mine + digit_of(low), 1u);
+                }
+                listed += (uint32_t)__popcll(all);
             }
-            listed += (uint32_t)__popcll(all);
         };
         for (uint32_t i = tid; i < kGroupWaves * bins; i += kGroupThreads) counts[i] = 0;
         __syncthreads();
         for (uint32_t c = 0; c < chunks; ++c) {
-            uint32_t key[kHeld];
-            fetch(c, key);
-#pragma unroll
-            for (int j = 0; j < kHeld; ++j) append(key[j], c * kGroupChunk + j * kGroupThreads + tid, true);
+            if (pass == 0) visit(reinterpret_cast<const Token *>(a.tokens), c * kGroupChunk, true);
+            else visit(keys_in + base, c * kGroupChunk, true);
         }
         if (pass == 0 && lane == 0) atomicAdd(&below_sum, below);
         __syncthreads();
@@ -256,7 +259,7 @@ __global__ void __launch_bounds__(kGroupThreads) group_kernel(GroupArgs a) {
             before += w < (int)wave ? s : 0u;
             all += s;
         }
-        if (pass == 0) base = below_sum;
+        if (pass == 0) base = uniform_u32(below_sum);
         const uint32_t first = base + before + incl - digit_total;
         if (tid < bins) {
 #pragma unroll
@@ -268,9 +271,9 @@ __global__ void __launch_bounds__(kGroupThreads) group_kernel(GroupArgs a) {
             for (uint32_t k0 = 0; k0 < listed; k0 += 64) {
                 const uint2 one = k0 + lane < listed ? list[k0 + lane] : uint2{kNoRow, 0};
                 const uint32_t digit = digit_of(one.x);
-                uint64_t same = __ballot(one.x != kNoRow);
+                uint64_t same = __builtin_amdgcn_ballot_w64(one.x != kNoRow);
                 for (uint32_t k = 0; k < a.bits; ++k) {
-                    const uint64_t set = __ballot((digit >> k) & 1u);
+                    const uint64_t set = __builtin_amdgcn_ballot_w64((digit >> k) & 1u);
                     same &= (digit >> k) & 1u ? set : ~set;
                 }
                 if (one.x != kNoRow) {
@@ -289,21 +292,15 @@ __global__ void __launch_bounds__(kGroupThreads) group_kernel(GroupArgs a) {
             place_list();
         } else {
             for (uint32_t c = 0; c < chunks; ++c) {
-                uint32_t key[kHeld];
-                fetch(c, key);
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    listed = 0;
-#pragma unroll
-                    for (int j = half * kHeld / 2; j < (half + 1) * kHeld / 2; ++j)
-                        append(key[j], c * kGroupChunk + j * kGroupThreads + tid, false);
-                    wave_lds_fence();
-                    place_list();
-                    wave_lds_fence();
-                }
+                listed = 0;
+                if (pass == 0) visit(reinterpret_cast<const Token *>(a.tokens), c * kGroupChunk, false);
+                else visit(keys_in + base, c * kGroupChunk, false);
+                wave_lds_fence();
+                place_list();
+                wave_lds_fence();
             }
         }
-        if (pass == 0) len = all;
+        if (pass == 0) len = uniform_u32(all);
         __syncthreads();
     }
     // positions that name no row come last
