@@ -147,10 +147,7 @@ __device__ __forceinline__ void zero_rows(O *table, uint64_t stride, uint32_t co
 }
 
 // ---------------------------------------------------------------- grouping
-constexpr int kGroupThreads = 1024, kGroupWaves = 16;
-constexpr int kHeld = 8;  // tokens that a lane has under way at a time (16: 0.4 to 1.5 us more, 4: 0.5 us less for 2304 and more for 65536)
-constexpr uint32_t kGroupChunk = kGroupThreads * kHeld;
-constexpr uint32_t kListed = 64 * kHeld;  // positions of its bucket that a wave keeps: those of a chunk at most
+constexpr uint32_t kListed = 64 * kHeld;  // positions of its bucket that a wave keeps: those of one look at most
 
 // Orders a wave's LDS stores before its loads of what other lanes stored.
 __device__ __forceinline__ void wave_lds_fence() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
@@ -162,8 +159,10 @@ __device__ __forceinline__ void wave_lds_fence() { asm volatile("s_waitcnt lgkmc
 // LDS; where they are too many it finds them again later) and counts them by digit,
 // the counts become places by a sum over digits and waves, and each wave
 // places its list, 64 positions at a time.  Lanes with one digit are ranked by
-// ballots, not by the order in which atomics arrive, so the result is always
-// the same.
+// ballots, not by the order in which atomics arrive, so positions of one
+// digit keep the order of the waves and of each wave's looks, and the result is always
+// the same.  In the passes after the first that has to be the order which the
+// passes before left, or rows that only their digits tell apart get mixed again (group_part).
 //
 // What bounds it is the latency of the tokens' loads in each CU: 9 us for 16384 tokens
 // of 64 bits, 21 for 65536, against 80 to 450 us of the sums behind it.  256 buckets, one a CU:
@@ -188,28 +187,29 @@ __global__ void __launch_bounds__(kGroupThreads) group_kernel(GroupArgs a) {
     for (uint32_t pass = 0; pass < a.passes; ++pass) {
         const uint32_t shift = pass * kDigitBits, to = (a.passes - 1 - pass) & 1u;
         const uint32_t *keys_in = a.keys[to ^ 1u], *order_in = a.order[to ^ 1u];
-        const uint32_t chunks = len / kGroupChunk + (len % kGroupChunk != 0);
+        const GroupPart part = group_part(pass == 0, wave, len);
         uint32_t below = 0, listed = 0;
         auto digit_of = [&](uint32_t key) { return (key >> shift) & (bins - 1); };
-        // The bucket's positions in the chunk of `in` from c0 on are listed behind the `listed`
-        // ones and, the first time, counted.  A CU looks at every token, so instructions count: a chunk
-        // that is not the last is loaded without clamping, and a token's words are compared apart (7% of
+        // The bucket's positions among those of `in` at p0 + j * step + lane are listed behind the `listed`
+        // ones and, the first time, counted.  A CU looks at every token, so instructions count: where no
+        // position is behind the end they are loaded without clamping, and a token's words are compared apart (7% of
         // a call on 65536 tokens of 32 bits and narrow rows, 1% of one on 64 bits).
-        auto visit = [&](const auto *in, uint32_t c0, bool count) {
+        auto look = [&](auto step, const auto *in, uint32_t p0, bool count) {
             typedef std::remove_cv_t<std::remove_pointer_t<decltype(in)>> Key;
+            constexpr uint32_t kStep = decltype(step)::value;
             Key key[kHeld];
-            if (len - c0 >= kGroupChunk) {
+            if (p0 + (kHeld - 1) * kStep + 64 <= part.end) {
 #pragma unroll
-                for (int j = 0; j < kHeld; ++j) key[j] = (in + c0 + j * kGroupThreads)[tid];
+                for (uint32_t j = 0; j < kHeld; ++j) key[j] = (in + p0 + j * kStep)[lane];
             } else {
 #pragma unroll
-                for (int j = 0; j < kHeld; ++j) key[j] = in[min(c0 + j * kGroupThreads + tid, len - 1)];
+                for (uint32_t j = 0; j < kHeld; ++j) key[j] = in[min(p0 + j * kStep + lane, part.end - 1)];
 #pragma unroll
-                for (int j = 0; j < kHeld; ++j)
-                    if (c0 + j * kGroupThreads + tid >= len) key[j] = ~Key(0);  // names no row
+                for (uint32_t j = 0; j < kHeld; ++j)
+                    if (p0 + j * kStep + lane >= part.end) key[j] = ~Key(0);  // names no row
             }
 #pragma unroll
-            for (int j = 0; j < kHeld; ++j) {
+            for (uint32_t j = 0; j < kHeld; ++j) {
                 const uint32_t low = low_word(key[j]);
                 uint32_t high = high_word(key[j]);
                 if constexpr (sizeof(Key) == 8) asm("" : "+v"(high));  // compared as a word, not with the low one
@@ -219,27 +219,28 @@ __global__ void __launch_bounds__(kGroupThreads) group_kernel(GroupArgs a) {
                 if (all == 0) continue;
                 if (have) {
                     const uint32_t at = listed + (uint32_t)__popcll(all & ((1ull << lane) - 1));
-                    if (at < kListed) list[at] = uint2{low, c0 + j * kGroupThreads + tid};
+                    if (at < kListed) list[at] = uint2{low, p0 + j * kStep + lane};
                     if (count) atomicAdd(mine + digit_of(low), 1u);
                 }
                 listed += (uint32_t)__popcll(all);
             }
         };
+        auto look_at = [&](uint32_t p0, bool count) {
+            if (pass == 0) look(Int<group_step(true)>(), reinterpret_cast<const Token *>(a.tokens), p0, count);
+            else look(Int<group_step(false)>(), keys_in + base, p0, count);
+        };
         for (uint32_t i = tid; i < kGroupWaves * bins; i += kGroupThreads) counts[i] = 0;
         __syncthreads();
-        for (uint32_t c = 0; c < chunks; ++c) {
-            if (pass == 0) visit(reinterpret_cast<const Token *>(a.tokens), c * kGroupChunk, true);
-            else visit(keys_in + base, c * kGroupChunk, true);
-        }
+        for (uint32_t p0 = part.first; p0 < part.end; p0 += part.look) look_at(p0, true);
         if (pass == 0 && lane == 0) atomicAdd(&below_sum, below);
         __syncthreads();
         // counts to places: thread d has digit d's of every wave
         uint32_t held[kGroupWaves], digit_total = 0;
         if (tid < bins) {
 #pragma unroll
-            for (int w = 0; w < kGroupWaves; ++w) held[w] = counts[w * bins + tid];
+            for (uint32_t w = 0; w < kGroupWaves; ++w) held[w] = counts[w * bins + tid];
 #pragma unroll
-            for (int w = 0; w < kGroupWaves; ++w) {
+            for (uint32_t w = 0; w < kGroupWaves; ++w) {
                 const uint32_t c = held[w];
                 held[w] = digit_total;
                 digit_total += c;
@@ -254,16 +255,16 @@ __global__ void __launch_bounds__(kGroupThreads) group_kernel(GroupArgs a) {
         __syncthreads();
         uint32_t before = 0, all = 0;
 #pragma unroll
-        for (int w = 0; w < kGroupWaves; ++w) {
+        for (uint32_t w = 0; w < kGroupWaves; ++w) {
             const uint32_t s = wave_sums[w];
-            before += w < (int)wave ? s : 0u;
+            before += w < wave ? s : 0u;
             all += s;
         }
         if (pass == 0) base = uniform_u32(below_sum);
         const uint32_t first = base + before + incl - digit_total;
         if (tid < bins) {
 #pragma unroll
-            for (int w = 0; w < kGroupWaves; ++w) counts[w * bins + tid] = held[w] + first;
+            for (uint32_t w = 0; w < kGroupWaves; ++w) counts[w * bins + tid] = held[w] + first;
         }
         __syncthreads();
         // places
@@ -291,10 +292,9 @@ __global__ void __launch_bounds__(kGroupThreads) group_kernel(GroupArgs a) {
         if (listed <= kListed) {
             place_list();
         } else {
-            for (uint32_t c = 0; c < chunks; ++c) {
+            for (uint32_t p0 = part.first; p0 < part.end; p0 += part.look) {
                 listed = 0;
-                if (pass == 0) visit(reinterpret_cast<const Token *>(a.tokens), c * kGroupChunk, false);
-                else visit(keys_in + base, c * kGroupChunk, false);
+                look_at(p0, false);
                 wave_lds_fence();
                 place_list();
                 wave_lds_fence();
