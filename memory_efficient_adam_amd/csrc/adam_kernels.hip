@@ -1076,14 +1076,17 @@ __device__ __forceinline__ void process_block(const StepArgs &a, const BlockCtx 
         }
         mmax = fmaxf(mmax, m_hi);
         // p = p*decay - step * m / (sqrt(v) * ibc2 + eps).  When every lane's
-        // group lies in the normal range (v at least 2^-96 for sqrt_rn; |m|
+        // group lies in the normal range (v at least 2^-96 and finite for sqrt_rn; |m|
         // in [2^-40, 2^40] for div_rn, whose divisor sqrt(v) * ibc2 + eps is
         // in [2^-40, 2^77] given ibc2 <= 2^12 and eps in [2^-40, 2^20]) the
         // wave takes the short sequences, otherwise the general ones.  Same
-        // bits either way; one decision per group lets a group's update start
+        // bits either way (an infinite v, which the square of a finite gradient of 2e19 is,
+        // moves p by m / inf = 0 in the general one and would make the short one's remainder NaN); one
+        // decision per group lets a group's update start
         // while the next group's loads are still in flight.
         const float(&vden)[kItems] = kAms ? wo : vo;
-        const bool in_range = a.fast_ok && v_lo >= 0x1p-96f && m_lo >= 0x1p-40f && m_hi <= 0x1p40f;
+        const bool in_range = a.fast_ok && v_lo >= 0x1p-96f && (kAms ? wmax : vmax) < __builtin_inff() && m_lo >= 0x1p-40f &&
+                              m_hi <= 0x1p40f;  // (vmax, wmax: of the groups so far)
         if (__all(in_range)) {
 #pragma unroll
             for (int i = 4 * j; i < 4 * j + 4; ++i) {

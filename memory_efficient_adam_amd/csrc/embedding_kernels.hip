@@ -329,7 +329,7 @@ __device__ __forceinline__ void update4(const SumArgs &a, f32x4 &p, f32x4 g, f32
 #pragma unroll
         for (int k = 0; k < 4; ++k) g[k] = fmaf(a.wd, p[k], g[k]);
     }
-    float m_lo = __builtin_inff(), m_hi = 0.0f, v_lo = __builtin_inff();
+    float m_lo = __builtin_inff(), m_hi = 0.0f, v_lo = __builtin_inff(), v_hi = 0.0f;
     f32x4 below;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -340,8 +340,9 @@ __device__ __forceinline__ void update4(const SumArgs &a, f32x4 &p, f32x4 g, f32
         m_lo = fminf(m_lo, fabsf(m[k]));
         m_hi = fmaxf(m_hi, fabsf(m[k]));
         v_lo = fminf(v_lo, below[k]);
+        v_hi = fmaxf(v_hi, below[k]);
     }
-    if (__all(n <= 0 || (a.fast_ok && v_lo >= 0x1p-96f && m_lo >= 0x1p-40f && m_hi <= 0x1p40f))) {
+    if (__all(n <= 0 || (a.fast_ok && v_lo >= 0x1p-96f && v_hi < __builtin_inff() && m_lo >= 0x1p-40f && m_hi <= 0x1p40f))) {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
             p[k] = fmaf(-a.step, div_rn(m[k], fmaf(sqrt_rn(below[k]), a.ibc2, a.eps)), p[k] * a.decay);
