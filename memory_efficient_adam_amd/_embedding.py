@@ -6,6 +6,7 @@ tensors' sizes, strides and types (the C call's shape, its checks, the workspace
 size) is remembered by exactly those, in _lookup_form and _gradient_form."""
 import ctypes
 import functools
+import math
 
 from . import _binding as B
 from ._binding import AdamError, _check, _on, adam_last_error
@@ -104,9 +105,14 @@ def _current_stream(device):
 
 
 # ---------------------------------------------------------------- lookup
+def _signed(scale):
+    """scale as a key: 0.0 and -0.0 are equal, but not what they make of a value."""
+    return scale, math.copysign(1.0, scale)
+
+
 @functools.lru_cache(maxsize=512)
 def _lookup_form(table_shape, table_stride, table_dtype, token_shape, token_dtype, out_shape, out_stride, out_dtype, scale):
-    """The C call's shape.  out_stride: None for a new tensor's."""
+    """The C call's shape.  out_stride: None for a new tensor's; scale: as _signed has it."""
     if len(table_shape) != 2:
         raise ValueError(f"table: expected (rows, cols), got {tuple(table_shape)}")
     rows, cols = table_shape
@@ -119,17 +125,18 @@ def _lookup_form(table_shape, table_stride, table_dtype, token_shape, token_dtyp
     return embedding_shape(rows, cols, count, _row_stride("table", table_shape, table_stride),
                            cols if out_stride is None else _row_stride("out", out_shape, out_stride),
                            _dtype("table", table_dtype), _dtype("dtype", out_dtype),
-                           _dtype("tokens", token_dtype, _TOKEN_DTYPES), scale)
+                           _dtype("tokens", token_dtype, _TOKEN_DTYPES), scale[0])
 
 
 def _lookup(table, tokens, scale, dtype, out):
     import torch
     if out is None:
-        shape = _lookup_form(table.shape, table.stride(), table.dtype, tokens.shape, tokens.dtype, None, None, dtype, scale)
+        shape = _lookup_form(table.shape, table.stride(), table.dtype, tokens.shape, tokens.dtype, None, None, dtype,
+                             _signed(scale))
         out = torch.empty((*tokens.shape, table.shape[1]), dtype=dtype, device=table.device)
     else:
         shape = _lookup_form(table.shape, table.stride(), table.dtype, tokens.shape, tokens.dtype, out.shape, out.stride(),
-                             dtype, scale)
+                             dtype, _signed(scale))
     tokens = tokens.contiguous()
     _check(library().embedding_lookup(shape, table.data_ptr(), tokens.data_ptr(), out.data_ptr(),
                                       _current_stream(table.get_device())))
@@ -201,7 +208,7 @@ def embedding_gradient_workspace_bytes(tokens, rows, cols):
 def _gradient_form(grad_shape, grad_stride, grad_dtype, token_shape, token_dtype, rows, out_shape, out_stride, out_dtype,
                    scale):
     """The C call's shape and the bytes of its workspace.  out_stride: None for a new
-    tensor's."""
+    tensor's; scale: as _signed has it."""
     if len(grad_shape) != len(token_shape) + 1 or grad_shape[:-1] != token_shape:
         raise ValueError(f"grad must have tokens' shape and one dimension more, got {tuple(grad_shape)} for "
                          f"{tuple(token_shape)}")
@@ -213,7 +220,7 @@ def _gradient_form(grad_shape, grad_stride, grad_dtype, token_shape, token_dtype
         count *= n
     shape = embedding_shape(rows, cols, count, cols if out_stride is None else _row_stride("out", out_shape, out_stride),
                             _row_stride("grad", grad_shape, grad_stride), _dtype("dtype", out_dtype),
-                            _dtype("grad", grad_dtype), _dtype("tokens", token_dtype, _TOKEN_DTYPES), scale)
+                            _dtype("grad", grad_dtype), _dtype("tokens", token_dtype, _TOKEN_DTYPES), scale[0])
     return shape, embedding_gradient_workspace_bytes(count, rows, cols)
 
 
@@ -247,12 +254,12 @@ def embedding_gradient(grad, tokens, rows, *, scale=1.0, dtype=None, out=None, a
             raise ValueError(f"rows must not be negative, got {rows}")
         dtype = dtype or torch.float32
         form = _gradient_form(grad.shape, grad.stride(), grad.dtype, tokens.shape, tokens.dtype, rows, None, None, dtype,
-                              float(scale))
+                              _signed(float(scale)))
     else:
         if dtype not in (None, out.dtype):
             raise ValueError(f"out has dtype {out.dtype}, not {dtype}")
         form = _gradient_form(grad.shape, grad.stride(), grad.dtype, tokens.shape, tokens.dtype, rows, out.shape,
-                              out.stride(), out.dtype, float(scale))
+                              out.stride(), out.dtype, _signed(float(scale)))
     shape, need = form
     with _on(_launching_stream(stream)):
         tokens = tokens.contiguous()
@@ -288,7 +295,7 @@ def embedding_adam_step(table, grad, tokens, buffers, *, amsgrad=False, scale=1.
     if grad.dim() == 0 or grad.shape[-1] != cols:
         raise ValueError(f"grad must have {cols} columns as the table has, got {tuple(grad.shape)}")
     shape, need = _gradient_form(grad.shape, grad.stride(), grad.dtype, tokens.shape, tokens.dtype, rows, table.shape,
-                                 (cols, 1), table.dtype, float(scale))
+                                 (cols, 1), table.dtype, _signed(float(scale)))
     want = _buffer_sizes(rows * cols, bool(amsgrad))
     if buffers.keys() != want.keys():
         raise ValueError(f"buffers must be exactly {sorted(want)}, got {sorted(buffers)}")
