@@ -104,6 +104,13 @@ def _current_stream(device):
     return torch._C._cuda_getCurrentRawStream(device)
 
 
+def _written(tensor):
+    """Counts a tensor that the library wrote as torch counts one written in place, so that a graph which
+    kept its old values raises in its backward pass.  (0.5 us)"""
+    import torch
+    torch._C._increment_version([tensor])
+
+
 # ---------------------------------------------------------------- lookup
 def _signed(scale):
     """scale as a key: 0.0 and -0.0 are equal, but not what they make of a value."""
@@ -130,7 +137,8 @@ def _lookup_form(table_shape, table_stride, table_dtype, token_shape, token_dtyp
 
 def _lookup(table, tokens, scale, dtype, out):
     import torch
-    if out is None:
+    given = out is not None
+    if not given:
         shape = _lookup_form(table.shape, table.stride(), table.dtype, tokens.shape, tokens.dtype, None, None, dtype,
                              _signed(scale))
         out = torch.empty((*tokens.shape, table.shape[1]), dtype=dtype, device=table.device)
@@ -140,6 +148,8 @@ def _lookup(table, tokens, scale, dtype, out):
     tokens = tokens.contiguous()
     _check(library().embedding_lookup(shape, table.data_ptr(), tokens.data_ptr(), out.data_ptr(),
                                       _current_stream(table.get_device())))
+    if given:
+        _written(out)
     return out
 
 
@@ -261,14 +271,17 @@ def embedding_gradient(grad, tokens, rows, *, scale=1.0, dtype=None, out=None, a
         form = _gradient_form(grad.shape, grad.stride(), grad.dtype, tokens.shape, tokens.dtype, rows, out.shape,
                               out.stride(), out.dtype, _signed(float(scale)))
     shape, need = form
+    given = out is not None
     with _on(_launching_stream(stream)):
         tokens = tokens.contiguous()
-        if out is None:
+        if not given:
             out = torch.empty((rows, grad.shape[-1]), dtype=dtype, device=grad.device)
         workspace, nbytes = _workspace(workspace, need, grad.device)
         _check(library().embedding_gradient(shape, grad.data_ptr(), tokens.data_ptr(), out.data_ptr(),
                                             1 if accumulate else 0, workspace.data_ptr(), nbytes,
                                             _current_stream(grad.get_device())))
+    if given:
+        _written(out)
     return out
 
 
@@ -300,9 +313,9 @@ def embedding_adam_step(table, grad, tokens, buffers, *, amsgrad=False, scale=1.
     if buffers.keys() != want.keys():
         raise ValueError(f"buffers must be exactly {sorted(want)}, got {sorted(buffers)}")
     state = (ctypes.c_void_p * len(B.BUFFERS))()
+    _check_tensors(*[("buffer " + name, buffers[name]) for name in want])
     for name, nbytes in want.items():
         b = buffers[name]
-        _check_tensors((f"buffer {name}", b))
         if b.numel() * b.element_size() != nbytes or not b.is_contiguous():
             raise ValueError(f"buffer {name}: must be a contiguous tensor of {nbytes} bytes")
         state[B.BUFFERS[name]] = b.data_ptr()
@@ -314,3 +327,4 @@ def embedding_adam_step(table, grad, tokens, buffers, *, amsgrad=False, scale=1.
         _check(library().embedding_adam_step(shape, table.data_ptr(), grad.data_ptr(), tokens.data_ptr(),
                                              ctypes.addressof(state), hp, layout, workspace.data_ptr(), nbytes,
                                              _current_stream(table.get_device())))
+    _written(table)

@@ -53,3 +53,30 @@ def test_a_scale_keeps_its_sign_whatever_was_called_before(calls):
         _each_call(scale=scale)
         assert [math.copysign(1.0, s) * abs(s) for s in calls.scales] == [scale] * 5
         assert [math.copysign(1.0, s) for s in calls.scales] == [math.copysign(1.0, scale)] * 5, scale
+
+
+def test_what_a_call_writes_is_seen_by_autograd(calls):
+    # a product that keeps x for its backward pass, x written over in between: torch's own calls make
+    # that an error, not a gradient of the new values
+    weight = torch.ones(3, 4, requires_grad=True)
+    table, tokens, grad = torch.ones(5, 4), torch.zeros(3, dtype=torch.int64), torch.ones(3, 4)
+    wide = torch.ones(5, 4, requires_grad=True)
+
+    def after(x, by, write):
+        loss = (x * by).sum()
+        write()
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()
+    out, dense = torch.ones(3, 4), torch.ones(5, 4)
+    after(out, weight, lambda: ma.embedding_lookup(table, tokens, out=out))
+    after(dense, wide, lambda: ma.embedding_gradient(grad, tokens, 5, out=dense))
+    after(dense, wide, lambda: ma.embedding_gradient(grad, tokens, 5, out=dense, accumulate=True))
+    after(table, wide, lambda: ma.embedding_adam_step(table, grad, tokens, _state(20), **HP))
+    # nothing that is only read, and tensors of inference mode have no count
+    before = [x._version for x in (table, tokens, grad)]
+    ma.embedding_lookup(table, tokens, out=out)
+    ma.embedding_gradient(grad, tokens, 5, out=dense)
+    assert [x._version for x in (table, tokens, grad)] == before
+    with torch.inference_mode():
+        ma.embedding_lookup(table, tokens, out=torch.empty(3, 4))
+        ma.embedding_gradient(grad, tokens, 5, out=torch.empty(5, 4))
