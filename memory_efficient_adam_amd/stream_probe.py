@@ -34,6 +34,7 @@ def library():
 # moment bytes per element (m, v) and scales per block of each storage, with
 # the AMSGrad maximum stored as v is
 _LAYOUT = {"bf16": (2, 2, 0), "q8": (1, 1, 2), "q8_v_only": (4, 1, 1)}
+_STORAGES = {name: STORAGES[name] for name in _LAYOUT}  # the probe has no fp32 moments
 
 
 def _grad_bytes(grad_dtype):
@@ -42,7 +43,7 @@ def _grad_bytes(grad_dtype):
 
 def adam_stream_probe_bytes(n_blocks, grad_dtype, storage, amsgrad=False):
     return int(library().adam_stream_probe_bytes(n_blocks, _grad_bytes(grad_dtype),
-                                                 STORAGES[storage], int(amsgrad)))
+                                                 _STORAGES[storage], int(amsgrad)))
 
 
 def probe_buffers_shape(n_blocks, grad_dtype, storage, amsgrad=False):
@@ -94,7 +95,7 @@ def adam_stream_probe(bufs, n_blocks, grad_dtype, storage, amsgrad=False, reside
     ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
     rc = library().adam_stream_probe(ptr(bufs["param"]), ptr(bufs["grad"]), ptr(bufs["m"]),
                                      ptr(bufs["v"]), ptr(bufs["w"]), ptr(bufs["scales"]),
-                                     n_blocks, _grad_bytes(grad_dtype), STORAGES[storage],
+                                     n_blocks, _grad_bytes(grad_dtype), _STORAGES[storage],
                                      int(amsgrad), resident_per_cu, stream.cuda_stream)
     if rc != 0:
         raise RuntimeError(f"adam_stream_probe returned {rc}")
