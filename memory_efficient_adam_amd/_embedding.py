@@ -181,8 +181,11 @@ def embedding_lookup(table, tokens, *, scale=1.0, dtype=None, out=None, stream=N
     (padding).  table: (rows, cols), fp32 or bf16, rows contiguous; tokens: int32 or
     int64, any shape.  dtype: the result's (default: the table's).  out: a
     tensor of tokens' shape + (cols,) to write instead of a new one.  If the table asks for
-    a gradient it gets the dense one of embedding_gradient (in a backward pass; neither the lookup
-    nor that pass in a graph capture, not in forward mode, and with no out)."""
+    a gradient it gets the dense one of embedding_gradient (in a backward pass; not in forward
+    mode, and with no out).  Neither that lookup nor its backward pass can be captured into a graph:
+    a leaf's gradient is summed on the stream of the eager graph that first asked for it, and while such a graph lives
+    a capture that meets it ends the process, which cannot be seen from here.  A captured step
+    records embedding_lookup under torch.no_grad(), and embedding_gradient or embedding_adam_step."""
     import torch
     _check_tensors(("table", table), ("tokens", tokens), ("out", out))
     if out is not None and dtype not in (None, out.dtype):

@@ -165,11 +165,14 @@ __device__ __forceinline__ void wave_lds_fence() { asm volatile("s_waitcnt lgkmc
 // passes before left, or rows that only their digits tell apart get mixed again (group_part).
 //
 // What bounds it is the latency of the tokens' loads in each CU: 9 us for 16384 tokens
-// of 64 bits, 21 for 65536, against 80 to 450 us of the sums behind it.  256 buckets, one a CU:
+// of 64 bits, 21 for 65536, against 80 to 450 us of the sums behind it, where the buckets have
+// much the same.  Where one has half of the tokens (ids in order of frequency) or all of them (one row),
+// its workgroup places them and looks at every token again: 18 and 52 us for half of
+// them, 60 us for 32768 tokens of one row.  256 buckets, one a CU:
 // with 128 the whole call on narrow rows takes 1 to 4% more and with 64 3 to 13%, though the
 // XCDs' caches then serve half and a quarter as much; and the largest table whose
-// rows one digit tells apart, 262144 rows, becomes smaller (5 us and more for a
-// second digit).
+// rows one digit tells apart, 262144 rows, becomes smaller (16384 tokens: 11 us there, 15 to 16 with
+// a second digit, 42 in order of frequency).
 template <class Token>
 __global__ void __launch_bounds__(kGroupThreads) group_kernel(GroupArgs a) {
     extern __shared__ uint2 shared[];  // [kGroupWaves][kListed] {row, position}, then counts [kGroupWaves][bins]

@@ -87,8 +87,8 @@ Span token_span(const embedding_shape *s, const void *tokens) { return Span{toke
 // Windows of 32 positions up to this many tokens, which gives more waves something to
 // do; of 64 beyond, which leaves fewer partial sums.  us for a bf16 gradient and 32000 x 4096,
 // 32 / 64: 8192 tokens as frequent as words are, as a step 94 / 100, added to a table 49 / 48,
-// all rows alike 165 / 168 and 67 / 69; 32768 tokens 258 / 251 and 148 / 128, all rows
-// alike 443 / 461 and 188 / 187.
+// every row as likely as the others 165 / 168 and 67 / 69; 32768 tokens 258 / 251 and 148 / 128,
+// every row as likely 443 / 461 and 188 / 187.
 constexpr int64_t kSmallTokens = 8192;
 
 struct Plan {
